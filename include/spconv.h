@@ -488,6 +488,186 @@ spconv_status spconv_select_dataflow(const void* d_feats, const void* d_weights,
                                      const double* thresholds, int32_t n_thresholds, int32_t reps, void* d_out,
                                      void* hip_stream, spconv_dataflow* best);
 
+/* ---- Attention over packed rows ----
+ *
+ * Softmax attention among the rows of one sequence (a frame's voxels, a
+ * window's, or a serialized scan), for many sequences of different lengths
+ * packed one after another:
+ *   s_ij = scale x q_i . k_j   over the keys j that query i sees,
+ *   lse_i = log sum_j exp(s_ij),   out_i = sum_j exp(s_ij - lse_i) v_j.
+ * A query that sees no key gets out_i = 0 and lse_i = -infinity.
+ *
+ * Sequence b holds the query rows [cu_q[b], cu_q[b + 1]) and the key rows
+ * [cu_k[b], cu_k[b + 1]) (device int32 offsets, batch + 1 each, not
+ * decreasing; equal neighbours are an empty sequence).  Rows before cu[0] or
+ * after cu[batch] belong to none: such queries see no key, such keys get zero
+ * gradients.  Offsets that break these rules give meaningless rows but no
+ * access outside the tensors.
+ *
+ * Visibility: the last query stands at the last key, so query i of a sequence
+ * with n_q queries and n_k keys stands at place p = i + n_k - n_q and sees the
+ * keys j with p - left <= j <= p + right (a negative bound: unbounded).
+ * right = 0 is causal attention; a single new query with n_q = 1 sees all
+ * keys up to its own.
+ *
+ * Heads: `heads` query heads share `kv_heads` key and value heads in groups of
+ * heads / kv_heads consecutive ones.  head_dim is a multiple of 8 up to 128.
+ * Each tensor is [rows][heads][head_dim] in dtype with its own row and head
+ * stride in elements (multiples of 16 bytes; 0 repeats an input), the last
+ * dimension contiguous, 16-byte aligned: q, k and v may be slices of one
+ * projection's output.  out is contiguous [total_q][heads][head_dim], lse
+ * fp32 [total_q][heads].
+ *
+ * Scores, softmax statistics and all sums are fp32.  F16 and BF16 round the
+ * probabilities (and the score gradients) to the dtype as operands of the
+ * matrix instructions; results are rounded once, to nearest even.  Every sum
+ * has a fixed order: the same call gives the same bits.
+ */
+typedef struct spconv_attention {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_row_stride, q_head_stride;
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t total_q, total_k;
+  int32_t batch, heads, kv_heads, head_dim;
+  int32_t left, right;
+  float scale;
+  int32_t dtype; /* spconv_dtype */
+} spconv_attention;
+
+/*
+ * Attention forward: writes d_out and d_lse, every row of them.  Asynchronous
+ * on hip_stream.  Few rows over long keys split the keys over workgroups and
+ * join the parts from the stream's cached workspace.  d_out and d_lse share
+ * no byte with an input.
+ *
+ * Errors: INVALID_ARG (NULL or misaligned pointer, negative or too large
+ * size (total rows x heads below 2^31), kv_heads not dividing heads, stride
+ * not a multiple of 16 bytes or negative, scale not positive and finite,
+ * d_out or d_lse overlapping an input), UNSUPPORTED (dtype, head_dim),
+ * OUT_OF_MEMORY, DEVICE.
+ */
+spconv_status spconv_attention_forward(const spconv_attention* args, void* d_out, float* d_lse, void* hip_stream);
+
+/*
+ * Gradients of the forward: from d_grad_out ([total_q][heads][head_dim], its
+ * own strides) and the forward's d_out and d_lse, writes every row of
+ * d_grad_q ([total_q][heads][head_dim]), d_grad_k and d_grad_v
+ * ([total_k][kv_heads][head_dim]), each in dtype with its own strides (which
+ * must keep rows and heads apart); a shared key head's gradient sums over the
+ * query heads of its group:
+ *   P_ij = exp(s_ij - lse_i),  D_i = grad_out_i . out_i,
+ *   dS_ij = P_ij (grad_out_i . v_j - D_i),
+ *   grad_q_i = scale sum_j dS_ij k_j,  grad_k_j = scale sum_i dS_ij q_i,
+ *   grad_v_j = sum_i P_ij grad_out_i.
+ * Repeated inputs (stride 0) get the gradient of each repetition.  The
+ * gradients share no byte with an input or with each other's values (slices
+ * of one buffer are fine).  Errors as for the forward.
+ */
+typedef struct spconv_attention_gradients {
+  const void* grad_out;
+  int64_t grad_out_row_stride, grad_out_head_stride;
+  void* grad_q;
+  int64_t grad_q_row_stride, grad_q_head_stride;
+  void* grad_k;
+  int64_t grad_k_row_stride, grad_k_head_stride;
+  void* grad_v;
+  int64_t grad_v_row_stride, grad_v_head_stride;
+} spconv_attention_gradients;
+
+spconv_status spconv_attention_backward(const spconv_attention* args, const void* d_out, const float* d_lse,
+                                        const spconv_attention_gradients* grads, void* hip_stream);
+
+/* ---- Head norm and position rotation ----
+ *
+ * One pass over the queries and keys of an attention: the RMS norm of every
+ * head and the rotation of its first rotary_dim elements by the row's
+ * position:
+ *   y_j = x_j w_j / sqrt(mean_i(x_i^2) + eps)     (weight NULL: y = x),
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos) for the pairs
+ *   p = 0 .. rotary_dim / 2 - 1, (a, b) = (2p, 2p + 1) when interleaved, else
+ *   (p, p + rotary_dim / 2).
+ * A position has `axes` components (1: the place in a sequence; 3: a voxel's
+ * z, y, x, read straight from [N][4] coordinates with a row stride of 4); the
+ * pairs are shared out evenly, n = rotary_dim / (2 axes) consecutive pairs
+ * per axis, and pair p takes row (component p / n) of the table, entry
+ * p mod n: d_table is fp32 [extent][n][2], cosine then sine
+ * (spconv_rotary_table makes one; any other angles, such as another scaling
+ * for long ranges, are a table of the caller's).  A component outside
+ * [0, extent) makes the pairs of its axis NaN (no read outside the table).
+ *
+ * rotary_dim = 0: the norm alone (table and positions may be NULL).  head_dim
+ * is a multiple of 8 up to 128, rotary_dim a multiple of 2 axes up to
+ * head_dim, axes in [1, 4].  The arithmetic is fp32, rounded once to dtype.
+ */
+typedef struct spconv_norm_rotary {
+  const void* q; /* [rows][q_heads][head_dim], strides as in spconv_attention */
+  const void* k; /* [rows][k_heads][head_dim] */
+  int64_t q_row_stride, q_head_stride;
+  int64_t k_row_stride, k_head_stride;
+  const void* q_weight; /* [head_dim] in dtype, 16-byte aligned, or NULL */
+  const void* k_weight;
+  const float* table;
+  const int32_t* positions;     /* [rows][axes] */
+  int64_t position_row_stride;  /* in elements */
+  int64_t rows;
+  int32_t q_heads, k_heads, head_dim; /* either heads may be 0: that tensor is absent */
+  int32_t rotary_dim, axes, extent;
+  int32_t interleaved; /* 0 or 1 */
+  float eps;
+  int32_t dtype; /* spconv_dtype */
+} spconv_norm_rotary;
+
+/* Writes d_q_out [rows][q_heads][head_dim] and d_k_out [rows][k_heads][head_dim]
+ * (strides in elements).  An output may be its own input with the same
+ * strides (in place), and otherwise shares no byte with an input.  Errors:
+ * INVALID_ARG, UNSUPPORTED (dtype, head_dim, rotary_dim), DEVICE. */
+spconv_status spconv_norm_rotary_forward(const spconv_norm_rotary* args, void* d_q_out, int64_t q_out_row_stride,
+                                         int64_t q_out_head_stride, void* d_k_out, int64_t k_out_row_stride,
+                                         int64_t k_out_head_stride, void* hip_stream);
+
+/*
+ * Gradients, from the forward's inputs (args: not its outputs) and the
+ * gradients of its outputs: with g the output's gradient turned back,
+ *   grad_weight_j = sum over rows and heads of g_j x_j r  (fp32 [head_dim]),
+ *   grad_x_j = r (g_j w_j - x_j r^2 mean_i(g_i w_i x_i)),  r = 1 / sqrt(mean_i(x_i^2) + eps).
+ * grad_q_weight / grad_k_weight are written when the weight is given and the
+ * pointer is not NULL.  Sums run in a fixed order.  A gradient may take the
+ * place of the gradient it is made from (same pointer and strides), and
+ * otherwise shares no byte with an input.  Errors as for the forward, and
+ * OUT_OF_MEMORY (the partial sums live in the stream's workspace).
+ */
+typedef struct spconv_norm_rotary_gradients {
+  const void* grad_q_out;
+  const void* grad_k_out;
+  int64_t grad_q_out_row_stride, grad_q_out_head_stride;
+  int64_t grad_k_out_row_stride, grad_k_out_head_stride;
+  void* grad_q;
+  void* grad_k;
+  int64_t grad_q_row_stride, grad_q_head_stride;
+  int64_t grad_k_row_stride, grad_k_head_stride;
+  float* grad_q_weight;
+  float* grad_k_weight;
+} spconv_norm_rotary_gradients;
+
+spconv_status spconv_norm_rotary_backward(const spconv_norm_rotary* args, const spconv_norm_rotary_gradients* grads,
+                                          void* hip_stream);
+
+/*
+ * The table of a rotation: d_table[p][i] = (cos, sin) of
+ * p x position_scale x base^(-i / pairs) for p < extent, i < pairs, computed
+ * in double precision and rounded to fp32.  Longer ranges than a model was
+ * trained on are reached by a position_scale below 1 or a larger base.
+ * Errors: INVALID_ARG (NULL or misaligned table, extent or pairs not in
+ * [1, 2^24], base not positive and finite, scale not finite), DEVICE.
+ */
+spconv_status spconv_rotary_table(float* d_table, int32_t extent, int32_t pairs, double base, double position_scale,
+                                  void* hip_stream);
+
 /* Releases a map.  Its buffers go back, in the order of the build's stream,
  * to that stream's cache of map blocks (or to the pool); the caller must not
  * free a map while work on another stream still reads it.  NULL is ignored. */

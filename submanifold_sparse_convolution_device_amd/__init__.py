@@ -42,6 +42,8 @@ EXPORTED = (
     "spconv_map_transpose", "spconv_map_geometry", "spconv_map_out_coords", "spconv_group_plan", "spconv_group_plan_counts",
     "spconv_forward_grouped", "spconv_select_dataflow", "spconv_map_free", "spconv_status_string",
     "spconv_last_error", "spconv_weights_prepare", "spconv_forward_prepared", "spconv_weights_free",
+    "spconv_attention_forward", "spconv_attention_backward", "spconv_norm_rotary_forward", "spconv_norm_rotary_backward",
+    "spconv_rotary_table",
 )
 MAP_KINDS = {0: "submanifold", 1: "strided", 2: "transposed"}
 DATAFLOWS = {0: "fused", 1: "grouped"}
@@ -52,6 +54,46 @@ class spconv_dataflow(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("groups", ctypes.c_int32), ("epsilon", ctypes.c_double),
                 ("S", ctypes.c_double), ("ms", ctypes.c_float), ("fused_ms", ctypes.c_float),
                 ("candidates", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class spconv_attention(ctypes.Structure):
+    """Mirror of the C struct spconv_attention."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [(n, ctypes.c_int64) for n in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                                                 "v_row_stride", "v_head_stride")]
+                + [(n, ctypes.c_void_p) for n in ("cu_q", "cu_k")]
+                + [(n, ctypes.c_int64) for n in ("total_q", "total_k")]
+                + [(n, ctypes.c_int32) for n in ("batch", "heads", "kv_heads", "head_dim", "left", "right")]
+                + [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)])
+
+
+class spconv_attention_gradients(ctypes.Structure):
+    """Mirror of the C struct spconv_attention_gradients."""
+    _fields_ = [f for n in ("grad_out", "grad_q", "grad_k", "grad_v")
+                for f in ((n, ctypes.c_void_p), (n + "_row_stride", ctypes.c_int64), (n + "_head_stride", ctypes.c_int64))]
+
+
+class spconv_norm_rotary(ctypes.Structure):
+    """Mirror of the C struct spconv_norm_rotary."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k")]
+                + [(n, ctypes.c_int64) for n in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride")]
+                + [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "table", "positions")]
+                + [(n, ctypes.c_int64) for n in ("position_row_stride", "rows")]
+                + [(n, ctypes.c_int32) for n in ("q_heads", "k_heads", "head_dim", "rotary_dim", "axes", "extent",
+                                                 "interleaved")]
+                + [("eps", ctypes.c_float), ("dtype", ctypes.c_int32)])
+
+
+class spconv_norm_rotary_gradients(ctypes.Structure):
+    """Mirror of the C struct spconv_norm_rotary_gradients."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("grad_q_out", "grad_k_out")]
+                + [(n, ctypes.c_int64) for n in ("grad_q_out_row_stride", "grad_q_out_head_stride",
+                                                 "grad_k_out_row_stride", "grad_k_out_head_stride")]
+                + [(n, ctypes.c_void_p) for n in ("grad_q", "grad_k")]
+                + [(n, ctypes.c_int64) for n in ("grad_q_row_stride", "grad_q_head_stride", "grad_k_row_stride",
+                                                 "grad_k_head_stride")]
+                + [(n, ctypes.c_void_p) for n in ("grad_q_weight", "grad_k_weight")])
+
 
 _LIB: Optional[ctypes.CDLL] = None
 
@@ -127,6 +169,17 @@ def lib() -> ctypes.CDLL:
     L.spconv_select_dataflow.argtypes = [vp, vp, vp, i32, i32, ctypes.c_int, ctypes.POINTER(f64), i32,
                                          ctypes.POINTER(f64), i32, i32, vp, vp, ctypes.POINTER(spconv_dataflow)]
     L.spconv_select_dataflow.restype = ctypes.c_int
+    pattn, pnorm = ctypes.POINTER(spconv_attention), ctypes.POINTER(spconv_norm_rotary)
+    L.spconv_attention_forward.argtypes = [pattn, vp, vp, vp]
+    L.spconv_attention_forward.restype = ctypes.c_int
+    L.spconv_attention_backward.argtypes = [pattn, vp, vp, ctypes.POINTER(spconv_attention_gradients), vp]
+    L.spconv_attention_backward.restype = ctypes.c_int
+    L.spconv_norm_rotary_forward.argtypes = [pnorm, vp, i64, i64, vp, i64, i64, vp]
+    L.spconv_norm_rotary_forward.restype = ctypes.c_int
+    L.spconv_norm_rotary_backward.argtypes = [pnorm, ctypes.POINTER(spconv_norm_rotary_gradients), vp]
+    L.spconv_norm_rotary_backward.restype = ctypes.c_int
+    L.spconv_rotary_table.argtypes = [vp, i32, i32, f64, f64, vp]
+    L.spconv_rotary_table.restype = ctypes.c_int
     L.spconv_map_free.argtypes, L.spconv_map_free.restype = [vp], None
     L.spconv_status_string.argtypes, L.spconv_status_string.restype = [ctypes.c_int], ctypes.c_char_p
     L.spconv_last_error.argtypes, L.spconv_last_error.restype = [], ctypes.c_char_p
@@ -299,6 +352,31 @@ def spconv_select_dataflow(d_feats: int, d_weights: int, handle: int, c_in: int,
     _check(lib().spconv_select_dataflow(d_feats, d_weights, handle, c_in, c_out, dtype, e, ne, t, nt, int(reps),
                                         d_out, hip_stream, ctypes.byref(best)))
     return best
+
+
+def spconv_attention_forward(args: spconv_attention, d_out: int, d_lse: int, hip_stream: int) -> None:
+    _check(lib().spconv_attention_forward(ctypes.byref(args), d_out, d_lse, hip_stream))
+
+
+def spconv_attention_backward(args: spconv_attention, d_out: int, d_lse: int, grads: spconv_attention_gradients,
+                              hip_stream: int) -> None:
+    _check(lib().spconv_attention_backward(ctypes.byref(args), d_out, d_lse, ctypes.byref(grads), hip_stream))
+
+
+def spconv_norm_rotary_forward(args: spconv_norm_rotary, d_q_out: int, q_out_row_stride: int, q_out_head_stride: int,
+                               d_k_out: int, k_out_row_stride: int, k_out_head_stride: int, hip_stream: int) -> None:
+    _check(lib().spconv_norm_rotary_forward(ctypes.byref(args), d_q_out, q_out_row_stride, q_out_head_stride,
+                                            d_k_out, k_out_row_stride, k_out_head_stride, hip_stream))
+
+
+def spconv_norm_rotary_backward(args: spconv_norm_rotary, grads: spconv_norm_rotary_gradients,
+                                hip_stream: int) -> None:
+    _check(lib().spconv_norm_rotary_backward(ctypes.byref(args), ctypes.byref(grads), hip_stream))
+
+
+def spconv_rotary_table(d_table: int, extent: int, pairs: int, base: float, position_scale: float,
+                        hip_stream: int) -> None:
+    _check(lib().spconv_rotary_table(d_table, extent, pairs, float(base), float(position_scale), hip_stream))
 
 
 def spconv_map_free(handle: int) -> None:
@@ -710,3 +788,233 @@ def forward_with(choice, feats, weights, kmap: SpconvMap, out=None):
     if choice["dataflow"] == "grouped":
         return forward_grouped(feats, weights, kmap, choice["epsilon"], choice["S"], out=out)
     return forward(feats, weights, kmap, out=out)
+
+
+# ------------------------------------------------------------------ attention over packed rows
+
+
+def _dtype_code(dtype):
+    global _DT
+    if _DT is None:
+        torch = _torch()
+        _DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    code = _DT.get(dtype)
+    if code is None:
+        raise SpconvError(4, f"dtype {dtype} not supported")
+    return code
+
+
+def _heads_tensor(name, t, like=None, shape=None):
+    """Checks a [rows, heads, head_dim] tensor whose last dimension is
+    contiguous; returns (pointer, row stride, head stride)."""
+    if not t.is_cuda or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise SpconvError(1, f"{name} must be a [rows, heads, head_dim] tensor on a HIP device with a contiguous last "
+                             "dimension")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise SpconvError(1, f"{name} must have the dtype and device of the other tensors")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise SpconvError(1, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _offsets_tensor(name, cu, device):
+    torch = _torch()
+    if not (cu.is_cuda and cu.device == device and cu.dtype == torch.int32 and cu.dim() == 1 and cu.is_contiguous()
+            and cu.shape[0] >= 1):
+        raise SpconvError(1, f"{name} must be a contiguous int32 [batch + 1] tensor on the tensors' device")
+    return cu.data_ptr()
+
+
+def _attention_args(q, k, v, cu_q, cu_k, causal, window, scale):
+    qp = _heads_tensor("q", q)
+    kp = _heads_tensor("k", k, q)
+    vp = _heads_tensor("v", v, q, k.shape)
+    code = _dtype_code(q.dtype)
+    if k.shape[2] != q.shape[2]:
+        raise SpconvError(1, f"q and k must share one head_dim, not {q.shape[2]} and {k.shape[2]}")
+    cu_k = cu_q if cu_k is None else cu_k
+    a = spconv_attention()
+    a.q, a.q_row_stride, a.q_head_stride = qp
+    a.k, a.k_row_stride, a.k_head_stride = kp
+    a.v, a.v_row_stride, a.v_head_stride = vp
+    a.cu_q, a.cu_k = _offsets_tensor("cu_q", cu_q, q.device), _offsets_tensor("cu_k", cu_k, q.device)
+    if cu_q.shape != cu_k.shape:
+        raise SpconvError(1, "cu_q and cu_k must hold the same number of sequences")
+    a.total_q, a.total_k, a.batch = q.shape[0], k.shape[0], cu_q.shape[0] - 1
+    a.heads, a.kv_heads, a.head_dim = q.shape[1], k.shape[1], q.shape[2]
+    left, right = window
+    a.left, a.right = max(-1, min(int(left), 1 << 30)), max(-1, min(int(right), 1 << 30))
+    if causal:
+        a.right = 0
+    a.scale = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
+    a.dtype = code
+    return a
+
+
+def attention(q, k, v, cu_q, cu_k=None, *, causal: bool = False, window=(-1, -1), scale: Optional[float] = None,
+              out=None, return_lse: bool = False):
+    """Softmax attention over packed sequences: q [total_q, heads, head_dim],
+    k and v [total_k, kv_heads, head_dim] (f32, f16 or bf16; any row and head
+    strides that are multiples of 16 bytes, so slices of one projection's
+    output serve), cu_q and cu_k int32 [batch + 1] row offsets of the
+    sequences on the device (cu_k None: the queries' own).
+
+    The last query of a sequence stands at its last key.  ``causal``: no key
+    after a query's place; ``window`` (left, right): only keys from place -
+    left to place + right, -1 for unbounded.  ``scale`` defaults to
+    head_dim ** -0.5.  A query that sees no key gets zeros.
+
+    Returns out [total_q, heads, head_dim], or (out, lse) with
+    ``return_lse``: lse fp32 [total_q, heads], what
+    :func:`attention_backward` needs."""
+    torch = _torch()
+    a = _attention_args(q, k, v, cu_q, cu_k, causal, window, scale)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif not (out.is_cuda and out.is_contiguous() and out.dtype == q.dtype and out.shape == q.shape):
+        raise SpconvError(1, "out must be a contiguous [total_q, heads, head_dim] tensor of the dtype")
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    with _OnDevice(q.device):
+        spconv_attention_forward(a, out.data_ptr(), lse.data_ptr(), _stream())
+    return (out, lse) if return_lse else out
+
+
+def attention_backward(grad_out, q, k, v, out, lse, cu_q, cu_k=None, *, causal: bool = False, window=(-1, -1),
+                       scale: Optional[float] = None, grads=None):
+    """Gradients (grad_q, grad_k, grad_v) of :func:`attention` from the
+    gradient of its output, its inputs, and its out and lse.  ``grads``: three
+    tensors to write, such as the slices of one projection's gradient."""
+    torch = _torch()
+    a = _attention_args(q, k, v, cu_q, cu_k, causal, window, scale)
+    if not (out.is_cuda and out.is_contiguous() and out.dtype == q.dtype and out.shape == q.shape):
+        raise SpconvError(1, "out must be the forward's contiguous [total_q, heads, head_dim] output")
+    if not (lse.is_cuda and lse.is_contiguous() and lse.dtype == torch.float32 and lse.shape == q.shape[:2]):
+        raise SpconvError(1, "lse must be the forward's contiguous fp32 [total_q, heads] output")
+    if grads is None:
+        grads = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                 torch.empty(k.shape, dtype=q.dtype, device=q.device),
+                 torch.empty(v.shape, dtype=q.dtype, device=q.device))
+    g = spconv_attention_gradients()
+    g.grad_out, g.grad_out_row_stride, g.grad_out_head_stride = _heads_tensor("grad_out", grad_out, q, q.shape)
+    g.grad_q, g.grad_q_row_stride, g.grad_q_head_stride = _heads_tensor("grad_q", grads[0], q, q.shape)
+    g.grad_k, g.grad_k_row_stride, g.grad_k_head_stride = _heads_tensor("grad_k", grads[1], q, k.shape)
+    g.grad_v, g.grad_v_row_stride, g.grad_v_head_stride = _heads_tensor("grad_v", grads[2], q, v.shape)
+    with _OnDevice(q.device):
+        spconv_attention_backward(a, out.data_ptr(), lse.data_ptr(), g, _stream())
+    return tuple(grads)
+
+
+# ------------------------------------------------------------------ head norm and position rotation
+
+
+def rotary_table(extent: int, pairs: int, base: float = 10000.0, position_scale: float = 1.0, device="cuda"):
+    """Cosines and sines [extent, pairs, 2] (fp32) of the angles
+    position * position_scale * base ** (-i / pairs), i < pairs."""
+    torch = _torch()
+    table = torch.empty((int(extent), int(pairs), 2), dtype=torch.float32, device=device)
+    with _OnDevice(table.device):
+        spconv_rotary_table(table.data_ptr(), int(extent), int(pairs), base, position_scale, _stream())
+    return table
+
+
+def _norm_rotary_args(q, k, q_weight, k_weight, table, positions, rotary_dim, interleaved, eps):
+    torch = _torch()
+    if q is None and k is None:
+        raise SpconvError(1, "q and k are both None")
+    like = k if q is None else q
+    a = spconv_norm_rotary()
+    a.rows, a.head_dim, a.dtype = like.shape[0], like.shape[-1], _dtype_code(like.dtype)
+    if q is not None:
+        a.q, a.q_row_stride, a.q_head_stride = _heads_tensor("q", q)
+        a.q_heads = q.shape[1]
+    if k is not None:
+        a.k, a.k_row_stride, a.k_head_stride = _heads_tensor("k", k, like, (a.rows, k.shape[1] if k.dim() == 3 else 0,
+                                                                          a.head_dim))
+        a.k_heads = k.shape[1]
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if not (w.is_cuda and w.device == like.device and w.is_contiguous() and w.dtype == like.dtype
+                and tuple(w.shape) == (a.head_dim,)):
+            raise SpconvError(1, f"{name} must be a contiguous [head_dim] tensor of the dtype on the tensors' device")
+        setattr(a, name, w.data_ptr())
+    a.eps, a.interleaved = float(eps), int(bool(interleaved))
+    if table is None:
+        if rotary_dim:
+            raise SpconvError(1, "a rotation needs a table and positions")
+        a.rotary_dim = 0
+        return a
+    if not (table.is_cuda and table.device == like.device and table.dtype == torch.float32 and table.dim() == 3
+            and table.shape[2] == 2 and table.is_contiguous()):
+        raise SpconvError(1, "table must be a contiguous fp32 [extent, pairs, 2] tensor on the tensors' device")
+    if positions is None or not (positions.is_cuda and positions.device == like.device
+                                 and positions.dtype == torch.int32 and positions.dim() in (1, 2)):
+        raise SpconvError(1, "positions must be an int32 [rows] or [rows, axes] tensor on the tensors' device")
+    axes = 1 if positions.dim() == 1 else positions.shape[1]
+    if positions.shape[0] != a.rows or (positions.dim() == 2 and axes > 1 and positions.stride(1) != 1):
+        raise SpconvError(1, f"positions must hold {a.rows} rows of contiguous components")
+    a.rotary_dim = 2 * axes * table.shape[1] if rotary_dim is None else int(rotary_dim)
+    if a.rotary_dim != 2 * axes * table.shape[1]:
+        raise SpconvError(1, f"rotary_dim = {a.rotary_dim} must be 2 x {axes} axes x {table.shape[1]} pairs of the table")
+    a.table, a.extent, a.axes = table.data_ptr(), table.shape[0], axes
+    a.positions, a.position_row_stride = positions.data_ptr(), positions.stride(0)
+    return a
+
+
+def norm_rotary(q, k, q_weight=None, k_weight=None, table=None, positions=None, *, rotary_dim: Optional[int] = None,
+                interleaved: bool = False, eps: float = 1e-6, out=None):
+    """The RMS norm of every head of q [rows, heads, head_dim] and
+    k [rows, kv_heads, head_dim] (weights [head_dim]; None: no norm) and the
+    rotation of each head's first ``rotary_dim`` elements by the row's
+    position, in one pass.
+
+    ``table`` (:func:`rotary_table`) holds rotary_dim / (2 axes) pairs;
+    ``positions`` is int32 [rows] or [rows, axes], such as ``coords[:, 1:]`` of
+    voxel coordinates.  ``interleaved``: pairs (2p, 2p + 1), else
+    (p, p + rotary_dim / 2).  A position outside the table gives NaN.
+
+    Returns (q', k'); ``out``: two tensors to write, which may be q and k
+    themselves.  Either of q and k may be None."""
+    torch = _torch()
+    a = _norm_rotary_args(q, k, q_weight, k_weight, table, positions, rotary_dim, interleaved, eps)
+    if out is None:
+        out = tuple(None if x is None else torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+    like = k if q is None else q
+    qo = (0, 0, 0) if q is None else _heads_tensor("q_out", out[0], like, q.shape)
+    ko = (0, 0, 0) if k is None else _heads_tensor("k_out", out[1], like, k.shape)
+    with _OnDevice(like.device):
+        spconv_norm_rotary_forward(a, *qo, *ko, _stream())
+    return tuple(out)
+
+
+def norm_rotary_backward(grad_q_out, grad_k_out, q, k, q_weight=None, k_weight=None, table=None, positions=None, *,
+                         rotary_dim: Optional[int] = None, interleaved: bool = False, eps: float = 1e-6, grads=None):
+    """Gradients (grad_q, grad_k, grad_q_weight, grad_k_weight) of
+    :func:`norm_rotary` from the gradients of its outputs and its inputs; the
+    weights' are fp32 [head_dim] (None without a weight).  ``grads``: two
+    tensors for grad_q and grad_k, which may be the outputs' gradients
+    themselves."""
+    torch = _torch()
+    a = _norm_rotary_args(q, k, q_weight, k_weight, table, positions, rotary_dim, interleaved, eps)
+    if grads is None:
+        grads = tuple(None if x is None else torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+    like = k if q is None else q
+    g = spconv_norm_rotary_gradients()
+    weights = [None, None]
+    for i, (name, x, w, go) in enumerate((("q", q, q_weight, grad_q_out), ("k", k, k_weight, grad_k_out))):
+        if x is None:
+            continue
+        p, r, h = _heads_tensor(f"grad_{name}_out", go, like, x.shape)
+        setattr(g, f"grad_{name}_out", p)
+        setattr(g, f"grad_{name}_out_row_stride", r)
+        setattr(g, f"grad_{name}_out_head_stride", h)
+        p, r, h = _heads_tensor(f"grad_{name}", grads[i], like, x.shape)
+        setattr(g, f"grad_{name}", p)
+        setattr(g, f"grad_{name}_row_stride", r)
+        setattr(g, f"grad_{name}_head_stride", h)
+        if w is not None:
+            weights[i] = torch.empty(a.head_dim, dtype=torch.float32, device=like.device)
+            setattr(g, f"grad_{name}_weight", weights[i].data_ptr())
+    with _OnDevice(like.device):
+        spconv_norm_rotary_backward(a, g, _stream())
+    return grads[0], grads[1], weights[0], weights[1]

@@ -522,6 +522,246 @@ spconv_status launch_fused(const spconv_map* map, const spconv::ForwardArgs& a, 
 bool same_plan(const spconv::GroupPlan& x, const spconv::GroupPlan& y) {
   return x.entries == y.entries && x.entry_group == y.entry_group;
 }
+
+// ---- Attention, head norm and rotation ----
+
+// Bytes that a [rows][heads][dim] tensor with these strides spans (0 when it
+// has no values).
+uint64_t span_bytes(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t dim, uint64_t es) {
+  if (rows <= 0 || heads <= 0) return 0;
+  return (static_cast<uint64_t>(rows - 1) * row_stride + static_cast<uint64_t>(heads - 1) * head_stride + dim) * es;
+}
+
+bool ranges_overlap(const void* p, uint64_t np, const void* q, uint64_t nq) {
+  const uint64_t a0 = reinterpret_cast<uintptr_t>(p), b0 = reinterpret_cast<uintptr_t>(q);
+  return np != 0 && nq != 0 && a0 < b0 + nq && b0 < a0 + np;
+}
+
+// A tensor argument of these operators.
+struct Strided {
+  const char* name;
+  const void* p;
+  int64_t rows, row_stride, heads, head_stride, dim;
+  uint64_t es;
+  uint64_t bytes() const { return span_bytes(rows, row_stride, heads, head_stride, dim, es); }
+};
+
+// Alignment, strides and size of a tensor; a written one must keep its rows
+// and heads apart.
+spconv_status check_strided(const Strided& t, bool written) {
+  if (t.rows == 0 || t.heads == 0) return SPCONV_OK;  // nothing of it is read or written
+  if (t.p == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "%s is NULL", t.name);
+  if (!aligned16(t.p)) return fail(SPCONV_ERR_INVALID_ARG, "%s is not 16-byte aligned", t.name);
+  const int64_t piece = static_cast<int64_t>(16 / t.es);
+  if (t.row_stride < 0 || t.head_stride < 0 || t.row_stride % piece != 0 || t.head_stride % piece != 0 ||
+      t.row_stride > (int64_t(1) << 31) || t.head_stride > (int64_t(1) << 40)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "%s: row stride %lld and head stride %lld must be multiples of %lld elements, not negative, below 2^31 and 2^40",
+                t.name, (long long)t.row_stride, (long long)t.head_stride, (long long)piece);
+  }
+  if (written) {
+    // rows of heads, or heads of rows
+    const bool by_rows = t.head_stride >= t.dim && t.row_stride >= (t.heads - 1) * t.head_stride + t.dim;
+    const bool by_heads = t.row_stride >= t.dim && t.head_stride >= (t.rows - 1) * t.row_stride + t.dim;
+    const bool one_row = t.rows == 1 && (t.heads == 1 || t.head_stride >= t.dim);
+    const bool one_head = t.heads == 1 && t.row_stride >= t.dim;
+    if (!by_rows && !by_heads && !one_row && !one_head) {
+      return fail(SPCONV_ERR_INVALID_ARG, "%s: row stride %lld and head stride %lld let values overlap", t.name,
+                  (long long)t.row_stride, (long long)t.head_stride);
+    }
+  }
+  return SPCONV_OK;
+}
+
+spconv_status check_apart(const Strided& out, const Strided& in) {
+  if (!ranges_overlap(out.p, out.bytes(), in.p, in.bytes())) return SPCONV_OK;
+  // Slices of one buffer interleave without sharing a byte: both walk rows by
+  // the same stride, and within a row they keep apart.
+  const uint64_t row = static_cast<uint64_t>(out.row_stride) * out.es;
+  if (out.row_stride == in.row_stride && out.es == in.es && row > 0) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(out.p), b = reinterpret_cast<uintptr_t>(in.p);
+    const uint64_t wa = span_bytes(1, 0, out.heads, out.head_stride, out.dim, out.es);
+    const uint64_t wb = span_bytes(1, 0, in.heads, in.head_stride, in.dim, in.es);
+    const uint64_t gap = b >= a ? (b - a) % row : (row - (a - b) % row) % row;  // from out's row to in's next start
+    if (gap >= wa && row - gap >= wb) return SPCONV_OK;
+  }
+  return fail(SPCONV_ERR_INVALID_ARG, "%s overlaps %s", out.name, in.name);
+}
+
+bool same_place(const Strided& a, const Strided& b) {
+  return a.p == b.p && a.row_stride == b.row_stride && a.head_stride == b.head_stride;
+}
+
+spconv_status check_head_dim(int32_t dtype, int32_t dim) {
+  if (dtype != SPCONV_F32 && dtype != SPCONV_F16 && dtype != SPCONV_BF16) {
+    return fail(SPCONV_ERR_UNSUPPORTED, "dtype %d not supported", dtype);
+  }
+  if (dim < 8 || dim > 128 || dim % 8 != 0) {
+    return fail(SPCONV_ERR_UNSUPPORTED, "head_dim = %d must be a multiple of 8 in [8, 128]", dim);
+  }
+  return SPCONV_OK;
+}
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1024;
+
+struct AttentionTensors {
+  Strided q, k, v, out, lse;
+};
+
+// Validates an attention call and fills its launch arguments.
+spconv_status attention_args(const spconv_attention* x, const void* d_out, const float* d_lse,
+                             spconv::AttentionArgs* a, AttentionTensors* t) {
+  if (x == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "args is NULL");
+  const spconv_status st = check_head_dim(x->dtype, x->head_dim);
+  if (st != SPCONV_OK) return st;
+  if (x->batch < 0 || x->batch > (1 << 24)) return fail(SPCONV_ERR_INVALID_ARG, "batch = %d must lie in [0, 2^24]", x->batch);
+  if (x->heads < 1 || x->kv_heads < 1 || x->heads % x->kv_heads != 0 || x->kv_heads > 65535) {
+    return fail(SPCONV_ERR_INVALID_ARG, "heads = %d must be a positive multiple of kv_heads = %d (at most 65535)", x->heads, x->kv_heads);
+  }
+  if (x->total_q < 0 || x->total_k < 0 || x->total_q > kMaxRows / x->heads || x->total_k > kMaxRows / x->kv_heads ||
+      x->total_q > (int64_t(1) << 30) || x->total_k > (int64_t(1) << 30)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "total_q = %lld, total_k = %lld: rows x heads must stay below 2^31 and rows below 2^30",
+                (long long)x->total_q, (long long)x->total_k);
+  }
+  if (!(x->scale > 0.f) || !std::isfinite(x->scale)) return fail(SPCONV_ERR_INVALID_ARG, "scale = %g must be positive and finite", x->scale);
+  if (x->cu_q == nullptr || x->cu_k == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "cu_q or cu_k is NULL");
+  if ((reinterpret_cast<uintptr_t>(x->cu_q) | reinterpret_cast<uintptr_t>(x->cu_k) | reinterpret_cast<uintptr_t>(d_lse)) & 3u) {
+    return fail(SPCONV_ERR_INVALID_ARG, "cu_q, cu_k and lse must be 4-byte aligned");
+  }
+  const uint64_t es = x->dtype == SPCONV_F32 ? 4u : 2u;
+  const int64_t hd = static_cast<int64_t>(x->heads) * x->head_dim;
+  t->q = {"q", x->q, x->total_q, x->q_row_stride, x->heads, x->q_head_stride, x->head_dim, es};
+  t->k = {"k", x->k, x->total_k, x->k_row_stride, x->kv_heads, x->k_head_stride, x->head_dim, es};
+  t->v = {"v", x->v, x->total_k, x->v_row_stride, x->kv_heads, x->v_head_stride, x->head_dim, es};
+  t->out = {"out", d_out, x->total_q, hd, x->heads, x->head_dim, x->head_dim, es};
+  t->lse = {"lse", d_lse, x->total_q, x->heads, 1, 0, x->heads, 4};
+  for (const Strided* s : {&t->q, &t->k, &t->v, &t->out}) {
+    const spconv_status e = check_strided(*s, false);
+    if (e != SPCONV_OK) return e;
+  }
+  if (x->total_q > 0 && d_lse == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "lse is NULL");
+  a->q = x->q;
+  a->k = x->k;
+  a->v = x->v;
+  a->q_row = x->q_row_stride;
+  a->q_head = x->q_head_stride;
+  a->k_row = x->k_row_stride;
+  a->k_head = x->k_head_stride;
+  a->v_row = x->v_row_stride;
+  a->v_head = x->v_head_stride;
+  a->cu_q = x->cu_q;
+  a->cu_k = x->cu_k;
+  a->batch = x->batch;
+  a->total_q = static_cast<int32_t>(x->total_q);
+  a->total_k = static_cast<int32_t>(x->total_k);
+  a->heads = x->heads;
+  a->kv_heads = x->kv_heads;
+  a->group = x->heads / x->kv_heads;
+  a->dim = x->head_dim;
+  if (a->group > 1) {
+    int l = 1;
+    while ((int64_t(1) << l) < a->group) ++l;
+    a->group_shift = l - 1;
+    a->group_magic = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + a->group - 1) / a->group);
+  }
+  // a bound past every row is none
+  a->left = x->left < 0 || x->left >= (1 << 30) ? -1 : x->left;
+  a->right = x->right < 0 || x->right >= (1 << 30) ? -1 : x->right;
+  a->scale = x->scale;
+  a->dtype = x->dtype;
+  a->out = const_cast<void*>(d_out);
+  a->lse = const_cast<float*>(d_lse);
+  return SPCONV_OK;
+}
+
+// The stream's workspace of `need` bytes for the launches that `launch` makes
+// (NULL when none is needed), held for this stream until they are enqueued.
+template <class F>
+spconv_status with_workspace(size_t need, hipStream_t stream, const char* what, F&& launch) {
+  if (need == 0) {
+    const hipError_t e = launch(static_cast<void*>(nullptr));
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, what);
+  }
+  int device = 0;
+  SPCONV_HIP(hipGetDevice(&device), "hipGetDevice");
+  hipMemPool_t pool = nullptr;
+  spconv_status st = pool_for(device, &pool);
+  if (st != SPCONV_OK) return st;
+  std::lock_guard<std::mutex> lock(g_cache_mu);
+  StreamCache* c = cache_for(device, stream);
+  st = grow_buffer(c->fwd, c->fwd_bytes, need, pool, stream, "workspace allocation");
+  if (st != SPCONV_OK) return st;
+  const hipError_t e = launch(c->fwd);
+  return e == hipSuccess ? SPCONV_OK : hip_fail(e, what);
+}
+
+// Validates a norm and rotation call and fills its launch arguments.
+spconv_status norm_rotary_args(const spconv_norm_rotary* x, spconv::NormRotaryArgs* a, Strided (&in)[2]) {
+  if (x == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "args is NULL");
+  const spconv_status st = check_head_dim(x->dtype, x->head_dim);
+  if (st != SPCONV_OK) return st;
+  if (x->q_heads < 0 || x->k_heads < 0 || x->rows < 0 || x->rows > (int64_t(1) << 30) ||
+      (x->q_heads > 0 && x->rows > kMaxRows / x->q_heads) || (x->k_heads > 0 && x->rows > kMaxRows / x->k_heads)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "rows = %lld, q_heads = %d, k_heads = %d: rows x heads must stay below 2^31 and rows below 2^30",
+                (long long)x->rows, x->q_heads, x->k_heads);
+  }
+  if (!(x->eps >= 0.f) || !std::isfinite(x->eps)) return fail(SPCONV_ERR_INVALID_ARG, "eps = %g must be finite and not negative", x->eps);
+  if (x->interleaved != 0 && x->interleaved != 1) return fail(SPCONV_ERR_INVALID_ARG, "interleaved = %d must be 0 or 1", x->interleaved);
+  if (x->rotary_dim < 0 || x->rotary_dim > x->head_dim) {
+    return fail(SPCONV_ERR_INVALID_ARG, "rotary_dim = %d must lie in [0, head_dim = %d]", x->rotary_dim, x->head_dim);
+  }
+  if (x->rotary_dim > 0) {
+    if (x->axes < 1 || x->axes > 4) return fail(SPCONV_ERR_INVALID_ARG, "axes = %d must lie in [1, 4]", x->axes);
+    if (x->rotary_dim % (2 * x->axes) != 0) {
+      return fail(SPCONV_ERR_UNSUPPORTED, "rotary_dim = %d must be a multiple of 2 axes = %d", x->rotary_dim, 2 * x->axes);
+    }
+    if (x->extent < 1 || x->extent > (1 << 24)) return fail(SPCONV_ERR_INVALID_ARG, "extent = %d must lie in [1, 2^24]", x->extent);
+    if (x->rows > 0 && (x->table == nullptr || x->positions == nullptr)) return fail(SPCONV_ERR_INVALID_ARG, "table or positions is NULL");
+    if ((reinterpret_cast<uintptr_t>(x->table) & 7u) || (reinterpret_cast<uintptr_t>(x->positions) & 3u)) {
+      return fail(SPCONV_ERR_INVALID_ARG, "table must be 8-byte and positions 4-byte aligned");
+    }
+    if (x->position_row_stride < 0 || x->position_row_stride > (int64_t(1) << 31)) {
+      return fail(SPCONV_ERR_INVALID_ARG, "position_row_stride = %lld must lie in [0, 2^31]", (long long)x->position_row_stride);
+    }
+  }
+  if (!aligned16(x->q_weight) || !aligned16(x->k_weight)) return fail(SPCONV_ERR_INVALID_ARG, "the weights must be 16-byte aligned");
+  const uint64_t es = x->dtype == SPCONV_F32 ? 4u : 2u;
+  in[0] = {"q", x->q, x->rows, x->q_row_stride, x->q_heads, x->q_head_stride, x->head_dim, es};
+  in[1] = {"k", x->k, x->rows, x->k_row_stride, x->k_heads, x->k_head_stride, x->head_dim, es};
+  for (int i = 0; i < 2; ++i) {
+    const spconv_status e = check_strided(in[i], false);
+    if (e != SPCONV_OK) return e;
+    a->t[i].x = in[i].p;
+    a->t[i].x_row = in[i].row_stride;
+    a->t[i].x_head = in[i].head_stride;
+    a->t[i].heads = static_cast<int32_t>(in[i].heads);
+  }
+  a->t[0].weight = x->q_weight;
+  a->t[1].weight = x->k_weight;
+  a->rows = static_cast<int32_t>(x->rows);
+  a->dim = x->head_dim;
+  a->rotary = x->rotary_dim;
+  a->axes = x->rotary_dim > 0 ? x->axes : 1;
+  a->interleaved = x->interleaved;
+  a->dtype = x->dtype;
+  a->eps = x->eps;
+  a->table = x->table;
+  a->extent = x->extent;
+  a->positions = x->positions;
+  a->pos_row = x->position_row_stride;
+  return SPCONV_OK;
+}
+
+// Nothing throws across the ABI: a host allocation that fails becomes a status.
+template <class F>
+spconv_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return SPCONV_ERR_OUT_OF_MEMORY;
+  } catch (...) {
+    return SPCONV_ERR_DEVICE;
+  }
+}
 }  // namespace
 
 extern "C" {
@@ -1360,6 +1600,161 @@ spconv_status spconv_select_dataflow(const void* d_feats, const void* d_weights,
   best->ms = win_ms;
   best->candidates = static_cast<int32_t>(cands.size());
   return SPCONV_OK;
+}
+
+spconv_status spconv_attention_forward(const spconv_attention* args, void* d_out, float* d_lse, void* hip_stream) {
+  return guarded([&]() -> spconv_status {
+    g_last_error.clear();
+    spconv::AttentionArgs a;
+    AttentionTensors t;
+    spconv_status st = attention_args(args, d_out, d_lse, &a, &t);
+    if (st != SPCONV_OK) return st;
+    for (const Strided* out : {&t.out, &t.lse}) {
+      for (const Strided* in : {&t.q, &t.k, &t.v}) {
+        st = check_apart(*out, *in);
+        if (st != SPCONV_OK) return st;
+      }
+    }
+    st = check_apart(t.out, t.lse);
+    if (st != SPCONV_OK) return st;
+    if (a.total_q == 0) return SPCONV_OK;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    return with_workspace(spconv::attention_workspace_bytes(a), stream, "attention launch",
+                          [&](void* ws) { return spconv::launch_attention(a, ws, stream); });
+  });
+}
+
+spconv_status spconv_attention_backward(const spconv_attention* args, const void* d_out, const float* d_lse,
+                                        const spconv_attention_gradients* grads, void* hip_stream) {
+  return guarded([&]() -> spconv_status {
+    g_last_error.clear();
+    spconv::AttentionArgs a;
+    AttentionTensors t;
+    spconv_status st = attention_args(args, d_out, d_lse, &a, &t);
+    if (st != SPCONV_OK) return st;
+    if (grads == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grads is NULL");
+    const uint64_t es = t.q.es;
+    const Strided go = {"grad_out", grads->grad_out, a.total_q, grads->grad_out_row_stride, a.heads, grads->grad_out_head_stride, a.dim, es};
+    const Strided gq = {"grad_q", grads->grad_q, a.total_q, grads->grad_q_row_stride, a.heads, grads->grad_q_head_stride, a.dim, es};
+    const Strided gk = {"grad_k", grads->grad_k, a.total_k, grads->grad_k_row_stride, a.kv_heads, grads->grad_k_head_stride, a.dim, es};
+    const Strided gv = {"grad_v", grads->grad_v, a.total_k, grads->grad_v_row_stride, a.kv_heads, grads->grad_v_head_stride, a.dim, es};
+    st = check_strided(go, false);
+    if (st != SPCONV_OK) return st;
+    for (const Strided* out : {&gq, &gk, &gv}) {
+      st = check_strided(*out, true);
+      if (st != SPCONV_OK) return st;
+      for (const Strided& in : {t.q, t.k, t.v, t.out, t.lse, go}) {
+        st = check_apart(*out, in);
+        if (st != SPCONV_OK) return st;
+      }
+    }
+    for (const auto& pair : {std::make_pair(&gq, &gk), std::make_pair(&gq, &gv), std::make_pair(&gk, &gv)}) {
+      st = check_apart(*pair.first, *pair.second);
+      if (st != SPCONV_OK) return st;
+    }
+    a.grad_out = go.p;
+    a.go_row = go.row_stride;
+    a.go_head = go.head_stride;
+    a.grad_q = grads->grad_q;
+    a.gq_row = gq.row_stride;
+    a.gq_head = gq.head_stride;
+    a.grad_k = grads->grad_k;
+    a.gk_row = gk.row_stride;
+    a.gk_head = gk.head_stride;
+    a.grad_v = grads->grad_v;
+    a.gv_row = gv.row_stride;
+    a.gv_head = gv.head_stride;
+    if (a.total_q == 0 && a.total_k == 0) return SPCONV_OK;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    return with_workspace(spconv::attention_backward_workspace_bytes(a), stream, "attention backward launch",
+                          [&](void* ws) { return spconv::launch_attention_backward(a, ws, stream); });
+  });
+}
+
+spconv_status spconv_norm_rotary_forward(const spconv_norm_rotary* args, void* d_q_out, int64_t q_out_row_stride,
+                                         int64_t q_out_head_stride, void* d_k_out, int64_t k_out_row_stride,
+                                         int64_t k_out_head_stride, void* hip_stream) {
+  return guarded([&]() -> spconv_status {
+    g_last_error.clear();
+    spconv::NormRotaryArgs a;
+    Strided in[2];
+    spconv_status st = norm_rotary_args(args, &a, in);
+    if (st != SPCONV_OK) return st;
+    Strided out[2] = {{"q_out", d_q_out, a.rows, q_out_row_stride, a.t[0].heads, q_out_head_stride, a.dim, in[0].es},
+                      {"k_out", d_k_out, a.rows, k_out_row_stride, a.t[1].heads, k_out_head_stride, a.dim, in[0].es}};
+    for (int i = 0; i < 2; ++i) {
+      st = check_strided(out[i], true);
+      for (int j = 0; j < 2 && st == SPCONV_OK; ++j)
+        if (i != j || !same_place(out[i], in[j])) st = check_apart(out[i], in[j]);
+      if (st != SPCONV_OK) return st;
+      a.t[i].y = const_cast<void*>(out[i].p);
+      a.t[i].y_row = out[i].row_stride;
+      a.t[i].y_head = out[i].head_stride;
+    }
+    st = check_apart(out[0], out[1]);
+    if (st != SPCONV_OK) return st;
+    const hipError_t e = spconv::launch_norm_rotary(a, static_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, "norm and rotation launch");
+  });
+}
+
+spconv_status spconv_norm_rotary_backward(const spconv_norm_rotary* args, const spconv_norm_rotary_gradients* grads,
+                                          void* hip_stream) {
+  return guarded([&]() -> spconv_status {
+    g_last_error.clear();
+    spconv::NormRotaryArgs a;
+    Strided in[2];
+    spconv_status st = norm_rotary_args(args, &a, in);
+    if (st != SPCONV_OK) return st;
+    if (grads == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grads is NULL");
+    if ((reinterpret_cast<uintptr_t>(grads->grad_q_weight) | reinterpret_cast<uintptr_t>(grads->grad_k_weight)) & 3u) {
+      return fail(SPCONV_ERR_INVALID_ARG, "the weight gradients must be 4-byte aligned");
+    }
+    const Strided g[2] = {
+        {"grad_q_out", grads->grad_q_out, a.rows, grads->grad_q_out_row_stride, a.t[0].heads, grads->grad_q_out_head_stride, a.dim, in[0].es},
+        {"grad_k_out", grads->grad_k_out, a.rows, grads->grad_k_out_row_stride, a.t[1].heads, grads->grad_k_out_head_stride, a.dim, in[0].es}};
+    const Strided gx[2] = {
+        {"grad_q", grads->grad_q, a.rows, grads->grad_q_row_stride, a.t[0].heads, grads->grad_q_head_stride, a.dim, in[0].es},
+        {"grad_k", grads->grad_k, a.rows, grads->grad_k_row_stride, a.t[1].heads, grads->grad_k_head_stride, a.dim, in[0].es}};
+    for (int i = 0; i < 2; ++i) {
+      st = check_strided(g[i], false);
+      if (st == SPCONV_OK) st = check_strided(gx[i], true);
+      for (int j = 0; j < 2 && st == SPCONV_OK; ++j) {
+        st = check_apart(gx[i], in[j]);
+        if (st == SPCONV_OK && (i != j || !same_place(gx[i], g[j]))) st = check_apart(gx[i], g[j]);
+      }
+      if (st != SPCONV_OK) return st;
+      a.t[i].grad = g[i].p;
+      a.t[i].g_row = g[i].row_stride;
+      a.t[i].g_head = g[i].head_stride;
+      a.t[i].grad_x = const_cast<void*>(gx[i].p);
+      a.t[i].gx_row = gx[i].row_stride;
+      a.t[i].gx_head = gx[i].head_stride;
+    }
+    st = check_apart(gx[0], gx[1]);
+    if (st != SPCONV_OK) return st;
+    a.t[0].grad_weight = grads->grad_q_weight;
+    a.t[1].grad_weight = grads->grad_k_weight;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    return with_workspace(spconv::norm_rotary_backward_workspace_bytes(a), stream, "norm and rotation backward launch",
+                          [&](void* ws) { return spconv::launch_norm_rotary_backward(a, ws, stream); });
+  });
+}
+
+spconv_status spconv_rotary_table(float* d_table, int32_t extent, int32_t pairs, double base, double position_scale,
+                                  void* hip_stream) {
+  g_last_error.clear();
+  if (d_table == nullptr || (reinterpret_cast<uintptr_t>(d_table) & 7u)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "table is NULL or not 8-byte aligned");
+  }
+  if (extent < 1 || extent > (1 << 24) || pairs < 1 || pairs > (1 << 24)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "extent = %d and pairs = %d must lie in [1, 2^24]", extent, pairs);
+  }
+  if (!(base > 0.0) || !std::isfinite(base) || !std::isfinite(position_scale)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "base = %g must be positive and finite, position_scale = %g finite", base, position_scale);
+  }
+  const hipError_t e = spconv::launch_rotary_table(d_table, extent, pairs, base, position_scale, static_cast<hipStream_t>(hip_stream));
+  return e == hipSuccess ? SPCONV_OK : hip_fail(e, "rotary table launch");
 }
 
 void spconv_map_free(spconv_map* map) {

@@ -1,0 +1,272 @@
+// Softmax attention over packed sequences, forward.
+//
+//   s_ij = scale q_i . k_j over the visible keys j of query i's sequence,
+//   lse_i = log sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j;
+//   a query without visible keys gets 0 and lse = -inf.
+//
+// One pass over the keys with the running maximum and sum of the softmax in
+// fp32 registers.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "attention_common.h"
+
+namespace spconv {
+namespace {
+
+using namespace attn;
+
+template <class T, int DP, int WAVES, int BN>
+__global__ __launch_bounds__(64 * WAVES) void k_attention(AttentionArgs a, int nsplit, float* part_out,
+                                                          float* part_lse) {
+  typedef Tile<T, DP> TL;
+  constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
+  constexpr int BM = 32 * WAVES;                // flattened rows per workgroup
+  constexpr int KS = PPR / 2;                   // pieces per half of a row
+  constexpr int NL = (BN * PPR + NT - 1) / NT;  // pieces each thread copies per tile
+  __shared__ uint4 ks[BN * PPR], vs[BN * PPR];
+
+  const Span sp = find_span<BM>(a, false, static_cast<int>(blockIdx.x));
+  if (!sp.any) return;
+  const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int rows = sp.nq * a.group;
+  const int shift = sp.nk - sp.nq;  // a query's place among the keys: its row + shift
+
+  // This lane's query row.
+  const int wr0 = sp.r0 + 32 * wave;
+  const int r = wr0 + (lane & 31);
+  const bool has_row = r < rows;
+  const int tok = div_group(a, has_row ? r : 0);
+  const int head = kvh * a.group + (has_row ? r - tok * a.group : 0);
+  uint4 qf[KS];
+  {
+    const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0 + tok) * a.q_row + static_cast<int64_t>(head) * a.q_head;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      const int piece = 2 * t + half;
+      qf[t] = has_row && piece * kPiece<T> < a.dim ? *reinterpret_cast<const uint4*>(src + piece * kPiece<T>) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  const int place = tok + shift;
+  const int lane_lo = a.left >= 0 ? place - a.left : 0;
+  const int lane_hi = a.right >= 0 ? min(place + a.right + 1, sp.nk) : sp.nk;
+  // Keys that the workgroup's rows, and this wave's, see.
+  const KeyRange wg = key_range(a, sp.nk, div_group(a, sp.r0) + shift, div_group(a, min(sp.r0 + BM, rows) - 1) + shift);
+  const bool wave_on = wr0 < rows;
+  const int wp0 = div_group(a, wave_on ? wr0 : 0) + shift, wp1 = div_group(a, wave_on ? min(wr0 + 32, rows) - 1 : 0) + shift;
+  const KeyRange wv = key_range(a, sp.nk, wp0, wp1);
+  const int full_lo = a.left >= 0 ? wp1 - a.left : 0;                        // keys from here on,
+  const int full_hi = a.right >= 0 ? min(wp0 + a.right + 1, sp.nk) : sp.nk;  // and below here, every row of the wave sees
+
+  const int blocks = wg.hi > wg.lo ? (wg.hi - wg.lo + BN - 1) / BN : 0;
+  const int jb0 = static_cast<int>(static_cast<int64_t>(blocks) * split / nsplit);
+  const int jb1 = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / nsplit);
+
+  const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head;
+  const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head;
+  uint4 kr[NL], vr[NL];
+  auto load = [&](int jb) {
+    const int j0 = wg.lo + jb * BN;
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+      const int j = j0 + row;
+      const bool ok = row < BN && j < sp.nk && piece * kPiece<T> < a.dim;
+      kr[n] = vr[n] = make_uint4(0, 0, 0, 0);
+      if (ok) {
+        kr[n] = *reinterpret_cast<const uint4*>(kbase + static_cast<int64_t>(sp.k0 + j) * a.k_row + piece * kPiece<T>);
+        vr[n] = *reinterpret_cast<const uint4*>(vbase + static_cast<int64_t>(sp.k0 + j) * a.v_row + piece * kPiece<T>);
+      }
+    }
+  };
+
+  floatx16 acc[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) acc[db] = floatx16(0.f);
+  float m = -INFINITY, l = 0.f;  // maximum (in log2 units, see below) and this half's sum
+  const float c = a.scale * kLog2e;
+
+  if (jb0 < jb1) load(jb0);
+  for (int jb = jb0; jb < jb1; ++jb) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+      if (row < BN) {
+        ks[TL::at(row, piece)] = kr[n];
+        vs[TL::at(row, piece)] = vr[n];
+      }
+    }
+    if (jb + 1 < jb1) load(jb + 1);
+    __syncthreads();
+    const int j0 = wg.lo + jb * BN;
+    if (!wave_on || j0 >= wv.hi || j0 + BN <= wv.lo) continue;
+
+    floatx16 s[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      s[b] = floatx16(0.f);
+#pragma unroll
+      for (int t = 0; t < KS; ++t)
+        s[b] = mma_piece<T>(TL::row_piece(ks, 32 * b + (lane & 31), 2 * t + half), qf[t], s[b]);
+    }
+    if (j0 < full_lo || j0 + BN > full_hi) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = j0 + 32 * b + 8 * (i / 4) + 4 * half + (i & 3);
+          s[b][i] = j >= lane_lo && j < lane_hi ? s[b][i] : -INFINITY;
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+    const float m_new = fmaxf(m, halves_max(top) * c);
+    // The sums are rescaled only when a row's maximum has grown by more than
+    // 2^8: until then its terms stay below 2^8 times the largest.
+    if (__any(m_new > m + 8.f)) {
+      const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
+      l *= alpha;
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[db][i] *= alpha;
+      m = m_new;
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float p[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p[i] = fast_exp2(__builtin_fmaf(s[b][i], c, -base));
+        l += p[i];
+      }
+      mma_transposed<T, DP, DB>(vs, 32 * b, lane, p, acc);
+    }
+  }
+
+  const float sum = halves_sum(l);
+  if (!has_row) return;
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // a NaN stays one
+  const float lse = sum == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+  const int64_t row_out = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
+  if (nsplit == 1) {
+    if (half == 0) a.lse[row_out] = lse;
+    T* dst = static_cast<T*>(a.out) + row_out * a.dim;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int d = db * 32 + 8 * g + 4 * half;
+        if (d < a.dim)
+          store4<T>(dst + d, acc[db][4 * g] * inv, acc[db][4 * g + 1] * inv, acc[db][4 * g + 2] * inv, acc[db][4 * g + 3] * inv);
+      }
+  } else {
+    const int64_t at = static_cast<int64_t>(split) * a.total_q * a.heads + row_out;
+    if (half == 0) part_lse[at] = lse;
+    float* dst = part_out + at * a.dim;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int d = db * 32 + 8 * g + 4 * half;
+        if (d < a.dim)
+          store4<float>(dst + d, acc[db][4 * g] * inv, acc[db][4 * g + 1] * inv, acc[db][4 * g + 2] * inv, acc[db][4 * g + 3] * inv);
+      }
+  }
+}
+
+// Joins the splits' outputs: out = sum_s exp(lse_s - lse) out_s.  Four values
+// per thread, in the order of the splits.
+template <class T>
+__global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int nsplit, const float* part_out,
+                                                        const float* part_lse) {
+  const int quads = a.dim / 4;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.heads;
+  const int64_t row = id / quads;
+  if (row >= rows) return;
+  const int quad = static_cast<int>(id - row * quads);
+  float top = -INFINITY;
+  for (int s = 0; s < nsplit; ++s) top = fmaxf(top, part_lse[s * rows + row]);
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, x = 0.f, y = 0.f, z = 0.f, w = 0.f;
+  for (int s = 0; s < nsplit; ++s) {
+    const float ls = part_lse[s * rows + row];
+    if (ls == -INFINITY) continue;
+    const float e = fast_exp2((ls - base) * kLog2e);
+    const float4 o = *reinterpret_cast<const float4*>(part_out + (s * rows + row) * a.dim + 4 * quad);
+    sum += e;
+    x += e * o.x;
+    y += e * o.y;
+    z += e * o.z;
+    w += e * o.w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  store4<T>(static_cast<T*>(a.out) + row * a.dim + 4 * quad, x * inv, y * inv, z * inv, w * inv);
+  if (quad == 0) a.lse[row] = sum == 0.f ? -INFINITY : base + __builtin_amdgcn_logf(sum) * kLn2;
+}
+
+struct Plan {
+  int waves;
+  int64_t slots;
+  int nsplit;
+};
+
+Plan make_forward_plan(const AttentionArgs& a) {
+  Plan p;
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
+  const int64_t mean = rows / std::max(a.batch, 1);
+  p.waves = mean <= 32 ? 1 : mean <= 64 ? 2 : 4;
+  p.slots = span_slots(rows, a.batch, 32 * p.waves);
+  const int64_t tiles = std::max<int64_t>(rows / (32 * p.waves), a.batch) * a.kv_heads * p.waves;
+  const int64_t keys = a.total_k / std::max(a.batch, 1);
+  int64_t split = std::min<int64_t>(2048 / std::max<int64_t>(tiles, 1), keys / 256);
+  if (a.left >= 0 && a.left < keys) split = std::min<int64_t>(split, a.left / 256);
+  p.nsplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(split, 64)));
+  return p;
+}
+
+}  // namespace
+
+size_t attention_workspace_bytes(const AttentionArgs& a) {
+  const Plan p = make_forward_plan(a);
+  if (p.nsplit == 1) return 0;
+  return static_cast<size_t>(p.nsplit) * a.total_q * a.heads * (a.dim + 1) * sizeof(float);
+}
+
+hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t stream) {
+  const Plan p = make_forward_plan(a);
+  float* part_out = static_cast<float*>(workspace);
+  float* part_lse = part_out + static_cast<int64_t>(p.nsplit) * a.total_q * a.heads * a.dim;
+  const hipError_t e = dispatch(a, [&](auto t, auto dp) -> hipError_t {
+    typedef decltype(t) T;
+    constexpr int DP = decltype(dp)::value;
+    const dim3 grid(static_cast<unsigned>(p.slots), static_cast<unsigned>(a.kv_heads), static_cast<unsigned>(p.nsplit));
+    constexpr int BN = sizeof(T) == 2 ? 64 : 32;
+    if (p.waves == 1) {
+      k_attention<T, DP, 1, 32><<<grid, 64, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+    } else if (p.waves == 2) {
+      k_attention<T, DP, 2, BN><<<grid, 128, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+    } else {
+      k_attention<T, DP, 4, BN><<<grid, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+    }
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || p.nsplit == 1) return e;
+  const int64_t quads = static_cast<int64_t>(a.total_q) * a.heads * (a.dim / 4);
+  const unsigned blocks = static_cast<unsigned>((quads + 255) / 256);
+  if (a.dtype == 0) k_attention_join<float><<<blocks, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+  else if (a.dtype == 1) k_attention_join<_Float16><<<blocks, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+  else k_attention_join<__bf16><<<blocks, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+  return hipGetLastError();
+}
+
+}  // namespace spconv

@@ -1,0 +1,486 @@
+// Gradients of softmax attention over packed sequences.
+//
+//   P_ij = exp(s_ij - lse_i),  D_i = dO_i . O_i,
+//   dS_ij = P_ij (dO_i . v_j - D_i),
+//   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dO_i,
+// the sums over i running over every query head that shares the key's head.
+//
+// Two kernels, one with a tile of queries resident that walks the keys (dq),
+// one with a tile of keys resident that walks the queries (dk, dv).  The
+// scores and dO V^T are computed in both, 14 products of d per pair instead
+// of 10, and in exchange every sum has one owner: no atomics, the same bits
+// on every run.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "attention_common.h"
+
+namespace spconv {
+namespace {
+
+using namespace attn;
+
+// fp16 operands of the gradients' products.  dS is as small as the output's
+// gradient times a probability, far below what fp16 holds, so each column
+// (lane) of a dS tile is scaled by a power of two that keeps its largest
+// value near 2^14, and the sums follow when the scale drops.  P^T takes the
+// fixed scale 2^14 (it is at most 1).  bf16 and fp32 need neither.
+template <class T>
+constexpr float kShift = __is_same(T, _Float16) ? 14.f : 0.f;
+
+template <class T, int DB>
+__device__ __forceinline__ void rescale(float (&ds)[16], float& factor, floatx16 (&acc)[DB]) {
+  if constexpr (__is_same(T, _Float16)) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(ds[i]));
+    top = halves_max(top);
+    if (__any(top * factor > 32768.f)) {
+      // 2^(14 - exponent of top), never above the factor so far
+      const int e = static_cast<int>((__builtin_bit_cast(uint32_t, top) >> 23) & 255) - 127;
+      const float now = fminf(factor, __builtin_ldexpf(1.f, 14 - e));
+      const float drop = now / factor;
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[db][i] *= drop;
+      factor = now;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ds[i] *= factor;
+  }
+}
+constexpr float kFirstFactor = 1.2676506002282294e30f;  // 2^100
+
+template <class T, int DP, int WAVES, int BN>
+__global__ __launch_bounds__(64 * WAVES) void k_attention_dq(AttentionArgs a, int nsplit, float* delta, float* part) {
+  typedef Tile<T, DP> TL;
+  constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
+  constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
+  __shared__ uint4 ks[BN * PPR], vs[BN * PPR];
+
+  const Span sp = find_span<BM>(a, false, static_cast<int>(blockIdx.x));
+  if (!sp.any) return;
+  const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int rows = sp.nq * a.group;
+  const int shift = sp.nk - sp.nq;
+
+  const int wr0 = sp.r0 + 32 * wave;
+  const int r = wr0 + (lane & 31);
+  const bool has_row = r < rows;
+  const int tok = div_group(a, has_row ? r : 0);
+  const int head = kvh * a.group + (has_row ? r - tok * a.group : 0);
+  const int64_t row_out = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
+  uint4 qf[KS], gf[KS];
+  float dot = 0.f;
+  {
+    const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0 + tok) * a.q_row + static_cast<int64_t>(head) * a.q_head;
+    const T* gsrc = static_cast<const T*>(a.grad_out) + static_cast<int64_t>(sp.q0 + tok) * a.go_row + static_cast<int64_t>(head) * a.go_head;
+    const T* osrc = static_cast<const T*>(a.out) + row_out * a.dim;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      const int e = (2 * t + half) * kPiece<T>;
+      const bool ok = has_row && e < a.dim;
+      qf[t] = ok ? *reinterpret_cast<const uint4*>(src + e) : make_uint4(0, 0, 0, 0);
+      gf[t] = ok ? *reinterpret_cast<const uint4*>(gsrc + e) : make_uint4(0, 0, 0, 0);
+      const uint4 o = ok ? *reinterpret_cast<const uint4*>(osrc + e) : make_uint4(0, 0, 0, 0);
+      typedef T piece_t __attribute__((ext_vector_type(kPiece<T>)));
+      const piece_t ov = __builtin_bit_cast(piece_t, o), gv = __builtin_bit_cast(piece_t, gf[t]);
+#pragma unroll
+      for (int u = 0; u < kPiece<T>; ++u) dot = __builtin_fmaf(to_f32(gv[u]), to_f32(ov[u]), dot);
+    }
+  }
+  dot = halves_sum(dot);
+  if (has_row && half == 0 && split == 0) delta[row_out] = dot;
+  // exp(s - lse) as exp2(s c - lse2); a row without keys, or past the end, has P = 0
+  float lse2 = INFINITY;
+  if (has_row) {
+    const float v = a.lse[row_out];
+    lse2 = v == -INFINITY ? INFINITY : v * kLog2e - kShift<T>;
+  }
+  const int place = tok + shift;
+  const int lane_lo = a.left >= 0 ? place - a.left : 0;
+  const int lane_hi = a.right >= 0 ? min(place + a.right + 1, sp.nk) : sp.nk;
+  const KeyRange wg = key_range(a, sp.nk, div_group(a, sp.r0) + shift, div_group(a, min(sp.r0 + BM, rows) - 1) + shift);
+  const bool wave_on = wr0 < rows;
+  const int wp0 = div_group(a, wave_on ? wr0 : 0) + shift, wp1 = div_group(a, wave_on ? min(wr0 + 32, rows) - 1 : 0) + shift;
+  const KeyRange wv = key_range(a, sp.nk, wp0, wp1);
+  const int full_lo = a.left >= 0 ? wp1 - a.left : 0;
+  const int full_hi = a.right >= 0 ? min(wp0 + a.right + 1, sp.nk) : sp.nk;
+
+  const int blocks = wg.hi > wg.lo ? (wg.hi - wg.lo + BN - 1) / BN : 0;
+  const int jb0 = static_cast<int>(static_cast<int64_t>(blocks) * split / nsplit);
+  const int jb1 = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / nsplit);
+
+  const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head;
+  const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head;
+  uint4 kr[NL], vr[NL];
+  auto load = [&](int jb) {
+    const int j0 = wg.lo + jb * BN;
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+      const int j = j0 + row;
+      kr[n] = vr[n] = make_uint4(0, 0, 0, 0);
+      if (row < BN && j < sp.nk && piece * kPiece<T> < a.dim) {
+        kr[n] = *reinterpret_cast<const uint4*>(kbase + static_cast<int64_t>(sp.k0 + j) * a.k_row + piece * kPiece<T>);
+        vr[n] = *reinterpret_cast<const uint4*>(vbase + static_cast<int64_t>(sp.k0 + j) * a.v_row + piece * kPiece<T>);
+      }
+    }
+  };
+
+  floatx16 acc[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) acc[db] = floatx16(0.f);
+  float factor = kFirstFactor;
+  const float c = a.scale * kLog2e;
+
+  if (jb0 < jb1) load(jb0);
+  for (int jb = jb0; jb < jb1; ++jb) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+      if (row < BN) {
+        ks[TL::at(row, piece)] = kr[n];
+        vs[TL::at(row, piece)] = vr[n];
+      }
+    }
+    if (jb + 1 < jb1) load(jb + 1);
+    __syncthreads();
+    const int j0 = wg.lo + jb * BN;
+    if (!wave_on || j0 >= wv.hi || j0 + BN <= wv.lo) continue;
+    const bool partial = j0 < full_lo || j0 + BN > full_hi;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      floatx16 s(0.f), dp(0.f);
+#pragma unroll
+      for (int t = 0; t < KS; ++t) {
+        s = mma_piece<T>(TL::row_piece(ks, 32 * b + (lane & 31), 2 * t + half), qf[t], s);
+        dp = mma_piece<T>(TL::row_piece(vs, 32 * b + (lane & 31), 2 * t + half), gf[t], dp);
+      }
+      float ds[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ds[i] = fast_exp2(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - dot);
+      if (partial) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = j0 + 32 * b + 8 * (i / 4) + 4 * half + (i & 3);
+          ds[i] = j >= lane_lo && j < lane_hi ? ds[i] : 0.f;
+        }
+      }
+      rescale<T, DB>(ds, factor, acc);
+      mma_transposed<T, DP, DB>(ks, 32 * b, lane, ds, acc);
+    }
+  }
+
+  if (!has_row) return;
+  const float mul = __is_same(T, _Float16) ? a.scale / factor * 6.103515625e-05f : a.scale;
+  float* pdst = part + (static_cast<int64_t>(split) * a.total_q * a.heads + row_out) * a.dim;
+  T* dst = static_cast<T*>(a.grad_q) + static_cast<int64_t>(sp.q0 + tok) * a.gq_row + static_cast<int64_t>(head) * a.gq_head;
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = db * 32 + 8 * g + 4 * half;
+      if (d >= a.dim) continue;
+      const float x = acc[db][4 * g] * mul, y = acc[db][4 * g + 1] * mul, z = acc[db][4 * g + 2] * mul, w = acc[db][4 * g + 3] * mul;
+      if (nsplit == 1) store4<T>(dst + d, x, y, z, w);
+      else store4<float>(pdst + d, x, y, z, w);
+    }
+}
+
+template <class T, int DP, int WAVES, int BN>
+__global__ __launch_bounds__(64 * WAVES) void k_attention_dkv(AttentionArgs a, int nsplit, const float* delta,
+                                                              float* part_k, float* part_v) {
+  typedef Tile<T, DP> TL;
+  constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
+  constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
+  static_assert(BN <= NT, "one thread per row of a tile");
+  __shared__ uint4 qs[BN * PPR], gs[BN * PPR];
+  __shared__ float4 row_lse[BN / 4], row_delta[BN / 4];
+  __shared__ int4 row_place[BN / 4];
+
+  const Span sp = find_span<BM>(a, true, static_cast<int>(blockIdx.x));
+  if (!sp.any) return;
+  const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int rows = sp.nq * a.group;
+  const int shift = sp.nk - sp.nq;
+
+  const int kw0 = sp.r0 + 32 * wave;
+  const int key = kw0 + (lane & 31);
+  const bool has_key = key < sp.nk;
+  const int64_t krow = static_cast<int64_t>(sp.k0 + (has_key ? key : 0));
+  uint4 kf[KS], vf[KS];
+  {
+    const T* src = static_cast<const T*>(a.k) + krow * a.k_row + static_cast<int64_t>(kvh) * a.k_head;
+    const T* vsrc = static_cast<const T*>(a.v) + krow * a.v_row + static_cast<int64_t>(kvh) * a.v_head;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      const int e = (2 * t + half) * kPiece<T>;
+      const bool ok = has_key && e < a.dim;
+      kf[t] = ok ? *reinterpret_cast<const uint4*>(src + e) : make_uint4(0, 0, 0, 0);
+      vf[t] = ok ? *reinterpret_cast<const uint4*>(vsrc + e) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  // Query rows that see a key of the workgroup: place - left <= key <= place + right.
+  const int kt1 = min(sp.r0 + BM, sp.nk);
+  const int i_lo = a.right >= 0 ? max(sp.r0 - a.right - shift, 0) : 0;
+  const int i_hi = a.left >= 0 ? min(kt1 + a.left - shift, sp.nq) : sp.nq;
+  const int f_lo = i_lo * a.group, f_hi = i_hi * a.group;
+  const int blocks = f_hi > f_lo ? (f_hi - f_lo + BN - 1) / BN : 0;
+  const int rb0 = static_cast<int>(static_cast<int64_t>(blocks) * split / nsplit);
+  const int rb1 = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / nsplit);
+  const bool wave_on = kw0 < sp.nk;
+  const int kw1 = min(kw0 + 32, sp.nk) - 1;  // last key of the wave
+
+  uint4 qr[NL], gr[NL];
+  float lse_r = INFINITY, delta_r = 0.f;
+  int place_r = 0;
+  auto load = [&](int rb) {
+    const int r0 = f_lo + rb * BN;
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+      const int r = r0 + row;
+      qr[n] = gr[n] = make_uint4(0, 0, 0, 0);
+      if (row < BN && r < rows && piece * kPiece<T> < a.dim) {
+        const int tok = div_group(a, r), head = kvh * a.group + r - tok * a.group;
+        qr[n] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0 + tok) * a.q_row + static_cast<int64_t>(head) * a.q_head + piece * kPiece<T>);
+        gr[n] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.grad_out) + static_cast<int64_t>(sp.q0 + tok) * a.go_row + static_cast<int64_t>(head) * a.go_head + piece * kPiece<T>);
+      }
+    }
+    if (tid < BN) {
+      const int r = r0 + tid;
+      lse_r = INFINITY;
+      delta_r = 0.f;
+      place_r = 0;
+      if (r < rows) {
+        const int tok = div_group(a, r), head = kvh * a.group + r - tok * a.group;
+        const int64_t at = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
+        const float v = a.lse[at];
+        lse_r = v == -INFINITY ? INFINITY : v * kLog2e - kShift<T>;
+        delta_r = delta[at];
+        place_r = tok + shift;
+      }
+    }
+  };
+
+  floatx16 dk[DB], dv[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) {
+    dk[db] = floatx16(0.f);
+    dv[db] = floatx16(0.f);
+  }
+  float factor = kFirstFactor;
+  const float c = a.scale * kLog2e;
+
+  if (rb0 < rb1) load(rb0);
+  for (int rb = rb0; rb < rb1; ++rb) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+      if (row < BN) {
+        qs[TL::at(row, piece)] = qr[n];
+        gs[TL::at(row, piece)] = gr[n];
+      }
+    }
+    if (tid < BN) {
+      reinterpret_cast<float*>(row_lse)[tid] = lse_r;
+      reinterpret_cast<float*>(row_delta)[tid] = delta_r;
+      reinterpret_cast<int*>(row_place)[tid] = place_r;
+    }
+    if (rb + 1 < rb1) load(rb + 1);
+    __syncthreads();
+    if (!wave_on) continue;
+    const int r0 = f_lo + rb * BN;
+    const int p0 = div_group(a, r0) + shift, p1 = div_group(a, min(r0 + BN, rows) - 1) + shift;  // places of the tile
+    if ((a.right >= 0 && kw0 > p1 + a.right) || (a.left >= 0 && kw1 < p0 - a.left)) continue;
+    const bool partial = (a.right >= 0 && kw1 > p0 + a.right) || (a.left >= 0 && kw0 < p1 - a.left);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      floatx16 s(0.f), dp(0.f);
+#pragma unroll
+      for (int t = 0; t < KS; ++t) {
+        s = mma_piece<T>(TL::row_piece(qs, 32 * b + (lane & 31), 2 * t + half), kf[t], s);
+        dp = mma_piece<T>(TL::row_piece(gs, 32 * b + (lane & 31), 2 * t + half), vf[t], dp);
+      }
+      float p[16], ds[16];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 ls = row_lse[8 * b + 2 * g + half], de = row_delta[8 * b + 2 * g + half];
+        const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, dv4[4] = {de.x, de.y, de.z, de.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = 4 * g + u;
+          p[i] = fast_exp2(__builtin_fmaf(s[i], c, -lv[u]));
+          ds[i] = p[i] * (dp[i] - dv4[u]);
+        }
+      }
+      if (partial) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int4 pl = row_place[8 * b + 2 * g + half];
+          const int pv[4] = {pl.x, pl.y, pl.z, pl.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const bool seen = (a.right < 0 || key <= pv[u] + a.right) && (a.left < 0 || key >= pv[u] - a.left);
+            p[4 * g + u] = seen ? p[4 * g + u] : 0.f;
+            ds[4 * g + u] = seen ? ds[4 * g + u] : 0.f;
+          }
+        }
+      }
+      mma_transposed<T, DP, DB>(gs, 32 * b, lane, p, dv);
+      rescale<T, DB>(ds, factor, dk);
+      mma_transposed<T, DP, DB>(qs, 32 * b, lane, ds, dk);
+    }
+  }
+
+  if (!has_key) return;
+  constexpr float unshift = __is_same(T, _Float16) ? 6.103515625e-05f : 1.f;  // 2^-14
+  const float mul = __is_same(T, _Float16) ? a.scale / factor * unshift : a.scale;
+  const int64_t at = (static_cast<int64_t>(split) * a.total_k * a.kv_heads + krow * a.kv_heads + kvh) * a.dim;
+  T* kdst = static_cast<T*>(a.grad_k) + krow * a.gk_row + static_cast<int64_t>(kvh) * a.gk_head;
+  T* vdst = static_cast<T*>(a.grad_v) + krow * a.gv_row + static_cast<int64_t>(kvh) * a.gv_head;
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = db * 32 + 8 * g + 4 * half;
+      if (d >= a.dim) continue;
+      const float x = dk[db][4 * g] * mul, y = dk[db][4 * g + 1] * mul, z = dk[db][4 * g + 2] * mul, w = dk[db][4 * g + 3] * mul;
+      const float x2 = dv[db][4 * g] * unshift, y2 = dv[db][4 * g + 1] * unshift, z2 = dv[db][4 * g + 2] * unshift, w2 = dv[db][4 * g + 3] * unshift;
+      if (nsplit == 1) {
+        store4<T>(kdst + d, x, y, z, w);
+        store4<T>(vdst + d, x2, y2, z2, w2);
+      } else {
+        store4<float>(part_k + at + d, x, y, z, w);
+        store4<float>(part_v + at + d, x2, y2, z2, w2);
+      }
+    }
+}
+
+// Adds the splits' partial gradients in order and rounds once.
+template <class T>
+__global__ __launch_bounds__(256) void k_attention_grad_join(const float* part, int nsplit, int64_t rows, int heads,
+                                                             int dim, T* dst, int64_t row_stride, int64_t head_stride) {
+  const int quads = dim / 4;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t rh = id / quads;
+  if (rh >= rows * heads) return;
+  const int quad = static_cast<int>(id - rh * quads);
+  const int64_t row = rh / heads;
+  const int head = static_cast<int>(rh - row * heads);
+  float x = 0.f, y = 0.f, z = 0.f, w = 0.f;
+  for (int s = 0; s < nsplit; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(part + (s * rows * heads + rh) * dim + 4 * quad);
+    x += v.x;
+    y += v.y;
+    z += v.z;
+    w += v.w;
+  }
+  store4<T>(dst + row * row_stride + head * head_stride + 4 * quad, x, y, z, w);
+}
+
+template <class T>
+void launch_join(const float* part, int nsplit, int64_t rows, int heads, int dim, void* dst, int64_t row_stride,
+                 int64_t head_stride, hipStream_t stream) {
+  const int64_t quads = rows * heads * (dim / 4);
+  k_attention_grad_join<T><<<static_cast<unsigned>((quads + 255) / 256), 256, 0, stream>>>(
+      part, nsplit, rows, heads, dim, static_cast<T*>(dst), row_stride, head_stride);
+}
+
+struct Plan {
+  int q_waves, k_waves;
+  int64_t q_slots, k_slots;
+  int q_split, k_split;
+};
+
+int waves_for(int64_t mean) { return mean <= 32 ? 1 : mean <= 64 ? 2 : 4; }
+
+Plan make_backward_plan(const AttentionArgs& a) {
+  Plan p;
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
+  const int64_t batch = std::max(a.batch, 1);
+  p.q_waves = waves_for(rows / batch);
+  p.k_waves = waves_for(a.total_k / batch);
+  p.q_slots = span_slots(rows, a.batch, 32 * p.q_waves);
+  p.k_slots = span_slots(a.total_k, a.batch, 32 * p.k_waves);
+  auto split = [&](int64_t tiles, int64_t depth) {
+    const int64_t s = std::min<int64_t>(1024 / std::max<int64_t>(tiles, 1), depth / 256);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, 32)));
+  };
+  int64_t q_depth = a.total_k / batch, k_depth = rows / batch;
+  if (a.left >= 0 && a.right >= 0) {
+    const int64_t band = static_cast<int64_t>(a.left) + a.right + 1;
+    q_depth = std::min<int64_t>(q_depth, band);
+    k_depth = std::min<int64_t>(k_depth, band * a.group);
+  }
+  p.q_split = split(std::max<int64_t>(rows / (32 * p.q_waves), a.batch) * a.kv_heads * p.q_waves, q_depth);
+  p.k_split = split(std::max<int64_t>(a.total_k / (32 * p.k_waves), a.batch) * a.kv_heads * p.k_waves, k_depth);
+  return p;
+}
+
+struct Workspace {
+  size_t delta, q, k, v, total;  // offsets in bytes
+};
+Workspace layout(const AttentionArgs& a, const Plan& p) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  const size_t nq = static_cast<size_t>(a.total_q) * a.heads, nk = static_cast<size_t>(a.total_k) * a.kv_heads;
+  Workspace w;
+  w.delta = 0;
+  w.q = up(nq * sizeof(float));
+  w.k = w.q + (p.q_split > 1 ? up(nq * a.dim * p.q_split * sizeof(float)) : 0);
+  const size_t part = p.k_split > 1 ? up(nk * a.dim * p.k_split * sizeof(float)) : 0;
+  w.v = w.k + part;
+  w.total = w.v + part;
+  return w;
+}
+
+}  // namespace
+
+size_t attention_backward_workspace_bytes(const AttentionArgs& a) { return layout(a, make_backward_plan(a)).total; }
+
+hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hipStream_t stream) {
+  const Plan p = make_backward_plan(a);
+  const Workspace w = layout(a, p);
+  char* base = static_cast<char*>(workspace);
+  float* delta = reinterpret_cast<float*>(base + w.delta);
+  float* part_q = reinterpret_cast<float*>(base + w.q);
+  float* part_k = reinterpret_cast<float*>(base + w.k);
+  float* part_v = reinterpret_cast<float*>(base + w.v);
+  return dispatch(a, [&](auto t, auto dp) -> hipError_t {
+    typedef decltype(t) T;
+    constexpr int DP = decltype(dp)::value;
+    constexpr int BN = 32;
+    if (a.total_q > 0) {
+      const dim3 grid(static_cast<unsigned>(p.q_slots), static_cast<unsigned>(a.kv_heads), static_cast<unsigned>(p.q_split));
+      if (p.q_waves == 1) k_attention_dq<T, DP, 1, BN><<<grid, 64, 0, stream>>>(a, p.q_split, delta, part_q);
+      else if (p.q_waves == 2) k_attention_dq<T, DP, 2, BN><<<grid, 128, 0, stream>>>(a, p.q_split, delta, part_q);
+      else k_attention_dq<T, DP, 4, BN><<<grid, 256, 0, stream>>>(a, p.q_split, delta, part_q);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      if (p.q_split > 1) launch_join<T>(part_q, p.q_split, a.total_q, a.heads, a.dim, a.grad_q, a.gq_row, a.gq_head, stream);
+    }
+    if (a.total_k > 0) {
+      const dim3 grid(static_cast<unsigned>(p.k_slots), static_cast<unsigned>(a.kv_heads), static_cast<unsigned>(p.k_split));
+      if (p.k_waves == 1) k_attention_dkv<T, DP, 1, BN><<<grid, 64, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
+      else if (p.k_waves == 2) k_attention_dkv<T, DP, 2, BN><<<grid, 128, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
+      else k_attention_dkv<T, DP, 4, BN><<<grid, 256, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      if (p.k_split > 1) {
+        launch_join<T>(part_k, p.k_split, a.total_k, a.kv_heads, a.dim, a.grad_k, a.gk_row, a.gk_head, stream);
+        launch_join<T>(part_v, p.k_split, a.total_k, a.kv_heads, a.dim, a.grad_v, a.gv_row, a.gv_head, stream);
+      }
+    }
+    return hipGetLastError();
+  });
+}
+
+}  // namespace spconv

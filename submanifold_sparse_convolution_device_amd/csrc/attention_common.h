@@ -1,0 +1,266 @@
+// Shared device code of the attention kernels (attention.hip,
+// attention_backward.hip): MFMA operands, LDS tiles, and the cut of packed
+// sequences into tiles of rows.
+//
+// Every product is a 32 x 32 MFMA tile C[m][n] = sum_k A[m][k] B[k][n], with
+// C in 16 registers per lane: lane l holds column n = l mod 32 and rows
+// m = 8 (i / 4) + 4 (l / 32) + i mod 4.  The contracted index may run in any
+// order that A and B share, and the kernels choose it so that a C tile (of
+// scores) is the B operand of the next product as it stands:
+//   16-bit types, 32x32x16: step s, half h = l / 32, element j is row
+//     16 s + 8 (j / 4) + 4 h + j mod 4, the C rows of registers 8 s + j;
+//   fp32, 32x32x2: step i, half h is row 8 (i / 4) + 4 h + i mod 4.
+// So the products run transposed: S^T = K Q^T puts a query in each lane's
+// column (its softmax needs one exchange, between the halves), and
+// O^T = V^T P^T takes P^T from registers and V^T through the transposing LDS
+// read (16 bits) or plain column reads (fp32).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+
+namespace spconv {
+namespace attn {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Elements per 16-byte piece.
+template <class T>
+constexpr int kPiece = 16 / static_cast<int>(sizeof(T));
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v) {
+  return static_cast<float>(v);
+}
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// max / sum of a value over the two halves (lanes l and l xor 32).
+struct HalfPair {
+  float lo, hi;
+};
+__device__ __forceinline__ HalfPair halves(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t lo = r[0], hi = r[1];  // scalars first: a bit cast of a vector's element reads element 0
+  return {__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+__device__ __forceinline__ float halves_max(float v) {
+  const HalfPair p = halves(v);
+  return fmaxf(p.lo, p.hi);
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  const HalfPair p = halves(v);
+  return p.lo + p.hi;
+}
+
+// C += A B over one 16-byte piece per lane of each operand (the piece of
+// half h is piece 2 t + h of the row): 16 contracted elements in 16 bits, 8
+// in fp32.
+template <class T>
+__device__ __forceinline__ floatx16 mma_piece(uint4 a, uint4 b, floatx16 c) {
+  if constexpr (__is_same(T, _Float16)) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+  } else if constexpr (__is_same(T, __bf16)) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  } else {
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, a.x), __builtin_bit_cast(float, b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, a.y), __builtin_bit_cast(float, b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, a.z), __builtin_bit_cast(float, b.z), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, a.w), __builtin_bit_cast(float, b.w), c, 0, 0, 0);
+    return c;
+  }
+}
+
+// A tile of rows in LDS, DP elements each, in 16-byte pieces that are XOR-ed
+// with a function of the row so that 16 rows of one column of pieces, and 4
+// rows of two neighbouring columns, fall on different banks.
+template <class T, int DP>
+struct Tile {
+  static constexpr int PPR = DP / kPiece<T>;  // pieces per row
+  // Bits of the piece index that the swizzle may change.
+  static constexpr int MASK = PPR % 16 == 0 ? 15 : PPR % 8 == 0 ? 7 : 3;
+  __device__ static __forceinline__ int swz(int row) {
+    if constexpr (MASK == 15) return ((row & 3) << 1 | (row >> 2 & 1) | (row & 8)) & MASK;
+    if constexpr (MASK == 7) return (row & 3) << 1 | (row >> 2 & 1);
+    return (row >> 1) & 3;
+  }
+  __device__ static __forceinline__ int at(int row, int piece) { return row * PPR + (piece ^ swz(row)); }
+  // A operand by rows: lane's row (m) and piece.
+  __device__ static __forceinline__ uint4 row_piece(const uint4* lds, int row, int piece) { return lds[at(row, piece)]; }
+};
+
+// C tiles of one contraction over the 32 rows row0 .. row0 + 31 of a tile:
+// acc[d][n] += sum_row tile[row][d] p[row][n] for DB blocks of 32 columns d;
+// p in C layout.  16-bit types round p to T (an operand of the matrix
+// instruction; the sums stay in fp32).
+template <class T, int DP, int DB>
+__device__ __forceinline__ void mma_transposed(const uint4* lds, int row0, int lane, const float (&p)[16],
+                                               floatx16 (&acc)[DB]) {
+  typedef Tile<T, DP> TL;
+  if constexpr (sizeof(T) == 2) {
+    typedef T tx8 __attribute__((ext_vector_type(8)));
+    const int g = lane & 15;
+    // Lane g of a group of 16 addresses 4 columns of row g / 4; it receives
+    // column g of the four rows.
+    const int row = row0 + 4 * (lane >> 5) + (g >> 2);
+    const int col = ((lane >> 4) & 1) * 16 + 4 * (g & 3);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      tx8 b;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) b[j] = static_cast<T>(p[8 * s + j]);
+#pragma unroll
+      for (int db = 0; db < DB; ++db) {
+        const int c = db * 32 + col;
+        s16x4 a[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = row + 16 * s + 8 * u;
+          const char* src = reinterpret_cast<const char*>(lds + TL::at(r, c / 8)) + (c & 4) * 2;
+          a[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)src);
+        }
+        uint4 av;
+        const auto a0 = __builtin_bit_cast(uint2, a[0]), a1 = __builtin_bit_cast(uint2, a[1]);
+        av.x = a0.x; av.y = a0.y; av.z = a1.x; av.w = a1.y;
+        acc[db] = mma_piece<T>(av, __builtin_bit_cast(uint4, b), acc[db]);
+      }
+    }
+  } else {
+    const int col = lane & 31;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = row0 + 8 * (i / 4) + 4 * (lane >> 5) + (i & 3);
+#pragma unroll
+      for (int db = 0; db < DB; ++db) {
+        const int c = db * 32 + col;
+        const float a = reinterpret_cast<const float*>(lds + TL::at(r, c / 4))[c & 3];
+        acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[i], acc[db], 0, 0, 0);
+      }
+    }
+  }
+}
+
+// Flattened row / group for rows below 2^31: with L = ceil(log2 group) and
+// magic = ceil(2^(31 + L) / group), the error of row x magic stays below
+// 2^(31 + L).
+__device__ __forceinline__ int div_group(const AttentionArgs& a, int row) {
+  if (a.group == 1) return row;
+  return static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.group_magic) >> a.group_shift);
+}
+
+// One tile's sequence: its rows on both sides and the first (flattened) row
+// of the tile in it.
+struct Span {
+  int q0, nq, k0, nk;  // first row and rows of the queries and of the keys
+  int r0;              // first row of the tile within the sequence
+  bool any;            // the tile has rows
+};
+
+// The offsets bound the sequences: bound(0) = 0, bound(i) = cu[i - 1] and a
+// last one of all rows, so rows before the first offset and after the last
+// one form sequences without a counterpart (computed as rows without keys).
+// Offsets are clamped to the rows there are: no access leaves the arrays
+// whatever they hold.
+__device__ __forceinline__ int bound(const int32_t* cu, int batch, int total, int i) {
+  if (i <= 0) return 0;
+  if (i > batch + 1) return total;
+  const int v = cu[i - 1];
+  return v < 0 ? 0 : v > total ? total : v;
+}
+
+// Sequence and tile of a slot.  Sequence b starts at slot
+// floor(bound(b) x mult / TILE) + b, which leaves every sequence at least
+// ceil(rows x mult / TILE) slots and needs no pass over the lengths before;
+// the wavefront finds b in rounds of 64 probes.
+template <int TILE>
+__device__ __forceinline__ Span find_span(const AttentionArgs& a, bool by_keys, int slot) {
+  const int lane = threadIdx.x & 63;
+  const int32_t* cu = by_keys ? a.cu_k : a.cu_q;
+  const int total = by_keys ? a.total_k : a.total_q;
+  const int mult = by_keys ? 1 : a.group;
+  auto start = [&](int b) {
+    return static_cast<int>(static_cast<int64_t>(bound(cu, a.batch, total, b)) * mult / TILE) + b;
+  };
+  int lo = 0, hi = a.batch + 2;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) >> 6;
+    const int at = lo + lane * step;
+    const bool le = at < hi && start(at) <= slot;
+    const int c = __builtin_popcountll(__ballot(le));
+    const int base = lo + (c > 0 ? c - 1 : 0) * step;
+    hi = min(base + step, hi);
+    lo = base;
+  }
+  const int b = __builtin_amdgcn_readfirstlane(lo);
+  Span s;
+  s.q0 = bound(a.cu_q, a.batch, a.total_q, b);
+  s.nq = max(bound(a.cu_q, a.batch, a.total_q, b + 1) - s.q0, 0);
+  s.k0 = bound(a.cu_k, a.batch, a.total_k, b);
+  s.nk = max(bound(a.cu_k, a.batch, a.total_k, b + 1) - s.k0, 0);
+  const int64_t rows = static_cast<int64_t>(by_keys ? s.nk : s.nq) * mult;
+  const int64_t r0 = static_cast<int64_t>(slot - start(b)) * TILE;
+  s.any = r0 >= 0 && r0 < rows;
+  s.r0 = s.any ? static_cast<int>(r0) : 0;
+  // a sequence before the first offset or after the last has no counterpart
+  if (b == 0 || b == a.batch + 1) (by_keys ? s.nq : s.nk) = 0;
+  s.q0 = __builtin_amdgcn_readfirstlane(s.q0);
+  s.nq = __builtin_amdgcn_readfirstlane(s.nq);
+  s.k0 = __builtin_amdgcn_readfirstlane(s.k0);
+  s.nk = __builtin_amdgcn_readfirstlane(s.nk);
+  s.r0 = __builtin_amdgcn_readfirstlane(s.r0);
+  return s;
+}
+
+// Slots that cover every tile of every sequence (find_span).
+inline int64_t span_slots(int64_t rows, int batch, int tile) { return rows / tile + batch + 2; }
+
+// Keys that the places p0 .. p1 see: [lo, hi).
+struct KeyRange {
+  int lo, hi;
+};
+__device__ __forceinline__ KeyRange key_range(const AttentionArgs& a, int nk, int p0, int p1) {
+  KeyRange r;
+  r.lo = a.left >= 0 ? max(p0 - a.left, 0) : 0;
+  r.hi = a.right >= 0 ? min(p1 + a.right + 1, nk) : nk;
+  return r;
+}
+
+// Stores 4 consecutive values as T.
+template <class T>
+__device__ __forceinline__ void store4(T* dst, float x, float y, float z, float w) {
+  typedef T tx4 __attribute__((ext_vector_type(4)));
+  tx4 v;
+  v[0] = static_cast<T>(x);
+  v[1] = static_cast<T>(y);
+  v[2] = static_cast<T>(z);
+  v[3] = static_cast<T>(w);
+  *reinterpret_cast<tx4*>(dst) = v;
+}
+
+// Runs f.template operator()<T, DP>() for the type and the padded head size
+// of `a`.
+template <class F>
+hipError_t dispatch(const AttentionArgs& a, F&& f) {
+  auto by_dim = [&](auto t) {
+    typedef decltype(t) T;
+    if (a.dim <= 32) return f(T{}, std::integral_constant<int, 32>{});
+    if (a.dim <= 64) return f(T{}, std::integral_constant<int, 64>{});
+    if (a.dim <= 96) return f(T{}, std::integral_constant<int, 96>{});
+    return f(T{}, std::integral_constant<int, 128>{});
+  };
+  if (a.dtype == 0) return by_dim(float{});
+  if (a.dtype == 1) return by_dim(static_cast<_Float16>(0));
+  return by_dim(static_cast<__bf16>(0.f));
+}
+
+}  // namespace attn
+}  // namespace spconv

@@ -266,4 +266,66 @@ bool grouped_supported(const ForwardArgs& a);
 size_t grouped_workspace_bytes(const ForwardArgs& a, const GroupPlan& p);
 hipError_t launch_forward_grouped(const ForwardArgs& a, const GroupPlan& p, void* workspace, hipStream_t stream);
 
+// ---- Attention over packed sequences (attention.hip, attention_backward.hip) ----
+// Rows of one kv head's queries are flattened as (row, head in group): the
+// `group` query heads that share a kv head follow one another, so a tile of
+// flattened rows shares every key and value row it reads.
+struct AttentionArgs {
+  const void* q = nullptr;   // [total_q][heads][dim], strides in elements
+  const void* k = nullptr;   // [total_k][kv_heads][dim]
+  const void* v = nullptr;
+  int64_t q_row = 0, q_head = 0, k_row = 0, k_head = 0, v_row = 0, v_head = 0;
+  const int32_t* cu_q = nullptr;  // batch + 1 row offsets
+  const int32_t* cu_k = nullptr;
+  int32_t batch = 0, total_q = 0, total_k = 0;
+  int32_t heads = 0, kv_heads = 0, group = 1, dim = 0;
+  uint32_t group_magic = 0;  // flattened row / group (see div_group)
+  int32_t group_shift = 0;
+  int32_t left = -1, right = -1;  // visible keys around a query's place, -1: unbounded
+  float scale = 0.f;
+  int32_t dtype = 0;
+  void* out = nullptr;  // contiguous [total_q][heads][dim]; the forward writes, the backward reads
+  float* lse = nullptr;  // [total_q][heads]
+  // backward
+  const void* grad_out = nullptr;  // [total_q][heads][dim], strides in elements
+  int64_t go_row = 0, go_head = 0;
+  void* grad_q = nullptr;
+  void* grad_k = nullptr;
+  void* grad_v = nullptr;
+  int64_t gq_row = 0, gq_head = 0, gk_row = 0, gk_head = 0, gv_row = 0, gv_head = 0;
+};
+size_t attention_workspace_bytes(const AttentionArgs& a);
+hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t stream);
+size_t attention_backward_workspace_bytes(const AttentionArgs& a);
+hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hipStream_t stream);
+
+// ---- Head norm and position rotation (norm_rotary.hip) ----
+struct NormRotaryTensor {
+  const void* x = nullptr;  // [rows][heads][dim], strides in elements
+  int64_t x_row = 0, x_head = 0;
+  const void* weight = nullptr;  // [dim], or NULL: no norm
+  void* y = nullptr;             // forward's output
+  int64_t y_row = 0, y_head = 0;
+  const void* grad = nullptr;  // gradient of the output
+  int64_t g_row = 0, g_head = 0;
+  void* grad_x = nullptr;
+  int64_t gx_row = 0, gx_head = 0;
+  float* grad_weight = nullptr;  // [dim]
+  int32_t heads = 0;
+};
+struct NormRotaryArgs {
+  NormRotaryTensor t[2];  // queries, keys (heads 0: absent)
+  int32_t rows = 0, dim = 0, rotary = 0, axes = 0, interleaved = 0, dtype = 0;
+  float eps = 0.f;
+  const float* table = nullptr;        // [extent][rotary / (2 axes)][2]: cosine, sine
+  int32_t extent = 0;
+  const int32_t* positions = nullptr;  // [rows][axes], row stride in elements
+  int64_t pos_row = 0;
+};
+hipError_t launch_norm_rotary(const NormRotaryArgs& a, hipStream_t stream);
+size_t norm_rotary_backward_workspace_bytes(const NormRotaryArgs& a);
+hipError_t launch_norm_rotary_backward(const NormRotaryArgs& a, void* workspace, hipStream_t stream);
+hipError_t launch_rotary_table(float* table, int32_t extent, int32_t pairs, double base, double scale,
+                               hipStream_t stream);
+
 }  // namespace spconv
