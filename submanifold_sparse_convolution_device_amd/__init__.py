@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import numpy as np
@@ -169,14 +170,14 @@ def lib() -> ctypes.CDLL:
     L.spconv_select_dataflow.argtypes = [vp, vp, vp, i32, i32, ctypes.c_int, ctypes.POINTER(f64), i32,
                                          ctypes.POINTER(f64), i32, i32, vp, vp, ctypes.POINTER(spconv_dataflow)]
     L.spconv_select_dataflow.restype = ctypes.c_int
-    pattn, pnorm = ctypes.POINTER(spconv_attention), ctypes.POINTER(spconv_norm_rotary)
-    L.spconv_attention_forward.argtypes = [pattn, vp, vp, vp]
+    # struct arguments as void*: a ctypes struct by reference, or packed bytes
+    L.spconv_attention_forward.argtypes = [vp, vp, vp, vp]
     L.spconv_attention_forward.restype = ctypes.c_int
-    L.spconv_attention_backward.argtypes = [pattn, vp, vp, ctypes.POINTER(spconv_attention_gradients), vp]
+    L.spconv_attention_backward.argtypes = [vp, vp, vp, vp, vp]
     L.spconv_attention_backward.restype = ctypes.c_int
-    L.spconv_norm_rotary_forward.argtypes = [pnorm, vp, i64, i64, vp, i64, i64, vp]
+    L.spconv_norm_rotary_forward.argtypes = [vp, vp, i64, i64, vp, i64, i64, vp]
     L.spconv_norm_rotary_forward.restype = ctypes.c_int
-    L.spconv_norm_rotary_backward.argtypes = [pnorm, ctypes.POINTER(spconv_norm_rotary_gradients), vp]
+    L.spconv_norm_rotary_backward.argtypes = [vp, vp, vp]
     L.spconv_norm_rotary_backward.restype = ctypes.c_int
     L.spconv_rotary_table.argtypes = [vp, i32, i32, f64, f64, vp]
     L.spconv_rotary_table.restype = ctypes.c_int
@@ -402,6 +403,42 @@ def _torch():
 def _stream() -> int:
     """Handle of torch's current stream on the current device."""
     return int(_torch().cuda.current_stream().cuda_stream)
+
+
+class _Call:
+    """The device of a call made current, and torch's current stream on it:
+    what :class:`_OnDevice` and :func:`_stream` do, at a tenth of the host time
+    (the stream's handle without a stream object)."""
+
+    __slots__ = ("idx", "prev")
+
+    def __init__(self, idx: int):
+        self.idx = idx
+
+    def __enter__(self) -> int:
+        cuda = _TORCH.cuda
+        cur = cuda.current_device()
+        self.prev = -1
+        if cur != self.idx:
+            self.prev = cur
+            cuda.set_device(self.idx)
+        return _TORCH._C._cuda_getCurrentRawStream(self.idx)
+
+    def __exit__(self, *exc):
+        if self.prev >= 0:
+            _TORCH.cuda.set_device(self.prev)
+
+
+_TORCH = None
+
+
+def _bind():
+    """torch and the library, for the calls below (loaded on the first one)."""
+    global _TORCH
+    if _TORCH is None or _LIB is None:
+        lib()
+        _TORCH = _torch()
+    return _TORCH, _LIB
 
 
 class _OnDevice:
@@ -792,6 +829,13 @@ def forward_with(choice, feats, weights, kmap: SpconvMap, out=None):
 
 # ------------------------------------------------------------------ attention over packed rows
 
+# The C structs as packed bytes (native sizes and alignment): one pack costs a
+# fraction of setting a ctypes struct's fields one by one.
+_PACK_ATTENTION = struct.Struct("@3P6q2P2q6ifi")
+_PACK_ATTENTION_GRADIENTS = struct.Struct("@" + "P2q" * 4)
+_PACK_NORM_ROTARY = struct.Struct("@2P4q4P2q7ifi0q")
+_PACK_NORM_ROTARY_GRADIENTS = struct.Struct("@2P4q2P4q2P")
+
 
 def _dtype_code(dtype):
     global _DT
@@ -807,48 +851,48 @@ def _dtype_code(dtype):
 def _heads_tensor(name, t, like=None, shape=None):
     """Checks a [rows, heads, head_dim] tensor whose last dimension is
     contiguous; returns (pointer, row stride, head stride)."""
-    if not t.is_cuda or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise SpconvError(1, f"{name} must be a [rows, heads, head_dim] tensor on a HIP device with a contiguous last "
-                             "dimension")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if t.dim() != 3 or not t.is_cuda:
+        raise SpconvError(1, f"{name} must be a [rows, heads, head_dim] tensor on a HIP device")
+    row, head, last = t.stride()
+    if last != 1 and t.shape[2] > 1:
+        raise SpconvError(1, f"{name} must have a contiguous last dimension")
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise SpconvError(1, f"{name} must have the dtype and device of the other tensors")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise SpconvError(1, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), row, head
 
 
-def _offsets_tensor(name, cu, device):
-    torch = _torch()
-    if not (cu.is_cuda and cu.device == device and cu.dtype == torch.int32 and cu.dim() == 1 and cu.is_contiguous()
+def _offsets_tensor(name, cu, device: int):
+    if not (cu.get_device() == device and cu.dtype is _TORCH.int32 and cu.dim() == 1 and cu.is_contiguous()
             and cu.shape[0] >= 1):
         raise SpconvError(1, f"{name} must be a contiguous int32 [batch + 1] tensor on the tensors' device")
     return cu.data_ptr()
 
 
 def _attention_args(q, k, v, cu_q, cu_k, causal, window, scale):
-    qp = _heads_tensor("q", q)
-    kp = _heads_tensor("k", k, q)
-    vp = _heads_tensor("v", v, q, k.shape)
+    """The packed spconv_attention of a call."""
+    qp, qr, qh = _heads_tensor("q", q)
+    kp, kr, kh = _heads_tensor("k", k, q)
+    vp, vr, vh = _heads_tensor("v", v, q, k.shape)
     code = _dtype_code(q.dtype)
-    if k.shape[2] != q.shape[2]:
-        raise SpconvError(1, f"q and k must share one head_dim, not {q.shape[2]} and {k.shape[2]}")
-    cu_k = cu_q if cu_k is None else cu_k
-    a = spconv_attention()
-    a.q, a.q_row_stride, a.q_head_stride = qp
-    a.k, a.k_row_stride, a.k_head_stride = kp
-    a.v, a.v_row_stride, a.v_head_stride = vp
-    a.cu_q, a.cu_k = _offsets_tensor("cu_q", cu_q, q.device), _offsets_tensor("cu_k", cu_k, q.device)
-    if cu_q.shape != cu_k.shape:
-        raise SpconvError(1, "cu_q and cu_k must hold the same number of sequences")
-    a.total_q, a.total_k, a.batch = q.shape[0], k.shape[0], cu_q.shape[0] - 1
-    a.heads, a.kv_heads, a.head_dim = q.shape[1], k.shape[1], q.shape[2]
+    total_q, heads, dim = q.shape
+    total_k, kv_heads, kdim = k.shape
+    if kdim != dim:
+        raise SpconvError(1, f"q and k must share one head_dim, not {dim} and {kdim}")
+    device = q.get_device()
+    cq = _offsets_tensor("cu_q", cu_q, device)
+    if cu_k is None or cu_k is cu_q:
+        ck = cq
+    else:
+        ck = _offsets_tensor("cu_k", cu_k, device)
+        if cu_q.shape != cu_k.shape:
+            raise SpconvError(1, "cu_q and cu_k must hold the same number of sequences")
     left, right = window
-    a.left, a.right = max(-1, min(int(left), 1 << 30)), max(-1, min(int(right), 1 << 30))
-    if causal:
-        a.right = 0
-    a.scale = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
-    a.dtype = code
-    return a
+    left, right = max(-1, min(int(left), 1 << 30)), max(-1, min(int(right), 1 << 30))
+    scale = float(dim) ** -0.5 if scale is None else min(max(float(scale), -1e38), 1e38) if scale == scale else 0.0
+    return _PACK_ATTENTION.pack(qp, kp, vp, qr, qh, kr, kh, vr, vh, cq, ck, total_q, total_k, cu_q.shape[0] - 1, heads,
+                                kv_heads, dim, left, 0 if causal else right, scale, code)
 
 
 def attention(q, k, v, cu_q, cu_k=None, *, causal: bool = False, window=(-1, -1), scale: Optional[float] = None,
@@ -867,15 +911,17 @@ def attention(q, k, v, cu_q, cu_k=None, *, causal: bool = False, window=(-1, -1)
     Returns out [total_q, heads, head_dim], or (out, lse) with
     ``return_lse``: lse fp32 [total_q, heads], what
     :func:`attention_backward` needs."""
-    torch = _torch()
+    torch, L = _bind()
     a = _attention_args(q, k, v, cu_q, cu_k, causal, window, scale)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif not (out.is_cuda and out.is_contiguous() and out.dtype == q.dtype and out.shape == q.shape):
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif not (out.get_device() == q.get_device() and out.is_contiguous() and out.dtype is q.dtype and out.shape == q.shape):
         raise SpconvError(1, "out must be a contiguous [total_q, heads, head_dim] tensor of the dtype")
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    with _OnDevice(q.device):
-        spconv_attention_forward(a, out.data_ptr(), lse.data_ptr(), _stream())
+    lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+    with _Call(q.get_device()) as stream:
+        rc = L.spconv_attention_forward(a, out.data_ptr(), lse.data_ptr(), stream)
+        if rc:
+            _check(rc)
     return (out, lse) if return_lse else out
 
 
@@ -884,23 +930,23 @@ def attention_backward(grad_out, q, k, v, out, lse, cu_q, cu_k=None, *, causal: 
     """Gradients (grad_q, grad_k, grad_v) of :func:`attention` from the
     gradient of its output, its inputs, and its out and lse.  ``grads``: three
     tensors to write, such as the slices of one projection's gradient."""
-    torch = _torch()
+    torch, L = _bind()
     a = _attention_args(q, k, v, cu_q, cu_k, causal, window, scale)
-    if not (out.is_cuda and out.is_contiguous() and out.dtype == q.dtype and out.shape == q.shape):
+    if not (out.get_device() == q.get_device() and out.is_contiguous() and out.dtype is q.dtype and out.shape == q.shape):
         raise SpconvError(1, "out must be the forward's contiguous [total_q, heads, head_dim] output")
-    if not (lse.is_cuda and lse.is_contiguous() and lse.dtype == torch.float32 and lse.shape == q.shape[:2]):
+    if not (lse.get_device() == q.get_device() and lse.is_contiguous() and lse.dtype is torch.float32
+            and lse.shape == q.shape[:2]):
         raise SpconvError(1, "lse must be the forward's contiguous fp32 [total_q, heads] output")
     if grads is None:
-        grads = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-                 torch.empty(k.shape, dtype=q.dtype, device=q.device),
-                 torch.empty(v.shape, dtype=q.dtype, device=q.device))
-    g = spconv_attention_gradients()
-    g.grad_out, g.grad_out_row_stride, g.grad_out_head_stride = _heads_tensor("grad_out", grad_out, q, q.shape)
-    g.grad_q, g.grad_q_row_stride, g.grad_q_head_stride = _heads_tensor("grad_q", grads[0], q, q.shape)
-    g.grad_k, g.grad_k_row_stride, g.grad_k_head_stride = _heads_tensor("grad_k", grads[1], q, k.shape)
-    g.grad_v, g.grad_v_row_stride, g.grad_v_head_stride = _heads_tensor("grad_v", grads[2], q, v.shape)
-    with _OnDevice(q.device):
-        spconv_attention_backward(a, out.data_ptr(), lse.data_ptr(), g, _stream())
+        grads = tuple(torch.empty_like(x, memory_format=torch.contiguous_format) for x in (q, k, v))
+    g = _PACK_ATTENTION_GRADIENTS.pack(*_heads_tensor("grad_out", grad_out, q, q.shape),
+                                       *_heads_tensor("grad_q", grads[0], q, q.shape),
+                                       *_heads_tensor("grad_k", grads[1], q, k.shape),
+                                       *_heads_tensor("grad_v", grads[2], q, v.shape))
+    with _Call(q.get_device()) as stream:
+        rc = L.spconv_attention_backward(a, out.data_ptr(), lse.data_ptr(), g, stream)
+        if rc:
+            _check(rc)
     return tuple(grads)
 
 
@@ -910,55 +956,59 @@ def attention_backward(grad_out, q, k, v, out, lse, cu_q, cu_k=None, *, causal: 
 def rotary_table(extent: int, pairs: int, base: float = 10000.0, position_scale: float = 1.0, device="cuda"):
     """Cosines and sines [extent, pairs, 2] (fp32) of the angles
     position * position_scale * base ** (-i / pairs), i < pairs."""
-    torch = _torch()
+    torch, _ = _bind()
     table = torch.empty((int(extent), int(pairs), 2), dtype=torch.float32, device=device)
-    with _OnDevice(table.device):
-        spconv_rotary_table(table.data_ptr(), int(extent), int(pairs), base, position_scale, _stream())
+    with _Call(table.get_device()) as stream:
+        spconv_rotary_table(table.data_ptr(), int(extent), int(pairs), base, position_scale, stream)
     return table
 
 
+_NO_TENSOR = (0, 0, 0)
+
+
 def _norm_rotary_args(q, k, q_weight, k_weight, table, positions, rotary_dim, interleaved, eps):
-    torch = _torch()
-    if q is None and k is None:
-        raise SpconvError(1, "q and k are both None")
+    """The packed spconv_norm_rotary of a call."""
     like = k if q is None else q
-    a = spconv_norm_rotary()
-    a.rows, a.head_dim, a.dtype = like.shape[0], like.shape[-1], _dtype_code(like.dtype)
-    if q is not None:
-        a.q, a.q_row_stride, a.q_head_stride = _heads_tensor("q", q)
-        a.q_heads = q.shape[1]
-    if k is not None:
-        a.k, a.k_row_stride, a.k_head_stride = _heads_tensor("k", k, like, (a.rows, k.shape[1] if k.dim() == 3 else 0,
-                                                                          a.head_dim))
-        a.k_heads = k.shape[1]
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+    if like is None:
+        raise SpconvError(1, "q and k are both None")
+    qp, qr, qh = _NO_TENSOR if q is None else _heads_tensor("q", q)
+    kp, kr, kh = _NO_TENSOR if k is None else _heads_tensor("k", k, like)
+    rows, _, dim = like.shape
+    code = _dtype_code(like.dtype)
+    if k is not None and (k.shape[0] != rows or k.shape[2] != dim):
+        raise SpconvError(1, f"q and k must share rows and head_dim, not {tuple(like.shape)} and {tuple(k.shape)}")
+    device = like.get_device()
+    weights = [0, 0]
+    for i, w in enumerate((q_weight, k_weight)):
         if w is None:
             continue
-        if not (w.is_cuda and w.device == like.device and w.is_contiguous() and w.dtype == like.dtype
-                and tuple(w.shape) == (a.head_dim,)):
-            raise SpconvError(1, f"{name} must be a contiguous [head_dim] tensor of the dtype on the tensors' device")
-        setattr(a, name, w.data_ptr())
-    a.eps, a.interleaved = float(eps), int(bool(interleaved))
+        if not (w.get_device() == device and w.dim() == 1 and w.shape[0] == dim and w.is_contiguous()
+                and w.dtype is like.dtype):
+            raise SpconvError(1, f"{'qk'[i]}_weight must be a contiguous [head_dim] tensor of the dtype on the tensors' device")
+        weights[i] = w.data_ptr()
+    tp = pp = pr = rotary = axes = extent = 0
     if table is None:
         if rotary_dim:
             raise SpconvError(1, "a rotation needs a table and positions")
-        a.rotary_dim = 0
-        return a
-    if not (table.is_cuda and table.device == like.device and table.dtype == torch.float32 and table.dim() == 3
-            and table.shape[2] == 2 and table.is_contiguous()):
-        raise SpconvError(1, "table must be a contiguous fp32 [extent, pairs, 2] tensor on the tensors' device")
-    if positions is None or not (positions.is_cuda and positions.device == like.device
-                                 and positions.dtype == torch.int32 and positions.dim() in (1, 2)):
-        raise SpconvError(1, "positions must be an int32 [rows] or [rows, axes] tensor on the tensors' device")
-    axes = 1 if positions.dim() == 1 else positions.shape[1]
-    if positions.shape[0] != a.rows or (positions.dim() == 2 and axes > 1 and positions.stride(1) != 1):
-        raise SpconvError(1, f"positions must hold {a.rows} rows of contiguous components")
-    a.rotary_dim = 2 * axes * table.shape[1] if rotary_dim is None else int(rotary_dim)
-    if a.rotary_dim != 2 * axes * table.shape[1]:
-        raise SpconvError(1, f"rotary_dim = {a.rotary_dim} must be 2 x {axes} axes x {table.shape[1]} pairs of the table")
-    a.table, a.extent, a.axes = table.data_ptr(), table.shape[0], axes
-    a.positions, a.position_row_stride = positions.data_ptr(), positions.stride(0)
-    return a
+    else:
+        if not (table.get_device() == device and table.dtype is _TORCH.float32 and table.dim() == 3
+                and table.shape[2] == 2 and table.is_contiguous()):
+            raise SpconvError(1, "table must be a contiguous fp32 [extent, pairs, 2] tensor on the tensors' device")
+        if positions is None or not (positions.get_device() == device and positions.dtype is _TORCH.int32
+                                     and positions.dim() in (1, 2)):
+            raise SpconvError(1, "positions must be an int32 [rows] or [rows, axes] tensor on the tensors' device")
+        strides = positions.stride()
+        axes = 1 if len(strides) == 1 else positions.shape[1]
+        if positions.shape[0] != rows or (axes > 1 and strides[1] != 1):
+            raise SpconvError(1, f"positions must hold {rows} rows of contiguous components")
+        extent, pairs, _ = table.shape
+        rotary = 2 * axes * pairs
+        if rotary_dim is not None and rotary_dim != rotary:
+            raise SpconvError(1, f"rotary_dim = {rotary_dim} must be 2 x {axes} axes x {pairs} pairs of the table")
+        tp, pp, pr = table.data_ptr(), positions.data_ptr(), strides[0]
+    return _PACK_NORM_ROTARY.pack(qp, kp, qr, qh, kr, kh, weights[0], weights[1], tp, pp, pr, rows,
+                                  0 if q is None else q.shape[1], 0 if k is None else k.shape[1], dim, rotary, axes,
+                                  extent, 1 if interleaved else 0, eps, code)
 
 
 def norm_rotary(q, k, q_weight=None, k_weight=None, table=None, positions=None, *, rotary_dim: Optional[int] = None,
@@ -975,15 +1025,18 @@ def norm_rotary(q, k, q_weight=None, k_weight=None, table=None, positions=None, 
 
     Returns (q', k'); ``out``: two tensors to write, which may be q and k
     themselves.  Either of q and k may be None."""
-    torch = _torch()
+    torch, L = _bind()
     a = _norm_rotary_args(q, k, q_weight, k_weight, table, positions, rotary_dim, interleaved, eps)
-    if out is None:
-        out = tuple(None if x is None else torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
     like = k if q is None else q
-    qo = (0, 0, 0) if q is None else _heads_tensor("q_out", out[0], like, q.shape)
-    ko = (0, 0, 0) if k is None else _heads_tensor("k_out", out[1], like, k.shape)
-    with _OnDevice(like.device):
-        spconv_norm_rotary_forward(a, *qo, *ko, _stream())
+    if out is None:
+        out = (None if q is None else torch.empty_like(q, memory_format=torch.contiguous_format),
+               None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format))
+    qo = _NO_TENSOR if q is None else _heads_tensor("q_out", out[0], like, q.shape)
+    ko = _NO_TENSOR if k is None else _heads_tensor("k_out", out[1], like, k.shape)
+    with _Call(like.get_device()) as stream:
+        rc = L.spconv_norm_rotary_forward(a, *qo, *ko, stream)
+        if rc:
+            _check(rc)
     return tuple(out)
 
 
@@ -994,27 +1047,26 @@ def norm_rotary_backward(grad_q_out, grad_k_out, q, k, q_weight=None, k_weight=N
     weights' are fp32 [head_dim] (None without a weight).  ``grads``: two
     tensors for grad_q and grad_k, which may be the outputs' gradients
     themselves."""
-    torch = _torch()
+    torch, L = _bind()
     a = _norm_rotary_args(q, k, q_weight, k_weight, table, positions, rotary_dim, interleaved, eps)
-    if grads is None:
-        grads = tuple(None if x is None else torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
     like = k if q is None else q
-    g = spconv_norm_rotary_gradients()
-    weights = [None, None]
-    for i, (name, x, w, go) in enumerate((("q", q, q_weight, grad_q_out), ("k", k, k_weight, grad_k_out))):
+    if grads is None:
+        grads = tuple(None if x is None else torch.empty_like(x, memory_format=torch.contiguous_format) for x in (q, k))
+    given, made, weights = [], [], [None, None]
+    for i, (x, w, go) in enumerate(((q, q_weight, grad_q_out), (k, k_weight, grad_k_out))):
         if x is None:
+            given.append(_NO_TENSOR)
+            made.append(_NO_TENSOR)
             continue
-        p, r, h = _heads_tensor(f"grad_{name}_out", go, like, x.shape)
-        setattr(g, f"grad_{name}_out", p)
-        setattr(g, f"grad_{name}_out_row_stride", r)
-        setattr(g, f"grad_{name}_out_head_stride", h)
-        p, r, h = _heads_tensor(f"grad_{name}", grads[i], like, x.shape)
-        setattr(g, f"grad_{name}", p)
-        setattr(g, f"grad_{name}_row_stride", r)
-        setattr(g, f"grad_{name}_head_stride", h)
+        given.append(_heads_tensor(f"grad_{'qk'[i]}_out", go, like, x.shape))
+        made.append(_heads_tensor(f"grad_{'qk'[i]}", grads[i], like, x.shape))
         if w is not None:
-            weights[i] = torch.empty(a.head_dim, dtype=torch.float32, device=like.device)
-            setattr(g, f"grad_{name}_weight", weights[i].data_ptr())
-    with _OnDevice(like.device):
-        spconv_norm_rotary_backward(a, g, _stream())
+            weights[i] = like.new_empty(like.shape[2], dtype=torch.float32)
+    (gqo, gko), (gq, gk) = given, made
+    g = _PACK_NORM_ROTARY_GRADIENTS.pack(gqo[0], gko[0], *gqo[1:], *gko[1:], gq[0], gk[0], *gq[1:], *gk[1:],
+                                         *(0 if w is None else w.data_ptr() for w in weights))
+    with _Call(like.get_device()) as stream:
+        rc = L.spconv_norm_rotary_backward(a, g, stream)
+        if rc:
+            _check(rc)
     return grads[0], grads[1], weights[0], weights[1]

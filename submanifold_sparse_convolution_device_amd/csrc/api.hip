@@ -657,12 +657,7 @@ spconv_status attention_args(const spconv_attention* x, const void* d_out, const
   a->kv_heads = x->kv_heads;
   a->group = x->heads / x->kv_heads;
   a->dim = x->head_dim;
-  if (a->group > 1) {
-    int l = 1;
-    while ((int64_t(1) << l) < a->group) ++l;
-    a->group_shift = l - 1;
-    a->group_magic = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + a->group - 1) / a->group);
-  }
+  a->by_group = spconv::make_fast_div(a->group);
   // a bound past every row is none
   a->left = x->left < 0 || x->left >= (1 << 30) ? -1 : x->left;
   a->right = x->right < 0 || x->right >= (1 << 30) ? -1 : x->right;
@@ -734,6 +729,7 @@ spconv_status norm_rotary_args(const spconv_norm_rotary* x, spconv::NormRotaryAr
     a->t[i].x_row = in[i].row_stride;
     a->t[i].x_head = in[i].head_stride;
     a->t[i].heads = static_cast<int32_t>(in[i].heads);
+    if (in[i].heads > 0) a->t[i].by_heads = spconv::make_fast_div(a->t[i].heads);
   }
   a->t[0].weight = x->q_weight;
   a->t[1].weight = x->k_weight;

@@ -149,13 +149,7 @@ __device__ __forceinline__ void mma_transposed(const uint4* lds, int row0, int l
   }
 }
 
-// Flattened row / group for rows below 2^31: with L = ceil(log2 group) and
-// magic = ceil(2^(31 + L) / group), the error of row x magic stays below
-// 2^(31 + L).
-__device__ __forceinline__ int div_group(const AttentionArgs& a, int row) {
-  if (a.group == 1) return row;
-  return static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.group_magic) >> a.group_shift);
-}
+__device__ __forceinline__ int div_group(const AttentionArgs& a, int row) { return fast_div(row, a.by_group); }
 
 // One tile's sequence: its rows on both sides and the first (flattened) row
 // of the tile in it.

@@ -266,6 +266,30 @@ bool grouped_supported(const ForwardArgs& a);
 size_t grouped_workspace_bytes(const ForwardArgs& a, const GroupPlan& p);
 hipError_t launch_forward_grouped(const ForwardArgs& a, const GroupPlan& p, void* workspace, hipStream_t stream);
 
+// Division of integers in [0, 2^31) by a fixed positive one: with
+// L = ceil(log2 d) and magic = ceil(2^(31 + L) / d), the error of n x magic
+// stays below 2^(31 + L).
+struct FastDiv {
+  int32_t d = 1;
+  int32_t shift = 0;
+  uint32_t magic = 0;
+};
+inline FastDiv make_fast_div(int32_t d) {
+  FastDiv f;
+  f.d = d;
+  if (d > 1) {
+    int l = 1;
+    while ((int64_t(1) << l) < d) ++l;
+    f.shift = l - 1;
+    f.magic = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + d - 1) / d);
+  }
+  return f;
+}
+__device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
+  if (f.d == 1) return n;
+  return static_cast<int>(__umulhi(static_cast<uint32_t>(n), f.magic) >> f.shift);
+}
+
 // ---- Attention over packed sequences (attention.hip, attention_backward.hip) ----
 // Rows of one kv head's queries are flattened as (row, head in group): the
 // `group` query heads that share a kv head follow one another, so a tile of
@@ -279,8 +303,7 @@ struct AttentionArgs {
   const int32_t* cu_k = nullptr;
   int32_t batch = 0, total_q = 0, total_k = 0;
   int32_t heads = 0, kv_heads = 0, group = 1, dim = 0;
-  uint32_t group_magic = 0;  // flattened row / group (see div_group)
-  int32_t group_shift = 0;
+  FastDiv by_group;
   int32_t left = -1, right = -1;  // visible keys around a query's place, -1: unbounded
   float scale = 0.f;
   int32_t dtype = 0;
@@ -312,6 +335,7 @@ struct NormRotaryTensor {
   int64_t gx_row = 0, gx_head = 0;
   float* grad_weight = nullptr;  // [dim]
   int32_t heads = 0;
+  FastDiv by_heads;
 };
 struct NormRotaryArgs {
   NormRotaryTensor t[2];  // queries, keys (heads 0: absent)

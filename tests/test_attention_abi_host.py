@@ -127,3 +127,14 @@ def test_struct_mirrors_have_the_c_sizes():
     for n, line in zip(names, got):
         cls = getattr(sp, n)
         assert [int(v) for v in line.split()] == [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_], n
+
+
+def test_packed_arguments_have_the_structs_layout():
+    """The packed bytes of the torch front end against the struct mirrors."""
+    for pack, cls in ((sp._PACK_ATTENTION, sp.spconv_attention), (sp._PACK_ATTENTION_GRADIENTS, sp.spconv_attention_gradients),
+                      (sp._PACK_NORM_ROTARY, sp.spconv_norm_rotary),
+                      (sp._PACK_NORM_ROTARY_GRADIENTS, sp.spconv_norm_rotary_gradients)):
+        values = [i + 1 for i in range(len(cls._fields_))]
+        got = cls.from_buffer_copy(pack.pack(*values))
+        assert pack.size == ctypes.sizeof(cls)
+        assert [getattr(got, f) for f, _ in cls._fields_] == values
