@@ -513,9 +513,10 @@ spconv_status spconv_select_dataflow(const void* d_feats, const void* d_weights,
  * Heads: `heads` query heads share `kv_heads` key and value heads in groups of
  * heads / kv_heads consecutive ones.  head_dim is a multiple of 8 up to 128.
  * Each tensor is [rows][heads][head_dim] in dtype with its own row and head
- * stride in elements (multiples of 16 bytes; 0 repeats an input), the last
- * dimension contiguous, 16-byte aligned: q, k and v may be slices of one
- * projection's output.  out is contiguous [total_q][heads][head_dim], lse
+ * stride in elements (multiples of 16 bytes; 0 repeats an input, other row
+ * strides are head_dim or more and at most 2^24 bytes), the last dimension
+ * contiguous, 16-byte aligned: q, k and v may be slices of one projection's
+ * output.  out is contiguous [total_q][heads][head_dim], lse
  * fp32 [total_q][heads].
  *
  * Scores, softmax statistics and all sums are fp32.  F16 and BF16 round the

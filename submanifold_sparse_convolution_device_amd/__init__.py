@@ -890,7 +890,9 @@ def _attention_args(q, k, v, cu_q, cu_k, causal, window, scale):
             raise SpconvError(1, "cu_q and cu_k must hold the same number of sequences")
     left, right = window
     left, right = max(-1, min(int(left), 1 << 30)), max(-1, min(int(right), 1 << 30))
-    scale = float(dim) ** -0.5 if scale is None else min(max(float(scale), -1e38), 1e38) if scale == scale else 0.0
+    scale = float(dim) ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < 3e38:  # an fp32 number
+        raise SpconvError(1, f"scale = {scale} must be positive and finite")
     return _PACK_ATTENTION.pack(qp, kp, vp, qr, qh, kr, kh, vr, vh, cq, ck, total_q, total_k, cu_q.shape[0] - 1, heads,
                                 kv_heads, dim, left, 0 if causal else right, scale, code)
 
@@ -1006,6 +1008,8 @@ def _norm_rotary_args(q, k, q_weight, k_weight, table, positions, rotary_dim, in
         if rotary_dim is not None and rotary_dim != rotary:
             raise SpconvError(1, f"rotary_dim = {rotary_dim} must be 2 x {axes} axes x {pairs} pairs of the table")
         tp, pp, pr = table.data_ptr(), positions.data_ptr(), strides[0]
+    if not 0.0 <= eps < 3e38:
+        raise SpconvError(1, f"eps = {eps} must be finite and not negative")
     return _PACK_NORM_ROTARY.pack(qp, kp, qr, qh, kr, kh, weights[0], weights[1], tp, pp, pr, rows,
                                   0 if q is None else q.shape[1], 0 if k is None else k.shape[1], dim, rotary, axes,
                                   extent, 1 if interleaved else 0, eps, code)

@@ -546,6 +546,9 @@ struct Strided {
   uint64_t bytes() const { return span_bytes(rows, row_stride, heads, head_stride, dim, es); }
 };
 
+// A tile's rows are read with 32-bit offsets from its first one.
+constexpr int64_t kMaxRowBytes = int64_t(1) << 24;
+
 // Alignment, strides and size of a tensor; a written one must keep its rows
 // and heads apart.
 spconv_status check_strided(const Strided& t, bool written) {
@@ -554,8 +557,9 @@ spconv_status check_strided(const Strided& t, bool written) {
   if (!aligned16(t.p)) return fail(SPCONV_ERR_INVALID_ARG, "%s is not 16-byte aligned", t.name);
   const int64_t piece = static_cast<int64_t>(16 / t.es);
   if (t.row_stride < 0 || t.head_stride < 0 || t.row_stride % piece != 0 || t.head_stride % piece != 0 ||
-      t.row_stride > (int64_t(1) << 31) || t.head_stride > (int64_t(1) << 40)) {
-    return fail(SPCONV_ERR_INVALID_ARG, "%s: row stride %lld and head stride %lld must be multiples of %lld elements, not negative, below 2^31 and 2^40",
+      t.row_stride * static_cast<int64_t>(t.es) > kMaxRowBytes || t.head_stride > (int64_t(1) << 40) ||
+      (t.row_stride != 0 && t.row_stride < t.dim)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "%s: row stride %lld (0, or head_dim and more, at most 2^24 bytes) and head stride %lld (at most 2^40) must be multiples of %lld elements, not negative",
                 t.name, (long long)t.row_stride, (long long)t.head_stride, (long long)piece);
   }
   if (written) {

@@ -19,7 +19,7 @@ namespace {
 using namespace attn;
 
 template <class T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(64 * WAVES) void k_attention(AttentionArgs a, int nsplit, float* part_out,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int nsplit, float* part_out,
                                                           float* part_lse) {
   typedef Tile<T, DP> TL;
   constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
@@ -31,7 +31,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention(AttentionArgs a, int n
   const Span sp = find_span<BM>(a, false, static_cast<int>(blockIdx.x));
   if (!sp.any) return;
   const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = sp.nq * a.group;
   const int shift = sp.nk - sp.nq;  // a query's place among the keys: its row + shift
 
@@ -65,21 +66,25 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention(AttentionArgs a, int n
   const int jb0 = static_cast<int>(static_cast<int64_t>(blocks) * split / nsplit);
   const int jb1 = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / nsplit);
 
-  const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head;
-  const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head;
+  const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head + static_cast<int64_t>(sp.k0) * a.k_row;
+  const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head + static_cast<int64_t>(sp.k0) * a.v_row;
+  const uint32_t kb = static_cast<uint32_t>(a.k_row * sizeof(T)), vb = static_cast<uint32_t>(a.v_row * sizeof(T));
   uint4 kr[NL], vr[NL];
+  uint32_t koff[NL], voff[NL];
+#pragma unroll
+  for (int n = 0; n < NL; ++n) {
+    const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+    const bool on = row < BN && piece * kPiece<T> < a.dim;
+    koff[n] = on ? row * kb + piece * 16 : kNowhere;
+    voff[n] = on ? row * vb + piece * 16 : kNowhere;
+  }
   auto load = [&](int jb) {
     const int j0 = wg.lo + jb * BN;
+    const auto kbuf = rows_buffer(kbase + j0 * a.k_row, sp.nk - j0, kb), vbuf = rows_buffer(vbase + j0 * a.v_row, sp.nk - j0, vb);
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
-      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
-      const int j = j0 + row;
-      const bool ok = row < BN && j < sp.nk && piece * kPiece<T> < a.dim;
-      kr[n] = vr[n] = make_uint4(0, 0, 0, 0);
-      if (ok) {
-        kr[n] = *reinterpret_cast<const uint4*>(kbase + static_cast<int64_t>(sp.k0 + j) * a.k_row + piece * kPiece<T>);
-        vr[n] = *reinterpret_cast<const uint4*>(vbase + static_cast<int64_t>(sp.k0 + j) * a.v_row + piece * kPiece<T>);
-      }
+      kr[n] = load_piece(kbuf, koff[n]);
+      vr[n] = load_piece(vbuf, voff[n]);
     }
   };
 
@@ -114,6 +119,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention(AttentionArgs a, int n
         s[b] = mma_piece<T>(TL::row_piece(ks, 32 * b + (lane & 31), 2 * t + half), qf[t], s[b]);
     }
     if (j0 < full_lo || j0 + BN > full_hi) {
+      keep_branch();
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll

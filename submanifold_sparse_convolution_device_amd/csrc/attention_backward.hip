@@ -55,7 +55,7 @@ __device__ __forceinline__ void rescale(float (&ds)[16], float& factor, floatx16
 constexpr float kFirstFactor = 1.2676506002282294e30f;  // 2^100
 
 template <class T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(64 * WAVES) void k_attention_dq(AttentionArgs a, int nsplit, float* delta, float* part) {
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int nsplit, float* delta, float* part) {
   typedef Tile<T, DP> TL;
   constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
@@ -64,7 +64,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_dq(AttentionArgs a, in
   const Span sp = find_span<BM>(a, false, static_cast<int>(blockIdx.x));
   if (!sp.any) return;
   const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = sp.nq * a.group;
   const int shift = sp.nk - sp.nq;
 
@@ -115,20 +116,25 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_dq(AttentionArgs a, in
   const int jb0 = static_cast<int>(static_cast<int64_t>(blocks) * split / nsplit);
   const int jb1 = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / nsplit);
 
-  const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head;
-  const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head;
+  const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head + static_cast<int64_t>(sp.k0) * a.k_row;
+  const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head + static_cast<int64_t>(sp.k0) * a.v_row;
+  const uint32_t kb = static_cast<uint32_t>(a.k_row * sizeof(T)), vb = static_cast<uint32_t>(a.v_row * sizeof(T));
   uint4 kr[NL], vr[NL];
+  uint32_t koff[NL], voff[NL];
+#pragma unroll
+  for (int n = 0; n < NL; ++n) {
+    const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+    const bool on = row < BN && piece * kPiece<T> < a.dim;
+    koff[n] = on ? row * kb + piece * 16 : kNowhere;
+    voff[n] = on ? row * vb + piece * 16 : kNowhere;
+  }
   auto load = [&](int jb) {
     const int j0 = wg.lo + jb * BN;
+    const auto kbuf = rows_buffer(kbase + j0 * a.k_row, sp.nk - j0, kb), vbuf = rows_buffer(vbase + j0 * a.v_row, sp.nk - j0, vb);
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
-      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
-      const int j = j0 + row;
-      kr[n] = vr[n] = make_uint4(0, 0, 0, 0);
-      if (row < BN && j < sp.nk && piece * kPiece<T> < a.dim) {
-        kr[n] = *reinterpret_cast<const uint4*>(kbase + static_cast<int64_t>(sp.k0 + j) * a.k_row + piece * kPiece<T>);
-        vr[n] = *reinterpret_cast<const uint4*>(vbase + static_cast<int64_t>(sp.k0 + j) * a.v_row + piece * kPiece<T>);
-      }
+      kr[n] = load_piece(kbuf, koff[n]);
+      vr[n] = load_piece(vbuf, voff[n]);
     }
   };
 
@@ -166,6 +172,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_dq(AttentionArgs a, in
 #pragma unroll
       for (int i = 0; i < 16; ++i) ds[i] = fast_exp2(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - dot);
       if (partial) {
+        keep_branch();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = j0 + 32 * b + 8 * (i / 4) + 4 * half + (i & 3);
@@ -194,7 +201,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_dq(AttentionArgs a, in
 }
 
 template <class T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(64 * WAVES) void k_attention_dkv(AttentionArgs a, int nsplit, const float* delta,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int nsplit, const float* delta,
                                                               float* part_k, float* part_v) {
   typedef Tile<T, DP> TL;
   constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
@@ -207,7 +214,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_dkv(AttentionArgs a, i
   const Span sp = find_span<BM>(a, true, static_cast<int>(blockIdx.x));
   if (!sp.any) return;
   const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = sp.nq * a.group;
   const int shift = sp.nk - sp.nq;
 
@@ -241,6 +249,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_dkv(AttentionArgs a, i
   uint4 qr[NL], gr[NL];
   float lse_r = INFINITY, delta_r = 0.f;
   int place_r = 0;
+  const T* qbase = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0) * a.q_row + static_cast<int64_t>(kvh) * a.group * a.q_head;
+  const T* gbase = static_cast<const T*>(a.grad_out) + static_cast<int64_t>(sp.q0) * a.go_row + static_cast<int64_t>(kvh) * a.group * a.go_head;
   auto load = [&](int rb) {
     const int r0 = f_lo + rb * BN;
 #pragma unroll
@@ -249,9 +259,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_dkv(AttentionArgs a, i
       const int r = r0 + row;
       qr[n] = gr[n] = make_uint4(0, 0, 0, 0);
       if (row < BN && r < rows && piece * kPiece<T> < a.dim) {
-        const int tok = div_group(a, r), head = kvh * a.group + r - tok * a.group;
-        qr[n] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0 + tok) * a.q_row + static_cast<int64_t>(head) * a.q_head + piece * kPiece<T>);
-        gr[n] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.grad_out) + static_cast<int64_t>(sp.q0 + tok) * a.go_row + static_cast<int64_t>(head) * a.go_head + piece * kPiece<T>);
+        const int tok = div_group(a, r), g = r - tok * a.group;
+        qr[n] = *reinterpret_cast<const uint4*>(qbase + tok * a.q_row + g * a.q_head + piece * kPiece<T>);
+        gr[n] = *reinterpret_cast<const uint4*>(gbase + tok * a.go_row + g * a.go_head + piece * kPiece<T>);
       }
     }
     if (tid < BN) {
@@ -323,6 +333,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_dkv(AttentionArgs a, i
         }
       }
       if (partial) {
+        keep_branch();
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int4 pl = row_place[8 * b + 2 * g + half];
