@@ -621,6 +621,9 @@ spconv_status attention_args(const spconv_attention* x, const void* d_out, const
   if (x->heads < 1 || x->kv_heads < 1 || x->heads % x->kv_heads != 0 || x->kv_heads > 65535) {
     return fail(SPCONV_ERR_INVALID_ARG, "heads = %d must be a positive multiple of kv_heads = %d (at most 65535)", x->heads, x->kv_heads);
   }
+  if (static_cast<int64_t>(x->batch + 2) * x->kv_heads > (int64_t(1) << 30)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "batch = %d x kv_heads = %d must stay below 2^30", x->batch, x->kv_heads);
+  }
   if (x->total_q < 0 || x->total_k < 0 || x->total_q > kMaxRows / x->heads || x->total_k > kMaxRows / x->kv_heads ||
       x->total_q > (int64_t(1) << 30) || x->total_k > (int64_t(1) << 30)) {
     return fail(SPCONV_ERR_INVALID_ARG, "total_q = %lld, total_k = %lld: rows x heads must stay below 2^31 and rows below 2^30",

@@ -18,19 +18,36 @@ namespace {
 
 using namespace attn;
 
-template <class T, int DP, int WAVES, int BN>
+// Keys per LDS tile, and tiles of K and V in LDS (two: one read, one filled;
+// a lone wave stages through one).  Tiles are as large as several workgroups
+// per CU allow: a short sequence then needs one tile, and one barrier, in all.
+template <class T, int DP, int WAVES>
+constexpr int kKeys = sizeof(T) == 4 ? 32 : DP == 32 ? (WAVES == 4 ? 128 : 64) : WAVES == 4 || (WAVES == 2 && DP == 64) ? 64 : 32;
+template <int WAVES>
+constexpr int kBuffers = WAVES == 1 ? 1 : 2;
+
+// One workgroup: 32 flattened query rows per wave, one kv head, and the key
+// tiles of one split.  Q stays in registers (operand B of S^T = K Q^T), K and
+// V pass through LDS, loaded a tile ahead into registers.
+template <class T, int DP, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int nsplit, float* part_out,
-                                                          float* part_lse) {
+                                                                                 float* part_lse) {
   typedef Tile<T, DP> TL;
-  constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
+  constexpr int BN = kKeys<T, DP, WAVES>, BUFS = kBuffers<WAVES>;
+  constexpr int NB = BN >= 64 ? 2 : 1;  // blocks of 32 keys per softmax step
+  constexpr int PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES;                // flattened rows per workgroup
   constexpr int KS = PPR / 2;                   // pieces per half of a row
   constexpr int NL = (BN * PPR + NT - 1) / NT;  // pieces each thread copies per tile
-  __shared__ uint4 ks[BN * PPR], vs[BN * PPR];
+  __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
-  const Span sp = find_span<BM>(a, false, static_cast<int>(blockIdx.x));
+  // Under a causal mask the last rows have the most keys: they go first.
+  // Consecutive workgroups, which go to different XCDs, take different kv
+  // heads, so that an XCD's L2 sees few heads.
+  const int turn = static_cast<int>(blockIdx.x / a.kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const int slots = static_cast<int>(gridDim.x / a.kv_heads), split = static_cast<int>(blockIdx.z);
+  const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - turn : turn);
   if (!sp.any) return;
-  const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = sp.nq * a.group;
@@ -87,6 +104,16 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       vr[n] = load_piece(vbuf, voff[n]);
     }
   };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+      if (row < BN) {
+        ks[buf][TL::at(row, piece)] = kr[n];
+        vs[buf][TL::at(row, piece)] = vr[n];
+      }
+    }
+  };
 
   floatx16 acc[DB];
 #pragma unroll
@@ -94,68 +121,71 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   float m = -INFINITY, l = 0.f;  // maximum (in log2 units, see below) and this half's sum
   const float c = a.scale * kLog2e;
 
-  if (jb0 < jb1) load(jb0);
+  if (jb0 < jb1) {
+    load(jb0);
+    if constexpr (BUFS == 2) store(0);
+  }
   for (int jb = jb0; jb < jb1; ++jb) {
     __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NL; ++n) {
-      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
-      if (row < BN) {
-        ks[TL::at(row, piece)] = kr[n];
-        vs[TL::at(row, piece)] = vr[n];
-      }
+    if constexpr (BUFS == 1) {
+      store(0);
+      __syncthreads();
     }
     if (jb + 1 < jb1) load(jb + 1);
-    __syncthreads();
-    const int j0 = wg.lo + jb * BN;
-    if (!wave_on || j0 >= wv.hi || j0 + BN <= wv.lo) continue;
-
-    floatx16 s[NB];
+    const int buf = BUFS == 2 ? (jb - jb0) & 1 : 0;
+    for (int step = 0; step < BN / 32; step += NB) {
+      const int j0 = wg.lo + jb * BN + 32 * step;
+      if (!wave_on || j0 >= wv.hi) break;
+      if (j0 + 32 * NB <= wv.lo) continue;
+      floatx16 s[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      s[b] = floatx16(0.f);
+      for (int b = 0; b < NB; ++b) {
+        s[b] = floatx16(0.f);
 #pragma unroll
-      for (int t = 0; t < KS; ++t)
-        s[b] = mma_piece<T>(TL::row_piece(ks, 32 * b + (lane & 31), 2 * t + half), qf[t], s[b]);
-    }
-    if (j0 < full_lo || j0 + BN > full_hi) {
-      keep_branch();
+        for (int t = 0; t < KS; ++t)
+          s[b] = mma_piece<T>(TL::row_piece(ks[buf], 32 * (step + b) + (lane & 31), 2 * t + half), qf[t], s[b]);
+      }
+      if (j0 < full_lo || j0 + 32 * NB > full_hi) {
+        keep_branch();
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = j0 + 32 * b + 8 * (i / 4) + 4 * half + (i & 3);
+            s[b][i] = j >= lane_lo && j < lane_hi ? s[b][i] : -INFINITY;
+          }
+      }
+      float top = s[0][0];
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = j0 + 32 * b + 8 * (i / 4) + 4 * half + (i & 3);
-          s[b][i] = j >= lane_lo && j < lane_hi ? s[b][i] : -INFINITY;
-        }
-    }
-    float top = s[0][0];
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+      const float m_new = fmaxf(m, halves_max(top) * c);
+      // The sums are rescaled only when a row's maximum has grown by more than
+      // 2^8: until then its terms stay below 2^8 times the largest.
+      if (__any(m_new > m + 8.f)) {
+        const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
+        l *= alpha;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+        for (int db = 0; db < DB; ++db)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-    const float m_new = fmaxf(m, halves_max(top) * c);
-    // The sums are rescaled only when a row's maximum has grown by more than
-    // 2^8: until then its terms stay below 2^8 times the largest.
-    if (__any(m_new > m + 8.f)) {
-      const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
-      l *= alpha;
-#pragma unroll
-      for (int db = 0; db < DB; ++db)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[db][i] *= alpha;
-      m = m_new;
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float p[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[i] = fast_exp2(__builtin_fmaf(s[b][i], c, -base));
-        l += p[i];
+          for (int i = 0; i < 16; ++i) acc[db][i] *= alpha;
+        m = m_new;
       }
-      mma_transposed<T, DP, DB>(vs, 32 * b, lane, p, acc);
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          p[i] = fast_exp2(__builtin_fmaf(s[b][i], c, -base));
+          l += p[i];
+        }
+        mma_transposed<T, DP, DB>(vs[buf], 32 * (step + b), lane, p, acc);
+      }
+      settle<T>();
     }
+    if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1);
   }
 
   const float sum = halves_sum(l);
@@ -255,15 +285,10 @@ hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t
   const hipError_t e = dispatch(a, [&](auto t, auto dp) -> hipError_t {
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value;
-    const dim3 grid(static_cast<unsigned>(p.slots), static_cast<unsigned>(a.kv_heads), static_cast<unsigned>(p.nsplit));
-    constexpr int BN = sizeof(T) == 2 ? 64 : 32;
-    if (p.waves == 1) {
-      k_attention<T, DP, 1, 32><<<grid, 64, 0, stream>>>(a, p.nsplit, part_out, part_lse);
-    } else if (p.waves == 2) {
-      k_attention<T, DP, 2, BN><<<grid, 128, 0, stream>>>(a, p.nsplit, part_out, part_lse);
-    } else {
-      k_attention<T, DP, 4, BN><<<grid, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
-    }
+    const dim3 grid(static_cast<unsigned>(p.slots * a.kv_heads), 1, static_cast<unsigned>(p.nsplit));
+    if (p.waves == 1) k_attention<T, DP, 1><<<grid, 64, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+    else if (p.waves == 2) k_attention<T, DP, 2><<<grid, 128, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+    else k_attention<T, DP, 4><<<grid, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.nsplit == 1) return e;

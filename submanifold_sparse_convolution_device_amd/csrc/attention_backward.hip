@@ -54,16 +54,25 @@ __device__ __forceinline__ void rescale(float (&ds)[16], float& factor, floatx16
 }
 constexpr float kFirstFactor = 1.2676506002282294e30f;  // 2^100
 
-template <class T, int DP, int WAVES, int BN>
+// Rows per LDS tile of the side that a workgroup walks, and tiles of its two
+// tensors in LDS (two: one read, one filled; a lone wave stages through one).
+template <class T, int DP, int WAVES>
+constexpr int kWalk = sizeof(T) == 4 ? 32 : DP == 32 ? (WAVES == 4 ? 128 : 64) : DP == 64 && WAVES > 1 ? 64 : 32;
+template <int WAVES>
+constexpr int kBuffers = WAVES == 1 ? 1 : 2;
+
+template <class T, int DP, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int nsplit, float* delta, float* part) {
   typedef Tile<T, DP> TL;
-  constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
+  constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
-  __shared__ uint4 ks[BN * PPR], vs[BN * PPR];
+  __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
-  const Span sp = find_span<BM>(a, false, static_cast<int>(blockIdx.x));
+  const int turn = static_cast<int>(blockIdx.x / a.kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const int split = static_cast<int>(blockIdx.z);
+  const int slots = static_cast<int>(gridDim.x / a.kv_heads);
+  const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - turn : turn);
   if (!sp.any) return;
-  const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = sp.nq * a.group;
@@ -144,44 +153,54 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   float factor = kFirstFactor;
   const float c = a.scale * kLog2e;
 
-  if (jb0 < jb1) load(jb0);
-  for (int jb = jb0; jb < jb1; ++jb) {
-    __syncthreads();
+  auto store = [&](int buf) {
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
       const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
       if (row < BN) {
-        ks[TL::at(row, piece)] = kr[n];
-        vs[TL::at(row, piece)] = vr[n];
+        ks[buf][TL::at(row, piece)] = kr[n];
+        vs[buf][TL::at(row, piece)] = vr[n];
       }
     }
-    if (jb + 1 < jb1) load(jb + 1);
+  };
+  if (jb0 < jb1) {
+    load(jb0);
+    if constexpr (BUFS == 2) store(0);
+  }
+  for (int jb = jb0; jb < jb1; ++jb) {
     __syncthreads();
-    const int j0 = wg.lo + jb * BN;
-    if (!wave_on || j0 >= wv.hi || j0 + BN <= wv.lo) continue;
-    const bool partial = j0 < full_lo || j0 + BN > full_hi;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    if constexpr (BUFS == 1) {
+      store(0);
+      __syncthreads();
+    }
+    if (jb + 1 < jb1) load(jb + 1);
+    const int buf = BUFS == 2 ? (jb - jb0) & 1 : 0;
+    for (int b = 0; b < BN / 32; ++b) {
+      const int j0 = wg.lo + jb * BN + 32 * b;
+      if (!wave_on || j0 >= wv.hi) break;
+      if (j0 + 32 <= wv.lo) continue;
       floatx16 s(0.f), dp(0.f);
 #pragma unroll
       for (int t = 0; t < KS; ++t) {
-        s = mma_piece<T>(TL::row_piece(ks, 32 * b + (lane & 31), 2 * t + half), qf[t], s);
-        dp = mma_piece<T>(TL::row_piece(vs, 32 * b + (lane & 31), 2 * t + half), gf[t], dp);
+        s = mma_piece<T>(TL::row_piece(ks[buf], 32 * b + (lane & 31), 2 * t + half), qf[t], s);
+        dp = mma_piece<T>(TL::row_piece(vs[buf], 32 * b + (lane & 31), 2 * t + half), gf[t], dp);
       }
       float ds[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) ds[i] = fast_exp2(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - dot);
-      if (partial) {
+      if (j0 < full_lo || j0 + 32 > full_hi) {
         keep_branch();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int j = j0 + 32 * b + 8 * (i / 4) + 4 * half + (i & 3);
+          const int j = j0 + 8 * (i / 4) + 4 * half + (i & 3);
           ds[i] = j >= lane_lo && j < lane_hi ? ds[i] : 0.f;
         }
       }
       rescale<T, DB>(ds, factor, acc);
-      mma_transposed<T, DP, DB>(ks, 32 * b, lane, ds, acc);
+      mma_transposed<T, DP, DB>(ks[buf], 32 * b, lane, ds, acc);
+      settle<T>();
     }
+    if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1);
   }
 
   if (!has_row) return;
@@ -200,20 +219,21 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     }
 }
 
-template <class T, int DP, int WAVES, int BN>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int nsplit, const float* delta,
+template <class T, int DP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int nsplit, const float* delta,
                                                               float* part_k, float* part_v) {
   typedef Tile<T, DP> TL;
-  constexpr int PPR = TL::PPR, DB = DP / 32, NB = BN / 32, NT = 64 * WAVES;
+  constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
-  static_assert(BN <= NT, "one thread per row of a tile");
-  __shared__ uint4 qs[BN * PPR], gs[BN * PPR];
-  __shared__ float4 row_lse[BN / 4], row_delta[BN / 4];
-  __shared__ int4 row_place[BN / 4];
+  constexpr int NR = (BN + NT - 1) / NT;  // rows whose statistics each thread copies
+  __shared__ uint4 qs[BUFS][BN * PPR], gs[BUFS][BN * PPR];
+  __shared__ float4 row_lse[BUFS][BN / 4], row_delta[BUFS][BN / 4];
+  __shared__ int4 row_place[BUFS][BN / 4];
 
-  const Span sp = find_span<BM>(a, true, static_cast<int>(blockIdx.x));
+  const int turn = static_cast<int>(blockIdx.x / a.kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const int split = static_cast<int>(blockIdx.z);
+  const Span sp = find_span<BM>(a, true, turn);
   if (!sp.any) return;
-  const int kvh = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = sp.nq * a.group;
@@ -247,8 +267,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const int kw1 = min(kw0 + 32, sp.nk) - 1;  // last key of the wave
 
   uint4 qr[NL], gr[NL];
-  float lse_r = INFINITY, delta_r = 0.f;
-  int place_r = 0;
+  float lse_r[NR], delta_r[NR];
+  int place_r[NR];
   const T* qbase = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0) * a.q_row + static_cast<int64_t>(kvh) * a.group * a.q_head;
   const T* gbase = static_cast<const T*>(a.grad_out) + static_cast<int64_t>(sp.q0) * a.go_row + static_cast<int64_t>(kvh) * a.group * a.go_head;
   auto load = [&](int rb) {
@@ -264,18 +284,38 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
         gr[n] = *reinterpret_cast<const uint4*>(gbase + tok * a.go_row + g * a.go_head + piece * kPiece<T>);
       }
     }
-    if (tid < BN) {
-      const int r = r0 + tid;
-      lse_r = INFINITY;
-      delta_r = 0.f;
-      place_r = 0;
-      if (r < rows) {
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int r = r0 + tid + n * NT;
+      lse_r[n] = INFINITY;
+      delta_r[n] = 0.f;
+      place_r[n] = 0;
+      if (tid + n * NT < BN && r < rows) {
         const int tok = div_group(a, r), head = kvh * a.group + r - tok * a.group;
         const int64_t at = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
         const float v = a.lse[at];
-        lse_r = v == -INFINITY ? INFINITY : v * kLog2e - kShift<T>;
-        delta_r = delta[at];
-        place_r = tok + shift;
+        lse_r[n] = v == -INFINITY ? INFINITY : v * kLog2e - kShift<T>;
+        delta_r[n] = delta[at];
+        place_r[n] = tok + shift;
+      }
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+      if (row < BN) {
+        qs[buf][TL::at(row, piece)] = qr[n];
+        gs[buf][TL::at(row, piece)] = gr[n];
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int row = tid + n * NT;
+      if (row < BN) {
+        reinterpret_cast<float*>(row_lse[buf])[row] = lse_r[n];
+        reinterpret_cast<float*>(row_delta[buf])[row] = delta_r[n];
+        reinterpret_cast<int*>(row_place[buf])[row] = place_r[n];
       }
     }
   };
@@ -289,41 +329,34 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   float factor = kFirstFactor;
   const float c = a.scale * kLog2e;
 
-  if (rb0 < rb1) load(rb0);
+  if (rb0 < rb1) {
+    load(rb0);
+    if constexpr (BUFS == 2) store(0);
+  }
   for (int rb = rb0; rb < rb1; ++rb) {
     __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NL; ++n) {
-      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
-      if (row < BN) {
-        qs[TL::at(row, piece)] = qr[n];
-        gs[TL::at(row, piece)] = gr[n];
-      }
-    }
-    if (tid < BN) {
-      reinterpret_cast<float*>(row_lse)[tid] = lse_r;
-      reinterpret_cast<float*>(row_delta)[tid] = delta_r;
-      reinterpret_cast<int*>(row_place)[tid] = place_r;
+    if constexpr (BUFS == 1) {
+      store(0);
+      __syncthreads();
     }
     if (rb + 1 < rb1) load(rb + 1);
-    __syncthreads();
-    if (!wave_on) continue;
-    const int r0 = f_lo + rb * BN;
-    const int p0 = div_group(a, r0) + shift, p1 = div_group(a, min(r0 + BN, rows) - 1) + shift;  // places of the tile
-    if ((a.right >= 0 && kw0 > p1 + a.right) || (a.left >= 0 && kw1 < p0 - a.left)) continue;
-    const bool partial = (a.right >= 0 && kw1 > p0 + a.right) || (a.left >= 0 && kw0 < p1 - a.left);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    const int buf = BUFS == 2 ? (rb - rb0) & 1 : 0;
+    for (int b = 0; b < BN / 32; ++b) {
+      const int r0 = f_lo + rb * BN + 32 * b;
+      if (!wave_on || r0 >= rows) break;
+      const int p0 = div_group(a, r0) + shift, p1 = div_group(a, min(r0 + 32, rows) - 1) + shift;  // places of the block
+      if (a.right >= 0 && kw0 > p1 + a.right) continue;
+      if (a.left >= 0 && kw1 < p0 - a.left) break;
       floatx16 s(0.f), dp(0.f);
 #pragma unroll
       for (int t = 0; t < KS; ++t) {
-        s = mma_piece<T>(TL::row_piece(qs, 32 * b + (lane & 31), 2 * t + half), kf[t], s);
-        dp = mma_piece<T>(TL::row_piece(gs, 32 * b + (lane & 31), 2 * t + half), vf[t], dp);
+        s = mma_piece<T>(TL::row_piece(qs[buf], 32 * b + (lane & 31), 2 * t + half), kf[t], s);
+        dp = mma_piece<T>(TL::row_piece(gs[buf], 32 * b + (lane & 31), 2 * t + half), vf[t], dp);
       }
       float p[16], ds[16];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float4 ls = row_lse[8 * b + 2 * g + half], de = row_delta[8 * b + 2 * g + half];
+        const float4 ls = row_lse[buf][8 * b + 2 * g + half], de = row_delta[buf][8 * b + 2 * g + half];
         const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, dv4[4] = {de.x, de.y, de.z, de.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -332,11 +365,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
           ds[i] = p[i] * (dp[i] - dv4[u]);
         }
       }
-      if (partial) {
+      if ((a.right >= 0 && kw1 > p0 + a.right) || (a.left >= 0 && kw0 < p1 - a.left)) {
         keep_branch();
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int4 pl = row_place[8 * b + 2 * g + half];
+          const int4 pl = row_place[buf][8 * b + 2 * g + half];
           const int pv[4] = {pl.x, pl.y, pl.z, pl.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -346,10 +379,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
           }
         }
       }
-      mma_transposed<T, DP, DB>(gs, 32 * b, lane, p, dv);
+      mma_transposed<T, DP, DB>(gs[buf], 32 * b, lane, p, dv);
       rescale<T, DB>(ds, factor, dk);
-      mma_transposed<T, DP, DB>(qs, 32 * b, lane, ds, dk);
+      mma_transposed<T, DP, DB>(qs[buf], 32 * b, lane, ds, dk);
+      settle<T>();
     }
+    if (BUFS == 2 && rb + 1 < rb1) store(buf ^ 1);
   }
 
   if (!has_key) return;
@@ -423,7 +458,7 @@ Plan make_backward_plan(const AttentionArgs& a) {
   p.q_slots = span_slots(rows, a.batch, 32 * p.q_waves);
   p.k_slots = span_slots(a.total_k, a.batch, 32 * p.k_waves);
   auto split = [&](int64_t tiles, int64_t depth) {
-    const int64_t s = std::min<int64_t>(1024 / std::max<int64_t>(tiles, 1), depth / 256);
+    const int64_t s = std::min<int64_t>(4096 / std::max<int64_t>(tiles, 1), depth / 256);
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, 32)));
   };
   int64_t q_depth = a.total_k / batch, k_depth = rows / batch;
@@ -468,21 +503,20 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
   return dispatch(a, [&](auto t, auto dp) -> hipError_t {
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value;
-    constexpr int BN = 32;
     if (a.total_q > 0) {
-      const dim3 grid(static_cast<unsigned>(p.q_slots), static_cast<unsigned>(a.kv_heads), static_cast<unsigned>(p.q_split));
-      if (p.q_waves == 1) k_attention_dq<T, DP, 1, BN><<<grid, 64, 0, stream>>>(a, p.q_split, delta, part_q);
-      else if (p.q_waves == 2) k_attention_dq<T, DP, 2, BN><<<grid, 128, 0, stream>>>(a, p.q_split, delta, part_q);
-      else k_attention_dq<T, DP, 4, BN><<<grid, 256, 0, stream>>>(a, p.q_split, delta, part_q);
+      const dim3 grid(static_cast<unsigned>(p.q_slots * a.kv_heads), 1, static_cast<unsigned>(p.q_split));
+      if (p.q_waves == 1) k_attention_dq<T, DP, 1><<<grid, 64, 0, stream>>>(a, p.q_split, delta, part_q);
+      else if (p.q_waves == 2) k_attention_dq<T, DP, 2><<<grid, 128, 0, stream>>>(a, p.q_split, delta, part_q);
+      else k_attention_dq<T, DP, 4><<<grid, 256, 0, stream>>>(a, p.q_split, delta, part_q);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.q_split > 1) launch_join<T>(part_q, p.q_split, a.total_q, a.heads, a.dim, a.grad_q, a.gq_row, a.gq_head, stream);
     }
     if (a.total_k > 0) {
-      const dim3 grid(static_cast<unsigned>(p.k_slots), static_cast<unsigned>(a.kv_heads), static_cast<unsigned>(p.k_split));
-      if (p.k_waves == 1) k_attention_dkv<T, DP, 1, BN><<<grid, 64, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
-      else if (p.k_waves == 2) k_attention_dkv<T, DP, 2, BN><<<grid, 128, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
-      else k_attention_dkv<T, DP, 4, BN><<<grid, 256, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
+      const dim3 grid(static_cast<unsigned>(p.k_slots * a.kv_heads), 1, static_cast<unsigned>(p.k_split));
+      if (p.k_waves == 1) k_attention_dkv<T, DP, 1><<<grid, 64, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
+      else if (p.k_waves == 2) k_attention_dkv<T, DP, 2><<<grid, 128, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
+      else k_attention_dkv<T, DP, 4><<<grid, 256, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.k_split > 1) {

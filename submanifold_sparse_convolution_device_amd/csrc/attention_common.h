@@ -169,6 +169,21 @@ __device__ __forceinline__ void mma_transposed(const uint4* lds, int row0, int l
   }
 }
 
+// Ends a step whose last instructions are matrix products: waits until their
+// sums can be read.  The hardware does not hold back a vector instruction
+// that reads an accumulator too early, and the compiler, which places the
+// waits, has been seen to omit them where two paths of different length lead
+// from the product to the read across blocks (the last accumulator register
+// then held the value before the product).  16 passes need 18 states, 8
+// passes 11; with the wait in the product's own block no path is shorter.
+template <class T>
+__device__ __forceinline__ void settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15");
+  if constexpr (sizeof(T) == 4) asm volatile("s_nop 7");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 __device__ __forceinline__ int div_group(const AttentionArgs& a, int row) { return fast_div(row, a.by_group); }
 
 // One tile's sequence: its rows on both sides and the first (flattened) row
@@ -194,43 +209,51 @@ __device__ __forceinline__ int bound(const int32_t* cu, int batch, int total, in
 // Sequence and tile of a slot.  Sequence b starts at slot
 // floor(bound(b) x mult / TILE) + b, which leaves every sequence at least
 // ceil(rows x mult / TILE) slots and needs no pass over the lengths before;
-// the wavefront finds b in rounds of 64 probes.
+// the wavefront finds b in rounds of 64 probes, the last of which holds its
+// bounds (one round up to 62 sequences, two up to 4094).
 template <int TILE>
 __device__ __forceinline__ Span find_span(const AttentionArgs& a, bool by_keys, int slot) {
   const int lane = threadIdx.x & 63;
   const int32_t* cu = by_keys ? a.cu_k : a.cu_q;
   const int total = by_keys ? a.total_k : a.total_q;
   const int mult = by_keys ? 1 : a.group;
-  auto start = [&](int b) {
-    return static_cast<int>(static_cast<int64_t>(bound(cu, a.batch, total, b)) * mult / TILE) + b;
-  };
-  int lo = 0, hi = a.batch + 2;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 63) >> 6;
+  const int last = a.batch + 2;  // bounds 0 .. last
+  int lo = 0, hi = last, step, v, c;
+  do {
+    step = (hi - lo + 63) >> 6;
     const int at = lo + lane * step;
-    const bool le = at < hi && start(at) <= slot;
-    const int c = __builtin_popcountll(__ballot(le));
-    const int base = lo + (c > 0 ? c - 1 : 0) * step;
-    hi = min(base + step, hi);
-    lo = base;
+    v = bound(cu, a.batch, total, min(at, last));
+    const int start = static_cast<int>(static_cast<int64_t>(v) * mult / TILE) + at;
+    c = max(__builtin_popcountll(__ballot(at < hi && start <= slot)), 1);
+    if (step == 1) break;
+    lo += (c - 1) * step;
+    hi = min(lo + step, hi);
+  } while (true);
+  const int b = __builtin_amdgcn_readfirstlane(lo + c - 1);
+  const int n = __builtin_amdgcn_readfirstlane(c);
+  const int r0 = __builtin_amdgcn_readlane(v, n - 1);
+  int r1 = n < 64 ? __builtin_amdgcn_readlane(v, n) : __builtin_amdgcn_readfirstlane(bound(cu, a.batch, total, b + 1));
+  const int nr = max(r1 - r0, 0);
+  int o0 = r0, no = nr;  // the other side
+  if (a.cu_q != a.cu_k || a.total_q != a.total_k) {
+    const int32_t* other = by_keys ? a.cu_q : a.cu_k;
+    const int ototal = by_keys ? a.total_q : a.total_k;
+    o0 = bound(other, a.batch, ototal, b);
+    no = max(bound(other, a.batch, ototal, b + 1) - o0, 0);
+    o0 = __builtin_amdgcn_readfirstlane(o0);
+    no = __builtin_amdgcn_readfirstlane(no);
   }
-  const int b = __builtin_amdgcn_readfirstlane(lo);
-  Span s;
-  s.q0 = bound(a.cu_q, a.batch, a.total_q, b);
-  s.nq = max(bound(a.cu_q, a.batch, a.total_q, b + 1) - s.q0, 0);
-  s.k0 = bound(a.cu_k, a.batch, a.total_k, b);
-  s.nk = max(bound(a.cu_k, a.batch, a.total_k, b + 1) - s.k0, 0);
-  const int64_t rows = static_cast<int64_t>(by_keys ? s.nk : s.nq) * mult;
-  const int64_t r0 = static_cast<int64_t>(slot - start(b)) * TILE;
-  s.any = r0 >= 0 && r0 < rows;
-  s.r0 = s.any ? static_cast<int>(r0) : 0;
   // a sequence before the first offset or after the last has no counterpart
-  if (b == 0 || b == a.batch + 1) (by_keys ? s.nq : s.nk) = 0;
-  s.q0 = __builtin_amdgcn_readfirstlane(s.q0);
-  s.nq = __builtin_amdgcn_readfirstlane(s.nq);
-  s.k0 = __builtin_amdgcn_readfirstlane(s.k0);
-  s.nk = __builtin_amdgcn_readfirstlane(s.nk);
-  s.r0 = __builtin_amdgcn_readfirstlane(s.r0);
+  if (b == 0 || b == a.batch + 1) no = 0;
+  Span s;
+  s.q0 = by_keys ? o0 : r0;
+  s.nq = by_keys ? no : nr;
+  s.k0 = by_keys ? r0 : o0;
+  s.nk = by_keys ? nr : no;
+  const int64_t rows = static_cast<int64_t>(nr) * mult;
+  const int64_t t0 = static_cast<int64_t>(slot - (static_cast<int>(static_cast<int64_t>(r0) * mult / TILE) + b)) * TILE;
+  s.any = t0 >= 0 && t0 < rows;
+  s.r0 = s.any ? static_cast<int>(t0) : 0;
   return s;
 }
 
