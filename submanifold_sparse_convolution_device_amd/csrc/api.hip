@@ -665,6 +665,7 @@ spconv_status attention_args(const spconv_attention* x, const void* d_out, const
   a->group = x->heads / x->kv_heads;
   a->dim = x->head_dim;
   a->by_group = spconv::make_fast_div(a->group);
+  a->by_kv_heads = spconv::make_fast_div(a->kv_heads);
   // a bound past every row is none
   a->left = x->left < 0 || x->left >= (1 << 30) ? -1 : x->left;
   a->right = x->right < 0 || x->right >= (1 << 30) ? -1 : x->right;

@@ -30,8 +30,8 @@ constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 // tiles of one split.  Q stays in registers (operand B of S^T = K Q^T), K and
 // V pass through LDS, loaded a tile ahead into registers.
 template <class T, int DP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int nsplit, float* part_out,
-                                                                                 float* part_lse) {
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int slots, int nsplit,
+                                                                                 float* part_out, float* part_lse) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kKeys<T, DP, WAVES>, BUFS = kBuffers<WAVES>;
   constexpr int NB = BN >= 64 ? 2 : 1;  // blocks of 32 keys per softmax step
@@ -44,8 +44,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   // Under a causal mask the last rows have the most keys: they go first.
   // Consecutive workgroups, which go to different XCDs, take different kv
   // heads, so that an XCD's L2 sees few heads.
-  const int turn = static_cast<int>(blockIdx.x / a.kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
-  const int slots = static_cast<int>(gridDim.x / a.kv_heads), split = static_cast<int>(blockIdx.z);
+  const int turn = fast_div(static_cast<int>(blockIdx.x), a.by_kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const int split = static_cast<int>(blockIdx.z);
   const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - turn : turn);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
@@ -80,8 +80,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const int full_hi = a.right >= 0 ? min(wp0 + a.right + 1, sp.nk) : sp.nk;  // and below here, every row of the wave sees
 
   const int blocks = wg.hi > wg.lo ? (wg.hi - wg.lo + BN - 1) / BN : 0;
-  const int jb0 = static_cast<int>(static_cast<int64_t>(blocks) * split / nsplit);
-  const int jb1 = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / nsplit);
+  const Share mine = share_of(blocks, split, nsplit);
+  const int jb0 = mine.first, jb1 = mine.end;
 
   const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head + static_cast<int64_t>(sp.k0) * a.k_row;
   const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head + static_cast<int64_t>(sp.k0) * a.v_row;
@@ -145,15 +145,21 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
         for (int t = 0; t < KS; ++t)
           s[b] = mma_piece<T>(TL::row_piece(ks[buf], 32 * (step + b) + (lane & 31), 2 * t + half), qf[t], s[b]);
       }
-      if (j0 < full_lo || j0 + 32 * NB > full_hi) {
+      if (j0 + 32 * NB > full_hi) {
         keep_branch();
+        const int end = lane_hi - j0 - 4 * half;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = j0 + 32 * b + 8 * (i / 4) + 4 * half + (i & 3);
-            s[b][i] = j >= lane_lo && j < lane_hi ? s[b][i] : -INFINITY;
-          }
+          for (int i = 0; i < 16; ++i) s[b][i] = 32 * b + c_row(i) < end ? s[b][i] : -INFINITY;
+      }
+      if (j0 < full_lo) {
+        keep_branch();
+        const int first = lane_lo - j0 - 4 * half;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[b][i] = 32 * b + c_row(i) >= first ? s[b][i] : -INFINITY;
       }
       float top = s[0][0];
 #pragma unroll
@@ -286,9 +292,9 @@ hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value;
     const dim3 grid(static_cast<unsigned>(p.slots * a.kv_heads), 1, static_cast<unsigned>(p.nsplit));
-    if (p.waves == 1) k_attention<T, DP, 1><<<grid, 64, 0, stream>>>(a, p.nsplit, part_out, part_lse);
-    else if (p.waves == 2) k_attention<T, DP, 2><<<grid, 128, 0, stream>>>(a, p.nsplit, part_out, part_lse);
-    else k_attention<T, DP, 4><<<grid, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+    if (p.waves == 1) k_attention<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.slots), p.nsplit, part_out, part_lse);
+    else if (p.waves == 2) k_attention<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.slots), p.nsplit, part_out, part_lse);
+    else k_attention<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.slots), p.nsplit, part_out, part_lse);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.nsplit == 1) return e;

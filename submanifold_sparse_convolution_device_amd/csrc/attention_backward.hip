@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "attention_common.h"
@@ -62,15 +63,15 @@ template <int WAVES>
 constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 
 template <class T, int DP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int nsplit, float* delta, float* part) {
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int nsplit,
+                                                                                    float* delta, float* part) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
   __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
-  const int turn = static_cast<int>(blockIdx.x / a.kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const int turn = fast_div(static_cast<int>(blockIdx.x), a.by_kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
   const int split = static_cast<int>(blockIdx.z);
-  const int slots = static_cast<int>(gridDim.x / a.kv_heads);
   const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - turn : turn);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
@@ -122,8 +123,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const int full_hi = a.right >= 0 ? min(wp0 + a.right + 1, sp.nk) : sp.nk;
 
   const int blocks = wg.hi > wg.lo ? (wg.hi - wg.lo + BN - 1) / BN : 0;
-  const int jb0 = static_cast<int>(static_cast<int64_t>(blocks) * split / nsplit);
-  const int jb1 = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / nsplit);
+  const Share mine = share_of(blocks, split, nsplit);
+  const int jb0 = mine.first, jb1 = mine.end;
 
   const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head + static_cast<int64_t>(sp.k0) * a.k_row;
   const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head + static_cast<int64_t>(sp.k0) * a.v_row;
@@ -188,13 +189,17 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       float ds[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) ds[i] = fast_exp2(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - dot);
-      if (j0 < full_lo || j0 + 32 > full_hi) {
+      if (j0 + 32 > full_hi) {
         keep_branch();
+        const int end = lane_hi - j0 - 4 * half;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = j0 + 8 * (i / 4) + 4 * half + (i & 3);
-          ds[i] = j >= lane_lo && j < lane_hi ? ds[i] : 0.f;
-        }
+        for (int i = 0; i < 16; ++i) ds[i] = c_row(i) < end ? ds[i] : 0.f;
+      }
+      if (j0 < full_lo) {
+        keep_branch();
+        const int first = lane_lo - j0 - 4 * half;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ds[i] = c_row(i) >= first ? ds[i] : 0.f;
       }
       rescale<T, DB>(ds, factor, acc);
       mma_transposed<T, DP, DB>(ks[buf], 32 * b, lane, ds, acc);
@@ -230,7 +235,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
   __shared__ float4 row_lse[BUFS][BN / 4], row_delta[BUFS][BN / 4];
   __shared__ int4 row_place[BUFS][BN / 4];
 
-  const int turn = static_cast<int>(blockIdx.x / a.kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const int turn = fast_div(static_cast<int>(blockIdx.x), a.by_kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
   const int split = static_cast<int>(blockIdx.z);
   const Span sp = find_span<BM>(a, true, turn);
   if (!sp.any) return;
@@ -261,8 +266,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
   const int i_hi = a.left >= 0 ? min(kt1 + a.left - shift, sp.nq) : sp.nq;
   const int f_lo = i_lo * a.group, f_hi = i_hi * a.group;
   const int blocks = f_hi > f_lo ? (f_hi - f_lo + BN - 1) / BN : 0;
-  const int rb0 = static_cast<int>(static_cast<int64_t>(blocks) * split / nsplit);
-  const int rb1 = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / nsplit);
+  const Share mine = share_of(blocks, split, nsplit);
+  const int rb0 = mine.first, rb1 = mine.end;
   const bool wave_on = kw0 < sp.nk;
   const int kw1 = min(kw0 + 32, sp.nk) - 1;  // last key of the wave
 
@@ -365,15 +370,18 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
           ds[i] = p[i] * (dp[i] - dv4[u]);
         }
       }
-      if ((a.right >= 0 && kw1 > p0 + a.right) || (a.left >= 0 && kw0 < p1 - a.left)) {
+      const bool cut_hi = a.right >= 0 && kw1 > p0 + a.right, cut_lo = a.left >= 0 && kw0 < p1 - a.left;
+      if (cut_hi || cut_lo) {
         keep_branch();
+        // places from first to last see the key
+        const int first = cut_hi ? key - a.right : INT_MIN, last = cut_lo ? key + a.left : INT_MAX;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int4 pl = row_place[buf][8 * b + 2 * g + half];
           const int pv[4] = {pl.x, pl.y, pl.z, pl.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const bool seen = (a.right < 0 || key <= pv[u] + a.right) && (a.left < 0 || key >= pv[u] - a.left);
+            const bool seen = pv[u] >= first && pv[u] <= last;
             p[4 * g + u] = seen ? p[4 * g + u] : 0.f;
             ds[4 * g + u] = seen ? ds[4 * g + u] : 0.f;
           }
@@ -505,9 +513,9 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
     constexpr int DP = decltype(dp)::value;
     if (a.total_q > 0) {
       const dim3 grid(static_cast<unsigned>(p.q_slots * a.kv_heads), 1, static_cast<unsigned>(p.q_split));
-      if (p.q_waves == 1) k_attention_dq<T, DP, 1><<<grid, 64, 0, stream>>>(a, p.q_split, delta, part_q);
-      else if (p.q_waves == 2) k_attention_dq<T, DP, 2><<<grid, 128, 0, stream>>>(a, p.q_split, delta, part_q);
-      else k_attention_dq<T, DP, 4><<<grid, 256, 0, stream>>>(a, p.q_split, delta, part_q);
+      if (p.q_waves == 1) k_attention_dq<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), p.q_split, delta, part_q);
+      else if (p.q_waves == 2) k_attention_dq<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), p.q_split, delta, part_q);
+      else k_attention_dq<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), p.q_split, delta, part_q);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.q_split > 1) launch_join<T>(part_q, p.q_split, a.total_q, a.heads, a.dim, a.grad_q, a.gq_row, a.gq_head, stream);

@@ -275,6 +275,20 @@ __device__ __forceinline__ KeyRange key_range(const AttentionArgs& a, int nk, in
 // masks of every tile and selects, 130 instructions a tile of 64 keys.
 __device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
 
+// The blocks of one split: an even share of [0, blocks).
+struct Share {
+  int first, end;
+};
+__device__ __forceinline__ Share share_of(int blocks, int split, int nsplit) {
+  if (nsplit == 1) return {0, blocks};
+  // blocks < 2^26 (32 rows each) and nsplit <= 64
+  const uint32_t b = static_cast<uint32_t>(blocks), n = static_cast<uint32_t>(nsplit), s = static_cast<uint32_t>(split);
+  return {static_cast<int>(b * s / n), static_cast<int>(b * (s + 1) / n)};
+}
+
+// Row of register i of a C tile within its 32, without the half's 4.
+__host__ __device__ constexpr int c_row(int i) { return 8 * (i / 4) + (i & 3); }
+
 // Stores 4 consecutive values as T.
 template <class T>
 __device__ __forceinline__ void store4(T* dst, float x, float y, float z, float w) {

@@ -303,7 +303,7 @@ struct AttentionArgs {
   const int32_t* cu_k = nullptr;
   int32_t batch = 0, total_q = 0, total_k = 0;
   int32_t heads = 0, kv_heads = 0, group = 1, dim = 0;
-  FastDiv by_group;
+  FastDiv by_group, by_kv_heads;
   int32_t left = -1, right = -1;  // visible keys around a query's place, -1: unbounded
   float scale = 0.f;
   int32_t dtype = 0;
