@@ -30,7 +30,7 @@ constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 // tiles of one split.  Q stays in registers (operand B of S^T = K Q^T), K and
 // V pass through LDS, loaded a tile ahead into registers.
 template <class T, int DP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int slots, int nsplit,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int slots, int run, int nsplit,
                                                                                  float* part_out, float* part_lse) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kKeys<T, DP, WAVES>, BUFS = kBuffers<WAVES>;
@@ -42,11 +42,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
   // Under a causal mask the last rows have the most keys: they go first.
-  // Consecutive workgroups, which go to different XCDs, take different kv
-  // heads, so that an XCD's L2 sees few heads.
-  const int turn = fast_div(static_cast<int>(blockIdx.x), a.by_kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const Place at = place_of(a, run);
+  if (at.slot >= slots) return;
+  const int kvh = at.kvh;
   const int split = static_cast<int>(blockIdx.z);
-  const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - turn : turn);
+  const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - at.slot : at.slot, slots);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -211,9 +211,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
           store4<T>(dst + d, acc[db][4 * g] * inv, acc[db][4 * g + 1] * inv, acc[db][4 * g + 2] * inv, acc[db][4 * g + 3] * inv);
       }
   } else {
-    const int64_t at = static_cast<int64_t>(split) * a.total_q * a.heads + row_out;
-    if (half == 0) part_lse[at] = lse;
-    float* dst = part_out + at * a.dim;
+    const int64_t at_out = static_cast<int64_t>(split) * a.total_q * a.heads + row_out;
+    if (half == 0) part_lse[at_out] = lse;
+    float* dst = part_out + at_out * a.dim;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -291,10 +291,11 @@ hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t
   const hipError_t e = dispatch(a, [&](auto t, auto dp) -> hipError_t {
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value;
-    const dim3 grid(static_cast<unsigned>(p.slots * a.kv_heads), 1, static_cast<unsigned>(p.nsplit));
-    if (p.waves == 1) k_attention<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.slots), p.nsplit, part_out, part_lse);
-    else if (p.waves == 2) k_attention<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.slots), p.nsplit, part_out, part_lse);
-    else k_attention<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.slots), p.nsplit, part_out, part_lse);
+    const int run = slot_run(a, p.slots);
+    const dim3 grid(static_cast<unsigned>(placed_slots(p.slots, run) * a.kv_heads), 1, static_cast<unsigned>(p.nsplit));
+    if (p.waves == 1) k_attention<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.slots), run, p.nsplit, part_out, part_lse);
+    else if (p.waves == 2) k_attention<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.slots), run, p.nsplit, part_out, part_lse);
+    else k_attention<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.slots), run, p.nsplit, part_out, part_lse);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.nsplit == 1) return e;

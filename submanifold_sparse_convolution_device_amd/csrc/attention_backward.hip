@@ -63,16 +63,18 @@ template <int WAVES>
 constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 
 template <class T, int DP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int nsplit,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int run, int nsplit,
                                                                                     float* delta, float* part) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
   __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
-  const int turn = fast_div(static_cast<int>(blockIdx.x), a.by_kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const Place at_block = place_of(a, run);
+  if (at_block.slot >= slots) return;
+  const int kvh = at_block.kvh;
   const int split = static_cast<int>(blockIdx.z);
-  const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - turn : turn);
+  const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - at_block.slot : at_block.slot, slots);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -225,7 +227,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
 }
 
 template <class T, int DP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int nsplit, const float* delta,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int slots, int run, int nsplit, const float* delta,
                                                               float* part_k, float* part_v) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
@@ -235,9 +237,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
   __shared__ float4 row_lse[BUFS][BN / 4], row_delta[BUFS][BN / 4];
   __shared__ int4 row_place[BUFS][BN / 4];
 
-  const int turn = fast_div(static_cast<int>(blockIdx.x), a.by_kv_heads), kvh = static_cast<int>(blockIdx.x) - turn * a.kv_heads;
+  const Place at_block = place_of(a, run);
+  if (at_block.slot >= slots) return;
+  const int kvh = at_block.kvh;
   const int split = static_cast<int>(blockIdx.z);
-  const Span sp = find_span<BM>(a, true, turn);
+  const Span sp = find_span<BM>(a, true, at_block.slot, slots);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -512,19 +516,21 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value;
     if (a.total_q > 0) {
-      const dim3 grid(static_cast<unsigned>(p.q_slots * a.kv_heads), 1, static_cast<unsigned>(p.q_split));
-      if (p.q_waves == 1) k_attention_dq<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), p.q_split, delta, part_q);
-      else if (p.q_waves == 2) k_attention_dq<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), p.q_split, delta, part_q);
-      else k_attention_dq<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), p.q_split, delta, part_q);
+      const int run = slot_run(a, p.q_slots);
+      const dim3 grid(static_cast<unsigned>(placed_slots(p.q_slots, run) * a.kv_heads), 1, static_cast<unsigned>(p.q_split));
+      if (p.q_waves == 1) k_attention_dq<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
+      else if (p.q_waves == 2) k_attention_dq<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
+      else k_attention_dq<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.q_split > 1) launch_join<T>(part_q, p.q_split, a.total_q, a.heads, a.dim, a.grad_q, a.gq_row, a.gq_head, stream);
     }
     if (a.total_k > 0) {
-      const dim3 grid(static_cast<unsigned>(p.k_slots * a.kv_heads), 1, static_cast<unsigned>(p.k_split));
-      if (p.k_waves == 1) k_attention_dkv<T, DP, 1><<<grid, 64, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
-      else if (p.k_waves == 2) k_attention_dkv<T, DP, 2><<<grid, 128, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
-      else k_attention_dkv<T, DP, 4><<<grid, 256, 0, stream>>>(a, p.k_split, delta, part_k, part_v);
+      const int run = slot_run(a, p.k_slots);
+      const dim3 grid(static_cast<unsigned>(placed_slots(p.k_slots, run) * a.kv_heads), 1, static_cast<unsigned>(p.k_split));
+      if (p.k_waves == 1) k_attention_dkv<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
+      else if (p.k_waves == 2) k_attention_dkv<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
+      else k_attention_dkv<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.k_split > 1) {

@@ -208,27 +208,39 @@ __device__ __forceinline__ int bound(const int32_t* cu, int batch, int total, in
 
 // Sequence and tile of a slot.  Sequence b starts at slot
 // floor(bound(b) x mult / TILE) + b, which leaves every sequence at least
-// ceil(rows x mult / TILE) slots and needs no pass over the lengths before;
-// the wavefront finds b in rounds of 64 probes, the last of which holds its
-// bounds (one round up to 62 sequences, two up to 4094).
+// ceil(rows x mult / TILE) slots and needs no pass over the lengths before.
+// The wavefront finds b by probing 64 sequences at a time: first those around
+// the place that equal lengths would give, which mostly ends the search in
+// one round of loads, else in rounds that narrow 64-fold.
 template <int TILE>
-__device__ __forceinline__ Span find_span(const AttentionArgs& a, bool by_keys, int slot) {
+__device__ __forceinline__ Span find_span(const AttentionArgs& a, bool by_keys, int slot, int slots) {
   const int lane = threadIdx.x & 63;
   const int32_t* cu = by_keys ? a.cu_k : a.cu_q;
   const int total = by_keys ? a.total_k : a.total_q;
   const int mult = by_keys ? 1 : a.group;
   const int last = a.batch + 2;  // bounds 0 .. last
-  int lo = 0, hi = last, step, v, c;
-  do {
-    step = (hi - lo + 63) >> 6;
+  int lo = 0, hi = last, step = 1, v, c;
+  auto probe = [&]() {
     const int at = lo + lane * step;
     v = bound(cu, a.batch, total, min(at, last));
     const int start = static_cast<int>(static_cast<int64_t>(v) * mult / TILE) + at;
-    c = max(__builtin_popcountll(__ballot(at < hi && start <= slot)), 1);
+    return __builtin_popcountll(__ballot(at < hi && start <= slot));
+  };
+  bool found = false;
+  if (last > 64) {
+    const float guess = static_cast<float>(slot) * static_cast<float>(last) / static_cast<float>(slots);
+    lo = min(max(static_cast<int>(guess) - 32, 0), last - 64);
+    c = probe();
+    found = c > 0 && (c < 64 || lo + 64 == last);
+    if (!found) lo = 0;
+  }
+  while (!found) {
+    step = (hi - lo + 63) >> 6;
+    c = max(probe(), 1);
     if (step == 1) break;
     lo += (c - 1) * step;
     hi = min(lo + step, hi);
-  } while (true);
+  }
   const int b = __builtin_amdgcn_readfirstlane(lo + c - 1);
   const int n = __builtin_amdgcn_readfirstlane(c);
   const int r0 = __builtin_amdgcn_readlane(v, n - 1);
@@ -274,6 +286,35 @@ __device__ __forceinline__ KeyRange key_range(const AttentionArgs& a, int nk, in
 // Keeps a rarely taken branch a branch: without it the compiler computes the
 // masks of every tile and selects, 130 instructions a tile of 64 keys.
 __device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
+
+// Slot and kv head of a workgroup.  Consecutive workgroups go to different
+// XCDs, each with its own L2 (8 of them).
+//   Heads first (run 0): an XCD sees few heads, whose keys and values fit its
+//   L2 while the tiles of a long sequence walk them.
+//   Runs of slots: an XCD takes `run` consecutive slots with all their heads.
+//   Rows shorter than a 128-byte line share it with the next head, so that
+//   heads on different XCDs would each fetch it.
+struct Place {
+  int slot, kvh;
+};
+constexpr int kXcds = 8;
+__device__ __forceinline__ Place place_of(const AttentionArgs& a, int run) {
+  const int id = static_cast<int>(blockIdx.x);
+  if (run == 0) {
+    const int slot = fast_div(id, a.by_kv_heads);
+    return {slot, id - slot * a.kv_heads};
+  }
+  const int j = id / kXcds, q = fast_div(j, a.by_kv_heads);
+  return {(q / run * kXcds + id % kXcds) * run + q % run, j - q * a.kv_heads};
+}
+inline int slot_run(const AttentionArgs& a, int64_t slots) {
+  const int bytes = a.dim * (a.dtype == 0 ? 4 : 2);
+  return bytes < 128 && a.kv_heads > 1 && slots >= 128 ? 4 : 0;  // (fewer would leave XCDs without work)
+}
+inline int64_t placed_slots(int64_t slots, int run) {
+  const int64_t unit = static_cast<int64_t>(run) * kXcds;
+  return run == 0 ? slots : (slots + unit - 1) / unit * unit;
+}
 
 // The blocks of one split: an even share of [0, blocks).
 struct Share {
