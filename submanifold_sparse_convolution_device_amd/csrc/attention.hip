@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "attention_common.h"
@@ -26,12 +27,22 @@ constexpr int kKeys = sizeof(T) == 4 ? 32 : DP == 32 ? (WAVES == 4 ? 128 : 64) :
 template <int WAVES>
 constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 
+// How the keys of few rows are cut: sequences of at most 32 flattened rows
+// (and some keys) go over chunks of 2^shift keys, one wave each, found by the
+// same slots on the key side; the workgroups after them take the sequences
+// that are left, a tile of rows at a time.  Balanced whatever the lengths.
+struct Chunks {
+  int slots = 0;  // 0: no chunks
+  int shift = 0;
+};
+__device__ __forceinline__ bool chunked(int rows, int nk) { return rows <= 32 && nk > 0; }
+
 // One workgroup: 32 flattened query rows per wave, one kv head, and the key
-// tiles of one split.  Q stays in registers (operand B of S^T = K Q^T), K and
-// V pass through LDS, loaded a tile ahead into registers.
+// tiles of one split or chunk.  Q stays in registers (operand B of
+// S^T = K Q^T), K and V pass through LDS, loaded a tile ahead into registers.
 template <class T, int DP, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int slots, int run, int nsplit,
-                                                                                 float* part_out, float* part_lse) {
+                                                                                 Chunks chunks, float* part_out, float* part_lse) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kKeys<T, DP, WAVES>, BUFS = kBuffers<WAVES>;
   constexpr int NB = BN >= 64 ? 2 : 1;  // blocks of 32 keys per softmax step
@@ -41,13 +52,32 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   constexpr int NL = (BN * PPR + NT - 1) / NT;  // pieces each thread copies per tile
   __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
-  // Under a causal mask the last rows have the most keys: they go first.
-  const Place at = place_of(a, run);
-  if (at.slot >= slots) return;
-  const int kvh = at.kvh;
   const int split = static_cast<int>(blockIdx.z);
-  const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - at.slot : at.slot, slots);
-  if (!sp.any) return;
+  int kvh, chunk0 = 0, chunk1 = INT_MAX;
+  int64_t part_row = -1;  // of the chunk's first row; -1: not a chunk
+  Span sp;
+  if (WAVES == 1 && chunks.slots > 0) {
+    const int slot = fast_div(static_cast<int>(blockIdx.x), a.by_kv_heads);
+    kvh = static_cast<int>(blockIdx.x) - slot * a.kv_heads;
+    if (slot < chunks.slots) {
+      sp = find_span(a, true, 1, chunks.shift, slot, chunks.slots);
+      if (!sp.any || sp.nq == 0 || !chunked(sp.nq * a.group, sp.nk)) return;
+      chunk0 = sp.r0;
+      chunk1 = sp.r0 + (1 << chunks.shift);
+      sp.r0 = 0;
+      part_row = (static_cast<int64_t>(slot) * a.kv_heads + kvh) * 32;
+    } else {
+      sp = find_span(a, false, a.group, tile_shift(WAVES), slot - chunks.slots, slots);
+      if (!sp.any || chunked(sp.nq * a.group, sp.nk)) return;
+    }
+  } else {
+    // Under a causal mask the last rows have the most keys: they go first.
+    const Place at = place_of(a, run);
+    if (at.slot >= slots) return;
+    kvh = at.kvh;
+    sp = find_span(a, false, a.group, tile_shift(WAVES), a.right >= 0 ? slots - 1 - at.slot : at.slot, slots);
+    if (!sp.any) return;
+  }
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = sp.nq * a.group;
@@ -70,14 +100,20 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   }
   const int place = tok + shift;
   const int lane_lo = a.left >= 0 ? place - a.left : 0;
-  const int lane_hi = a.right >= 0 ? min(place + a.right + 1, sp.nk) : sp.nk;
+  const int key_end = WAVES == 1 ? min(sp.nk, chunk1) : sp.nk;
+  const int lane_hi = a.right >= 0 ? min(place + a.right + 1, key_end) : key_end;
   // Keys that the workgroup's rows, and this wave's, see.
-  const KeyRange wg = key_range(a, sp.nk, div_group(a, sp.r0) + shift, div_group(a, min(sp.r0 + BM, rows) - 1) + shift);
+  KeyRange wg = key_range(a, sp.nk, div_group(a, sp.r0) + shift, div_group(a, min(sp.r0 + BM, rows) - 1) + shift);
+  if (WAVES == 1) {
+    wg.lo = max(wg.lo, chunk0);
+    wg.hi = min(wg.hi, chunk1);
+  }
   const bool wave_on = wr0 < rows;
   const int wp0 = div_group(a, wave_on ? wr0 : 0) + shift, wp1 = div_group(a, wave_on ? min(wr0 + 32, rows) - 1 : 0) + shift;
-  const KeyRange wv = key_range(a, sp.nk, wp0, wp1);
+  KeyRange wv = key_range(a, sp.nk, wp0, wp1);
+  if (WAVES == 1) wv.hi = min(wv.hi, chunk1);
   const int full_lo = a.left >= 0 ? wp1 - a.left : 0;                        // keys from here on,
-  const int full_hi = a.right >= 0 ? min(wp0 + a.right + 1, sp.nk) : sp.nk;  // and below here, every row of the wave sees
+  const int full_hi = a.right >= 0 ? min(wp0 + a.right + 1, key_end) : key_end;  // and below here, every row of the wave sees
 
   const int blocks = wg.hi > wg.lo ? (wg.hi - wg.lo + BN - 1) / BN : 0;
   const Share mine = share_of(blocks, split, nsplit);
@@ -199,7 +235,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // a NaN stays one
   const float lse = sum == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
   const int64_t row_out = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
-  if (nsplit == 1) {
+  if (nsplit == 1 && (WAVES > 1 || part_row < 0)) {
     if (half == 0) a.lse[row_out] = lse;
     T* dst = static_cast<T*>(a.out) + row_out * a.dim;
 #pragma unroll
@@ -211,7 +247,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
           store4<T>(dst + d, acc[db][4 * g] * inv, acc[db][4 * g + 1] * inv, acc[db][4 * g + 2] * inv, acc[db][4 * g + 3] * inv);
       }
   } else {
-    const int64_t at_out = static_cast<int64_t>(split) * a.total_q * a.heads + row_out;
+    const int64_t at_out = WAVES == 1 && part_row >= 0 ? part_row + r : static_cast<int64_t>(split) * a.total_q * a.heads + row_out;
     if (half == 0) part_lse[at_out] = lse;
     float* dst = part_out + at_out * a.dim;
 #pragma unroll
@@ -225,86 +261,143 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   }
 }
 
-// Joins the splits' outputs: out = sum_s exp(lse_s - lse) out_s.  Four values
-// per thread, in the order of the splits.
+// Joins parts of one output row: out = sum_p exp(lse_p - lse) out_p, for the
+// rows first, first + step, ... of the parts.  A workgroup of 256: dim / 4
+// lanes take 4 columns each, in 256 / (dim / 4) interleaved groups of parts,
+// whose sums are added in a fixed order.
+template <class T>
+__device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* part_out, const float* part_lse, int64_t first,
+                                           int64_t step, int parts, int64_t row_out) {
+  __shared__ float4 acc_s[256];
+  __shared__ float top_s[256], sum_s[256];
+  const int quads = a.dim / 4, groups = 256 / quads, g = static_cast<int>(threadIdx.x) / quads, quad = static_cast<int>(threadIdx.x) - g * quads;
+  float top = -INFINITY, sum = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (g < groups) {
+    for (int p = g; p < parts; p += groups) top = fmaxf(top, part_lse[first + p * step]);
+    for (int p = g; p < parts; p += groups) {
+      const float ls = part_lse[first + p * step];
+      const float4 o = *reinterpret_cast<const float4*>(part_out + (first + p * step) * a.dim + 4 * quad);
+      const float e = ls == -INFINITY ? 0.f : fast_exp2((ls - top) * kLog2e);
+      sum += e;
+      x.x += e * o.x;
+      x.y += e * o.y;
+      x.z += e * o.z;
+      x.w += e * o.w;
+    }
+  }
+  acc_s[threadIdx.x] = x;
+  top_s[threadIdx.x] = top;
+  sum_s[threadIdx.x] = sum;
+  __syncthreads();
+  if (g != 0) return;
+  float all = -INFINITY;
+  for (int q = 0; q < groups; ++q) all = fmaxf(all, top_s[q * quads + quad]);
+  sum = 0.f;
+  x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = 0; q < groups; ++q) {
+    const float t = top_s[q * quads + quad];
+    if (t == -INFINITY) continue;
+    const float e = fast_exp2((t - all) * kLog2e);
+    const float4 o = acc_s[q * quads + quad];
+    sum += e * sum_s[q * quads + quad];
+    x.x += e * o.x;
+    x.y += e * o.y;
+    x.z += e * o.z;
+    x.w += e * o.w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  store4<T>(static_cast<T*>(a.out) + row_out * a.dim + 4 * quad, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  if (quad == 0) a.lse[row_out] = sum == 0.f ? -INFINITY : all + __builtin_amdgcn_logf(sum) * kLn2;
+}
+
+// Splits: part s of row r is at s x rows + r.
 template <class T>
 __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int nsplit, const float* part_out,
                                                         const float* part_lse) {
-  const int quads = a.dim / 4;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t rows = static_cast<int64_t>(a.total_q) * a.heads;
-  const int64_t row = id / quads;
-  if (row >= rows) return;
-  const int quad = static_cast<int>(id - row * quads);
-  float top = -INFINITY;
-  for (int s = 0; s < nsplit; ++s) top = fmaxf(top, part_lse[s * rows + row]);
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, x = 0.f, y = 0.f, z = 0.f, w = 0.f;
-  for (int s = 0; s < nsplit; ++s) {
-    const float ls = part_lse[s * rows + row];
-    if (ls == -INFINITY) continue;
-    const float e = fast_exp2((ls - base) * kLog2e);
-    const float4 o = *reinterpret_cast<const float4*>(part_out + (s * rows + row) * a.dim + 4 * quad);
-    sum += e;
-    x += e * o.x;
-    y += e * o.y;
-    z += e * o.z;
-    w += e * o.w;
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  store4<T>(static_cast<T*>(a.out) + row * a.dim + 4 * quad, x * inv, y * inv, z * inv, w * inv);
-  if (quad == 0) a.lse[row] = sum == 0.f ? -INFINITY : base + __builtin_amdgcn_logf(sum) * kLn2;
+  join_parts<T>(a, part_out, part_lse, blockIdx.x, static_cast<int64_t>(a.total_q) * a.heads, nsplit, blockIdx.x);
+}
+
+// Chunks: one workgroup per query row and head.
+template <class T>
+__global__ __launch_bounds__(256) void k_attention_join_chunks(AttentionArgs a, Chunks chunks, const float* part_out,
+                                                               const float* part_lse) {
+  const int head = static_cast<int>(blockIdx.y);
+  const Span sp = find_span(a, false, 1, 0, static_cast<int>(blockIdx.x), a.total_q + a.batch + 2);
+  if (!sp.any || !chunked(sp.nq * a.group, sp.nk)) return;
+  const int kvh = div_group(a, head), r = sp.r0 * a.group + head - kvh * a.group;
+  const int slot0 = (sp.k0 >> chunks.shift) + sp.seq;
+  const int parts = (sp.nk + (1 << chunks.shift) - 1) >> chunks.shift;
+  join_parts<T>(a, part_out, part_lse, (static_cast<int64_t>(slot0) * a.kv_heads + kvh) * 32 + r, static_cast<int64_t>(a.kv_heads) * 32,
+                parts, static_cast<int64_t>(sp.q0 + sp.r0) * a.heads + head);
 }
 
 struct Plan {
   int waves;
   int64_t slots;
   int nsplit;
+  Chunks chunks;
+  int64_t parts;  // rows of the partial outputs
 };
 
+// Sequences of few rows over long keys (32 flattened rows in the mean, keys
+// that fill a chunk) go by chunks; else the tiles of rows split the keys when
+// they would leave SIMDs idle.
 Plan make_forward_plan(const AttentionArgs& a) {
   Plan p;
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
-  const int64_t mean = rows / std::max(a.batch, 1);
+  const int64_t batch = std::max(a.batch, 1), mean = rows / batch, keys = a.total_k / batch;
   p.waves = mean <= 32 ? 1 : mean <= 64 ? 2 : 4;
+  p.nsplit = 1;
+  p.parts = 0;
+  if (p.waves == 1 && keys >= 256) {
+    // about 4096 waves: two per SIMD, twice over
+    const int64_t want = static_cast<int64_t>(a.total_k) * a.kv_heads / 4096;
+    p.chunks.shift = 6;
+    while (p.chunks.shift < 10 && (int64_t(1) << p.chunks.shift) < want) ++p.chunks.shift;
+    p.chunks.slots = static_cast<int>(span_slots(a.total_k, a.batch, 1 << p.chunks.shift));
+    p.slots = span_slots(rows, a.batch, 32);
+    p.parts = static_cast<int64_t>(p.chunks.slots) * a.kv_heads * 32;
+    return p;
+  }
   p.slots = span_slots(rows, a.batch, 32 * p.waves);
   const int64_t tiles = std::max<int64_t>(rows / (32 * p.waves), a.batch) * a.kv_heads * p.waves;
-  const int64_t keys = a.total_k / std::max(a.batch, 1);
   int64_t split = std::min<int64_t>(2048 / std::max<int64_t>(tiles, 1), keys / 256);
   if (a.left >= 0 && a.left < keys) split = std::min<int64_t>(split, a.left / 256);
   p.nsplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(split, 64)));
+  if (p.nsplit > 1) p.parts = static_cast<int64_t>(p.nsplit) * a.total_q * a.heads;
   return p;
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(const AttentionArgs& a) {
-  const Plan p = make_forward_plan(a);
-  if (p.nsplit == 1) return 0;
-  return static_cast<size_t>(p.nsplit) * a.total_q * a.heads * (a.dim + 1) * sizeof(float);
+  return static_cast<size_t>(make_forward_plan(a).parts) * (a.dim + 1) * sizeof(float);
 }
 
 hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t stream) {
   const Plan p = make_forward_plan(a);
   float* part_out = static_cast<float*>(workspace);
-  float* part_lse = part_out + static_cast<int64_t>(p.nsplit) * a.total_q * a.heads * a.dim;
-  const hipError_t e = dispatch(a, [&](auto t, auto dp) -> hipError_t {
+  float* part_lse = part_out + p.parts * a.dim;
+  return dispatch(a, [&](auto t, auto dp) -> hipError_t {
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value;
-    const int run = slot_run(a, p.slots);
-    const dim3 grid(static_cast<unsigned>(placed_slots(p.slots, run) * a.kv_heads), 1, static_cast<unsigned>(p.nsplit));
-    if (p.waves == 1) k_attention<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.slots), run, p.nsplit, part_out, part_lse);
-    else if (p.waves == 2) k_attention<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.slots), run, p.nsplit, part_out, part_lse);
-    else k_attention<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.slots), run, p.nsplit, part_out, part_lse);
+    const int run = slot_run(a, p.slots), slots = static_cast<int>(p.slots);
+    const int64_t placed = p.chunks.slots > 0 ? p.chunks.slots + p.slots : placed_slots(p.slots, run);
+    const dim3 grid(static_cast<unsigned>(placed * a.kv_heads), 1, static_cast<unsigned>(p.nsplit));
+    if (p.waves == 1) k_attention<T, DP, 1><<<grid, 64, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
+    else if (p.waves == 2) k_attention<T, DP, 2><<<grid, 128, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
+    else k_attention<T, DP, 4><<<grid, 256, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.parts == 0) return e;
+    if (p.chunks.slots > 0) {
+      const dim3 rows(static_cast<unsigned>(a.total_q + a.batch + 2), static_cast<unsigned>(a.heads));
+      k_attention_join_chunks<T><<<rows, 256, 0, stream>>>(a, p.chunks, part_out, part_lse);
+    } else {
+      k_attention_join<T><<<static_cast<unsigned>(a.total_q) * static_cast<unsigned>(a.heads), 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+    }
     return hipGetLastError();
   });
-  if (e != hipSuccess || p.nsplit == 1) return e;
-  const int64_t quads = static_cast<int64_t>(a.total_q) * a.heads * (a.dim / 4);
-  const unsigned blocks = static_cast<unsigned>((quads + 255) / 256);
-  if (a.dtype == 0) k_attention_join<float><<<blocks, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
-  else if (a.dtype == 1) k_attention_join<_Float16><<<blocks, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
-  else k_attention_join<__bf16><<<blocks, 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
-  return hipGetLastError();
 }
 
 }  // namespace spconv

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   if (at_block.slot >= slots) return;
   const int kvh = at_block.kvh;
   const int split = static_cast<int>(blockIdx.z);
-  const Span sp = find_span<BM>(a, false, a.right >= 0 ? slots - 1 - at_block.slot : at_block.slot, slots);
+  const Span sp = find_span(a, false, a.group, tile_shift(WAVES), a.right >= 0 ? slots - 1 - at_block.slot : at_block.slot, slots);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
   if (at_block.slot >= slots) return;
   const int kvh = at_block.kvh;
   const int split = static_cast<int>(blockIdx.z);
-  const Span sp = find_span<BM>(a, true, at_block.slot, slots);
+  const Span sp = find_span(a, true, 1, tile_shift(WAVES), at_block.slot, slots);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);

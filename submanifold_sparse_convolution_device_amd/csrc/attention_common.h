@@ -191,6 +191,7 @@ __device__ __forceinline__ int div_group(const AttentionArgs& a, int row) { retu
 struct Span {
   int q0, nq, k0, nk;  // first row and rows of the queries and of the keys
   int r0;              // first row of the tile within the sequence
+  int seq, slot0;      // the sequence (as a bound's index) and its first slot
   bool any;            // the tile has rows
 };
 
@@ -206,24 +207,23 @@ __device__ __forceinline__ int bound(const int32_t* cu, int batch, int total, in
   return v < 0 ? 0 : v > total ? total : v;
 }
 
-// Sequence and tile of a slot.  Sequence b starts at slot
-// floor(bound(b) x mult / TILE) + b, which leaves every sequence at least
-// ceil(rows x mult / TILE) slots and needs no pass over the lengths before.
+// Sequence and tile of a slot, for tiles of 2^shift of the queries' flattened
+// rows (mult = group), rows (mult = 1) or keys.  Sequence b starts at slot
+// floor(bound(b) x mult / 2^shift) + b, which leaves every sequence at least
+// ceil(rows x mult / 2^shift) slots and needs no pass over the lengths before.
 // The wavefront finds b by probing 64 sequences at a time: first those around
 // the place that equal lengths would give, which mostly ends the search in
 // one round of loads, else in rounds that narrow 64-fold.
-template <int TILE>
-__device__ __forceinline__ Span find_span(const AttentionArgs& a, bool by_keys, int slot, int slots) {
+__device__ __forceinline__ Span find_span(const AttentionArgs& a, bool by_keys, int mult, int shift, int slot, int slots) {
   const int lane = threadIdx.x & 63;
   const int32_t* cu = by_keys ? a.cu_k : a.cu_q;
   const int total = by_keys ? a.total_k : a.total_q;
-  const int mult = by_keys ? 1 : a.group;
   const int last = a.batch + 2;  // bounds 0 .. last
   int lo = 0, hi = last, step = 1, v, c;
   auto probe = [&]() {
     const int at = lo + lane * step;
     v = bound(cu, a.batch, total, min(at, last));
-    const int start = static_cast<int>(static_cast<int64_t>(v) * mult / TILE) + at;
+    const int start = static_cast<int>((static_cast<int64_t>(v) * mult) >> shift) + at;
     return __builtin_popcountll(__ballot(at < hi && start <= slot));
   };
   bool found = false;
@@ -263,7 +263,9 @@ __device__ __forceinline__ Span find_span(const AttentionArgs& a, bool by_keys, 
   s.k0 = by_keys ? r0 : o0;
   s.nk = by_keys ? nr : no;
   const int64_t rows = static_cast<int64_t>(nr) * mult;
-  const int64_t t0 = static_cast<int64_t>(slot - (static_cast<int>(static_cast<int64_t>(r0) * mult / TILE) + b)) * TILE;
+  s.slot0 = static_cast<int>((static_cast<int64_t>(r0) * mult) >> shift) + b;
+  const int64_t t0 = static_cast<int64_t>(slot - s.slot0) << shift;
+  s.seq = b;
   s.any = t0 >= 0 && t0 < rows;
   s.r0 = s.any ? static_cast<int>(t0) : 0;
   return s;
@@ -329,6 +331,9 @@ __device__ __forceinline__ Share share_of(int blocks, int split, int nsplit) {
 
 // Row of register i of a C tile within its 32, without the half's 4.
 __host__ __device__ constexpr int c_row(int i) { return 8 * (i / 4) + (i & 3); }
+
+// log2 of a wavefront count's tile: 32 rows per wave.
+constexpr int tile_shift(int waves) { return waves == 1 ? 5 : waves == 2 ? 6 : 7; }
 
 // Stores 4 consecutive values as T.
 template <class T>
