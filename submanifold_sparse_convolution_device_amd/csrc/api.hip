@@ -618,8 +618,8 @@ spconv_status attention_args(const spconv_attention* x, const void* d_out, const
   const spconv_status st = check_head_dim(x->dtype, x->head_dim);
   if (st != SPCONV_OK) return st;
   if (x->batch < 0 || x->batch > (1 << 24)) return fail(SPCONV_ERR_INVALID_ARG, "batch = %d must lie in [0, 2^24]", x->batch);
-  if (x->heads < 1 || x->kv_heads < 1 || x->heads % x->kv_heads != 0 || x->kv_heads > 65535) {
-    return fail(SPCONV_ERR_INVALID_ARG, "heads = %d must be a positive multiple of kv_heads = %d (at most 65535)", x->heads, x->kv_heads);
+  if (x->heads < 1 || x->kv_heads < 1 || x->heads % x->kv_heads != 0 || x->heads > 65535) {
+    return fail(SPCONV_ERR_INVALID_ARG, "heads = %d (at most 65535) must be a positive multiple of kv_heads = %d", x->heads, x->kv_heads);
   }
   if (static_cast<int64_t>(x->batch + 2) * x->kv_heads > (int64_t(1) << 30)) {
     return fail(SPCONV_ERR_INVALID_ARG, "batch = %d x kv_heads = %d must stay below 2^30", x->batch, x->kv_heads);

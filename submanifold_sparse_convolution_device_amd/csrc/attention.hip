@@ -40,7 +40,7 @@ __device__ __forceinline__ bool chunked(int rows, int nk) { return rows <= 32 &&
 // One workgroup: 32 flattened query rows per wave, one kv head, and the key
 // tiles of one split or chunk.  Q stays in registers (operand B of
 // S^T = K Q^T), K and V pass through LDS, loaded a tile ahead into registers.
-template <class T, int DP, int WAVES>
+template <class T, int DP, int DQ, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int slots, int run, int nsplit,
                                                                                  Chunks chunks, float* part_out, float* part_lse) {
   typedef Tile<T, DP> TL;
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   constexpr int NB = BN >= 64 ? 2 : 1;  // blocks of 32 keys per softmax step
   constexpr int PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES;                // flattened rows per workgroup
-  constexpr int KS = PPR / 2;                   // pieces per half of a row
+  constexpr int KS = DQ / (2 * kPiece<T>);      // pieces per half of a row
   constexpr int NL = (BN * PPR + NT - 1) / NT;  // pieces each thread copies per tile
   __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
@@ -311,11 +311,34 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* 
   if (quad == 0) a.lse[row_out] = sum == 0.f ? -INFINITY : all + __builtin_amdgcn_logf(sum) * kLn2;
 }
 
-// Splits: part s of row r is at s x rows + r.
+// Splits: part s of row r is at s x rows + r.  Few parts of many rows: four
+// columns per thread.
 template <class T>
 __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int nsplit, const float* part_out,
                                                         const float* part_lse) {
-  join_parts<T>(a, part_out, part_lse, blockIdx.x, static_cast<int64_t>(a.total_q) * a.heads, nsplit, blockIdx.x);
+  const int quads = a.dim / 4;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.heads;
+  const int64_t row = id / quads;
+  if (row >= rows) return;
+  const int quad = static_cast<int>(id - row * quads);
+  float top = -INFINITY;
+  for (int s = 0; s < nsplit; ++s) top = fmaxf(top, part_lse[s * rows + row]);
+  float sum = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < nsplit; ++s) {
+    const float ls = part_lse[s * rows + row];
+    const float4 o = *reinterpret_cast<const float4*>(part_out + (s * rows + row) * a.dim + 4 * quad);
+    const float e = ls == -INFINITY ? 0.f : fast_exp2((ls - top) * kLog2e);
+    sum += e;
+    x.x += e * o.x;
+    x.y += e * o.y;
+    x.z += e * o.z;
+    x.w += e * o.w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  store4<T>(static_cast<T*>(a.out) + row * a.dim + 4 * quad, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  if (quad == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
 }
 
 // Chunks: one workgroup per query row and head.
@@ -347,7 +370,8 @@ Plan make_forward_plan(const AttentionArgs& a) {
   Plan p;
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
   const int64_t batch = std::max(a.batch, 1), mean = rows / batch, keys = a.total_k / batch;
-  p.waves = mean <= 32 ? 1 : mean <= 64 ? 2 : 4;
+  const Cut cut = cut_rows(a, mean, rows, band_depth(a, keys, 1));
+  p.waves = cut.waves;
   p.nsplit = 1;
   p.parts = 0;
   if (p.waves == 1 && keys >= 256) {
@@ -361,10 +385,7 @@ Plan make_forward_plan(const AttentionArgs& a) {
     return p;
   }
   p.slots = span_slots(rows, a.batch, 32 * p.waves);
-  const int64_t tiles = std::max<int64_t>(rows / (32 * p.waves), a.batch) * a.kv_heads * p.waves;
-  int64_t split = std::min<int64_t>(2048 / std::max<int64_t>(tiles, 1), keys / 256);
-  if (a.left >= 0 && a.left < keys) split = std::min<int64_t>(split, a.left / 256);
-  p.nsplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(split, 64)));
+  p.nsplit = cut.split;
   if (p.nsplit > 1) p.parts = static_cast<int64_t>(p.nsplit) * a.total_q * a.heads;
   return p;
 }
@@ -379,22 +400,23 @@ hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t
   const Plan p = make_forward_plan(a);
   float* part_out = static_cast<float*>(workspace);
   float* part_lse = part_out + p.parts * a.dim;
-  return dispatch(a, [&](auto t, auto dp) -> hipError_t {
+  return dispatch(a, [&](auto t, auto dp, auto dq) -> hipError_t {
     typedef decltype(t) T;
-    constexpr int DP = decltype(dp)::value;
+    constexpr int DP = decltype(dp)::value, DQ = decltype(dq)::value;
     const int run = slot_run(a, p.slots), slots = static_cast<int>(p.slots);
     const int64_t placed = p.chunks.slots > 0 ? p.chunks.slots + p.slots : placed_slots(p.slots, run);
     const dim3 grid(static_cast<unsigned>(placed * a.kv_heads), 1, static_cast<unsigned>(p.nsplit));
-    if (p.waves == 1) k_attention<T, DP, 1><<<grid, 64, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
-    else if (p.waves == 2) k_attention<T, DP, 2><<<grid, 128, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
-    else k_attention<T, DP, 4><<<grid, 256, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
+    if (p.waves == 1) k_attention<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
+    else if (p.waves == 2) k_attention<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
+    else k_attention<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.parts == 0) return e;
     if (p.chunks.slots > 0) {
       const dim3 rows(static_cast<unsigned>(a.total_q + a.batch + 2), static_cast<unsigned>(a.heads));
       k_attention_join_chunks<T><<<rows, 256, 0, stream>>>(a, p.chunks, part_out, part_lse);
     } else {
-      k_attention_join<T><<<static_cast<unsigned>(a.total_q) * static_cast<unsigned>(a.heads), 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
+      const int64_t quads = static_cast<int64_t>(a.total_q) * a.heads * (a.dim / 4);
+      k_attention_join<T><<<static_cast<unsigned>((quads + 255) / 256), 256, 0, stream>>>(a, p.nsplit, part_out, part_lse);
     }
     return hipGetLastError();
   });

@@ -62,12 +62,12 @@ constexpr int kWalk = sizeof(T) == 4 ? 32 : DP == 32 ? (WAVES == 4 ? 128 : 64) :
 template <int WAVES>
 constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 
-template <class T, int DP, int WAVES>
+template <class T, int DP, int DQ, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int run, int nsplit,
                                                                                     float* delta, float* part) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
-  constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
+  constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece<T>), NL = (BN * PPR + NT - 1) / NT;
   __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
   const Place at_block = place_of(a, run);
@@ -226,12 +226,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     }
 }
 
-template <class T, int DP, int WAVES>
+template <class T, int DP, int DQ, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int slots, int run, int nsplit, const float* delta,
                                                               float* part_k, float* part_v) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
-  constexpr int BM = 32 * WAVES, KS = PPR / 2, NL = (BN * PPR + NT - 1) / NT;
+  constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece<T>), NL = (BN * PPR + NT - 1) / NT;
   constexpr int NR = (BN + NT - 1) / NT;  // rows whose statistics each thread copies
   __shared__ uint4 qs[BUFS][BN * PPR], gs[BUFS][BN * PPR];
   __shared__ float4 row_lse[BUFS][BN / 4], row_delta[BUFS][BN / 4];
@@ -459,28 +459,18 @@ struct Plan {
   int q_split, k_split;
 };
 
-int waves_for(int64_t mean) { return mean <= 32 ? 1 : mean <= 64 ? 2 : 4; }
-
 Plan make_backward_plan(const AttentionArgs& a) {
   Plan p;
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
   const int64_t batch = std::max(a.batch, 1);
-  p.q_waves = waves_for(rows / batch);
-  p.k_waves = waves_for(a.total_k / batch);
+  const Cut q = cut_rows(a, rows / batch, rows, band_depth(a, a.total_k / batch, 1));
+  const Cut k = cut_rows(a, a.total_k / batch, a.total_k, band_depth(a, a.total_q / batch, a.group));
+  p.q_waves = q.waves;
+  p.k_waves = k.waves;
+  p.q_split = q.split;
+  p.k_split = k.split;
   p.q_slots = span_slots(rows, a.batch, 32 * p.q_waves);
   p.k_slots = span_slots(a.total_k, a.batch, 32 * p.k_waves);
-  auto split = [&](int64_t tiles, int64_t depth) {
-    const int64_t s = std::min<int64_t>(4096 / std::max<int64_t>(tiles, 1), depth / 256);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s, 32)));
-  };
-  int64_t q_depth = a.total_k / batch, k_depth = rows / batch;
-  if (a.left >= 0 && a.right >= 0) {
-    const int64_t band = static_cast<int64_t>(a.left) + a.right + 1;
-    q_depth = std::min<int64_t>(q_depth, band);
-    k_depth = std::min<int64_t>(k_depth, band * a.group);
-  }
-  p.q_split = split(std::max<int64_t>(rows / (32 * p.q_waves), a.batch) * a.kv_heads * p.q_waves, q_depth);
-  p.k_split = split(std::max<int64_t>(a.total_k / (32 * p.k_waves), a.batch) * a.kv_heads * p.k_waves, k_depth);
   return p;
 }
 
@@ -512,15 +502,15 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
   float* part_q = reinterpret_cast<float*>(base + w.q);
   float* part_k = reinterpret_cast<float*>(base + w.k);
   float* part_v = reinterpret_cast<float*>(base + w.v);
-  return dispatch(a, [&](auto t, auto dp) -> hipError_t {
+  return dispatch(a, [&](auto t, auto dp, auto dq) -> hipError_t {
     typedef decltype(t) T;
-    constexpr int DP = decltype(dp)::value;
+    constexpr int DP = decltype(dp)::value, DQ = decltype(dq)::value;
     if (a.total_q > 0) {
       const int run = slot_run(a, p.q_slots);
       const dim3 grid(static_cast<unsigned>(placed_slots(p.q_slots, run) * a.kv_heads), 1, static_cast<unsigned>(p.q_split));
-      if (p.q_waves == 1) k_attention_dq<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
-      else if (p.q_waves == 2) k_attention_dq<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
-      else k_attention_dq<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
+      if (p.q_waves == 1) k_attention_dq<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
+      else if (p.q_waves == 2) k_attention_dq<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
+      else k_attention_dq<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.q_split > 1) launch_join<T>(part_q, p.q_split, a.total_q, a.heads, a.dim, a.grad_q, a.gq_row, a.gq_head, stream);
@@ -528,9 +518,9 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
     if (a.total_k > 0) {
       const int run = slot_run(a, p.k_slots);
       const dim3 grid(static_cast<unsigned>(placed_slots(p.k_slots, run) * a.kv_heads), 1, static_cast<unsigned>(p.k_split));
-      if (p.k_waves == 1) k_attention_dkv<T, DP, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
-      else if (p.k_waves == 2) k_attention_dkv<T, DP, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
-      else k_attention_dkv<T, DP, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
+      if (p.k_waves == 1) k_attention_dkv<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
+      else if (p.k_waves == 2) k_attention_dkv<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
+      else k_attention_dkv<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.k_split > 1) {

@@ -18,6 +18,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "internal.h"
 
 namespace spconv {
@@ -347,20 +349,50 @@ __device__ __forceinline__ void store4(T* dst, float x, float y, float z, float 
   *reinterpret_cast<tx4*>(dst) = v;
 }
 
-// Runs f.template operator()<T, DP>() for the type and the padded head size
-// of `a`.
+// Calls f(type, DP, DQ): the head size rounded up to 32 (the blocks of the
+// products that end in it) and to 16 (the steps of those over it).
 template <class F>
 hipError_t dispatch(const AttentionArgs& a, F&& f) {
   auto by_dim = [&](auto t) {
     typedef decltype(t) T;
-    if (a.dim <= 32) return f(T{}, std::integral_constant<int, 32>{});
-    if (a.dim <= 64) return f(T{}, std::integral_constant<int, 64>{});
-    if (a.dim <= 96) return f(T{}, std::integral_constant<int, 96>{});
-    return f(T{}, std::integral_constant<int, 128>{});
+#define SPCONV_DIM(q) \
+  if (a.dim <= q) return f(T{}, std::integral_constant<int, (q + 31) / 32 * 32>{}, std::integral_constant<int, q>{});
+    SPCONV_DIM(16)
+    SPCONV_DIM(32)
+    SPCONV_DIM(48)
+    SPCONV_DIM(64)
+    SPCONV_DIM(80)
+    SPCONV_DIM(96)
+    SPCONV_DIM(112)
+#undef SPCONV_DIM
+    return f(T{}, std::integral_constant<int, 128>{}, std::integral_constant<int, 128>{});
   };
   if (a.dtype == 0) return by_dim(float{});
   if (a.dtype == 1) return by_dim(static_cast<_Float16>(0));
   return by_dim(static_cast<__bf16>(0.f));
+}
+
+// How `rows` rows per kv head, `mean` in a sequence, that each walk `depth`
+// rows of the other side, become workgroups: 32 rows per wave; the walk is
+// split (into parts of at least 256, in fp32 128) until there are two waves
+// per SIMD twice over; and where that leaves less than two workgroups per CU,
+// two waves instead of four spread more evenly.
+struct Cut {
+  int waves, split;
+};
+inline Cut cut_rows(const AttentionArgs& a, int64_t mean, int64_t rows, int64_t depth) {
+  Cut c;
+  c.waves = mean <= 32 ? 1 : mean <= 64 ? 2 : 4;
+  const int64_t tiles = std::max<int64_t>(rows / (32 * c.waves), std::max(a.batch, 1)) * a.kv_heads;
+  const int64_t most = depth / (a.dtype == 0 ? 128 : 256), want = 4096 / (tiles * c.waves);
+  c.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(most, want), 16)));
+  if (c.waves == 4 && tiles * c.split < 512) c.waves = 2;
+  return c;
+}
+// Rows of the other side that a row's band reaches, of `rows` (times `group`).
+inline int64_t band_depth(const AttentionArgs& a, int64_t rows, int64_t group) {
+  if (a.left < 0 || a.right < 0) return rows * group;
+  return std::min<int64_t>(rows, static_cast<int64_t>(a.left) + a.right + 1) * group;
 }
 
 }  // namespace attn
