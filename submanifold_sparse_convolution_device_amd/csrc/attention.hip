@@ -42,7 +42,8 @@ __device__ __forceinline__ bool chunked(int rows, int nk) { return rows <= 32 &&
 // S^T = K Q^T), K and V pass through LDS, loaded a tile ahead into registers.
 template <class T, int DP, int DQ, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention(AttentionArgs a, int slots, int run, int nsplit,
-                                                                                 Chunks chunks, float* part_out, float* part_lse) {
+                                                                                 Chunks chunks, const int32_t* order, float* part_out,
+                                                                                 float* part_lse) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kKeys<T, DP, WAVES>, BUFS = kBuffers<WAVES>;
   constexpr int NB = BN >= 64 ? 2 : 1;  // blocks of 32 keys per softmax step
@@ -52,13 +53,14 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   constexpr int NL = (BN * PPR + NT - 1) / NT;  // pieces each thread copies per tile
   __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
-  const int split = static_cast<int>(blockIdx.z);
+  // a tile's splits follow one another (nsplit is a power of two)
+  const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
   int kvh, chunk0 = 0, chunk1 = INT_MAX;
   int64_t part_row = -1;  // of the chunk's first row; -1: not a chunk
   Span sp;
   if (WAVES == 1 && chunks.slots > 0) {
-    const int slot = fast_div(static_cast<int>(blockIdx.x), a.by_kv_heads);
-    kvh = static_cast<int>(blockIdx.x) - slot * a.kv_heads;
+    const int slot = fast_div(id, a.by_kv_heads);
+    kvh = id - slot * a.kv_heads;
     if (slot < chunks.slots) {
       sp = find_span(a, true, 1, chunks.shift, slot, chunks.slots);
       if (!sp.any || sp.nq == 0 || !chunked(sp.nq * a.group, sp.nk)) return;
@@ -71,11 +73,13 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       if (!sp.any || chunked(sp.nq * a.group, sp.nk)) return;
     }
   } else {
-    // Under a causal mask the last rows have the most keys: they go first.
-    const Place at = place_of(a, run);
+    // The longest tiles first: by the order given, or under a causal mask the
+    // last rows, which have the most keys.
+    const Place at = place_of(a, id, run);
     if (at.slot >= slots) return;
     kvh = at.kvh;
-    sp = find_span(a, false, a.group, tile_shift(WAVES), a.right >= 0 ? slots - 1 - at.slot : at.slot, slots);
+    const int slot = order != nullptr ? order[at.slot] : a.right >= 0 ? slots - 1 - at.slot : at.slot;
+    sp = find_span(a, false, a.group, tile_shift(WAVES), slot, slots);
     if (!sp.any) return;
   }
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
@@ -355,12 +359,15 @@ __global__ __launch_bounds__(256) void k_attention_join_chunks(AttentionArgs a, 
                 parts, static_cast<int64_t>(sp.q0 + sp.r0) * a.heads + head);
 }
 
+__global__ __launch_bounds__(1024) void k_attention_order(AttentionArgs a, OrderJob job) { order_slots(a, job); }
+
 struct Plan {
   int waves;
   int64_t slots;
   int nsplit;
   Chunks chunks;
   int64_t parts;  // rows of the partial outputs
+  bool ordered = false;
 };
 
 // Sequences of few rows over long keys (32 flattened rows in the mean, keys
@@ -387,28 +394,37 @@ Plan make_forward_plan(const AttentionArgs& a) {
   p.slots = span_slots(rows, a.batch, 32 * p.waves);
   p.nsplit = cut.split;
   if (p.nsplit > 1) p.parts = static_cast<int64_t>(p.nsplit) * a.total_q * a.heads;
+  p.ordered = order_pays(a, p.slots, p.nsplit, 2);
   return p;
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(const AttentionArgs& a) {
-  return static_cast<size_t>(make_forward_plan(a).parts) * (a.dim + 1) * sizeof(float);
+  const Plan p = make_forward_plan(a);
+  return static_cast<size_t>(p.parts) * (a.dim + 1) * sizeof(float) + (p.ordered ? static_cast<size_t>(p.slots) * sizeof(int32_t) : 0);
 }
 
 hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t stream) {
   const Plan p = make_forward_plan(a);
   float* part_out = static_cast<float*>(workspace);
   float* part_lse = part_out + p.parts * a.dim;
+  int32_t* order = p.ordered ? reinterpret_cast<int32_t*>(part_lse + p.parts) : nullptr;
+  if (p.ordered) {
+    const OrderJob job = {order, false, a.group, tile_shift(p.waves), static_cast<int>(p.slots)};
+    k_attention_order<<<1, 1024, 0, stream>>>(a, job);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   return dispatch(a, [&](auto t, auto dp, auto dq) -> hipError_t {
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value, DQ = decltype(dq)::value;
-    const int run = slot_run(a, p.slots), slots = static_cast<int>(p.slots);
+    const int run = p.ordered ? 0 : slot_run(a, p.slots), slots = static_cast<int>(p.slots);
     const int64_t placed = p.chunks.slots > 0 ? p.chunks.slots + p.slots : placed_slots(p.slots, run);
-    const dim3 grid(static_cast<unsigned>(placed * a.kv_heads), 1, static_cast<unsigned>(p.nsplit));
-    if (p.waves == 1) k_attention<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
-    else if (p.waves == 2) k_attention<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
-    else k_attention<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, part_out, part_lse);
+    const dim3 grid(static_cast<unsigned>(placed * a.kv_heads * p.nsplit));
+    if (p.waves == 1) k_attention<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, order, part_out, part_lse);
+    else if (p.waves == 2) k_attention<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, order, part_out, part_lse);
+    else k_attention<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, order, part_out, part_lse);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.parts == 0) return e;
     if (p.chunks.slots > 0) {

@@ -63,18 +63,19 @@ template <int WAVES>
 constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 
 template <class T, int DP, int DQ, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int run, int nsplit,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int run, int nsplit, const int32_t* order,
                                                                                     float* delta, float* part) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece<T>), NL = (BN * PPR + NT - 1) / NT;
   __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
 
-  const Place at_block = place_of(a, run);
+  const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
+  const Place at_block = place_of(a, id, run);
   if (at_block.slot >= slots) return;
   const int kvh = at_block.kvh;
-  const int split = static_cast<int>(blockIdx.z);
-  const Span sp = find_span(a, false, a.group, tile_shift(WAVES), a.right >= 0 ? slots - 1 - at_block.slot : at_block.slot, slots);
+  const Span sp = find_span(a, false, a.group, tile_shift(WAVES),
+                            order != nullptr ? order[at_block.slot] : a.right >= 0 ? slots - 1 - at_block.slot : at_block.slot, slots);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -227,7 +228,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
 }
 
 template <class T, int DP, int DQ, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int slots, int run, int nsplit, const float* delta,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int slots, int run, int nsplit, const int32_t* order, const float* delta,
                                                               float* part_k, float* part_v) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
@@ -237,11 +238,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
   __shared__ float4 row_lse[BUFS][BN / 4], row_delta[BUFS][BN / 4];
   __shared__ int4 row_place[BUFS][BN / 4];
 
-  const Place at_block = place_of(a, run);
+  const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
+  const Place at_block = place_of(a, id, run);
   if (at_block.slot >= slots) return;
   const int kvh = at_block.kvh;
-  const int split = static_cast<int>(blockIdx.z);
-  const Span sp = find_span(a, true, 1, tile_shift(WAVES), at_block.slot, slots);
+  const Span sp = find_span(a, true, 1, tile_shift(WAVES), order != nullptr ? order[at_block.slot] : at_block.slot, slots);
   if (!sp.any) return;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -453,10 +454,15 @@ void launch_join(const float* part, int nsplit, int64_t rows, int heads, int dim
       part, nsplit, rows, heads, dim, static_cast<T*>(dst), row_stride, head_stride);
 }
 
+__global__ __launch_bounds__(1024) void k_attention_grad_order(AttentionArgs a, OrderJob q, OrderJob k) {
+  order_slots(a, blockIdx.x == 0 ? q : k);
+}
+
 struct Plan {
   int q_waves, k_waves;
   int64_t q_slots, k_slots;
   int q_split, k_split;
+  bool ordered;
 };
 
 Plan make_backward_plan(const AttentionArgs& a) {
@@ -471,11 +477,12 @@ Plan make_backward_plan(const AttentionArgs& a) {
   p.k_split = k.split;
   p.q_slots = span_slots(rows, a.batch, 32 * p.q_waves);
   p.k_slots = span_slots(a.total_k, a.batch, 32 * p.k_waves);
+  p.ordered = order_pays(a, p.q_slots, p.q_split, 7) && order_pays(a, p.k_slots, p.k_split, 7);
   return p;
 }
 
 struct Workspace {
-  size_t delta, q, k, v, total;  // offsets in bytes
+  size_t delta, q, k, v, q_order, k_order, total;  // offsets in bytes
 };
 Workspace layout(const AttentionArgs& a, const Plan& p) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -486,7 +493,9 @@ Workspace layout(const AttentionArgs& a, const Plan& p) {
   w.k = w.q + (p.q_split > 1 ? up(nq * a.dim * p.q_split * sizeof(float)) : 0);
   const size_t part = p.k_split > 1 ? up(nk * a.dim * p.k_split * sizeof(float)) : 0;
   w.v = w.k + part;
-  w.total = w.v + part;
+  w.q_order = w.v + part;
+  w.k_order = w.q_order + (p.ordered ? up(static_cast<size_t>(p.q_slots) * sizeof(int32_t)) : 0);
+  w.total = w.k_order + (p.ordered ? up(static_cast<size_t>(p.k_slots) * sizeof(int32_t)) : 0);
   return w;
 }
 
@@ -502,25 +511,34 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
   float* part_q = reinterpret_cast<float*>(base + w.q);
   float* part_k = reinterpret_cast<float*>(base + w.k);
   float* part_v = reinterpret_cast<float*>(base + w.v);
+  int32_t* q_order = p.ordered ? reinterpret_cast<int32_t*>(base + w.q_order) : nullptr;
+  int32_t* k_order = p.ordered ? reinterpret_cast<int32_t*>(base + w.k_order) : nullptr;
+  if (p.ordered) {
+    const OrderJob q = {q_order, false, a.group, tile_shift(p.q_waves), static_cast<int>(p.q_slots)};
+    const OrderJob k = {k_order, true, 1, tile_shift(p.k_waves), static_cast<int>(p.k_slots)};
+    k_attention_grad_order<<<2, 1024, 0, stream>>>(a, q, k);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   return dispatch(a, [&](auto t, auto dp, auto dq) -> hipError_t {
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value, DQ = decltype(dq)::value;
     if (a.total_q > 0) {
-      const int run = slot_run(a, p.q_slots);
-      const dim3 grid(static_cast<unsigned>(placed_slots(p.q_slots, run) * a.kv_heads), 1, static_cast<unsigned>(p.q_split));
-      if (p.q_waves == 1) k_attention_dq<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
-      else if (p.q_waves == 2) k_attention_dq<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
-      else k_attention_dq<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, delta, part_q);
+      const int run = p.ordered ? 0 : slot_run(a, p.q_slots);
+      const dim3 grid(static_cast<unsigned>(placed_slots(p.q_slots, run) * a.kv_heads * p.q_split));
+      if (p.q_waves == 1) k_attention_dq<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, delta, part_q);
+      else if (p.q_waves == 2) k_attention_dq<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, delta, part_q);
+      else k_attention_dq<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, delta, part_q);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.q_split > 1) launch_join<T>(part_q, p.q_split, a.total_q, a.heads, a.dim, a.grad_q, a.gq_row, a.gq_head, stream);
     }
     if (a.total_k > 0) {
-      const int run = slot_run(a, p.k_slots);
-      const dim3 grid(static_cast<unsigned>(placed_slots(p.k_slots, run) * a.kv_heads), 1, static_cast<unsigned>(p.k_split));
-      if (p.k_waves == 1) k_attention_dkv<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
-      else if (p.k_waves == 2) k_attention_dkv<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
-      else k_attention_dkv<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, delta, part_k, part_v);
+      const int run = p.ordered ? 0 : slot_run(a, p.k_slots);
+      const dim3 grid(static_cast<unsigned>(placed_slots(p.k_slots, run) * a.kv_heads * p.k_split));
+      if (p.k_waves == 1) k_attention_dkv<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, delta, part_k, part_v);
+      else if (p.k_waves == 2) k_attention_dkv<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, delta, part_k, part_v);
+      else k_attention_dkv<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, delta, part_k, part_v);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.k_split > 1) {

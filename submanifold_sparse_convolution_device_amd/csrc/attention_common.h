@@ -266,7 +266,7 @@ __device__ __forceinline__ Span find_span(const AttentionArgs& a, bool by_keys, 
   s.nk = by_keys ? nr : no;
   const int64_t rows = static_cast<int64_t>(nr) * mult;
   s.slot0 = static_cast<int>((static_cast<int64_t>(r0) * mult) >> shift) + b;
-  const int64_t t0 = static_cast<int64_t>(slot - s.slot0) << shift;
+  const int64_t t0 = (static_cast<int64_t>(slot) - s.slot0) * (int64_t(1) << shift);
   s.seq = b;
   s.any = t0 >= 0 && t0 < rows;
   s.r0 = s.any ? static_cast<int>(t0) : 0;
@@ -302,8 +302,7 @@ struct Place {
   int slot, kvh;
 };
 constexpr int kXcds = 8;
-__device__ __forceinline__ Place place_of(const AttentionArgs& a, int run) {
-  const int id = static_cast<int>(blockIdx.x);
+__device__ __forceinline__ Place place_of(const AttentionArgs& a, int id, int run) {
   if (run == 0) {
     const int slot = fast_div(id, a.by_kv_heads);
     return {slot, id - slot * a.kv_heads};
@@ -318,6 +317,88 @@ inline int slot_run(const AttentionArgs& a, int64_t slots) {
 inline int64_t placed_slots(int64_t slots, int run) {
   const int64_t unit = static_cast<int64_t>(run) * kXcds;
   return run == 0 ? slots : (slots + unit - 1) / unit * unit;
+}
+
+// Order of the slots by falling work (the other side's blocks of 32 that the
+// slot's tile walks), for launches of few rounds of workgroups, where a long
+// tile that starts late leaves the rest of the chip idle: a counting sort
+// over 8 buckets per octave in one workgroup.  Slots of one bucket take any
+// order, which no result depends on; slots without a tile go last.
+struct OrderJob {
+  int32_t* order = nullptr;  // NULL: none
+  bool by_keys = false;
+  int mult = 1, shift = 0, slots = 0;
+};
+constexpr int kOrderBuckets = 256, kOrderSlots = 2560;
+__device__ __forceinline__ int order_bucket(int work) {
+  if (work <= 0) return 0;
+  const int top = 31 - __clz(work);
+  const int frac = top >= 3 ? (work >> (top - 3)) & 7 : (work << (3 - top)) & 7;
+  return min(1 + 8 * top + frac, kOrderBuckets - 1);
+}
+__device__ __forceinline__ void order_slots(const AttentionArgs& a, const OrderJob& job) {
+  __shared__ __align__(16) int start[kOrderBuckets];
+  __shared__ uint8_t bucket_of[kOrderSlots];
+  const int tid = static_cast<int>(threadIdx.x), nt = static_cast<int>(blockDim.x);
+  for (int i = tid; i < kOrderBuckets; i += nt) start[i] = 0;
+  // slots that broken offsets leave to no sequence stay in the order
+  for (int i = tid; i < job.slots; i += nt) bucket_of[i] = kOrderBuckets - 1;
+  __syncthreads();
+  const int32_t* cu = job.by_keys ? a.cu_k : a.cu_q;
+  const int32_t* oc = job.by_keys ? a.cu_q : a.cu_k;
+  const int total = job.by_keys ? a.total_k : a.total_q, ototal = job.by_keys ? a.total_q : a.total_k;
+  // what the tile that starts at row r0 of n rows walks of the other side's m
+  auto walk = [&](int r0, int n, int m) {
+    const int rows = job.by_keys ? n : n * job.mult, r1 = min(r0 + (1 << job.shift), rows) - 1;
+    if (job.by_keys) {
+      const int to = n - m;  // a key's place among the queries: its row - to
+      const int lo = a.right >= 0 ? max(r0 - a.right - to, 0) : 0, hi = a.left >= 0 ? min(r1 + a.left - to + 1, m) : m;
+      return (max(hi - lo, 0) * a.group + 31) / 32;
+    }
+    const KeyRange k = key_range(a, m, div_group(a, r0) + m - n, div_group(a, r1) + m - n);
+    return (max(k.hi - k.lo, 0) + 31) / 32;
+  };
+  for (int b = tid >> 5; b < a.batch + 2; b += nt >> 5) {
+    const int r = bound(cu, a.batch, total, b), rn = bound(cu, a.batch, total, b + 1), n = max(rn - r, 0);
+    const int o = bound(oc, a.batch, ototal, b), on = bound(oc, a.batch, ototal, b + 1);
+    const int m = b == 0 || b == a.batch + 1 ? 0 : max(on - o, 0);
+    const int slot0 = static_cast<int>((static_cast<int64_t>(r) * job.mult) >> job.shift) + b;
+    const int next = b == a.batch + 1 ? job.slots : static_cast<int>((static_cast<int64_t>(rn) * job.mult) >> job.shift) + b + 1;
+    for (int slot = slot0 + (tid & 31); slot < min(next, job.slots); slot += 32) {
+      const int64_t r0 = static_cast<int64_t>(slot - slot0) << job.shift;
+      const int w = r0 < static_cast<int64_t>(n) * job.mult ? 1 + walk(static_cast<int>(r0), n, m) : 0;
+      const int bucket = kOrderBuckets - 1 - order_bucket(w);  // the most work first
+      bucket_of[slot] = static_cast<uint8_t>(bucket);
+      atomicAdd(&start[bucket], 1);
+    }
+  }
+  __syncthreads();
+  // exclusive prefix sum over the 256 buckets: 4 per lane of the first wave
+  if (tid < 64) {
+    const int4 c = reinterpret_cast<const int4*>(start)[tid];
+    const int sum = c.x + c.y + c.z + c.w;
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(incl, d);
+      if (tid >= d) incl += v;
+    }
+    const int e = incl - sum;
+    reinterpret_cast<int4*>(start)[tid] = make_int4(e, e + c.x, e + c.x + c.y, e + c.x + c.y + c.z);
+  }
+  __syncthreads();
+  for (int slot = tid; slot < job.slots; slot += nt) {
+    const int at = atomicAdd(&start[bucket_of[slot]], 1);
+    if (at < job.slots) job.order[at] = slot;
+  }
+}
+// Whether the sort, about 5 us, pays: few rounds of workgroups, and enough
+// work (multiply-adds of one product, `products` of them) for them to last.
+inline bool order_pays(const AttentionArgs& a, int64_t slots, int split, double products) {
+  const int64_t groups = slots * a.kv_heads * split;
+  double work = static_cast<double>(a.total_q) * a.heads * (static_cast<double>(a.total_k) / std::max(a.batch, 1)) * a.dim * products;
+  if (a.left >= 0 || a.right >= 0) work /= 2;
+  return a.batch <= 1024 && slots <= kOrderSlots && groups >= 512 && groups <= 2560 && work >= (a.dtype == 0 ? 3e9 : 2.4e10);
 }
 
 // The blocks of one split: an even share of [0, blocks).
@@ -385,7 +466,8 @@ inline Cut cut_rows(const AttentionArgs& a, int64_t mean, int64_t rows, int64_t 
   c.waves = mean <= 32 ? 1 : mean <= 64 ? 2 : 4;
   const int64_t tiles = std::max<int64_t>(rows / (32 * c.waves), std::max(a.batch, 1)) * a.kv_heads;
   const int64_t most = depth / (a.dtype == 0 ? 128 : 256), want = 4096 / (tiles * c.waves);
-  c.split = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(most, want), 16)));
+  c.split = 1;  // a power of two
+  while (c.split < 16 && 2 * c.split <= std::min(most, want)) c.split *= 2;
   if (c.waves == 4 && tiles * c.split < 512) c.waves = 2;
   return c;
 }
