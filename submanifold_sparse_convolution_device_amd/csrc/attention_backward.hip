@@ -64,7 +64,7 @@ constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 
 template <class T, int DP, int DQ, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int run, int nsplit, const int32_t* order,
-                                                                                    float* delta, float* part) {
+                                                                                    float2* stats, float* part) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece<T>), NL = (BN * PPR + NT - 1) / NT;
@@ -108,12 +108,14 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     }
   }
   dot = halves_sum(dot);
-  if (has_row && half == 0 && split == 0) delta[row_out] = dot;
   // exp(s - lse) as exp2(s c - lse2); a row without keys, or past the end, has P = 0
   float lse2 = INFINITY;
   if (has_row) {
     const float v = a.lse[row_out];
     lse2 = v == -INFINITY ? INFINITY : v * kLog2e - kShift<T>;
+    // for the other kernel, in the order in which it walks the rows
+    if (half == 0 && split == 0)
+      stats[static_cast<int64_t>(kvh) * a.total_q * a.group + static_cast<int64_t>(sp.q0) * a.group + r] = make_float2(lse2, dot);
   }
   const int place = tok + shift;
   const int lane_lo = a.left >= 0 ? place - a.left : 0;
@@ -228,14 +230,14 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
 }
 
 template <class T, int DP, int DQ, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int slots, int run, int nsplit, const int32_t* order, const float* delta,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) void k_attention_dkv(AttentionArgs a, int slots, int run, int nsplit, const int32_t* order, const float2* stats,
                                                               float* part_k, float* part_v) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece<T>), NL = (BN * PPR + NT - 1) / NT;
   constexpr int NR = (BN + NT - 1) / NT;  // rows whose statistics each thread copies
   __shared__ uint4 qs[BUFS][BN * PPR], gs[BUFS][BN * PPR];
-  __shared__ float4 row_lse[BUFS][BN / 4], row_delta[BUFS][BN / 4];
+  __shared__ float4 row_lse[BUFS][BN / 4], row_delta[BUFS][BN / 4];  // lse in log2 units and shifted, D
   __shared__ int4 row_place[BUFS][BN / 4];
 
   const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
@@ -281,17 +283,31 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
   int place_r[NR];
   const T* qbase = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0) * a.q_row + static_cast<int64_t>(kvh) * a.group * a.q_head;
   const T* gbase = static_cast<const T*>(a.grad_out) + static_cast<int64_t>(sp.q0) * a.go_row + static_cast<int64_t>(kvh) * a.group * a.go_head;
+  const float2* sbase = stats + (static_cast<int64_t>(kvh) * a.total_q + sp.q0) * a.group;
+  const uint32_t qb = static_cast<uint32_t>(a.q_row * sizeof(T)), gb = static_cast<uint32_t>(a.go_row * sizeof(T));
   auto load = [&](int rb) {
     const int r0 = f_lo + rb * BN;
+    if (a.group == 1) {
+      // flattened rows are rows: the offsets within a tile are the same for all
+      const auto qbuf = rows_buffer(qbase + r0 * a.q_row, rows - r0, qb), gbuf = rows_buffer(gbase + r0 * a.go_row, rows - r0, gb);
 #pragma unroll
-    for (int n = 0; n < NL; ++n) {
-      const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
-      const int r = r0 + row;
-      qr[n] = gr[n] = make_uint4(0, 0, 0, 0);
-      if (row < BN && r < rows && piece * kPiece<T> < a.dim) {
-        const int tok = div_group(a, r), g = r - tok * a.group;
-        qr[n] = *reinterpret_cast<const uint4*>(qbase + tok * a.q_row + g * a.q_head + piece * kPiece<T>);
-        gr[n] = *reinterpret_cast<const uint4*>(gbase + tok * a.go_row + g * a.go_head + piece * kPiece<T>);
+      for (int n = 0; n < NL; ++n) {
+        const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+        const bool on = row < BN && piece * kPiece<T> < a.dim;
+        qr[n] = load_piece(qbuf, on ? row * qb + piece * 16 : kNowhere);
+        gr[n] = load_piece(gbuf, on ? row * gb + piece * 16 : kNowhere);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
+        const int r = r0 + row;
+        qr[n] = gr[n] = make_uint4(0, 0, 0, 0);
+        if (row < BN && r < rows && piece * kPiece<T> < a.dim) {
+          const int tok = div_group(a, r), g = r - tok * a.group;
+          qr[n] = *reinterpret_cast<const uint4*>(qbase + tok * a.q_row + g * a.q_head + piece * kPiece<T>);
+          gr[n] = *reinterpret_cast<const uint4*>(gbase + tok * a.go_row + g * a.go_head + piece * kPiece<T>);
+        }
       }
     }
 #pragma unroll
@@ -301,12 +317,10 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
       delta_r[n] = 0.f;
       place_r[n] = 0;
       if (tid + n * NT < BN && r < rows) {
-        const int tok = div_group(a, r), head = kvh * a.group + r - tok * a.group;
-        const int64_t at = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
-        const float v = a.lse[at];
-        lse_r[n] = v == -INFINITY ? INFINITY : v * kLog2e - kShift<T>;
-        delta_r[n] = delta[at];
-        place_r[n] = tok + shift;
+        const float2 st = sbase[r];
+        lse_r[n] = st.x;
+        delta_r[n] = st.y;
+        place_r[n] = div_group(a, r) + shift;
       }
     }
   };
@@ -482,14 +496,14 @@ Plan make_backward_plan(const AttentionArgs& a) {
 }
 
 struct Workspace {
-  size_t delta, q, k, v, q_order, k_order, total;  // offsets in bytes
+  size_t stats, q, k, v, q_order, k_order, total;  // offsets in bytes
 };
 Workspace layout(const AttentionArgs& a, const Plan& p) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const size_t nq = static_cast<size_t>(a.total_q) * a.heads, nk = static_cast<size_t>(a.total_k) * a.kv_heads;
   Workspace w;
-  w.delta = 0;
-  w.q = up(nq * sizeof(float));
+  w.stats = 0;
+  w.q = up(nq * sizeof(float2));
   w.k = w.q + (p.q_split > 1 ? up(nq * a.dim * p.q_split * sizeof(float)) : 0);
   const size_t part = p.k_split > 1 ? up(nk * a.dim * p.k_split * sizeof(float)) : 0;
   w.v = w.k + part;
@@ -507,7 +521,7 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
   const Plan p = make_backward_plan(a);
   const Workspace w = layout(a, p);
   char* base = static_cast<char*>(workspace);
-  float* delta = reinterpret_cast<float*>(base + w.delta);
+  float2* stats = reinterpret_cast<float2*>(base + w.stats);
   float* part_q = reinterpret_cast<float*>(base + w.q);
   float* part_k = reinterpret_cast<float*>(base + w.k);
   float* part_v = reinterpret_cast<float*>(base + w.v);
@@ -526,9 +540,9 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
     if (a.total_q > 0) {
       const int run = p.ordered ? 0 : slot_run(a, p.q_slots);
       const dim3 grid(static_cast<unsigned>(placed_slots(p.q_slots, run) * a.kv_heads * p.q_split));
-      if (p.q_waves == 1) k_attention_dq<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, delta, part_q);
-      else if (p.q_waves == 2) k_attention_dq<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, delta, part_q);
-      else k_attention_dq<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, delta, part_q);
+      if (p.q_waves == 1) k_attention_dq<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, stats, part_q);
+      else if (p.q_waves == 2) k_attention_dq<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, stats, part_q);
+      else k_attention_dq<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, stats, part_q);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.q_split > 1) launch_join<T>(part_q, p.q_split, a.total_q, a.heads, a.dim, a.grad_q, a.gq_row, a.gq_head, stream);
@@ -536,9 +550,9 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
     if (a.total_k > 0) {
       const int run = p.ordered ? 0 : slot_run(a, p.k_slots);
       const dim3 grid(static_cast<unsigned>(placed_slots(p.k_slots, run) * a.kv_heads * p.k_split));
-      if (p.k_waves == 1) k_attention_dkv<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, delta, part_k, part_v);
-      else if (p.k_waves == 2) k_attention_dkv<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, delta, part_k, part_v);
-      else k_attention_dkv<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, delta, part_k, part_v);
+      if (p.k_waves == 1) k_attention_dkv<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, stats, part_k, part_v);
+      else if (p.k_waves == 2) k_attention_dkv<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, stats, part_k, part_v);
+      else k_attention_dkv<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, stats, part_k, part_v);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       if (p.k_split > 1) {
