@@ -49,9 +49,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   constexpr int NB = BN >= 64 ? 2 : 1;  // blocks of 32 keys per softmax step
   constexpr int PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES;                // flattened rows per workgroup
-  constexpr int KS = DQ / (2 * kPiece<T>);      // pieces per half of a row
+  constexpr int KS = DQ / (2 * kPiece);      // pieces per half of a row
   constexpr int NL = (BN * PPR + NT - 1) / NT;  // pieces each thread copies per tile
-  __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
+  __shared__ uint4 ks[BUFS][kPlanes<T> * BN * PPR], vs[BUFS][kPlanes<T> * BN * PPR];
 
   // a tile's splits follow one another (nsplit is a power of two)
   const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
@@ -93,13 +93,13 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const bool has_row = r < rows;
   const int tok = div_group(a, has_row ? r : 0);
   const int head = kvh * a.group + (has_row ? r - tok * a.group : 0);
-  uint4 qf[KS];
+  Frag<T> qf[KS];
   {
     const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0 + tok) * a.q_row + static_cast<int64_t>(head) * a.q_head;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
       const int piece = 2 * t + half;
-      qf[t] = has_row && piece * kPiece<T> < a.dim ? *reinterpret_cast<const uint4*>(src + piece * kPiece<T>) : make_uint4(0, 0, 0, 0);
+      qf[t] = to_frag<T>(load_piece(src + piece * kPiece, has_row && piece * kPiece < a.dim));
     }
   }
   const int place = tok + shift;
@@ -126,22 +126,22 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head + static_cast<int64_t>(sp.k0) * a.k_row;
   const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head + static_cast<int64_t>(sp.k0) * a.v_row;
   const uint32_t kb = static_cast<uint32_t>(a.k_row * sizeof(T)), vb = static_cast<uint32_t>(a.v_row * sizeof(T));
-  uint4 kr[NL], vr[NL];
+  Raw<T> kr[NL], vr[NL];
   uint32_t koff[NL], voff[NL];
 #pragma unroll
   for (int n = 0; n < NL; ++n) {
     const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
-    const bool on = row < BN && piece * kPiece<T> < a.dim;
-    koff[n] = on ? row * kb + piece * 16 : kNowhere;
-    voff[n] = on ? row * vb + piece * 16 : kNowhere;
+    const bool on = row < BN && piece * kPiece < a.dim;
+    koff[n] = on ? row * kb + piece * kPieceBytes<T> : kNowhere;
+    voff[n] = on ? row * vb + piece * kPieceBytes<T> : kNowhere;
   }
   auto load = [&](int jb) {
     const int j0 = wg.lo + jb * BN;
     const auto kbuf = rows_buffer(kbase + j0 * a.k_row, sp.nk - j0, kb), vbuf = rows_buffer(vbase + j0 * a.v_row, sp.nk - j0, vb);
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
-      kr[n] = load_piece(kbuf, koff[n]);
-      vr[n] = load_piece(vbuf, voff[n]);
+      kr[n] = load_piece<T>(kbuf, koff[n]);
+      vr[n] = load_piece<T>(vbuf, voff[n]);
     }
   };
   auto store = [&](int buf) {
@@ -149,8 +149,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     for (int n = 0; n < NL; ++n) {
       const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
       if (row < BN) {
-        ks[buf][TL::at(row, piece)] = kr[n];
-        vs[buf][TL::at(row, piece)] = vr[n];
+        TL::template store<BN>(ks[buf], row, piece, kr[n]);
+        TL::template store<BN>(vs[buf], row, piece, vr[n]);
       }
     }
   };
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
         s[b] = floatx16(0.f);
 #pragma unroll
         for (int t = 0; t < KS; ++t)
-          s[b] = mma_piece<T>(TL::row_piece(ks[buf], 32 * (step + b) + (lane & 31), 2 * t + half), qf[t], s[b]);
+          s[b] = mma_frag<T>(TL::template row_frag<BN>(ks[buf], 32 * (step + b) + (lane & 31), 2 * t + half), qf[t], s[b]);
       }
       if (j0 + 32 * NB > full_hi) {
         keep_branch();
@@ -227,9 +227,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
           p[i] = fast_exp2(__builtin_fmaf(s[b][i], c, -base));
           l += p[i];
         }
-        mma_transposed<T, DP, DB>(vs[buf], 32 * (step + b), lane, p, acc);
+        mma_transposed<T, DP, DB, BN>(vs[buf], 32 * (step + b), lane, p, acc);
       }
-      settle<T>();
+      settle();
     }
     if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1);
   }

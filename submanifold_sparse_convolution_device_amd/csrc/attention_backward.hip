@@ -67,8 +67,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
                                                                                     float2* stats, float* part) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
-  constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece<T>), NL = (BN * PPR + NT - 1) / NT;
-  __shared__ uint4 ks[BUFS][BN * PPR], vs[BUFS][BN * PPR];
+  constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece), NL = (BN * PPR + NT - 1) / NT;
+  __shared__ uint4 ks[BUFS][kPlanes<T> * BN * PPR], vs[BUFS][kPlanes<T> * BN * PPR];
 
   const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
   const Place at_block = place_of(a, id, run);
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const int tok = div_group(a, has_row ? r : 0);
   const int head = kvh * a.group + (has_row ? r - tok * a.group : 0);
   const int64_t row_out = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
-  uint4 qf[KS], gf[KS];
+  Frag<T> qf[KS], gf[KS];
   float dot = 0.f;
   {
     const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0 + tok) * a.q_row + static_cast<int64_t>(head) * a.q_head;
@@ -96,15 +96,18 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     const T* osrc = static_cast<const T*>(a.out) + row_out * a.dim;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      const int e = (2 * t + half) * kPiece<T>;
+      const int e = (2 * t + half) * kPiece;
       const bool ok = has_row && e < a.dim;
-      qf[t] = ok ? *reinterpret_cast<const uint4*>(src + e) : make_uint4(0, 0, 0, 0);
-      gf[t] = ok ? *reinterpret_cast<const uint4*>(gsrc + e) : make_uint4(0, 0, 0, 0);
-      const uint4 o = ok ? *reinterpret_cast<const uint4*>(osrc + e) : make_uint4(0, 0, 0, 0);
-      typedef T piece_t __attribute__((ext_vector_type(kPiece<T>)));
-      const piece_t ov = __builtin_bit_cast(piece_t, o), gv = __builtin_bit_cast(piece_t, gf[t]);
+      const Raw<T> g = load_piece(gsrc + e, ok), o = load_piece(osrc + e, ok);
+      qf[t] = to_frag<T>(load_piece(src + e, ok));
+      gf[t] = to_frag<T>(g);
+      typedef T part_t __attribute__((ext_vector_type(16 / sizeof(T))));
 #pragma unroll
-      for (int u = 0; u < kPiece<T>; ++u) dot = __builtin_fmaf(to_f32(gv[u]), to_f32(ov[u]), dot);
+      for (int w = 0; w < static_cast<int>(sizeof(T) / 2); ++w) {
+        const part_t ov = __builtin_bit_cast(part_t, o.v[w]), gv = __builtin_bit_cast(part_t, g.v[w]);
+#pragma unroll
+        for (int u = 0; u < static_cast<int>(16 / sizeof(T)); ++u) dot = __builtin_fmaf(to_f32(gv[u]), to_f32(ov[u]), dot);
+      }
     }
   }
   dot = halves_sum(dot);
@@ -134,22 +137,22 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const T* kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(kvh) * a.k_head + static_cast<int64_t>(sp.k0) * a.k_row;
   const T* vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(kvh) * a.v_head + static_cast<int64_t>(sp.k0) * a.v_row;
   const uint32_t kb = static_cast<uint32_t>(a.k_row * sizeof(T)), vb = static_cast<uint32_t>(a.v_row * sizeof(T));
-  uint4 kr[NL], vr[NL];
+  Raw<T> kr[NL], vr[NL];
   uint32_t koff[NL], voff[NL];
 #pragma unroll
   for (int n = 0; n < NL; ++n) {
     const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
-    const bool on = row < BN && piece * kPiece<T> < a.dim;
-    koff[n] = on ? row * kb + piece * 16 : kNowhere;
-    voff[n] = on ? row * vb + piece * 16 : kNowhere;
+    const bool on = row < BN && piece * kPiece < a.dim;
+    koff[n] = on ? row * kb + piece * kPieceBytes<T> : kNowhere;
+    voff[n] = on ? row * vb + piece * kPieceBytes<T> : kNowhere;
   }
   auto load = [&](int jb) {
     const int j0 = wg.lo + jb * BN;
     const auto kbuf = rows_buffer(kbase + j0 * a.k_row, sp.nk - j0, kb), vbuf = rows_buffer(vbase + j0 * a.v_row, sp.nk - j0, vb);
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
-      kr[n] = load_piece(kbuf, koff[n]);
-      vr[n] = load_piece(vbuf, voff[n]);
+      kr[n] = load_piece<T>(kbuf, koff[n]);
+      vr[n] = load_piece<T>(vbuf, voff[n]);
     }
   };
 
@@ -164,8 +167,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     for (int n = 0; n < NL; ++n) {
       const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
       if (row < BN) {
-        ks[buf][TL::at(row, piece)] = kr[n];
-        vs[buf][TL::at(row, piece)] = vr[n];
+        TL::template store<BN>(ks[buf], row, piece, kr[n]);
+        TL::template store<BN>(vs[buf], row, piece, vr[n]);
       }
     }
   };
@@ -188,8 +191,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       floatx16 s(0.f), dp(0.f);
 #pragma unroll
       for (int t = 0; t < KS; ++t) {
-        s = mma_piece<T>(TL::row_piece(ks[buf], 32 * b + (lane & 31), 2 * t + half), qf[t], s);
-        dp = mma_piece<T>(TL::row_piece(vs[buf], 32 * b + (lane & 31), 2 * t + half), gf[t], dp);
+        s = mma_frag<T>(TL::template row_frag<BN>(ks[buf], 32 * b + (lane & 31), 2 * t + half), qf[t], s);
+        dp = mma_frag<T>(TL::template row_frag<BN>(vs[buf], 32 * b + (lane & 31), 2 * t + half), gf[t], dp);
       }
       float ds[16];
 #pragma unroll
@@ -207,8 +210,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
         for (int i = 0; i < 16; ++i) ds[i] = c_row(i) >= first ? ds[i] : 0.f;
       }
       rescale<T, DB>(ds, factor, acc);
-      mma_transposed<T, DP, DB>(ks[buf], 32 * b, lane, ds, acc);
-      settle<T>();
+      mma_transposed<T, DP, DB, BN>(ks[buf], 32 * b, lane, ds, acc);
+      settle();
     }
     if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1);
   }
@@ -234,9 +237,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
                                                               float* part_k, float* part_v) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
-  constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece<T>), NL = (BN * PPR + NT - 1) / NT;
+  constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece), NL = (BN * PPR + NT - 1) / NT;
   constexpr int NR = (BN + NT - 1) / NT;  // rows whose statistics each thread copies
-  __shared__ uint4 qs[BUFS][BN * PPR], gs[BUFS][BN * PPR];
+  __shared__ uint4 qs[BUFS][kPlanes<T> * BN * PPR], gs[BUFS][kPlanes<T> * BN * PPR];
   __shared__ float4 row_lse[BUFS][BN / 4], row_delta[BUFS][BN / 4];  // lse in log2 units and shifted, D
   __shared__ int4 row_place[BUFS][BN / 4];
 
@@ -255,16 +258,16 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
   const int key = kw0 + (lane & 31);
   const bool has_key = key < sp.nk;
   const int64_t krow = static_cast<int64_t>(sp.k0 + (has_key ? key : 0));
-  uint4 kf[KS], vf[KS];
+  Frag<T> kf[KS], vf[KS];
   {
     const T* src = static_cast<const T*>(a.k) + krow * a.k_row + static_cast<int64_t>(kvh) * a.k_head;
     const T* vsrc = static_cast<const T*>(a.v) + krow * a.v_row + static_cast<int64_t>(kvh) * a.v_head;
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      const int e = (2 * t + half) * kPiece<T>;
+      const int e = (2 * t + half) * kPiece;
       const bool ok = has_key && e < a.dim;
-      kf[t] = ok ? *reinterpret_cast<const uint4*>(src + e) : make_uint4(0, 0, 0, 0);
-      vf[t] = ok ? *reinterpret_cast<const uint4*>(vsrc + e) : make_uint4(0, 0, 0, 0);
+      kf[t] = to_frag<T>(load_piece(src + e, ok));
+      vf[t] = to_frag<T>(load_piece(vsrc + e, ok));
     }
   }
   // Query rows that see a key of the workgroup: place - left <= key <= place + right.
@@ -278,7 +281,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
   const bool wave_on = kw0 < sp.nk;
   const int kw1 = min(kw0 + 32, sp.nk) - 1;  // last key of the wave
 
-  uint4 qr[NL], gr[NL];
+  Raw<T> qr[NL], gr[NL];
   float lse_r[NR], delta_r[NR];
   int place_r[NR];
   const T* qbase = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0) * a.q_row + static_cast<int64_t>(kvh) * a.group * a.q_head;
@@ -293,21 +296,19 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
         const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
-        const bool on = row < BN && piece * kPiece<T> < a.dim;
-        qr[n] = load_piece(qbuf, on ? row * qb + piece * 16 : kNowhere);
-        gr[n] = load_piece(gbuf, on ? row * gb + piece * 16 : kNowhere);
+        const bool on = row < BN && piece * kPiece < a.dim;
+        qr[n] = load_piece<T>(qbuf, on ? row * qb + piece * kPieceBytes<T> : kNowhere);
+        gr[n] = load_piece<T>(gbuf, on ? row * gb + piece * kPieceBytes<T> : kNowhere);
       }
     } else {
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
         const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
         const int r = r0 + row;
-        qr[n] = gr[n] = make_uint4(0, 0, 0, 0);
-        if (row < BN && r < rows && piece * kPiece<T> < a.dim) {
-          const int tok = div_group(a, r), g = r - tok * a.group;
-          qr[n] = *reinterpret_cast<const uint4*>(qbase + tok * a.q_row + g * a.q_head + piece * kPiece<T>);
-          gr[n] = *reinterpret_cast<const uint4*>(gbase + tok * a.go_row + g * a.go_head + piece * kPiece<T>);
-        }
+        const bool on = row < BN && r < rows && piece * kPiece < a.dim;
+        const int tok = div_group(a, on ? r : 0), g = on ? r - tok * a.group : 0;
+        qr[n] = load_piece(qbase + tok * a.q_row + g * a.q_head + piece * kPiece, on);
+        gr[n] = load_piece(gbase + tok * a.go_row + g * a.go_head + piece * kPiece, on);
       }
     }
 #pragma unroll
@@ -329,8 +330,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
     for (int n = 0; n < NL; ++n) {
       const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
       if (row < BN) {
-        qs[buf][TL::at(row, piece)] = qr[n];
-        gs[buf][TL::at(row, piece)] = gr[n];
+        TL::template store<BN>(qs[buf], row, piece, qr[n]);
+        TL::template store<BN>(gs[buf], row, piece, gr[n]);
       }
     }
 #pragma unroll
@@ -374,8 +375,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
       floatx16 s(0.f), dp(0.f);
 #pragma unroll
       for (int t = 0; t < KS; ++t) {
-        s = mma_piece<T>(TL::row_piece(qs[buf], 32 * b + (lane & 31), 2 * t + half), kf[t], s);
-        dp = mma_piece<T>(TL::row_piece(gs[buf], 32 * b + (lane & 31), 2 * t + half), vf[t], dp);
+        s = mma_frag<T>(TL::template row_frag<BN>(qs[buf], 32 * b + (lane & 31), 2 * t + half), kf[t], s);
+        dp = mma_frag<T>(TL::template row_frag<BN>(gs[buf], 32 * b + (lane & 31), 2 * t + half), vf[t], dp);
       }
       float p[16], ds[16];
 #pragma unroll
@@ -406,10 +407,10 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
           }
         }
       }
-      mma_transposed<T, DP, DB>(gs[buf], 32 * b, lane, p, dv);
+      mma_transposed<T, DP, DB, BN>(gs[buf], 32 * b, lane, p, dv);
       rescale<T, DB>(ds, factor, dk);
-      mma_transposed<T, DP, DB>(qs[buf], 32 * b, lane, ds, dk);
-      settle<T>();
+      mma_transposed<T, DP, DB, BN>(qs[buf], 32 * b, lane, ds, dk);
+      settle();
     }
     if (BUFS == 2 && rb + 1 < rb1) store(buf ^ 1);
   }

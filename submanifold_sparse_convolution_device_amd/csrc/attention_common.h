@@ -7,13 +7,18 @@
 // m = 8 (i / 4) + 4 (l / 32) + i mod 4.  The contracted index may run in any
 // order that A and B share, and the kernels choose it so that a C tile (of
 // scores) is the B operand of the next product as it stands:
-//   16-bit types, 32x32x16: step s, half h = l / 32, element j is row
-//     16 s + 8 (j / 4) + 4 h + j mod 4, the C rows of registers 8 s + j;
-//   fp32, 32x32x2: step i, half h is row 8 (i / 4) + 4 h + i mod 4.
-// So the products run transposed: S^T = K Q^T puts a query in each lane's
-// column (its softmax needs one exchange, between the halves), and
-// O^T = V^T P^T takes P^T from registers and V^T through the transposing LDS
-// read (16 bits) or plain column reads (fp32).
+// step s, half h = l / 32, element j is row 16 s + 8 (j / 4) + 4 h + j mod 4,
+// the C rows of registers 8 s + j.  So the products run transposed:
+// S^T = K Q^T puts a query in each lane's column (its softmax needs one
+// exchange, between the halves), and O^T = V^T P^T takes P^T from registers
+// and V^T through the transposing LDS read.
+//
+// fp32 runs on the bf16 matrix unit, 16 times the rate of the fp32 one: a
+// value splits exactly into three bf16 planes of 8 significant bits (by
+// truncation: x = hi + mid + lo), and a product is the six of the nine plane
+// products that reach 2^-24 of it, summed in fp32:
+//   hi hi + (hi mid + mid hi) + (hi lo + mid mid + lo hi);
+// what is left out is below 2^-23 of |a b|, the size of an fp32 rounding.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -34,9 +39,11 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Elements per 16-byte piece.
+// bf16 planes that hold one operand (fp32: three).
 template <class T>
-constexpr int kPiece = 16 / static_cast<int>(sizeof(T));
+constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+// A piece is 8 consecutive values: 16 bytes of each plane.
+constexpr int kPiece = 8;
 
 template <class T>
 __device__ __forceinline__ float to_f32(T v) {
@@ -77,24 +84,115 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const void* base, 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(min(bytes, static_cast<uint64_t>(0x7fffffff))),
                                            kBufferWord3);
 }
-__device__ __forceinline__ uint4 load_piece(__amdgpu_buffer_rsrc_t rsrc, uint32_t offset) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, static_cast<int>(offset), 0, 0));
+// A piece as it lies in memory.
+template <class T>
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+};
+template <class T>
+constexpr uint32_t kPieceBytes = kPiece * sizeof(T);
+
+template <class T>
+__device__ __forceinline__ Raw<T> load_piece(__amdgpu_buffer_rsrc_t rsrc, uint32_t offset) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+    r.v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, static_cast<int>(offset + 16 * i), 0, 0));
+  return r;
+}
+template <class T>
+__device__ __forceinline__ Raw<T> load_piece(const T* src, bool on) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+    r.v[i] = on ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+  return r;
 }
 
-// C += A B over one 16-byte piece per lane of each operand (the piece of
-// half h is piece 2 t + h of the row): 16 contracted elements in 16 bits, 8
-// in fp32.
+// A piece as an operand: one register quad per plane.
 template <class T>
-__device__ __forceinline__ floatx16 mma_piece(uint4 a, uint4 b, floatx16 c) {
-  if constexpr (__is_same(T, _Float16)) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
-  } else if constexpr (__is_same(T, __bf16)) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+struct Frag {
+  uint4 v[kPlanes<T>];
+};
+
+// The three planes of two fp32 values, two bf16 in a word each.  An infinity
+// or NaN stays in the first plane alone.
+struct Split2 {
+  uint32_t hi, mid, lo;
+};
+template <bool FINITE>
+__device__ __forceinline__ Split2 split2(float x, float y) {
+  auto high = [](float f) { return __builtin_bit_cast(uint32_t, f) & 0xffff0000u; };
+  // the words' upper halves, y's above x's
+  auto pair = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };
+  const uint32_t hx = high(x), hy = high(y);
+  float rx = x - __builtin_bit_cast(float, hx), ry = y - __builtin_bit_cast(float, hy);  // exact
+  if constexpr (!FINITE) {
+    rx = fabsf(x) < INFINITY ? rx : 0.f;
+    ry = fabsf(y) < INFINITY ? ry : 0.f;
+  }
+  const uint32_t mx = high(rx), my = high(ry);
+  const float lx = rx - __builtin_bit_cast(float, mx), ly = ry - __builtin_bit_cast(float, my);
+  return {pair(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)),
+          pair(__builtin_bit_cast(uint32_t, rx), __builtin_bit_cast(uint32_t, ry)),
+          pair(__builtin_bit_cast(uint32_t, lx), __builtin_bit_cast(uint32_t, ly))};
+}
+template <bool FINITE>
+__device__ __forceinline__ Frag<float> split8(const float (&x)[8]) {
+  const Split2 a = split2<FINITE>(x[0], x[1]), b = split2<FINITE>(x[2], x[3]), c = split2<FINITE>(x[4], x[5]), d = split2<FINITE>(x[6], x[7]);
+  Frag<float> f;
+  f.v[0] = make_uint4(a.hi, b.hi, c.hi, d.hi);
+  f.v[1] = make_uint4(a.mid, b.mid, c.mid, d.mid);
+  f.v[2] = make_uint4(a.lo, b.lo, c.lo, d.lo);
+  return f;
+}
+template <class T>
+__device__ __forceinline__ Frag<T> to_frag(const Raw<T>& r) {
+  if constexpr (sizeof(T) == 4) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 q = r.v[i / 4];
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      x[i] = __builtin_bit_cast(float, w[i & 3]);
+    }
+    return split8<false>(x);
   } else {
-    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, a.x), __builtin_bit_cast(float, b.x), c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, a.y), __builtin_bit_cast(float, b.y), c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, a.z), __builtin_bit_cast(float, b.z), c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, a.w), __builtin_bit_cast(float, b.w), c, 0, 0, 0);
+    return {{r.v[0]}};
+  }
+}
+// The operand of 8 values held in fp32 (rounded to T, or split).
+template <class T>
+__device__ __forceinline__ Frag<T> make_frag(const float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    return split8<true>(x);
+  } else {
+    typedef T tx8 __attribute__((ext_vector_type(8)));
+    tx8 b;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = static_cast<T>(x[j]);
+    return {{__builtin_bit_cast(uint4, b)}};
+  }
+}
+
+// C += A B over one piece per lane of each operand (half h's is piece
+// 2 t + h of the row): 16 contracted values.
+template <class T>
+__device__ __forceinline__ floatx16 mma_frag(const Frag<T>& a, const Frag<T>& b, floatx16 c) {
+  if constexpr (__is_same(T, _Float16)) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a.v[0]), __builtin_bit_cast(half8, b.v[0]), c, 0, 0, 0);
+  } else {
+    auto term = [&](int i, int j) {
+      c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.v[i]), __builtin_bit_cast(bf16x8, b.v[j]), c, 0, 0, 0);
+    };
+    if constexpr (sizeof(T) == 4) {
+      term(2, 0);
+      term(1, 1);
+      term(0, 2);
+      term(1, 0);
+      term(0, 1);
+    }
+    term(0, 0);
     return c;
   }
 }
@@ -108,7 +206,7 @@ __device__ __forceinline__ floatx16 mma_piece(uint4 a, uint4 b, floatx16 c) {
 // 128 bf16 columns, against 16 for rows laid out plainly.
 template <class T, int DP>
 struct Tile {
-  static constexpr int PPR = DP / kPiece<T>;  // pieces per row
+  static constexpr int PPR = DP / kPiece;  // pieces per row
   static_assert(PPR % 4 == 0, "rows of whole 64-byte groups");
   __device__ static __forceinline__ int swz(int row) {
     if constexpr (PPR % 16 == 0) return (row & 3) << 2 | (row >> 2 & 1) << 1 | (row >> 3 & 1);
@@ -116,57 +214,56 @@ struct Tile {
     return (row >> 2 & 1) << 1 | (row >> 3 & 1);
   }
   __device__ static __forceinline__ int at(int row, int piece) { return row * PPR + (piece ^ swz(row)); }
-  // A operand by rows: lane's row (m) and piece.
-  __device__ static __forceinline__ uint4 row_piece(const uint4* lds, int row, int piece) { return lds[at(row, piece)]; }
+  // A operand by rows: lane's row (m) and piece, of a tile of ROWS rows.
+  template <int ROWS>
+  __device__ static __forceinline__ Frag<T> row_frag(const uint4* lds, int row, int piece) {
+    Frag<T> f;
+#pragma unroll
+    for (int p = 0; p < kPlanes<T>; ++p) f.v[p] = lds[p * ROWS * PPR + at(row, piece)];
+    return f;
+  }
+  template <int ROWS>
+  __device__ static __forceinline__ void store(uint4* lds, int row, int piece, const Raw<T>& r) {
+    const Frag<T> f = to_frag<T>(r);
+#pragma unroll
+    for (int p = 0; p < kPlanes<T>; ++p) lds[p * ROWS * PPR + at(row, piece)] = f.v[p];
+  }
 };
 
 // C tiles of one contraction over the 32 rows row0 .. row0 + 31 of a tile:
 // acc[d][n] += sum_row tile[row][d] p[row][n] for DB blocks of 32 columns d;
 // p in C layout.  16-bit types round p to T (an operand of the matrix
 // instruction; the sums stay in fp32).
-template <class T, int DP, int DB>
+template <class T, int DP, int DB, int ROWS>
 __device__ __forceinline__ void mma_transposed(const uint4* lds, int row0, int lane, const float (&p)[16],
                                                floatx16 (&acc)[DB]) {
   typedef Tile<T, DP> TL;
-  if constexpr (sizeof(T) == 2) {
-    typedef T tx8 __attribute__((ext_vector_type(8)));
-    const int g = lane & 15;
-    // Lane g of a group of 16 addresses 4 columns of row g / 4; it receives
-    // column g of the four rows.
-    const int row = row0 + 4 * (lane >> 5) + (g >> 2);
-    const int col = ((lane >> 4) & 1) * 16 + 4 * (g & 3);
+  const int g = lane & 15;
+  // Lane g of a group of 16 addresses 4 columns of row g / 4; it receives
+  // column g of the four rows.
+  const int row = row0 + 4 * (lane >> 5) + (g >> 2);
+  const int col = ((lane >> 4) & 1) * 16 + 4 * (g & 3);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      tx8 b;
+  for (int s = 0; s < 2; ++s) {
+    float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) b[j] = static_cast<T>(p[8 * s + j]);
+    for (int j = 0; j < 8; ++j) x[j] = p[8 * s + j];
+    const Frag<T> b = make_frag<T>(x);
 #pragma unroll
-      for (int db = 0; db < DB; ++db) {
-        const int c = db * 32 + col;
-        s16x4 a[2];
+    for (int db = 0; db < DB; ++db) {
+      const int c = db * 32 + col;
+      Frag<T> a;
+#pragma unroll
+      for (int q = 0; q < kPlanes<T>; ++q) {
+        uint2 half[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int r = row + 16 * s + 8 * u;
-          const char* src = reinterpret_cast<const char*>(lds + TL::at(r, c / 8)) + (c & 4) * 2;
-          a[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)src);
+          const char* src = reinterpret_cast<const char*>(lds + q * ROWS * TL::PPR + TL::at(row + 16 * s + 8 * u, c / 8)) + (c & 4) * 2;
+          half[u] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)src));
         }
-        uint4 av;
-        const auto a0 = __builtin_bit_cast(uint2, a[0]), a1 = __builtin_bit_cast(uint2, a[1]);
-        av.x = a0.x; av.y = a0.y; av.z = a1.x; av.w = a1.y;
-        acc[db] = mma_piece<T>(av, __builtin_bit_cast(uint4, b), acc[db]);
+        a.v[q] = make_uint4(half[0].x, half[0].y, half[1].x, half[1].y);
       }
-    }
-  } else {
-    const int col = lane & 31;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = row0 + 8 * (i / 4) + 4 * (lane >> 5) + (i & 3);
-#pragma unroll
-      for (int db = 0; db < DB; ++db) {
-        const int c = db * 32 + col;
-        const float a = reinterpret_cast<const float*>(lds + TL::at(r, c / 4))[c & 3];
-        acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[i], acc[db], 0, 0, 0);
-      }
+      acc[db] = mma_frag<T>(a, b, acc[db]);
     }
   }
 }
@@ -176,13 +273,11 @@ __device__ __forceinline__ void mma_transposed(const uint4* lds, int row0, int l
 // that reads an accumulator too early, and the compiler, which places the
 // waits, has been seen to omit them where two paths of different length lead
 // from the product to the read across blocks (the last accumulator register
-// then held the value before the product).  16 passes need 18 states, 8
-// passes 11; with the wait in the product's own block no path is shorter.
-template <class T>
+// then held the value before the product).  8 passes need 12 states; with the
+// wait in the product's own block no path is shorter.
 __device__ __forceinline__ void settle() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_nop 15");
-  if constexpr (sizeof(T) == 4) asm volatile("s_nop 7");
   __builtin_amdgcn_sched_barrier(0);
 }
 
