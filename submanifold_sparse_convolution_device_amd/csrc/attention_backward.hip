@@ -439,34 +439,55 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
     }
 }
 
-// Adds the splits' partial gradients in order and rounds once.
+// One tensor's partial gradients: [nsplit][rows][heads][dim].
+struct JoinJob {
+  const float* part = nullptr;
+  int nsplit = 0;  // 1: nothing to join
+  int64_t rows = 0;
+  int heads = 0;
+  void* dst = nullptr;
+  int64_t row_stride = 0, head_stride = 0;
+  unsigned first_block = 0;
+};
+struct JoinJobs {
+  JoinJob job[3];
+};
+
+// Adds the splits' partial gradients in order and rounds once, for all three
+// tensors in one launch; four columns per thread.
 template <class T>
-__global__ __launch_bounds__(256) void k_attention_grad_join(const float* part, int nsplit, int64_t rows, int heads,
-                                                             int dim, T* dst, int64_t row_stride, int64_t head_stride) {
+__global__ __launch_bounds__(256) void k_attention_grad_join(JoinJobs jobs, int dim) {
+  const int which = blockIdx.x >= jobs.job[2].first_block ? 2 : blockIdx.x >= jobs.job[1].first_block ? 1 : 0;
+  const JoinJob& j = jobs.job[which];
   const int quads = dim / 4;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t id = static_cast<int64_t>(blockIdx.x - j.first_block) * 256 + threadIdx.x;
   const int64_t rh = id / quads;
-  if (rh >= rows * heads) return;
+  if (rh >= j.rows * j.heads) return;
   const int quad = static_cast<int>(id - rh * quads);
-  const int64_t row = rh / heads;
-  const int head = static_cast<int>(rh - row * heads);
+  const int64_t row = rh / j.heads;
+  const int head = static_cast<int>(rh - row * j.heads);
   float x = 0.f, y = 0.f, z = 0.f, w = 0.f;
-  for (int s = 0; s < nsplit; ++s) {
-    const float4 v = *reinterpret_cast<const float4*>(part + (s * rows * heads + rh) * dim + 4 * quad);
+  for (int s = 0; s < j.nsplit; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(j.part + (s * j.rows * j.heads + rh) * dim + 4 * quad);
     x += v.x;
     y += v.y;
     z += v.z;
     w += v.w;
   }
-  store4<T>(dst + row * row_stride + head * head_stride + 4 * quad, x, y, z, w);
+  store4<T>(static_cast<T*>(j.dst) + row * j.row_stride + head * j.head_stride + 4 * quad, x, y, z, w);
 }
 
+// Launches the join of the jobs that have parts.
 template <class T>
-void launch_join(const float* part, int nsplit, int64_t rows, int heads, int dim, void* dst, int64_t row_stride,
-                 int64_t head_stride, hipStream_t stream) {
-  const int64_t quads = rows * heads * (dim / 4);
-  k_attention_grad_join<T><<<static_cast<unsigned>((quads + 255) / 256), 256, 0, stream>>>(
-      part, nsplit, rows, heads, dim, static_cast<T*>(dst), row_stride, head_stride);
+hipError_t launch_joins(JoinJobs jobs, int dim, hipStream_t stream) {
+  unsigned blocks = 0;
+  for (JoinJob& j : jobs.job) {
+    j.first_block = blocks;
+    if (j.nsplit > 1) blocks += static_cast<unsigned>((j.rows * j.heads * (dim / 4) + 255) / 256);
+  }
+  if (blocks == 0) return hipSuccess;
+  k_attention_grad_join<T><<<blocks, 256, 0, stream>>>(jobs, dim);
+  return hipGetLastError();
 }
 
 __global__ __launch_bounds__(1024) void k_attention_grad_order(AttentionArgs a, OrderJob q, OrderJob k) {
@@ -546,7 +567,6 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
       else k_attention_dq<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, stats, part_q);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      if (p.q_split > 1) launch_join<T>(part_q, p.q_split, a.total_q, a.heads, a.dim, a.grad_q, a.gq_row, a.gq_head, stream);
     }
     if (a.total_k > 0) {
       const int run = p.ordered ? 0 : slot_run(a, p.k_slots);
@@ -556,12 +576,11 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
       else k_attention_dkv<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, stats, part_k, part_v);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      if (p.k_split > 1) {
-        launch_join<T>(part_k, p.k_split, a.total_k, a.kv_heads, a.dim, a.grad_k, a.gk_row, a.gk_head, stream);
-        launch_join<T>(part_v, p.k_split, a.total_k, a.kv_heads, a.dim, a.grad_v, a.gv_row, a.gv_head, stream);
-      }
     }
-    return hipGetLastError();
+    const JoinJobs jobs = {{{part_q, p.q_split, a.total_q, a.heads, a.grad_q, a.gq_row, a.gq_head},
+                            {part_k, p.k_split, a.total_k, a.kv_heads, a.grad_k, a.gk_row, a.gk_head},
+                            {part_v, p.k_split, a.total_k, a.kv_heads, a.grad_v, a.gv_row, a.gv_head}}};
+    return launch_joins<T>(jobs, a.dim, stream);
   });
 }
 
