@@ -52,6 +52,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   constexpr int KS = DQ / (2 * kPiece);      // pieces per half of a row
   constexpr int NL = (BN * PPR + NT - 1) / NT;  // pieces each thread copies per tile
   __shared__ uint4 ks[BUFS][kPlanes<T> * BN * PPR], vs[BUFS][kPlanes<T> * BN * PPR];
+  __shared__ int scrubbed[WAVES];  // whether the wave found infinities or NaN in values of edge tiles
 
   // a tile's splits follow one another (nsplit is a power of two)
   const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
@@ -144,7 +145,19 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       vr[n] = load_piece<T>(vbuf, voff[n]);
     }
   };
-  auto store = [&](int buf) {
+  // Edge tiles hold keys that some row of the workgroup does not see: their
+  // values that are not finite go into LDS as zeros, and reach the rows that
+  // see them after the loop.
+  const int edge_hi = a.right >= 0 ? min(div_group(a, sp.r0) + shift + a.right + 1, key_end) : key_end;
+  const int edge_lo = a.left >= 0 ? div_group(a, min(sp.r0 + BM, rows) - 1) + shift - a.left : 0;
+  auto is_edge = [&](int jb) { return wg.lo + (jb + 1) * BN > edge_hi || wg.lo + jb * BN < edge_lo; };
+  auto store = [&](int buf, int jb) {
+    if (is_edge(jb)) {
+      bool met = false;
+#pragma unroll
+      for (int n = 0; n < NL; ++n) met |= scrub<T>(vr[n]);
+      if (__any(met)) scrubbed[wave] = 1;
+    }
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
       const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
@@ -163,12 +176,13 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
 
   if (jb0 < jb1) {
     load(jb0);
-    if constexpr (BUFS == 2) store(0);
+    scrubbed[wave] = 0;
+    if constexpr (BUFS == 2) store(0, jb0);
   }
   for (int jb = jb0; jb < jb1; ++jb) {
     __syncthreads();
     if constexpr (BUFS == 1) {
-      store(0);
+      store(0, jb);
       __syncthreads();
     }
     if (jb + 1 < jb1) load(jb + 1);
@@ -231,9 +245,31 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       }
       settle();
     }
-    if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1);
+    if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1, jb + 1);
   }
 
+  if (jb0 < jb1) {
+    int met = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) met |= scrubbed[w];  // (a barrier has passed since the last was set)
+    if (__builtin_amdgcn_readfirstlane(met)) {
+      for (int jb = jb0; jb < jb1; ++jb) {
+        if (!is_edge(jb)) continue;
+        const int j1 = min(wg.lo + (jb + 1) * BN, lane_hi);
+        for (int j = max(wg.lo + jb * BN, lane_lo); has_row && j < j1; ++j) {
+          const T* src = vbase + j * a.v_row;
+#pragma unroll
+          for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int d = db * 32 + 4 * half + c_row(i);
+              const float x = d < a.dim ? to_f32(src[d]) : 0.f;
+              acc[db][i] += fabsf(x) < INFINITY ? 0.f : x;
+            }
+        }
+      }
+    }
+  }
   const float sum = halves_sum(l);
   if (!has_row) return;
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // a NaN stays one

@@ -116,9 +116,10 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   if (has_row) {
     const float v = a.lse[row_out];
     lse2 = v == -INFINITY ? INFINITY : v * kLog2e - kShift<T>;
-    // for the other kernel, in the order in which it walks the rows
+    // for the other kernel, in the order in which it walks the rows; a D that
+    // is not finite makes NaN of both
     if (half == 0 && split == 0)
-      stats[static_cast<int64_t>(kvh) * a.total_q * a.group + static_cast<int64_t>(sp.q0) * a.group + r] = make_float2(lse2, dot);
+      stats[static_cast<int64_t>(kvh) * a.total_q * a.group + static_cast<int64_t>(sp.q0) * a.group + r] = make_float2(__builtin_fmaf(0.f, dot, lse2), dot);
   }
   const int place = tok + shift;
   const int lane_lo = a.left >= 0 ? place - a.left : 0;
@@ -162,7 +163,15 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   float factor = kFirstFactor;
   const float c = a.scale * kLog2e;
 
-  auto store = [&](int buf) {
+  // Keys that some row of the workgroup does not see go into LDS with their
+  // infinities and NaN as zeros: rows that do see them have a NaN lse.
+  const int edge_hi = a.right >= 0 ? min(div_group(a, sp.r0) + shift + a.right + 1, sp.nk) : sp.nk;
+  const int edge_lo = a.left >= 0 ? div_group(a, min(sp.r0 + BM, rows) - 1) + shift - a.left : 0;
+  auto store = [&](int buf, int jb) {
+    if (wg.lo + (jb + 1) * BN > edge_hi || wg.lo + jb * BN < edge_lo) {
+#pragma unroll
+      for (int n = 0; n < NL; ++n) scrub<T>(kr[n]);
+    }
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
       const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
@@ -174,12 +183,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   };
   if (jb0 < jb1) {
     load(jb0);
-    if constexpr (BUFS == 2) store(0);
+    if constexpr (BUFS == 2) store(0, jb0);
   }
   for (int jb = jb0; jb < jb1; ++jb) {
     __syncthreads();
     if constexpr (BUFS == 1) {
-      store(0);
+      store(0, jb);
       __syncthreads();
     }
     if (jb + 1 < jb1) load(jb + 1);
@@ -213,7 +222,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       mma_transposed<T, DP, DB, BN>(ks[buf], 32 * b, lane, ds, acc);
       settle();
     }
-    if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1);
+    if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1, jb + 1);
   }
 
   if (!has_row) return;
@@ -325,7 +334,19 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
       }
     }
   };
-  auto store = [&](int buf) {
+  // Rows that do not see every key of the workgroup go into LDS with their
+  // infinities and NaN as zeros: the keys that they do see get NaN from their
+  // lse (q) or D (grad_out, through the lse too: see the statistics).
+  auto store = [&](int buf, int rb) {
+    const int r0 = f_lo + rb * BN;
+    const int p0 = div_group(a, r0) + shift, p1 = div_group(a, min(r0 + BN, rows) - 1) + shift;
+    if ((a.right >= 0 && kt1 - 1 > p0 + a.right) || (a.left >= 0 && sp.r0 < p1 - a.left)) {
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        scrub<T>(qr[n]);
+        scrub<T>(gr[n]);
+      }
+    }
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
       const int slot = tid + n * NT, row = slot / PPR, piece = slot % PPR;
@@ -356,12 +377,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
 
   if (rb0 < rb1) {
     load(rb0);
-    if constexpr (BUFS == 2) store(0);
+    if constexpr (BUFS == 2) store(0, rb0);
   }
   for (int rb = rb0; rb < rb1; ++rb) {
     __syncthreads();
     if constexpr (BUFS == 1) {
-      store(0);
+      store(0, rb);
       __syncthreads();
     }
     if (rb + 1 < rb1) load(rb + 1);
@@ -412,7 +433,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
       mma_transposed<T, DP, DB, BN>(qs[buf], 32 * b, lane, ds, dk);
       settle();
     }
-    if (BUFS == 2 && rb + 1 < rb1) store(buf ^ 1);
+    if (BUFS == 2 && rb + 1 < rb1) store(buf ^ 1, rb + 1);
   }
 
   if (!has_key) return;

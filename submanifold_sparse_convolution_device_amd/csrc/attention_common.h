@@ -109,6 +109,26 @@ __device__ __forceinline__ Raw<T> load_piece(const T* src, bool on) {
   return r;
 }
 
+// Sets the infinities and NaN of a piece to zero and returns whether there
+// were any.  For rows that some of a tile's columns do not see: in a matrix
+// product even a factor of zero would make NaN of them.
+template <class T>
+__device__ __forceinline__ bool scrub(Raw<T>& r) {
+  constexpr uint32_t top = sizeof(T) == 4 ? 0x7f800000u : __is_same(T, _Float16) ? 0x7c007c00u : 0x7f807f80u;  // exponents
+  constexpr uint32_t carry = sizeof(T) == 4 ? 0x00800000u : __is_same(T, _Float16) ? 0x04000400u : 0x00800080u;
+  uint32_t any = 0;
+  auto clean = [&](uint32_t w) {
+    // an exponent of ones carries into the sign's place
+    const uint32_t bad = ((w & top) + carry) & (sizeof(T) == 4 ? 0x80000000u : 0x80008000u);
+    any |= bad;
+    return w & ~(sizeof(T) == 4 ? static_cast<uint32_t>(static_cast<int32_t>(bad) >> 31) : (bad >> 15) * 0xffffu);
+  };
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+    r.v[i] = make_uint4(clean(r.v[i].x), clean(r.v[i].y), clean(r.v[i].z), clean(r.v[i].w));
+  return any != 0;
+}
+
 // A piece as an operand: one register quad per plane.
 template <class T>
 struct Frag {

@@ -208,6 +208,61 @@ def test_other_sequences_values_do_not_leak(sp, dtype):
     assert bool(torch.isnan(out[33:73]).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [32, 72, 128])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("n", [40, 200])
+def test_hidden_values_do_not_leak(sp, dtype, dim, value, n):
+    """A value that is not finite in one row reaches the queries that see the
+    row, in its own column, and no other ones: forward (v), and of the
+    gradients those of rows that neither see it nor are seen by it."""
+    cu = ref.offsets([n])
+    host, dev, grad = _inputs(dim, n, n, 2, 1, dim, dtype)
+    at, c = n - 7, cu.to(DEV)
+    clean = ref.attention(*host, cu, cu, causal=True, window=(12, 0), grad=grad)
+    how = dict(causal=True, window=(12, 0))
+    v = dev[2].clone()
+    v[at, 0, 5] = value
+    out = sp.attention(dev[0], dev[1], v, c, **how)
+    sees = torch.zeros(n, dtype=torch.bool)
+    sees[at:min(n, at + 13)] = True
+    _near("out", out[~sees.to(DEV)], clean["out"][~sees], clean["out_tol"][~sees])
+    got = out[sees.to(DEV)].double().cpu()
+    assert bool(torch.isnan(got[:, :, 5]).all() if math.isnan(value) else (got[:, :, 5] == value).all())
+    others = [i for i in range(dim) if i != 5]
+    assert bool(torch.isfinite(got[:, :, others]).all())
+    # gradients: a key, and a query's output gradient
+    out, lse = sp.attention(*dev, c, return_lse=True, **how)
+    k = dev[1].clone()
+    k[at] = value
+    bad_out, bad_lse = sp.attention(dev[0], k, dev[2], c, return_lse=True, **how)
+    gq, gk, gv = sp.attention_backward(grad.to(DEV), dev[0], k, dev[2], bad_out, bad_lse, c, **how)
+    apart = torch.arange(n) < at - 12  # keys that no query in sight of the bad one sees
+    _near("grad_q", gq[:at], clean["grad_q"][:at], clean["grad_q_tol"][:at])
+    _near("grad_k", gk[apart.to(DEV)], clean["grad_k"][apart], clean["grad_k_tol"][apart])
+    _near("grad_v", gv[apart.to(DEV)], clean["grad_v"][apart], clean["grad_v_tol"][apart])
+    g = grad.to(DEV).clone()
+    g[at, 1, 3] = value
+    gq, gk, gv = sp.attention_backward(g, *dev, out, lse, c, **how)
+    seen_by = torch.zeros(n, dtype=torch.bool)
+    seen_by[at - 12:at + 1] = True
+    rest = torch.arange(n) != at
+    _near("grad_q", gq[rest.to(DEV)], clean["grad_q"][rest], clean["grad_q_tol"][rest])
+    _near("grad_k", gk[~seen_by.to(DEV)], clean["grad_k"][~seen_by], clean["grad_k_tol"][~seen_by])
+    _near("grad_v", gv[~seen_by.to(DEV)], clean["grad_v"][~seen_by], clean["grad_v_tol"][~seen_by])
+    assert not bool(torch.isfinite(gv[seen_by.to(DEV), 0, 3]).any())
+    assert not bool(torch.isfinite(gk[seen_by.to(DEV)]).any())
+
+
+def test_tiles_in_order_of_work(sp):
+    """Lengths and sizes for which the tiles are sorted by work first."""
+    lengths = [2400, 1, 0, 130]
+    cu = ref.offsets(lengths)
+    n = int(cu[-1])
+    host, dev, grad = _inputs(13, n, n, 8, 8, 64, "f32")
+    _check(sp, host, dev, grad, cu, cu)
+
+
 def test_offsets_that_break_the_rules_stay_inside(sp):
     """Decreasing, negative and too large offsets: no access outside the
     tensors (the call returns; its rows mean nothing)."""
