@@ -5,9 +5,9 @@ import os
 
 import pytest
 
-import sanitized_build
 import submanifold_sparse_convolution_device_amd as sp
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 1 << 20  # never dereferenced: every case fails validation first
 
 
@@ -122,7 +122,7 @@ def test_struct_mirrors_have_the_c_sizes():
         with open(os.path.join(d, "t.c"), "w") as f:
             f.write(src)
         exe = os.path.join(d, "t")
-        subprocess.run(["gcc", "-I", os.path.join(sanitized_build.ROOT, "include"), "-o", exe, os.path.join(d, "t.c")], check=True)
+        subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), "-o", exe, os.path.join(d, "t.c")], check=True)
         got = subprocess.run([exe], capture_output=True, text=True, check=True).stdout.splitlines()
     for n, line in zip(names, got):
         cls = getattr(sp, n)
@@ -138,3 +138,25 @@ def test_packed_arguments_have_the_structs_layout():
         got = cls.from_buffer_copy(pack.pack(*values))
         assert pack.size == ctypes.sizeof(cls)
         assert [getattr(got, f) for f, _ in cls._fields_] == values
+
+
+def test_entry_points_under_sanitizers():
+    """This file's tests against the library's host code built with
+    AddressSanitizer and UndefinedBehaviorSanitizer."""
+    import subprocess
+    import sys
+    if os.environ.get("SPCONV_LIB_PATH"):
+        pytest.skip("already in the sanitized run")
+    sanitized_build = pytest.importorskip("sanitized_build")
+    runtime = sanitized_build.clang_asan_runtime()
+    if not runtime or not os.path.exists(sanitized_build.HIPCC):
+        pytest.skip("no hipcc or clang ASan runtime")
+    env = dict(os.environ, LD_PRELOAD=runtime, SPCONV_LIB_PATH=sanitized_build.build_library(),
+               ASAN_OPTIONS="detect_leaks=0:abort_on_error=0:halt_on_error=1",
+               UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
+    r = subprocess.run([sys.executable, "-m", "pytest", os.path.basename(__file__), "-q", "-x", "-s", "-p", "no:cacheprovider",
+                        "--deselect", "test_attention_abi_host.py::test_struct_mirrors_have_the_c_sizes"],
+                       cwd=os.path.dirname(os.path.abspath(__file__)), env=env, capture_output=True, text=True, timeout=900)
+    out = r.stdout + r.stderr
+    assert "runtime error" not in out and "ERROR: AddressSanitizer" not in out, out[-4000:]
+    assert r.returncode == 0 and " passed" in out, out[-4000:]
