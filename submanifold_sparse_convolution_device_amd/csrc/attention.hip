@@ -271,33 +271,16 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     }
   }
   const float sum = halves_sum(l);
-  if (!has_row) return;
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // a NaN stays one
   const float lse = sum == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
   const int64_t row_out = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
   if (nsplit == 1 && (WAVES > 1 || part_row < 0)) {
-    if (half == 0) a.lse[row_out] = lse;
-    T* dst = static_cast<T*>(a.out) + row_out * a.dim;
-#pragma unroll
-    for (int db = 0; db < DB; ++db)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int d = db * 32 + 8 * g + 4 * half;
-        if (d < a.dim)
-          store4<T>(dst + d, acc[db][4 * g] * inv, acc[db][4 * g + 1] * inv, acc[db][4 * g + 2] * inv, acc[db][4 * g + 3] * inv);
-      }
+    if (has_row && half == 0) a.lse[row_out] = lse;
+    store_row<T, DB>(static_cast<T*>(a.out) + row_out * a.dim, acc, inv, half, a.dim, has_row);
   } else {
     const int64_t at_out = WAVES == 1 && part_row >= 0 ? part_row + r : static_cast<int64_t>(split) * a.total_q * a.heads + row_out;
-    if (half == 0) part_lse[at_out] = lse;
-    float* dst = part_out + at_out * a.dim;
-#pragma unroll
-    for (int db = 0; db < DB; ++db)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int d = db * 32 + 8 * g + 4 * half;
-        if (d < a.dim)
-          store4<float>(dst + d, acc[db][4 * g] * inv, acc[db][4 * g + 1] * inv, acc[db][4 * g + 2] * inv, acc[db][4 * g + 3] * inv);
-      }
+    if (has_row && half == 0) part_lse[at_out] = lse;
+    store_row<float, DB>(part_out + at_out * a.dim, acc, inv, half, a.dim, has_row);
   }
 }
 

@@ -225,20 +225,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1, jb + 1);
   }
 
-  if (!has_row) return;
   const float mul = __is_same(T, _Float16) ? a.scale / factor * 6.103515625e-05f : a.scale;
-  float* pdst = part + (static_cast<int64_t>(split) * a.total_q * a.heads + row_out) * a.dim;
-  T* dst = static_cast<T*>(a.grad_q) + static_cast<int64_t>(sp.q0 + tok) * a.gq_row + static_cast<int64_t>(head) * a.gq_head;
-#pragma unroll
-  for (int db = 0; db < DB; ++db)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int d = db * 32 + 8 * g + 4 * half;
-      if (d >= a.dim) continue;
-      const float x = acc[db][4 * g] * mul, y = acc[db][4 * g + 1] * mul, z = acc[db][4 * g + 2] * mul, w = acc[db][4 * g + 3] * mul;
-      if (nsplit == 1) store4<T>(dst + d, x, y, z, w);
-      else store4<float>(pdst + d, x, y, z, w);
-    }
+  if (nsplit == 1)
+    store_row<T, DB>(static_cast<T*>(a.grad_q) + static_cast<int64_t>(sp.q0 + tok) * a.gq_row + static_cast<int64_t>(head) * a.gq_head, acc, mul,
+                     half, a.dim, has_row);
+  else
+    store_row<float, DB>(part + (static_cast<int64_t>(split) * a.total_q * a.heads + row_out) * a.dim, acc, mul, half, a.dim, has_row);
 }
 
 template <class T, int DP, int DQ, int WAVES>
@@ -436,28 +428,16 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
     if (BUFS == 2 && rb + 1 < rb1) store(buf ^ 1, rb + 1);
   }
 
-  if (!has_key) return;
   constexpr float unshift = __is_same(T, _Float16) ? 6.103515625e-05f : 1.f;  // 2^-14
   const float mul = __is_same(T, _Float16) ? a.scale / factor * unshift : a.scale;
-  const int64_t at = (static_cast<int64_t>(split) * a.total_k * a.kv_heads + krow * a.kv_heads + kvh) * a.dim;
-  T* kdst = static_cast<T*>(a.grad_k) + krow * a.gk_row + static_cast<int64_t>(kvh) * a.gk_head;
-  T* vdst = static_cast<T*>(a.grad_v) + krow * a.gv_row + static_cast<int64_t>(kvh) * a.gv_head;
-#pragma unroll
-  for (int db = 0; db < DB; ++db)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int d = db * 32 + 8 * g + 4 * half;
-      if (d >= a.dim) continue;
-      const float x = dk[db][4 * g] * mul, y = dk[db][4 * g + 1] * mul, z = dk[db][4 * g + 2] * mul, w = dk[db][4 * g + 3] * mul;
-      const float x2 = dv[db][4 * g] * unshift, y2 = dv[db][4 * g + 1] * unshift, z2 = dv[db][4 * g + 2] * unshift, w2 = dv[db][4 * g + 3] * unshift;
-      if (nsplit == 1) {
-        store4<T>(kdst + d, x, y, z, w);
-        store4<T>(vdst + d, x2, y2, z2, w2);
-      } else {
-        store4<float>(part_k + at + d, x, y, z, w);
-        store4<float>(part_v + at + d, x2, y2, z2, w2);
-      }
-    }
+  if (nsplit == 1) {
+    store_row<T, DB>(static_cast<T*>(a.grad_k) + krow * a.gk_row + static_cast<int64_t>(kvh) * a.gk_head, dk, mul, half, a.dim, has_key);
+    store_row<T, DB>(static_cast<T*>(a.grad_v) + krow * a.gv_row + static_cast<int64_t>(kvh) * a.gv_head, dv, unshift, half, a.dim, has_key);
+  } else {
+    const int64_t at = (static_cast<int64_t>(split) * a.total_k * a.kv_heads + krow * a.kv_heads + kvh) * a.dim;
+    store_row<float, DB>(part_k + at, dk, mul, half, a.dim, has_key);
+    store_row<float, DB>(part_v + at, dv, unshift, half, a.dim, has_key);
+  }
 }
 
 // One tensor's partial gradients: [nsplit][rows][heads][dim].

@@ -545,6 +545,44 @@ __device__ __forceinline__ void store4(T* dst, float x, float y, float z, float 
   *reinterpret_cast<tx4*>(dst) = v;
 }
 
+// Stores a lane's column of C tiles as a row of T, 8 consecutive values at a
+// time: the halves exchange registers so that each holds whole pieces (half
+// 0 those of columns 16 i, half 1 those of 16 i + 8), two for one of four.
+template <class T, int DB>
+__device__ __forceinline__ void store_row(T* dst, const floatx16 (&acc)[DB], float mul, int half, int dim, bool on) {
+  typedef T tx4 __attribute__((ext_vector_type(4)));
+  constexpr int W = sizeof(T);  // words of 4 values
+  struct Words {
+    uint32_t w[W];
+  };
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Words q[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        tx4 v;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = static_cast<T>(acc[db][8 * i + 4 * g + u] * mul);
+        q[g] = __builtin_bit_cast(Words, v);
+      }
+      uint32_t piece[2 * W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const auto r = __builtin_amdgcn_permlane32_swap(q[0].w[w], q[1].w[w], false, false);
+        piece[w] = r[0];
+        piece[W + w] = r[1];
+      }
+      const int d = db * 32 + 16 * i + 8 * half;
+      if (on && d < dim) {
+#pragma unroll
+        for (int w = 0; w < 2 * W; w += 4)
+          *reinterpret_cast<uint4*>(reinterpret_cast<char*>(dst + d) + 4 * w) = make_uint4(piece[w], piece[w + 1], piece[w + 2], piece[w + 3]);
+      }
+    }
+}
+
 // Calls f(type, DP, DQ): the head size rounded up to 32 (the blocks of the
 // products that end in it) and to 16 (the steps of those over it).
 template <class F>
