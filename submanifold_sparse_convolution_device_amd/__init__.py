@@ -405,28 +405,19 @@ def _stream() -> int:
     return int(_torch().cuda.current_stream().cuda_stream)
 
 
-class _Call:
-    """The device of a call made current, and torch's current stream on it:
-    what :class:`_OnDevice` and :func:`_stream` do, at a tenth of the host time
-    (the stream's handle without a stream object)."""
-
-    __slots__ = ("idx", "prev")
-
-    def __init__(self, idx: int):
-        self.idx = idx
-
-    def __enter__(self) -> int:
-        cuda = _TORCH.cuda
-        cur = cuda.current_device()
-        self.prev = -1
-        if cur != self.idx:
-            self.prev = cur
-            cuda.set_device(self.idx)
-        return _TORCH._C._cuda_getCurrentRawStream(self.idx)
-
-    def __exit__(self, *exc):
-        if self.prev >= 0:
-            _TORCH.cuda.set_device(self.prev)
+def _run(device: int, call, *args) -> None:
+    """call(*args, stream) with ``device`` current, on torch's current stream
+    there, and its status checked: what :class:`_OnDevice` and :func:`_stream`
+    do, at a tenth of the host time (the stream's handle without a stream
+    object)."""
+    C = _TORCH._C
+    if C._cuda_getDevice() == device:
+        rc = call(*args, C._cuda_getCurrentRawStream(device))
+    else:
+        with _TORCH.cuda.device(device):
+            rc = call(*args, C._cuda_getCurrentRawStream(device))
+    if rc:
+        _check(rc)
 
 
 _TORCH = None
@@ -920,10 +911,7 @@ def attention(q, k, v, cu_q, cu_k=None, *, causal: bool = False, window=(-1, -1)
     elif not (out.get_device() == q.get_device() and out.is_contiguous() and out.dtype is q.dtype and out.shape == q.shape):
         raise SpconvError(1, "out must be a contiguous [total_q, heads, head_dim] tensor of the dtype")
     lse = q.new_empty(q.shape[:2], dtype=torch.float32)
-    with _Call(q.get_device()) as stream:
-        rc = L.spconv_attention_forward(a, out.data_ptr(), lse.data_ptr(), stream)
-        if rc:
-            _check(rc)
+    _run(q.get_device(), L.spconv_attention_forward, a, out.data_ptr(), lse.data_ptr())
     return (out, lse) if return_lse else out
 
 
@@ -945,10 +933,7 @@ def attention_backward(grad_out, q, k, v, out, lse, cu_q, cu_k=None, *, causal: 
                                        *_heads_tensor("grad_q", grads[0], q, q.shape),
                                        *_heads_tensor("grad_k", grads[1], q, k.shape),
                                        *_heads_tensor("grad_v", grads[2], q, v.shape))
-    with _Call(q.get_device()) as stream:
-        rc = L.spconv_attention_backward(a, out.data_ptr(), lse.data_ptr(), g, stream)
-        if rc:
-            _check(rc)
+    _run(q.get_device(), L.spconv_attention_backward, a, out.data_ptr(), lse.data_ptr(), g)
     return tuple(grads)
 
 
@@ -958,10 +943,9 @@ def attention_backward(grad_out, q, k, v, out, lse, cu_q, cu_k=None, *, causal: 
 def rotary_table(extent: int, pairs: int, base: float = 10000.0, position_scale: float = 1.0, device="cuda"):
     """Cosines and sines [extent, pairs, 2] (fp32) of the angles
     position * position_scale * base ** (-i / pairs), i < pairs."""
-    torch, _ = _bind()
+    torch, L = _bind()
     table = torch.empty((int(extent), int(pairs), 2), dtype=torch.float32, device=device)
-    with _Call(table.get_device()) as stream:
-        spconv_rotary_table(table.data_ptr(), int(extent), int(pairs), base, position_scale, stream)
+    _run(table.get_device(), L.spconv_rotary_table, table.data_ptr(), int(extent), int(pairs), float(base), float(position_scale))
     return table
 
 
@@ -1037,10 +1021,7 @@ def norm_rotary(q, k, q_weight=None, k_weight=None, table=None, positions=None, 
                None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format))
     qo = _NO_TENSOR if q is None else _heads_tensor("q_out", out[0], like, q.shape)
     ko = _NO_TENSOR if k is None else _heads_tensor("k_out", out[1], like, k.shape)
-    with _Call(like.get_device()) as stream:
-        rc = L.spconv_norm_rotary_forward(a, *qo, *ko, stream)
-        if rc:
-            _check(rc)
+    _run(like.get_device(), L.spconv_norm_rotary_forward, a, *qo, *ko)
     return tuple(out)
 
 
@@ -1069,8 +1050,5 @@ def norm_rotary_backward(grad_q_out, grad_k_out, q, k, q_weight=None, k_weight=N
     (gqo, gko), (gq, gk) = given, made
     g = _PACK_NORM_ROTARY_GRADIENTS.pack(gqo[0], gko[0], *gqo[1:], *gko[1:], gq[0], gk[0], *gq[1:], *gk[1:],
                                          *(0 if w is None else w.data_ptr() for w in weights))
-    with _Call(like.get_device()) as stream:
-        rc = L.spconv_norm_rotary_backward(a, g, stream)
-        if rc:
-            _check(rc)
+    _run(like.get_device(), L.spconv_norm_rotary_backward, a, g)
     return grads[0], grads[1], weights[0], weights[1]
