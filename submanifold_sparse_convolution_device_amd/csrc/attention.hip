@@ -296,17 +296,27 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* 
   const int quads = a.dim / 4, groups = 256 / quads, g = static_cast<int>(threadIdx.x) / quads, quad = static_cast<int>(threadIdx.x) - g * quads;
   float top = -INFINITY, sum = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (g < groups) {
-    for (int p = g; p < parts; p += groups) top = fmaxf(top, part_lse[first + p * step]);
-    for (int p = g; p < parts; p += groups) {
-      const float ls = part_lse[first + p * step];
-      const float4 o = *reinterpret_cast<const float4*>(part_out + (first + p * step) * a.dim + 4 * quad);
-      const float e = ls == -INFINITY ? 0.f : fast_exp2((ls - top) * kLog2e);
-      sum += e;
-      x.x += e * o.x;
-      x.y += e * o.y;
-      x.z += e * o.z;
-      x.w += e * o.w;
+  constexpr int kBatch = 4;  // parts whose loads are issued together
+  for (int p0 = g; g < groups && p0 < parts; p0 += kBatch * groups) {
+    float ls[kBatch];
+    float4 o[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t row = first + min(p0 + i * groups, parts - 1) * step;
+      ls[i] = part_lse[row];
+      o[i] = *reinterpret_cast<const float4*>(part_out + row * a.dim + 4 * quad);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (p0 + i * groups >= parts || ls[i] == -INFINITY) continue;
+      const float now = fmaxf(top, ls[i]);
+      const float keep = fast_exp2((top - now) * kLog2e), e = fast_exp2((ls[i] - now) * kLog2e);
+      top = now;
+      sum = sum * keep + e;
+      x.x = x.x * keep + e * o[i].x;
+      x.y = x.y * keep + e * o[i].y;
+      x.z = x.z * keep + e * o[i].z;
+      x.w = x.w * keep + e * o[i].w;
     }
   }
   acc_s[threadIdx.x] = x;
