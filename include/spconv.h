@@ -519,10 +519,16 @@ spconv_status spconv_select_dataflow(const void* d_feats, const void* d_weights,
  * output.  out is contiguous [total_q][heads][head_dim], lse
  * fp32 [total_q][heads].
  *
+ * Infinities and NaN of a key or value row reach only the queries that see the
+ * row, and those of a query or output gradient only the gradients of keys that
+ * it sees.
+ *
  * Scores, softmax statistics and all sums are fp32.  F16 and BF16 round the
  * probabilities (and the score gradients) to the dtype as operands of the
- * matrix instructions; results are rounded once, to nearest even.  Every sum
- * has a fixed order: the same call gives the same bits.
+ * matrix instructions; F32 operands are used whole (split exactly into three
+ * bf16 parts each, the products down to 2^-24 of each other summed in fp32).
+ * Results are rounded once, to nearest even.  Every sum has a fixed order: the
+ * same call gives the same bits.
  */
 typedef struct spconv_attention {
   const void* q;

@@ -19,6 +19,9 @@
 // products that reach 2^-24 of it, summed in fp32:
 //   hi hi + (hi mid + mid hi) + (hi lo + mid mid + lo hi);
 // what is left out is below 2^-23 of |a b|, the size of an fp32 rounding.
+// Against products on the fp32 matrix unit: a band of 200 rows over heads of
+// 40 takes 29 us instead of 40, frames of 24 channels with gradients 104
+// instead of 143, both as near to 64 bits as before.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -412,7 +415,9 @@ __device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
 //   L2 while the tiles of a long sequence walk them.
 //   Runs of slots: an XCD takes `run` consecutive slots with all their heads.
 //   Rows shorter than a 128-byte line share it with the next head, so that
-//   heads on different XCDs would each fetch it.
+//   heads on different XCDs would each fetch it: with 64-byte rows (1200
+//   windows, 8 heads of 32) the gradients take 308 and 234 us instead of 331
+//   and 264, and HBM reads fall to what there is to read.
 struct Place {
   int slot, kvh;
 };
@@ -507,8 +512,10 @@ __device__ __forceinline__ void order_slots(const AttentionArgs& a, const OrderJ
     if (at < job.slots) job.order[at] = slot;
   }
 }
-// Whether the sort, about 5 us, pays: few rounds of workgroups, and enough
+// Whether the sort, about 4 us, pays: few rounds of workgroups, and enough
 // work (multiply-adds of one product, `products` of them) for them to last.
+// Causal sequences of up to 4096 rows with gradients: 173 and 124 us instead
+// of 220 and 141; frames of 500 to 4000 rows, forward: 157 instead of 180.
 inline bool order_pays(const AttentionArgs& a, int64_t slots, int split, double products) {
   const int64_t groups = slots * a.kv_heads * split;
   double work = static_cast<double>(a.total_q) * a.heads * (static_cast<double>(a.total_k) / std::max(a.batch, 1)) * a.dim * products;
