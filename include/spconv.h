@@ -521,7 +521,8 @@ spconv_status spconv_select_dataflow(const void* d_feats, const void* d_weights,
  *
  * Infinities and NaN of a key or value row reach only the queries that see the
  * row, and those of a query or output gradient only the gradients of keys that
- * it sees.
+ * it sees.  An infinite value gives an infinite output (in F16, NaN where the
+ * probability rounds to zero); F32 scores of an infinite query or key are NaN.
  *
  * Scores, softmax statistics and all sums are fp32.  F16 and BF16 round the
  * probabilities (and the score gradients) to the dtype as operands of the

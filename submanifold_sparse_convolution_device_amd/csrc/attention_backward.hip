@@ -171,8 +171,10 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const float c = a.scale * kLog2e;
 
   // Keys that some row of the workgroup does not see go into LDS with their
-  // infinities and NaN as zeros: rows that do see them have a NaN lse.
-  const int edge_hi = a.right >= 0 ? min(div_group(a, sp.r0) + shift + a.right + 1, sp.nk) : sp.nk;
+  // infinities and NaN as zeros: rows that do see them have a NaN lse.  What
+  // lies past the sequence's end is zero as loaded, unless the rows repeat one.
+  const int edge_end = a.k_row != 0 ? INT_MAX : sp.nk;
+  const int edge_hi = a.right >= 0 ? min(div_group(a, sp.r0) + shift + a.right + 1, edge_end) : edge_end;
   const int edge_lo = a.left >= 0 ? div_group(a, min(sp.r0 + BM, rows) - 1) + shift - a.left : 0;
   auto store = [&](int buf, int jb) {
     if (wg.lo + (jb + 1) * BN > edge_hi || wg.lo + jb * BN < edge_lo) {

@@ -209,6 +209,32 @@ def test_other_sequences_values_do_not_leak(sp, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n", [3, 40, 150])
+def test_one_row_repeated(sp, dtype, n):
+    """Keys and values that repeat one row (row stride 0), an infinity in it:
+    every query gets that row, whatever tiles the sequence ends in."""
+    cu = ref.offsets([n]).to(DEV)
+    host, dev, grad = _inputs(n, n, 1, 2, 2, 48, dtype)
+    k = dev[1].expand(n, 2, 48)
+    v = dev[2].clone()
+    v[0, 1, 5] = math.inf
+    v = v.expand(n, 2, 48)
+    assert k.stride(0) == 0 and v.stride(0) == 0
+    out, lse = sp.attention(dev[0], k, v, cu, return_lse=True)
+    # equal scores: weights 1 / n each, in one order of sums (and the rounding to dtype, at most |v| eps)
+    eps = torch.finfo(DT[dtype]).eps
+    bound = (4 * eps + 2.0 ** -20) * host[2].double().abs().expand(n, 2, 48) + 1e-30
+    want = v.double().cpu()
+    _near("out", out, want, torch.where(torch.isinf(want), 1.0, bound))
+    # a key with an infinity: no query's gradient is finite where its scores are not, and none hangs on it elsewhere
+    bad = dev[1].clone()
+    bad[0, 0, 7] = math.inf
+    o, l = sp.attention(dev[0], bad.expand(n, 2, 48), dev[2].expand(n, 2, 48), cu, return_lse=True)
+    gq, _, _ = sp.attention_backward(grad.to(DEV), dev[0], bad.expand(n, 2, 48), dev[2].expand(n, 2, 48), o, l, cu)
+    assert bool(torch.isfinite(gq[:, 1]).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("dim", [32, 72, 128])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("n", [40, 200])
