@@ -10,9 +10,9 @@
 // exponential takes two slots) beside DP / 4 matrix ones, so heads of 32 are
 // bound by the vector unit and heads of 128 by how the two units overlap.
 // Measured: 4 sequences of up to 8192 rows, 16 heads of 128 over 4 key heads,
-// causal bf16, 0.90 TFLOP of visible pairs: 1016 us, 886 TFLOP/s (matrix unit
+// causal bf16, 0.90 TFLOP of visible pairs: 1000 us, 900 TFLOP/s (matrix unit
 // 47% busy, vector unit 46%); 8 frames of up to 4000 rows, 8 heads of 32, f16:
-// 144 us, 507 TFLOP/s (vector unit 75% busy).
+// 140 us, 522 TFLOP/s (vector unit 75% busy).
 //
 // A query tile is 32 rows per wave, the wave's columns in every product: its
 // softmax needs one exchange between the lane halves and no LDS.  Computing

@@ -15,7 +15,7 @@
 // unit for long sequences (causal f16, 14.6k rows, 8 heads of 64 over 2: 125
 // and 180 us for the 10 products' 0.12 TFLOP), and by the latency of each
 // workgroup's few dependent loads for short ones (1200 windows of up to 343
-// rows, 8 heads of 32, bf16: 227 and 305 us, of which 138 and 129 us remain
+// rows, 8 heads of 32, bf16: 222 and 300 us, of which 138 and 129 us remain
 // when no tile is walked; the bytes alone would take 125 and 124).
 #include <hip/hip_runtime.h>
 
