@@ -11,8 +11,8 @@
 // bound by the vector unit and heads of 128 by how the two units overlap.
 // Measured: 4 sequences of up to 8192 rows, 16 heads of 128 over 4 key heads,
 // causal bf16, 0.90 TFLOP of visible pairs: 1000 us, 900 TFLOP/s (matrix unit
-// 47% busy, vector unit 46%); 8 frames of up to 4000 rows, 8 heads of 32, f16:
-// 140 us, 522 TFLOP/s (vector unit 75% busy).
+// 42% busy, vector unit 41%); 8 frames of up to 4000 rows, 8 heads of 32, f16:
+// 140 us, 522 TFLOP/s (vector unit 83% busy).
 //
 // A query tile is 32 rows per wave, the wave's columns in every product: its
 // softmax needs one exchange between the lane halves and no LDS.  Computing
