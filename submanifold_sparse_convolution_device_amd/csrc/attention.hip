@@ -347,9 +347,10 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* 
   sum = 0.f;
   x = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int q = 0; q < groups; ++q) {
-    const float t = top_s[q * quads + quad];
-    if (t == -INFINITY) continue;
-    const float e = fast_exp2((t - all) * kLog2e);
+    // A group without parts has a sum of 0.  (Its maximum does not tell: parts
+    // whose lse is NaN leave that at -inf as well, and must reach the row.)
+    if (sum_s[q * quads + quad] == 0.f) continue;
+    const float e = fast_exp2((top_s[q * quads + quad] - all) * kLog2e);
     const float4 o = acc_s[q * quads + quad];
     sum += e * sum_s[q * quads + quad];
     x.x += e * o.x;
