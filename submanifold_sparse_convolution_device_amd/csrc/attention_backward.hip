@@ -326,7 +326,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
       const int r = r0 + tid + n * NT;
       lse_r[n] = INFINITY;
       delta_r[n] = 0.f;
-      place_r[n] = 0;
+      place_r[n] = INT_MIN;
       if (tid + n * NT < BN && r < rows) {
         const float2 st = sbase[r];
         lse_r[n] = st.x;
@@ -413,10 +413,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && DP <= 64 ? 2 : 1) voi
         }
       }
       const bool cut_hi = a.right >= 0 && kw1 > p0 + a.right, cut_lo = a.left >= 0 && kw0 < p1 - a.left;
-      if (cut_hi || cut_lo) {
+      if (cut_hi || cut_lo || r0 + 32 > rows) {
         keep_branch();
-        // places from first to last see the key
-        const int first = cut_hi ? key - a.right : INT_MIN, last = cut_lo ? key + a.left : INT_MAX;
+        // places from first to last see the key; rows past the end stand below
+        // all: their scores with a key that is not finite are NaN (of a
+        // zero), which their lse of +inf does not take out
+        const int first = cut_hi ? key - a.right : INT_MIN + 1, last = cut_lo ? key + a.left : INT_MAX;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int4 pl = row_place[buf][8 * b + 2 * g + half];

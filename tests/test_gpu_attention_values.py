@@ -109,3 +109,31 @@ def test_few_queries_over_strided_keys(sp, dtype):
     out, lse = sp.attention(q.to(DEV)[..., 8:56], k.to(DEV).transpose(0, 1), v.to(DEV)[..., :48].expand(n, 3, 48), cu_q.to(DEV),
                             cu_k.to(DEV), causal=True, return_lse=True)
     _check_rows(out, lse, want, torch.zeros(len(LONG), 6, dtype=torch.bool))
+
+
+# ------------------------------------------------------------------ gradients of keys
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [32, 72, 128])
+@pytest.mark.parametrize("nq,nk,window", [(10, 64, (5, -1)), (45, 300, (70, 0)), (300, 430, (20, -1)), (3, 40, (0, 0))])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_unseen_keys_have_zero_gradients(sp, dtype, dim, nq, nk, window, value):
+    """Keys and values that are not finite and that no query sees: gradients of
+    exactly 0, beside tiles of rows that end past the last query."""
+    cu_q, cu_k = ref.offsets([nq, 1]), ref.offsets([nk, 30])
+    host, dev, grad = _inputs(dim + nk, nq + 1, nk + 30, 2, 1, dim, dtype)
+    want = ref.attention(*host, cu_q, cu_k, grad=grad, window=window)
+    unseen = nk - nq - window[0]  # the first keys
+    assert unseen > 0
+    k, v = dev[1].clone(), dev[2].clone()
+    k[:unseen:3] = value
+    v[1:unseen:3] = value
+    k[unseen - 1], v[unseen - 1] = value, value
+    cq, ck = cu_q.to(DEV), cu_k.to(DEV)
+    out, lse = sp.attention(dev[0], k, v, cq, ck, window=window, return_lse=True)
+    _near("out", out, want["out"], want["out_tol"])
+    got = sp.attention_backward(grad.to(DEV), dev[0], k, v, out, lse, cq, ck, window=window)
+    for n, x in zip(("grad_q", "grad_k", "grad_v"), got):
+        _near(n, x, want[n], want[n + "_tol"])
+    assert bool((got[1][:unseen] == 0).all()) and bool((got[2][:unseen] == 0).all())
