@@ -76,6 +76,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
   constexpr int BM = 32 * WAVES, KS = DQ / (2 * kPiece), NL = (BN * PPR + NT - 1) / NT;
   __shared__ uint4 ks[BUFS][kPlanes<T> * BN * PPR], vs[BUFS][kPlanes<T> * BN * PPR];
+  __shared__ int scrubbed[BUFS][WAVES];  // whether the wave found infinities or NaN in its part of an edge tile's keys
+  __shared__ uint32_t bad_keys[BUFS][BN / 32];  // and then, which keys hold them
 
   const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
   const Place at_block = place_of(a, id, run);
@@ -170,16 +172,22 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   float factor = kFirstFactor;
   const float c = a.scale * kLog2e;
 
-  // Keys that some row of the workgroup does not see go into LDS with their
-  // infinities and NaN as zeros: rows that do see them have a NaN lse.  What
+  // Edge tiles hold keys that some row of the workgroup does not see: these go
+  // into LDS with their infinities and NaN as zeros.  A row that sees such a
+  // key has a NaN lse, or a score of -inf with it: its dS is set to 0 in the
+  // loop, and what 0 or NaN times the key gives follows after the loop.  What
   // lies past the sequence's end is zero as loaded, unless the rows repeat one.
   const int edge_end = a.k_row != 0 ? INT_MAX : sp.nk;
   const int edge_hi = a.right >= 0 ? min(div_group(a, sp.r0) + shift + a.right + 1, edge_end) : edge_end;
   const int edge_lo = a.left >= 0 ? div_group(a, min(sp.r0 + BM, rows) - 1) + shift - a.left : 0;
+  auto is_edge = [&](int jb) { return wg.lo + (jb + 1) * BN > edge_hi || wg.lo + jb * BN < edge_lo; };
+  uint64_t met_tiles = 0;  // edge tiles with such keys, by their number modulo 64
   auto store = [&](int buf, int jb) {
-    if (wg.lo + (jb + 1) * BN > edge_hi || wg.lo + jb * BN < edge_lo) {
+    if (is_edge(jb)) {
+      bool met = false;
 #pragma unroll
-      for (int n = 0; n < NL; ++n) scrub<T>(kr[n]);
+      for (int n = 0; n < NL; ++n) met |= scrub<T>(kr[n]);
+      scrubbed[buf][wave] = __any(met);
     }
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
@@ -202,6 +210,17 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     }
     if (jb + 1 < jb1) load(jb + 1);
     const int buf = BUFS == 2 ? (jb - jb0) & 1 : 0;
+    int met = 0;
+    if (is_edge(jb)) {
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) met |= scrubbed[buf][w];
+      met = __builtin_amdgcn_readfirstlane(met);
+      if (met) {
+        met_tiles |= uint64_t(1) << (jb & 63);
+        for (int b = 0; b < BN / 32; ++b)  // (every wave writes the same)
+          bad_keys[buf][b] = rows_not_finite(kbase, a.k_row, wg.lo + jb * BN + 32 * b, sp.nk, a.dim, lane);
+      }
+    }
     for (int b = 0; b < BN / 32; ++b) {
       const int j0 = wg.lo + jb * BN + 32 * b;
       if (!wave_on || j0 >= wv.hi) break;
@@ -227,11 +246,38 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
 #pragma unroll
         for (int i = 0; i < 16; ++i) ds[i] = c_row(i) >= first ? ds[i] : 0.f;
       }
+      if (met) {
+        keep_branch();
+        const uint32_t bad = bad_keys[buf][b] >> (4 * half);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ds[i] = (bad >> c_row(i) & 1) == 0 ? ds[i] : 0.f;
+      }
       rescale<T, DB>(ds, factor, acc);
       mma_transposed<T, DP, DB, BN>(ks[buf], 32 * b, lane, ds, acc);
       settle();
     }
     if (BUFS == 2 && jb + 1 < jb1) store(buf ^ 1, jb + 1);
+  }
+  if (met_tiles != 0) {
+    for (int jb = jb0; jb < jb1; ++jb) {
+      if ((met_tiles >> (jb & 63) & 1) == 0 || !is_edge(jb)) continue;
+      const int j1 = min(wg.lo + (jb + 1) * BN, lane_hi);
+      for (int j = max(wg.lo + jb * BN, lane_lo); has_row && j < j1; ++j) {
+        const T* src = kbase + j * a.k_row;
+        bool bad = false;
+        for (int e = 0; e < a.dim; ++e) bad |= !(fabsf(to_f32(src[e])) < INFINITY);
+        if (!bad) continue;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int d = db * 32 + 4 * half + c_row(i);
+            const float x = d < a.dim ? to_f32(src[d]) : 0.f;
+            // 0 times the value, or a NaN of the row's lse
+            acc[db][i] += 0.f * x + 0.f * lse2;
+          }
+      }
+    }
   }
 
   const float mul = __is_same(T, _Float16) ? a.scale / factor * 6.103515625e-05f : a.scale;

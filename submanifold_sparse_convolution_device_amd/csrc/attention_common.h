@@ -132,6 +132,23 @@ __device__ __forceinline__ bool scrub(Raw<T>& r) {
   return any != 0;
 }
 
+// Which of the 32 rows row0 .. row0 + 31 (below `end`) of a tensor hold an
+// infinity or NaN, as bits; for the rare tile that holds one somewhere.
+template <class T>
+__device__ __forceinline__ uint32_t rows_not_finite(const T* base, int64_t row_stride, int row0, int end, int dim, int lane) {
+  asm volatile("" : "+v"(lane));  // keeps the addresses out of the registers of the loop around the rare call
+  const int row = row0 + (lane & 31);
+  bool bad = false;
+  if (row < end) {
+    for (int e = (lane >> 5) * kPiece; e < dim; e += 2 * kPiece) {
+      Raw<T> r = load_piece(base + row * row_stride + e, true);
+      bad |= scrub<T>(r);
+    }
+  }
+  const uint64_t both = __ballot(bad);
+  return static_cast<uint32_t>(both | both >> 32);
+}
+
 // A piece as an operand: one register quad per plane.
 template <class T>
 struct Frag {

@@ -137,3 +137,44 @@ def test_unseen_keys_have_zero_gradients(sp, dtype, dim, nq, nk, window, value):
     for n, x in zip(("grad_q", "grad_k", "grad_v"), got):
         _near(n, x, want[n], want[n + "_tol"])
     assert bool((got[1][:unseen] == 0).all()) and bool((got[2][:unseen] == 0).all())
+
+
+# ------------------------------------------------------------------ scores of minus infinity
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [32, 72, 128])
+@pytest.mark.parametrize("n,at", [(400, 10), (400, 300), (1100, 300)])
+@pytest.mark.parametrize("how", [dict(causal=True), dict(window=(40, 0)), dict(window=(-1, 25))])
+def test_one_infinite_component_of_a_key(sp, dtype, dim, n, at, how):
+    """A key with one infinite component where every query is negative: its
+    scores are -inf and its probabilities 0, so it changes nothing, but for
+    0 x inf = NaN in that column of the gradients of the queries that see it.
+    In fp32 such a score is NaN, and so are the rows that see it."""
+    cu, col = ref.offsets([n]), 5
+    q, k, v = _inputs(dim + n, n, n, 2, 1, dim, dtype)[0]
+    grad = torch.randn(n, 2, dim, generator=torch.Generator().manual_seed(at)).to(DT[dtype])
+    q[:, :, col] = -1.0
+    k[at, 0, col] = 300.0 * dim ** 0.5  # a score near -300: a probability of 0 as well
+    want = ref.attention(q, k, v, cu, cu, grad=grad, **how)
+    k[at, 0, col] = math.inf
+    dev = tuple(t.to(DEV) for t in (q, k, v))
+    out, lse = sp.attention(*dev, cu.to(DEV), return_lse=True, **how)
+    gq, gk, gv = sp.attention_backward(grad.to(DEV), *dev, out, lse, cu.to(DEV), **how)
+    sees = ref.visible(n, n, how.get("causal", False), how.get("window", (-1, -1)))[:, at]
+    if dtype == "f32":
+        for x in (out, lse, gq):
+            assert bool(torch.isnan(x[sees.to(DEV)]).all())
+        _near("out", out[~sees.to(DEV)], want["out"][~sees], want["out_tol"][~sees])
+        _near("grad_q", gq[~sees.to(DEV)], want["grad_q"][~sees], want["grad_q_tol"][~sees])
+        return
+    _near("out", out, want["out"], want["out_tol"])
+    _near("lse", lse, want["lse"], want["lse_tol"])
+    assert bool(torch.isnan(gq[sees.to(DEV)][..., col]).all())
+    hit = torch.zeros(n, 2, dim, dtype=torch.bool)
+    hit[sees, :, col] = True
+    _near("grad_q", gq[~hit.to(DEV)], want["grad_q"][~hit], want["grad_q_tol"][~hit])
+    assert bool((gk[at] == 0).all()) and bool((gv[at] == 0).all())
+    rest = torch.arange(n) != at
+    _near("grad_k", gk[rest.to(DEV)], want["grad_k"][rest], want["grad_k_tol"][rest])
+    _near("grad_v", gv[rest.to(DEV)], want["grad_v"][rest], want["grad_v_tol"][rest])
