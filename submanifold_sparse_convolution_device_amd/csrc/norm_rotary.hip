@@ -63,7 +63,10 @@ enum Turn { kNone, kInterleaved, kInterleavedWide, kHalves, kHalvesWide };
 
 // Cosine and sine of the angles of the pairs that this lane's elements
 // e0 .. e0 + E - 1 belong to: E / 2 pairs when interleaved, else E.  A
-// position outside the table turns by NaN; elements past R by nothing.
+// position outside the table turns by NaN.  Elements past R are copied: the
+// other member that their pair lacks counts as a zero (an infinity of their
+// own would make NaN of the factor 0), signed so that even their zeros keep
+// their signs: y x 1 + (-0) = y.
 template <class T, Turn TURN>
 struct Angles {
   static constexpr int E = kE<T>;
@@ -102,22 +105,28 @@ struct Angles {
 #pragma unroll
       for (int q = 0; q < G; ++q) {
         c[u + q] = !on ? 1.f : in ? v[2 * q] : __builtin_nanf("");
-        s[u + q] = !on ? 0.f : in ? v[2 * q + 1] : __builtin_nanf("");
+        s[u + q] = !on ? -0.f : in ? v[2 * q + 1] : __builtin_nanf("");
       }
     }
   }
 
   // Turns y forward (SIGN 1) or back (-1).  stage: the unit's LDS, where each
-  // lane finds its pairs' other members (halves only).
+  // lane finds its pairs' other members (halves only); zero: the place of
+  // four zeros from there (lack).
   template <int SIGN>
-  __device__ __forceinline__ void turn(const NormRotaryArgs& a, float* stage, int e0, float (&y)[E]) const {
+  __device__ __forceinline__ void turn(const NormRotaryArgs& a, float* stage, int zero, int e0, float (&y)[E]) const {
     if constexpr (TURN == kNone) return;
     if constexpr (TURN == kInterleaved || TURN == kInterleavedWide) {
+      // Pieces of 8 past R skip the turn (frames of 16 heads of 32, bf16: 317 us,
+      // 321 by selects alone); for those of 4 selects alone are faster (57.5
+      // against 58.3 us for 30k rows of 9 heads of 40 with the gradient).
+      if (E == 8 && e0 >= a.rotary) return;
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         const float x0 = y[2 * u], x1 = y[2 * u + 1], sn = SIGN > 0 ? s[u] : -s[u];
-        y[2 * u] = x0 * c[u] - x1 * sn;
-        y[2 * u + 1] = x0 * sn + x1 * c[u];
+        const bool on = (TURN == kInterleavedWide && E == 8) || e0 + 2 * u < a.rotary;  // (a wide piece lies on one side)
+        y[2 * u] = on ? x0 * c[u] - x1 * sn : x0;
+        y[2 * u + 1] = on ? x0 * sn + x1 * c[u] : x1;
       }
     } else {
       const int half = a.rotary / 2;
@@ -130,7 +139,7 @@ struct Angles {
       for (int u = 0; u < E; u += G) {
         const int e = e0 + u;
         const bool low = e < half;
-        const int at = e >= a.rotary ? e : low ? e + half : e - half;
+        const int at = e >= a.rotary ? zero : low ? e + half : e - half;
         float o[G];
         if constexpr (G == 4) {
           const float4 x = *reinterpret_cast<const float4*>(stage + at);
@@ -152,6 +161,9 @@ struct Angles {
   }
 };
 
+// What stands for the missing member in a pass of that sign.
+constexpr float lack(int sign) { return sign > 0 ? 0.f : -0.f; }
+
 constexpr int kWaves = 4;
 // Units per lane in flight: their loads are issued together.
 constexpr int kUnits = 4;
@@ -159,13 +171,15 @@ constexpr int kUnits = 4;
 template <class T, int LPR, Turn TURN>
 __global__ __launch_bounds__(64 * kWaves) void k_norm_rotary(NormRotaryArgs a, int first_blocks) {
   constexpr int E = kE<T>, UPW = 64 / LPR, UPB = kWaves * UPW;  // units per wavefront and block pass
-  __shared__ float4 stage[TURN >= kHalves ? kWaves * 64 * E / 4 : 1];
+  __shared__ float4 stage[TURN >= kHalves ? kWaves * 64 * E / 4 + kWaves : 1];
   const bool second = static_cast<int>(blockIdx.x) >= first_blocks;
   const NormRotaryTensor& t = a.t[second ? 1 : 0];
   const int block = second ? blockIdx.x - first_blocks : blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e0 = lane % LPR * E;
   float* mine = reinterpret_cast<float*>(stage) + (TURN >= kHalves ? (wave * 64 + lane / LPR * LPR) * E : 0);
+  const int zero = kWaves * 64 * E + 4 * wave - (wave * 64 + lane / LPR * LPR) * E;  // a wave's own
+  if (TURN >= kHalves && lane < 4) mine[zero + lane] = lack(1);
   const bool on = e0 < a.dim;
   const int units = a.rows * t.heads;
   const int u0 = block * (UPB * kUnits) + wave * UPW + lane / LPR;
@@ -201,7 +215,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_norm_rotary(NormRotaryArgs a, i
 #pragma unroll
       for (int u = 0; u < E; ++u) x[u] = x[u] * r * w[u];
     }
-    ang[i].template turn<1>(a, mine, e0, x);
+    ang[i].template turn<1>(a, mine, zero, e0, x);
     if (ok[i] && on) *reinterpret_cast<uint4*>(static_cast<T*>(t.y) + row[i] * t.y_row + head[i] * t.y_head + e0) = pack<T>(x);
   }
 }
@@ -212,7 +226,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_norm_rotary(NormRotaryArgs a, i
 template <class T, int LPR, Turn TURN>
 __global__ __launch_bounds__(64 * kWaves) void k_norm_rotary_backward(NormRotaryArgs a, int first_blocks, float* part) {
   constexpr int E = kE<T>, UPW = 64 / LPR, UPB = kWaves * UPW, U = 2;
-  __shared__ float4 stage[kWaves * 64 * E / 4];
+  __shared__ float4 stage[kWaves * 64 * E / 4 + kWaves];
   const bool second = static_cast<int>(blockIdx.x) >= first_blocks;
   const NormRotaryTensor& t = a.t[second ? 1 : 0];
   const int block = second ? blockIdx.x - first_blocks : blockIdx.x;
@@ -220,6 +234,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_norm_rotary_backward(NormRotary
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e0 = lane % LPR * E;
   float* mine = reinterpret_cast<float*>(stage) + (wave * 64 + lane / LPR * LPR) * E;
+  const int zero = kWaves * 64 * E + 4 * wave - (wave * 64 + lane / LPR * LPR) * E;  // a wave's own
+  if (TURN >= kHalves && lane < 4) mine[zero + lane] = lack(-1);
   const bool on = e0 < a.dim;
   const int units = a.rows * t.heads;
   const int64_t step = static_cast<int64_t>(blocks) * (UPB * U);
@@ -250,7 +266,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_norm_rotary_backward(NormRotary
     for (int i = 0; i < U; ++i) {
       float x[E], g[E];
       unpack<T>(gr[i], g);
-      ang[i].template turn<-1>(a, mine, e0, g);
+      ang[i].template turn<-1>(a, mine, zero, e0, g);
       if (t.weight != nullptr) {
         unpack<T>(xr[i], x);
         float sq = 0.f, gx = 0.f, gw[E];
