@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   }
   const float sum = halves_sum(l);
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // a NaN stays one
-  const float lse = sum == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+  const float lse = sum == 0.f ? -INFINITY : ln_scaled(m, sum);
   const int64_t row_out = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
   if (nsplit == 1 && (WAVES > 1 || part_row < 0)) {
     if (has_row && half == 0) a.lse[row_out] = lse;
@@ -360,7 +360,7 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* 
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   store4<T>(static_cast<T*>(a.out) + row_out * a.dim + 4 * quad, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-  if (quad == 0) a.lse[row_out] = sum == 0.f ? -INFINITY : all + __builtin_amdgcn_logf(sum) * kLn2;
+  if (quad == 0) a.lse[row_out] = sum == 0.f ? -INFINITY : all + ln_scaled(0.f, sum);
 }
 
 // Splits: part s of row r is at s x rows + r.  Few parts of many rows: four
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int nsp
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   store4<T>(static_cast<T*>(a.out) + row * a.dim + 4 * quad, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-  if (quad == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
+  if (quad == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + ln_scaled(0.f, sum);
 }
 
 // Chunks: one workgroup per query row and head.

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   float lse2 = INFINITY;
   if (has_row) {
     const float v = a.lse[row_out];
-    lse2 = v == -INFINITY ? INFINITY : v * kLog2e - kShift<T>;
+    lse2 = v == -INFINITY ? INFINITY : log2_units(v) - kShift<T>;
     // for the other kernel, in the order in which it walks the rows; a D that
     // is not finite makes NaN of both
     if (half == 0 && split == 0)

@@ -178,3 +178,29 @@ def test_one_infinite_component_of_a_key(sp, dtype, dim, n, at, how):
     rest = torch.arange(n) != at
     _near("grad_k", gk[rest.to(DEV)], want["grad_k"][rest], want["grad_k_tol"][rest])
     _near("grad_v", gv[rest.to(DEV)], want["grad_v"][rest], want["grad_v_tol"][rest])
+
+
+# ------------------------------------------------------------------ lse
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("longest", [256, 1500])
+def test_lse_is_not_biased(sp, dtype, longest):
+    """Equal scores s of n keys: lse = s + ln n.  Its roundings have either
+    sign, so their mean over many (n, s) is near 0.  In units of 2^-24 lse:
+    single errors of up to about 3 leave 3 / sqrt(1800) = 0.07 of the mean; the
+    logarithm of a mantissa, of size 1 or less and off by up to one unit in its
+    last place, leaves up to 2^-24 ln 2 of about 5, 0.14; together 0.25.  (The
+    gradients take exp(s - lse): a bias there is one of every gradient.)
+    longest 1500: by parts, which are joined."""
+    lengths = list(range(20, 256)) if longest == 256 else list(range(300, 1500, 5))
+    pairs = [(n, s) for n in lengths for s in (0.0, 0.375, 0.5, 1.0, 1.25, 2.5, 3.0, 4.0)]
+    cu_k = ref.offsets([n for n, _ in pairs])
+    q, k = torch.zeros(len(pairs), 1, 8), torch.zeros(int(cu_k[-1]), 1, 8)
+    q[:, 0, 2], k[:, 0, 2] = torch.tensor([s for _, s in pairs]), 1.0
+    q, k = q.to(DT[dtype]).to(DEV), k.to(DT[dtype]).to(DEV)
+    _, lse = sp.attention(q, k, k, ref.offsets([1] * len(pairs)).to(DEV), cu_k.to(DEV), scale=1.0, return_lse=True)
+    want = torch.tensor([s + math.log(n) for n, s in pairs], dtype=torch.float64)
+    off = (lse.double().cpu()[:, 0] - want) / want / 2.0 ** -24
+    print(f"[lse] {dtype} {longest}: mean {float(off.mean()):.3f}, largest {float(off.abs().max()):.2f}")
+    assert abs(float(off.mean())) <= 0.25
