@@ -14,14 +14,16 @@
 // and V^T through the transposing LDS read.
 //
 // fp32 runs on the bf16 matrix unit, 16 times the rate of the fp32 one: a
-// value splits exactly into three bf16 planes of 8 significant bits (by
-// truncation: x = hi + mid + lo), and a product is the six of the nine plane
-// products that reach 2^-24 of it, summed in fp32:
+// value splits exactly into three bf16 planes of 8 significant bits (each the
+// nearest to what is left: x = hi + mid + lo, for x in [1, 2) |mid| <= 2^-8 and
+// |lo| <= 2^-17), and a product is the six of the nine plane products
+// that reach 2^-24 of it, summed in fp32:
 //   hi hi + (hi mid + mid hi) + (hi lo + mid mid + lo hi);
-// what is left out is below 2^-23 of |a b|, the size of an fp32 rounding.
+// what is left out is at most 2 x 2^-8 x 2^-17 = 2^-24 of |a b|, half a unit
+// of fp32's rounding, and of either sign.
 // Against products on the fp32 matrix unit: a band of 200 rows over heads of
 // 40 takes 29 us instead of 40, frames of 24 channels with gradients 104
-// instead of 143, both as near to 64 bits as before.
+// instead of 143.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -172,27 +174,29 @@ struct Frag {
   uint4 v[kPlanes<T>];
 };
 
-// The three planes of two fp32 values, two bf16 in a word each.  An infinity
-// or NaN stays in the first plane alone.
+// The three planes of two fp32 values, two bf16 in a word each, rounded to
+// nearest: what a plane leaves is at most half a unit of it, with a sign of
+// its own (planes cut off towards zero leave twice as much in the first and
+// the second, all of the value's sign, so that sums drift).  Values that
+// round to a bf16 infinity keep the largest bf16 instead; an infinity or NaN
+// has a NaN in its last plane, which makes NaN of all that it meets.
 struct Split2 {
   uint32_t hi, mid, lo;
 };
 template <bool FINITE>
 __device__ __forceinline__ Split2 split2(float x, float y) {
-  auto high = [](float f) { return __builtin_bit_cast(uint32_t, f) & 0xffff0000u; };
-  // the words' upper halves, y's above x's
-  auto pair = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };
-  const uint32_t hx = high(x), hy = high(y);
-  float rx = x - __builtin_bit_cast(float, hx), ry = y - __builtin_bit_cast(float, hy);  // exact
-  if constexpr (!FINITE) {
-    rx = fabsf(x) < INFINITY ? rx : 0.f;
-    ry = fabsf(y) < INFINITY ? ry : 0.f;
-  }
-  const uint32_t mx = high(rx), my = high(ry);
-  const float lx = rx - __builtin_bit_cast(float, mx), ly = ry - __builtin_bit_cast(float, my);
-  return {pair(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)),
-          pair(__builtin_bit_cast(uint32_t, rx), __builtin_bit_cast(uint32_t, ry)),
-          pair(__builtin_bit_cast(uint32_t, lx), __builtin_bit_cast(uint32_t, ly))};
+  typedef float floatx2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  constexpr float top = 3.3895313892515355e38f;  // the largest bf16
+  auto pair = [](float f, float g) { return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{f, g}), bf16x2)); };
+  auto first = [](uint32_t w) { return __builtin_bit_cast(float, w << 16); };
+  auto second = [](uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); };
+  Split2 r;
+  r.hi = FINITE ? pair(x, y) : pair(__builtin_amdgcn_fmed3f(x, -top, top), __builtin_amdgcn_fmed3f(y, -top, top));
+  const float rx = x - first(r.hi), ry = y - second(r.hi);  // exact
+  r.mid = pair(rx, ry);
+  r.lo = pair(rx - first(r.mid), ry - second(r.mid));  // exact
+  return r;
 }
 template <bool FINITE>
 __device__ __forceinline__ Frag<float> split8(const float (&x)[8]) {

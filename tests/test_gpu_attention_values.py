@@ -204,3 +204,66 @@ def test_lse_is_not_biased(sp, dtype, longest):
     off = (lse.double().cpu()[:, 0] - want) / want / 2.0 ** -24
     print(f"[lse] {dtype} {longest}: mean {float(off.mean()):.3f}, largest {float(off.abs().max()):.2f}")
     assert abs(float(off.mean())) <= 0.25
+
+
+# ------------------------------------------------------------------ fp32 products
+
+
+def test_fp32_products_at_the_worst_mantissas(sp):
+    """One key whose score is the single product a b: what the products of
+    three-part operands leave out is at most 2^-24 of it.  lse = ln 2 x (scale
+    log2(e) x a b): beside that, one rounding of the product's sum (two
+    allowed, 2^-24 each, for the order in the matrix unit), one of the
+    multiplication by the constant and one by ln 2."""
+    e = 2.0 ** -24
+    values = [1 + 2.0 ** -7 - 2.0 ** -23, 1 + 2.0 ** -7 + 2.0 ** -8 - 2.0 ** -16 - 2.0 ** -23, 1 + 2.0 ** -8 - 2.0 ** -23, 2 - 2.0 ** -23,
+              1 + 2.0 ** -15 - 2.0 ** -23, 1.0, 4 / 3, 1.9921865]
+    g = torch.Generator().manual_seed(1)
+    a = torch.cat([torch.tensor(values, dtype=torch.float64), 1 + torch.rand(2000, generator=g, dtype=torch.float64)]).float()
+    n = len(a)
+    cu = ref.offsets([1] * n)
+    c = torch.tensor(1.0, dtype=torch.float32) * torch.tensor(1.4426950408889634, dtype=torch.float32)
+    ln2 = torch.tensor(0.6931471805599453, dtype=torch.float32)
+    for b in (a, a.flip(0)):
+        q, k = torch.zeros(n, 1, 8), torch.zeros(n, 1, 8)
+        q[:, 0, 3], k[:, 0, 3] = a, b
+        _, lse = sp.attention(q.to(DEV), k.to(DEV), k.to(DEV), cu.to(DEV), scale=1.0, return_lse=True)
+        got = lse.double().cpu()[:, 0] / (float(c) * float(ln2))
+        exact = a.double() * b.double()
+        off = ((got - exact).abs() / exact) / e
+        assert float(off.max()) <= 5.0, f"{float(off.max()):.2f} x 2^-24 of the product"
+
+
+def test_fp32_operands_over_the_whole_range(sp):
+    """The largest and smallest normal values: the three parts of an operand
+    hold them without overflow, seen or hidden."""
+    top = torch.finfo(torch.float32).max
+    cu = ref.offsets([80]).to(DEV)
+    q, k, v = torch.zeros(80, 1, 16), torch.zeros(80, 1, 16), torch.ones(80, 1, 16)
+    v[:, 0, 0], v[:, 0, 1], v[:, 0, 2], v[::2, 0, 3] = top, -top, 2.0 ** -120, -top
+    # every row sees itself: weight 1, and the sum of the parts is the value
+    out = sp.attention(q.to(DEV), k.to(DEV), v.to(DEV), cu, window=(0, 0)).cpu()
+    assert torch.equal(out, v)
+    # causal: the largest values of the keys after a row leave it alone (40 equal weights of 1: 48 roundings at most)
+    v = torch.ones(80, 1, 16)
+    v[40:] = -top
+    out = sp.attention(q.to(DEV), k.to(DEV), v.to(DEV), cu, causal=True).double().cpu()
+    assert bool(((out[:40] - 1).abs() <= 48 * 2.0 ** -24).all())
+    # a product of the largest and a small value: equal scores of 4
+    q[:, 0, 1], k[:, 0, 1] = top, 2.0 ** -126
+    _, lse = sp.attention(q.to(DEV), k.to(DEV), v.to(DEV), cu, scale=1.0, return_lse=True)
+    want = top * 2.0 ** -126 + math.log(80)
+    assert bool(((lse.double().cpu() - want).abs() <= 100 * 2.0 ** -24 * want).all())
+
+
+@pytest.mark.parametrize("value", [-1.0, -1.2345678, 0.0, 1.2345678])
+@pytest.mark.parametrize("n", [50, 300])
+def test_fp32_scores_of_an_infinite_key_are_nan(sp, value, n):
+    """Whatever the query's mantissa and sign."""
+    cu = ref.offsets([n]).to(DEV)
+    q, k, v = (t.clone() for t in _inputs(n, n, n, 1, 1, 32, "f32")[1])
+    q[:, :, 4] = value
+    k[n // 2, 0, 4] = math.inf
+    out, lse = sp.attention(q, k, v, cu, causal=True, return_lse=True)
+    assert bool(torch.isnan(out[n // 2:]).all()) and bool(torch.isnan(lse[n // 2:]).all())
+    assert bool(torch.isfinite(out[:n // 2]).all())
