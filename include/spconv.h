@@ -590,6 +590,30 @@ typedef struct spconv_attention_gradients {
 spconv_status spconv_attention_backward(const spconv_attention* args, const void* d_out, const float* d_lse,
                                         const spconv_attention_gradients* grads, void* hip_stream);
 
+/*
+ * The same calls with a workspace of the caller's, for callers that capture
+ * them in a graph or keep device memory to themselves: no device allocator is
+ * called and nothing of the stream's cache is used.  d_workspace (16-byte
+ * aligned, sharing no byte with the other tensors) holds workspace_bytes, at
+ * least what spconv_attention_workspace returns for the same args (of which
+ * it reads the sizes alone, so the pointers may still be NULL; either result
+ * pointer may be NULL).  Calls that may overlap in time, such as the replays
+ * of two graphs, need a workspace each, and a graph's must live as long as
+ * the graph.
+ *
+ * spconv_attention_forward and spconv_attention_backward on a stream under
+ * graph capture: INVALID_ARG when the call needs a workspace.
+ *
+ * Errors as for those calls, and INVALID_ARG for a workspace that is NULL,
+ * misaligned, too small or overlapping (none is needed for 0 bytes).
+ */
+spconv_status spconv_attention_workspace(const spconv_attention* args, uint64_t* forward_bytes, uint64_t* backward_bytes);
+spconv_status spconv_attention_forward_noalloc(const spconv_attention* args, void* d_out, float* d_lse, void* d_workspace,
+                                               uint64_t workspace_bytes, void* hip_stream);
+spconv_status spconv_attention_backward_noalloc(const spconv_attention* args, const void* d_out, const float* d_lse,
+                                                const spconv_attention_gradients* grads, void* d_workspace,
+                                                uint64_t workspace_bytes, void* hip_stream);
+
 /* ---- Head norm and position rotation ----
  *
  * One pass over the queries and keys of an attention: the RMS norm of every
@@ -664,6 +688,13 @@ typedef struct spconv_norm_rotary_gradients {
 
 spconv_status spconv_norm_rotary_backward(const spconv_norm_rotary* args, const spconv_norm_rotary_gradients* grads,
                                           void* hip_stream);
+
+/* The gradients with a workspace of the caller's, as for attention:
+ * spconv_norm_rotary_workspace returns its bytes, and on a stream under graph
+ * capture only this variant runs (spconv_norm_rotary_forward needs none). */
+spconv_status spconv_norm_rotary_workspace(int32_t head_dim, uint64_t* backward_bytes);
+spconv_status spconv_norm_rotary_backward_noalloc(const spconv_norm_rotary* args, const spconv_norm_rotary_gradients* grads,
+                                                  void* d_workspace, uint64_t workspace_bytes, void* hip_stream);
 
 /*
  * The table of a rotation: d_table[p][i] = (cos, sin) of

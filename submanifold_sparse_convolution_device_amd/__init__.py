@@ -44,7 +44,8 @@ EXPORTED = (
     "spconv_forward_grouped", "spconv_select_dataflow", "spconv_map_free", "spconv_status_string",
     "spconv_last_error", "spconv_weights_prepare", "spconv_forward_prepared", "spconv_weights_free",
     "spconv_attention_forward", "spconv_attention_backward", "spconv_norm_rotary_forward", "spconv_norm_rotary_backward",
-    "spconv_rotary_table",
+    "spconv_rotary_table", "spconv_attention_workspace", "spconv_attention_forward_noalloc", "spconv_attention_backward_noalloc",
+    "spconv_norm_rotary_workspace", "spconv_norm_rotary_backward_noalloc",
 )
 MAP_KINDS = {0: "submanifold", 1: "strided", 2: "transposed"}
 DATAFLOWS = {0: "fused", 1: "grouped"}
@@ -179,6 +180,16 @@ def lib() -> ctypes.CDLL:
     L.spconv_norm_rotary_forward.restype = ctypes.c_int
     L.spconv_norm_rotary_backward.argtypes = [vp, vp, vp]
     L.spconv_norm_rotary_backward.restype = ctypes.c_int
+    L.spconv_attention_workspace.argtypes = [vp, vp, vp]
+    L.spconv_attention_workspace.restype = ctypes.c_int
+    L.spconv_attention_forward_noalloc.argtypes = [vp, vp, vp, vp, ctypes.c_uint64, vp]
+    L.spconv_attention_forward_noalloc.restype = ctypes.c_int
+    L.spconv_attention_backward_noalloc.argtypes = [vp, vp, vp, vp, vp, ctypes.c_uint64, vp]
+    L.spconv_attention_backward_noalloc.restype = ctypes.c_int
+    L.spconv_norm_rotary_workspace.argtypes = [i32, vp]
+    L.spconv_norm_rotary_workspace.restype = ctypes.c_int
+    L.spconv_norm_rotary_backward_noalloc.argtypes = [vp, vp, vp, ctypes.c_uint64, vp]
+    L.spconv_norm_rotary_backward_noalloc.restype = ctypes.c_int
     L.spconv_rotary_table.argtypes = [vp, i32, i32, f64, f64, vp]
     L.spconv_rotary_table.restype = ctypes.c_int
     L.spconv_map_free.argtypes, L.spconv_map_free.restype = [vp], None
@@ -364,6 +375,41 @@ def spconv_attention_backward(args: spconv_attention, d_out: int, d_lse: int, gr
     _check(lib().spconv_attention_backward(ctypes.byref(args), d_out, d_lse, ctypes.byref(grads), hip_stream))
 
 
+def spconv_attention_workspace(args: spconv_attention) -> Tuple[int, int]:
+    """Bytes of workspace of the forward and of the gradient."""
+    return _attention_workspace(ctypes.byref(args))
+
+
+def _attention_workspace(args) -> Tuple[int, int]:
+    f, b = ctypes.c_uint64(), ctypes.c_uint64()
+    _check(lib().spconv_attention_workspace(args, ctypes.byref(f), ctypes.byref(b)))
+    return f.value, b.value
+
+
+def spconv_attention_forward_noalloc(args: spconv_attention, d_out: int, d_lse: int, d_workspace: int, workspace_bytes: int,
+                                     hip_stream: int) -> None:
+    _check(lib().spconv_attention_forward_noalloc(ctypes.byref(args), d_out, d_lse, d_workspace, workspace_bytes, hip_stream))
+
+
+def spconv_attention_backward_noalloc(args: spconv_attention, d_out: int, d_lse: int, grads: spconv_attention_gradients,
+                                      d_workspace: int, workspace_bytes: int, hip_stream: int) -> None:
+    _check(lib().spconv_attention_backward_noalloc(ctypes.byref(args), d_out, d_lse, ctypes.byref(grads), d_workspace,
+                                                   workspace_bytes, hip_stream))
+
+
+def spconv_norm_rotary_workspace(head_dim: int) -> int:
+    """Bytes of workspace of the gradient."""
+    b = ctypes.c_uint64()
+    _check(lib().spconv_norm_rotary_workspace(head_dim, ctypes.byref(b)))
+    return b.value
+
+
+def spconv_norm_rotary_backward_noalloc(args: spconv_norm_rotary, grads: spconv_norm_rotary_gradients, d_workspace: int,
+                                        workspace_bytes: int, hip_stream: int) -> None:
+    _check(lib().spconv_norm_rotary_backward_noalloc(ctypes.byref(args), ctypes.byref(grads), d_workspace, workspace_bytes,
+                                                     hip_stream))
+
+
 def spconv_norm_rotary_forward(args: spconv_norm_rotary, d_q_out: int, q_out_row_stride: int, q_out_head_stride: int,
                                d_k_out: int, k_out_row_stride: int, k_out_head_stride: int, hip_stream: int) -> None:
     _check(lib().spconv_norm_rotary_forward(ctypes.byref(args), d_q_out, q_out_row_stride, q_out_head_stride,
@@ -409,15 +455,29 @@ def _run(device: int, call, *args) -> None:
     """call(*args, stream) with ``device`` current, on torch's current stream
     there, and its status checked: what :class:`_OnDevice` and :func:`_stream`
     do, at a tenth of the host time (the stream's handle without a stream
-    object)."""
+    object).
+
+    A call that needs a workspace is refused under graph capture and runs with
+    one of torch's allocator instead, which the graph keeps."""
     C = _TORCH._C
-    if C._cuda_getDevice() == device:
-        rc = call(*args, C._cuda_getCurrentRawStream(device))
-    else:
+    if C._cuda_getDevice() != device:
         with _TORCH.cuda.device(device):
-            rc = call(*args, C._cuda_getCurrentRawStream(device))
+            return _run(device, call, *args)
+    rc = call(*args, C._cuda_getCurrentRawStream(device))
+    if rc and call.__name__ in _WORKSPACES and _TORCH.cuda.is_current_stream_capturing():
+        workspace = _TORCH.empty(_WORKSPACES[call.__name__](args[0]), dtype=_TORCH.uint8, device=f"cuda:{device}")
+        rc = getattr(_LIB, call.__name__ + "_noalloc")(*args, workspace.data_ptr(), workspace.numel(),
+                                                       C._cuda_getCurrentRawStream(device))
     if rc:
         _check(rc)
+
+
+# Bytes of workspace of the calls that have a _noalloc variant, from their packed arguments.
+_WORKSPACES = {
+    "spconv_attention_forward": lambda a: _attention_workspace(a)[0],
+    "spconv_attention_backward": lambda a: _attention_workspace(a)[1],
+    "spconv_norm_rotary_backward": lambda a: spconv_norm_rotary_workspace(spconv_norm_rotary.from_buffer_copy(a).head_dim),
+}
 
 
 _TORCH = None

@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <string>
@@ -611,9 +612,9 @@ struct AttentionTensors {
   Strided q, k, v, out, lse;
 };
 
-// Validates an attention call and fills its launch arguments.
-spconv_status attention_args(const spconv_attention* x, const void* d_out, const float* d_lse,
-                             spconv::AttentionArgs* a, AttentionTensors* t) {
+// Validates the sizes of an attention call and fills them in: all that its
+// launches, and so its workspace, depend on.
+spconv_status attention_sizes(const spconv_attention* x, spconv::AttentionArgs* a) {
   if (x == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "args is NULL");
   const spconv_status st = check_head_dim(x->dtype, x->head_dim);
   if (st != SPCONV_OK) return st;
@@ -629,6 +630,27 @@ spconv_status attention_args(const spconv_attention* x, const void* d_out, const
     return fail(SPCONV_ERR_INVALID_ARG, "total_q = %lld, total_k = %lld: rows x heads must stay below 2^31 and rows below 2^30",
                 (long long)x->total_q, (long long)x->total_k);
   }
+  a->batch = x->batch;
+  a->total_q = static_cast<int32_t>(x->total_q);
+  a->total_k = static_cast<int32_t>(x->total_k);
+  a->heads = x->heads;
+  a->kv_heads = x->kv_heads;
+  a->group = x->heads / x->kv_heads;
+  a->dim = x->head_dim;
+  a->by_group = spconv::make_fast_div(a->group);
+  a->by_kv_heads = spconv::make_fast_div(a->kv_heads);
+  // a bound past every row is none
+  a->left = x->left < 0 || x->left >= (1 << 30) ? -1 : x->left;
+  a->right = x->right < 0 || x->right >= (1 << 30) ? -1 : x->right;
+  a->dtype = x->dtype;
+  return SPCONV_OK;
+}
+
+// Validates an attention call and fills its launch arguments.
+spconv_status attention_args(const spconv_attention* x, const void* d_out, const float* d_lse,
+                             spconv::AttentionArgs* a, AttentionTensors* t) {
+  const spconv_status st = attention_sizes(x, a);
+  if (st != SPCONV_OK) return st;
   if (!(x->scale > 0.f) || !std::isfinite(x->scale)) return fail(SPCONV_ERR_INVALID_ARG, "scale = %g must be positive and finite", x->scale);
   if (x->cu_q == nullptr || x->cu_k == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "cu_q or cu_k is NULL");
   if ((reinterpret_cast<uintptr_t>(x->cu_q) | reinterpret_cast<uintptr_t>(x->cu_k) | reinterpret_cast<uintptr_t>(d_lse)) & 3u) {
@@ -657,32 +679,49 @@ spconv_status attention_args(const spconv_attention* x, const void* d_out, const
   a->v_head = x->v_head_stride;
   a->cu_q = x->cu_q;
   a->cu_k = x->cu_k;
-  a->batch = x->batch;
-  a->total_q = static_cast<int32_t>(x->total_q);
-  a->total_k = static_cast<int32_t>(x->total_k);
-  a->heads = x->heads;
-  a->kv_heads = x->kv_heads;
-  a->group = x->heads / x->kv_heads;
-  a->dim = x->head_dim;
-  a->by_group = spconv::make_fast_div(a->group);
-  a->by_kv_heads = spconv::make_fast_div(a->kv_heads);
-  // a bound past every row is none
-  a->left = x->left < 0 || x->left >= (1 << 30) ? -1 : x->left;
-  a->right = x->right < 0 || x->right >= (1 << 30) ? -1 : x->right;
   a->scale = x->scale;
-  a->dtype = x->dtype;
   a->out = const_cast<void*>(d_out);
   a->lse = const_cast<float*>(d_lse);
   return SPCONV_OK;
 }
 
-// The stream's workspace of `need` bytes for the launches that `launch` makes
-// (NULL when none is needed), held for this stream until they are enqueued.
+// A workspace that the caller gives.
+struct CallerWorkspace {
+  void* p;
+  uint64_t bytes;
+};
+
+// `launch` with a workspace of `need` bytes (NULL when none is needed): the
+// caller's, which must keep apart from `tensors`, or else the stream's, held
+// for this stream until the launches are enqueued.  A captured call must
+// bring its own: the graph would keep the address of a buffer that the
+// stream's later calls replace, and an allocation under capture would belong
+// to the graph while the cache hands it to calls outside.
 template <class F>
-spconv_status with_workspace(size_t need, hipStream_t stream, const char* what, F&& launch) {
+spconv_status with_workspace(size_t need, const CallerWorkspace* own, std::initializer_list<const Strided*> tensors, hipStream_t stream,
+                             const char* what, F&& launch) {
   if (need == 0) {
     const hipError_t e = launch(static_cast<void*>(nullptr));
     return e == hipSuccess ? SPCONV_OK : hip_fail(e, what);
+  }
+  if (own != nullptr) {
+    if (own->p == nullptr || own->bytes < need) {
+      return fail(SPCONV_ERR_INVALID_ARG, "the call needs %zu bytes of workspace, %llu given", need,
+                  (unsigned long long)(own->p == nullptr ? 0 : own->bytes));
+    }
+    if (!aligned16(own->p)) return fail(SPCONV_ERR_INVALID_ARG, "the workspace is not 16-byte aligned");
+    for (const Strided* t : tensors) {
+      if (ranges_overlap(own->p, need, t->p, t->bytes())) return fail(SPCONV_ERR_INVALID_ARG, "the workspace overlaps %s", t->name);
+    }
+    const hipError_t e = launch(own->p);
+    return e == hipSuccess ? SPCONV_OK : hip_fail(e, what);
+  }
+  if (stream != nullptr) {  // (the null stream cannot be captured)
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    SPCONV_HIP(hipStreamIsCapturing(stream, &capture), "hipStreamIsCapturing");
+    if (capture != hipStreamCaptureStatusNone) {
+      return fail(SPCONV_ERR_INVALID_ARG, "under graph capture this call needs a workspace of %zu bytes of the caller's (the _noalloc entry points)", need);
+    }
   }
   int device = 0;
   SPCONV_HIP(hipGetDevice(&device), "hipGetDevice");
@@ -753,6 +792,114 @@ spconv_status norm_rotary_args(const spconv_norm_rotary* x, spconv::NormRotaryAr
   a->positions = x->positions;
   a->pos_row = x->position_row_stride;
   return SPCONV_OK;
+}
+
+spconv_status attention_forward(const spconv_attention* args, void* d_out, float* d_lse, const CallerWorkspace* own, void* hip_stream) {
+  g_last_error.clear();
+  spconv::AttentionArgs a;
+  AttentionTensors t;
+  spconv_status st = attention_args(args, d_out, d_lse, &a, &t);
+  if (st != SPCONV_OK) return st;
+  for (const Strided* out : {&t.out, &t.lse}) {
+    for (const Strided* in : {&t.q, &t.k, &t.v}) {
+      st = check_apart(*out, *in);
+      if (st != SPCONV_OK) return st;
+    }
+  }
+  st = check_apart(t.out, t.lse);
+  if (st != SPCONV_OK) return st;
+  if (a.total_q == 0) return SPCONV_OK;
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  return with_workspace(spconv::attention_workspace_bytes(a), own, {&t.q, &t.k, &t.v, &t.out, &t.lse}, stream, "attention launch",
+                        [&](void* ws) { return spconv::launch_attention(a, ws, stream); });
+}
+
+spconv_status attention_backward(const spconv_attention* args, const void* d_out, const float* d_lse,
+                                 const spconv_attention_gradients* grads, const CallerWorkspace* own, void* hip_stream) {
+  g_last_error.clear();
+  spconv::AttentionArgs a;
+  AttentionTensors t;
+  spconv_status st = attention_args(args, d_out, d_lse, &a, &t);
+  if (st != SPCONV_OK) return st;
+  if (grads == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grads is NULL");
+  const uint64_t es = t.q.es;
+  const Strided go = {"grad_out", grads->grad_out, a.total_q, grads->grad_out_row_stride, a.heads, grads->grad_out_head_stride, a.dim, es};
+  const Strided gq = {"grad_q", grads->grad_q, a.total_q, grads->grad_q_row_stride, a.heads, grads->grad_q_head_stride, a.dim, es};
+  const Strided gk = {"grad_k", grads->grad_k, a.total_k, grads->grad_k_row_stride, a.kv_heads, grads->grad_k_head_stride, a.dim, es};
+  const Strided gv = {"grad_v", grads->grad_v, a.total_k, grads->grad_v_row_stride, a.kv_heads, grads->grad_v_head_stride, a.dim, es};
+  st = check_strided(go, false);
+  if (st != SPCONV_OK) return st;
+  for (const Strided* out : {&gq, &gk, &gv}) {
+    st = check_strided(*out, true);
+    if (st != SPCONV_OK) return st;
+    for (const Strided& in : {t.q, t.k, t.v, t.out, t.lse, go}) {
+      st = check_apart(*out, in);
+      if (st != SPCONV_OK) return st;
+    }
+  }
+  for (const auto& pair : {std::make_pair(&gq, &gk), std::make_pair(&gq, &gv), std::make_pair(&gk, &gv)}) {
+    st = check_apart(*pair.first, *pair.second);
+    if (st != SPCONV_OK) return st;
+  }
+  a.grad_out = go.p;
+  a.go_row = go.row_stride;
+  a.go_head = go.head_stride;
+  a.grad_q = grads->grad_q;
+  a.gq_row = gq.row_stride;
+  a.gq_head = gq.head_stride;
+  a.grad_k = grads->grad_k;
+  a.gk_row = gk.row_stride;
+  a.gk_head = gk.head_stride;
+  a.grad_v = grads->grad_v;
+  a.gv_row = gv.row_stride;
+  a.gv_head = gv.head_stride;
+  if (a.total_q == 0 && a.total_k == 0) return SPCONV_OK;
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  return with_workspace(spconv::attention_backward_workspace_bytes(a), own, {&t.q, &t.k, &t.v, &t.out, &t.lse, &go, &gq, &gk, &gv}, stream,
+                        "attention backward launch",
+                        [&](void* ws) { return spconv::launch_attention_backward(a, ws, stream); });
+}
+
+spconv_status norm_rotary_backward(const spconv_norm_rotary* args, const spconv_norm_rotary_gradients* grads, const CallerWorkspace* own,
+                                   void* hip_stream) {
+  g_last_error.clear();
+  spconv::NormRotaryArgs a;
+  Strided in[2];
+  spconv_status st = norm_rotary_args(args, &a, in);
+  if (st != SPCONV_OK) return st;
+  if (grads == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grads is NULL");
+  if ((reinterpret_cast<uintptr_t>(grads->grad_q_weight) | reinterpret_cast<uintptr_t>(grads->grad_k_weight)) & 3u) {
+    return fail(SPCONV_ERR_INVALID_ARG, "the weight gradients must be 4-byte aligned");
+  }
+  const Strided g[2] = {
+      {"grad_q_out", grads->grad_q_out, a.rows, grads->grad_q_out_row_stride, a.t[0].heads, grads->grad_q_out_head_stride, a.dim, in[0].es},
+      {"grad_k_out", grads->grad_k_out, a.rows, grads->grad_k_out_row_stride, a.t[1].heads, grads->grad_k_out_head_stride, a.dim, in[0].es}};
+  const Strided gx[2] = {
+      {"grad_q", grads->grad_q, a.rows, grads->grad_q_row_stride, a.t[0].heads, grads->grad_q_head_stride, a.dim, in[0].es},
+      {"grad_k", grads->grad_k, a.rows, grads->grad_k_row_stride, a.t[1].heads, grads->grad_k_head_stride, a.dim, in[0].es}};
+  for (int i = 0; i < 2; ++i) {
+    st = check_strided(g[i], false);
+    if (st == SPCONV_OK) st = check_strided(gx[i], true);
+    for (int j = 0; j < 2 && st == SPCONV_OK; ++j) {
+      st = check_apart(gx[i], in[j]);
+      if (st == SPCONV_OK && (i != j || !same_place(gx[i], g[j]))) st = check_apart(gx[i], g[j]);
+    }
+    if (st != SPCONV_OK) return st;
+    a.t[i].grad = g[i].p;
+    a.t[i].g_row = g[i].row_stride;
+    a.t[i].g_head = g[i].head_stride;
+    a.t[i].grad_x = const_cast<void*>(gx[i].p);
+    a.t[i].gx_row = gx[i].row_stride;
+    a.t[i].gx_head = gx[i].head_stride;
+  }
+  st = check_apart(gx[0], gx[1]);
+  if (st != SPCONV_OK) return st;
+  a.t[0].grad_weight = grads->grad_q_weight;
+  a.t[1].grad_weight = grads->grad_k_weight;
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  return with_workspace(spconv::norm_rotary_backward_workspace_bytes(a), own, {&in[0], &in[1], &g[0], &g[1], &gx[0], &gx[1]}, stream,
+                        "norm and rotation backward launch",
+                        [&](void* ws) { return spconv::launch_norm_rotary_backward(a, ws, stream); });
 }
 
 // Nothing throws across the ABI: a host allocation that fails becomes a status.
@@ -1607,71 +1754,36 @@ spconv_status spconv_select_dataflow(const void* d_feats, const void* d_weights,
 }
 
 spconv_status spconv_attention_forward(const spconv_attention* args, void* d_out, float* d_lse, void* hip_stream) {
-  return guarded([&]() -> spconv_status {
-    g_last_error.clear();
-    spconv::AttentionArgs a;
-    AttentionTensors t;
-    spconv_status st = attention_args(args, d_out, d_lse, &a, &t);
-    if (st != SPCONV_OK) return st;
-    for (const Strided* out : {&t.out, &t.lse}) {
-      for (const Strided* in : {&t.q, &t.k, &t.v}) {
-        st = check_apart(*out, *in);
-        if (st != SPCONV_OK) return st;
-      }
-    }
-    st = check_apart(t.out, t.lse);
-    if (st != SPCONV_OK) return st;
-    if (a.total_q == 0) return SPCONV_OK;
-    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-    return with_workspace(spconv::attention_workspace_bytes(a), stream, "attention launch",
-                          [&](void* ws) { return spconv::launch_attention(a, ws, stream); });
-  });
+  return guarded([&] { return attention_forward(args, d_out, d_lse, nullptr, hip_stream); });
+}
+
+spconv_status spconv_attention_forward_noalloc(const spconv_attention* args, void* d_out, float* d_lse, void* d_workspace,
+                                               uint64_t workspace_bytes, void* hip_stream) {
+  const CallerWorkspace own = {d_workspace, workspace_bytes};
+  return guarded([&] { return attention_forward(args, d_out, d_lse, &own, hip_stream); });
 }
 
 spconv_status spconv_attention_backward(const spconv_attention* args, const void* d_out, const float* d_lse,
                                         const spconv_attention_gradients* grads, void* hip_stream) {
+  return guarded([&] { return attention_backward(args, d_out, d_lse, grads, nullptr, hip_stream); });
+}
+
+spconv_status spconv_attention_backward_noalloc(const spconv_attention* args, const void* d_out, const float* d_lse,
+                                                const spconv_attention_gradients* grads, void* d_workspace, uint64_t workspace_bytes,
+                                                void* hip_stream) {
+  const CallerWorkspace own = {d_workspace, workspace_bytes};
+  return guarded([&] { return attention_backward(args, d_out, d_lse, grads, &own, hip_stream); });
+}
+
+spconv_status spconv_attention_workspace(const spconv_attention* args, uint64_t* forward_bytes, uint64_t* backward_bytes) {
   return guarded([&]() -> spconv_status {
     g_last_error.clear();
     spconv::AttentionArgs a;
-    AttentionTensors t;
-    spconv_status st = attention_args(args, d_out, d_lse, &a, &t);
+    const spconv_status st = attention_sizes(args, &a);
     if (st != SPCONV_OK) return st;
-    if (grads == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grads is NULL");
-    const uint64_t es = t.q.es;
-    const Strided go = {"grad_out", grads->grad_out, a.total_q, grads->grad_out_row_stride, a.heads, grads->grad_out_head_stride, a.dim, es};
-    const Strided gq = {"grad_q", grads->grad_q, a.total_q, grads->grad_q_row_stride, a.heads, grads->grad_q_head_stride, a.dim, es};
-    const Strided gk = {"grad_k", grads->grad_k, a.total_k, grads->grad_k_row_stride, a.kv_heads, grads->grad_k_head_stride, a.dim, es};
-    const Strided gv = {"grad_v", grads->grad_v, a.total_k, grads->grad_v_row_stride, a.kv_heads, grads->grad_v_head_stride, a.dim, es};
-    st = check_strided(go, false);
-    if (st != SPCONV_OK) return st;
-    for (const Strided* out : {&gq, &gk, &gv}) {
-      st = check_strided(*out, true);
-      if (st != SPCONV_OK) return st;
-      for (const Strided& in : {t.q, t.k, t.v, t.out, t.lse, go}) {
-        st = check_apart(*out, in);
-        if (st != SPCONV_OK) return st;
-      }
-    }
-    for (const auto& pair : {std::make_pair(&gq, &gk), std::make_pair(&gq, &gv), std::make_pair(&gk, &gv)}) {
-      st = check_apart(*pair.first, *pair.second);
-      if (st != SPCONV_OK) return st;
-    }
-    a.grad_out = go.p;
-    a.go_row = go.row_stride;
-    a.go_head = go.head_stride;
-    a.grad_q = grads->grad_q;
-    a.gq_row = gq.row_stride;
-    a.gq_head = gq.head_stride;
-    a.grad_k = grads->grad_k;
-    a.gk_row = gk.row_stride;
-    a.gk_head = gk.head_stride;
-    a.grad_v = grads->grad_v;
-    a.gv_row = gv.row_stride;
-    a.gv_head = gv.head_stride;
-    if (a.total_q == 0 && a.total_k == 0) return SPCONV_OK;
-    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-    return with_workspace(spconv::attention_backward_workspace_bytes(a), stream, "attention backward launch",
-                          [&](void* ws) { return spconv::launch_attention_backward(a, ws, stream); });
+    if (forward_bytes != nullptr) *forward_bytes = a.total_q == 0 ? 0 : spconv::attention_workspace_bytes(a);
+    if (backward_bytes != nullptr) *backward_bytes = a.total_q == 0 && a.total_k == 0 ? 0 : spconv::attention_backward_workspace_bytes(a);
+    return SPCONV_OK;
   });
 }
 
@@ -1704,45 +1816,24 @@ spconv_status spconv_norm_rotary_forward(const spconv_norm_rotary* args, void* d
 
 spconv_status spconv_norm_rotary_backward(const spconv_norm_rotary* args, const spconv_norm_rotary_gradients* grads,
                                           void* hip_stream) {
-  return guarded([&]() -> spconv_status {
-    g_last_error.clear();
-    spconv::NormRotaryArgs a;
-    Strided in[2];
-    spconv_status st = norm_rotary_args(args, &a, in);
-    if (st != SPCONV_OK) return st;
-    if (grads == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grads is NULL");
-    if ((reinterpret_cast<uintptr_t>(grads->grad_q_weight) | reinterpret_cast<uintptr_t>(grads->grad_k_weight)) & 3u) {
-      return fail(SPCONV_ERR_INVALID_ARG, "the weight gradients must be 4-byte aligned");
-    }
-    const Strided g[2] = {
-        {"grad_q_out", grads->grad_q_out, a.rows, grads->grad_q_out_row_stride, a.t[0].heads, grads->grad_q_out_head_stride, a.dim, in[0].es},
-        {"grad_k_out", grads->grad_k_out, a.rows, grads->grad_k_out_row_stride, a.t[1].heads, grads->grad_k_out_head_stride, a.dim, in[0].es}};
-    const Strided gx[2] = {
-        {"grad_q", grads->grad_q, a.rows, grads->grad_q_row_stride, a.t[0].heads, grads->grad_q_head_stride, a.dim, in[0].es},
-        {"grad_k", grads->grad_k, a.rows, grads->grad_k_row_stride, a.t[1].heads, grads->grad_k_head_stride, a.dim, in[0].es}};
-    for (int i = 0; i < 2; ++i) {
-      st = check_strided(g[i], false);
-      if (st == SPCONV_OK) st = check_strided(gx[i], true);
-      for (int j = 0; j < 2 && st == SPCONV_OK; ++j) {
-        st = check_apart(gx[i], in[j]);
-        if (st == SPCONV_OK && (i != j || !same_place(gx[i], g[j]))) st = check_apart(gx[i], g[j]);
-      }
-      if (st != SPCONV_OK) return st;
-      a.t[i].grad = g[i].p;
-      a.t[i].g_row = g[i].row_stride;
-      a.t[i].g_head = g[i].head_stride;
-      a.t[i].grad_x = const_cast<void*>(gx[i].p);
-      a.t[i].gx_row = gx[i].row_stride;
-      a.t[i].gx_head = gx[i].head_stride;
-    }
-    st = check_apart(gx[0], gx[1]);
-    if (st != SPCONV_OK) return st;
-    a.t[0].grad_weight = grads->grad_q_weight;
-    a.t[1].grad_weight = grads->grad_k_weight;
-    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-    return with_workspace(spconv::norm_rotary_backward_workspace_bytes(a), stream, "norm and rotation backward launch",
-                          [&](void* ws) { return spconv::launch_norm_rotary_backward(a, ws, stream); });
-  });
+  return guarded([&] { return norm_rotary_backward(args, grads, nullptr, hip_stream); });
+}
+
+spconv_status spconv_norm_rotary_backward_noalloc(const spconv_norm_rotary* args, const spconv_norm_rotary_gradients* grads,
+                                                  void* d_workspace, uint64_t workspace_bytes, void* hip_stream) {
+  const CallerWorkspace own = {d_workspace, workspace_bytes};
+  return guarded([&] { return norm_rotary_backward(args, grads, &own, hip_stream); });
+}
+
+spconv_status spconv_norm_rotary_workspace(int32_t head_dim, uint64_t* backward_bytes) {
+  g_last_error.clear();
+  const spconv_status st = check_head_dim(SPCONV_F32, head_dim);
+  if (st != SPCONV_OK) return st;
+  if (backward_bytes == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "backward_bytes is NULL");
+  spconv::NormRotaryArgs a;
+  a.dim = head_dim;
+  *backward_bytes = spconv::norm_rotary_backward_workspace_bytes(a);
+  return SPCONV_OK;
 }
 
 spconv_status spconv_rotary_table(float* d_table, int32_t extent, int32_t pairs, double base, double position_scale,
