@@ -554,7 +554,9 @@ typedef struct spconv_attention {
  * no byte with an input.
  *
  * Errors: INVALID_ARG (NULL or misaligned pointer, negative or too large
- * size (total rows x heads below 2^31), kv_heads not dividing heads, stride
+ * size (rows x heads below 2^31; a launch below 2^32 work items, about 2 for
+ * each row and head and 64 to 256 for each sequence and key head), kv_heads
+ * not dividing heads, stride
  * not a multiple of 16 bytes or negative, scale not positive and finite,
  * d_out or d_lse overlapping an input), UNSUPPORTED (dtype, head_dim),
  * OUT_OF_MEMORY, DEVICE.
@@ -657,7 +659,8 @@ typedef struct spconv_norm_rotary {
 /* Writes d_q_out [rows][q_heads][head_dim] and d_k_out [rows][k_heads][head_dim]
  * (strides in elements).  An output may be its own input with the same
  * strides (in place), and otherwise shares no byte with an input.  Errors:
- * INVALID_ARG, UNSUPPORTED (dtype, head_dim, rotary_dim), DEVICE. */
+ * INVALID_ARG (also for 2^32 work items, one of 64 bytes of a tensor each),
+ * UNSUPPORTED (dtype, head_dim, rotary_dim), DEVICE. */
 spconv_status spconv_norm_rotary_forward(const spconv_norm_rotary* args, void* d_q_out, int64_t q_out_row_stride,
                                          int64_t q_out_head_stride, void* d_k_out, int64_t k_out_row_stride,
                                          int64_t k_out_head_stride, void* hip_stream);
@@ -702,7 +705,7 @@ spconv_status spconv_norm_rotary_backward_noalloc(const spconv_norm_rotary* args
  * in double precision and rounded to fp32.  Longer ranges than a model was
  * trained on are reached by a position_scale below 1 or a larger base.
  * Errors: INVALID_ARG (NULL or misaligned table, extent or pairs not in
- * [1, 2^24], base not positive and finite, scale not finite), DEVICE.
+ * [1, 2^24] or their product not below 2^32, base not positive and finite, scale not finite), DEVICE.
  */
 spconv_status spconv_rotary_table(float* d_table, int32_t extent, int32_t pairs, double base, double position_scale,
                                   void* hip_stream);

@@ -646,6 +646,12 @@ spconv_status attention_sizes(const spconv_attention* x, spconv::AttentionArgs* 
   return SPCONV_OK;
 }
 
+// A call whose launches are larger than a dispatch can be.
+spconv_status check_work_items(uint64_t items) {
+  if (items <= spconv::kMaxWorkItems) return SPCONV_OK;
+  return fail(SPCONV_ERR_INVALID_ARG, "the call takes %llu work items in one launch, of at most 2^32 - 1: split it", (unsigned long long)items);
+}
+
 // Validates an attention call and fills its launch arguments.
 spconv_status attention_args(const spconv_attention* x, const void* d_out, const float* d_lse,
                              spconv::AttentionArgs* a, AttentionTensors* t) {
@@ -807,6 +813,7 @@ spconv_status attention_forward(const spconv_attention* args, void* d_out, float
     }
   }
   st = check_apart(t.out, t.lse);
+  if (st == SPCONV_OK) st = check_work_items(spconv::attention_work_items(a));
   if (st != SPCONV_OK) return st;
   if (a.total_q == 0) return SPCONV_OK;
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
@@ -853,6 +860,8 @@ spconv_status attention_backward(const spconv_attention* args, const void* d_out
   a.grad_v = grads->grad_v;
   a.gv_row = gv.row_stride;
   a.gv_head = gv.head_stride;
+  st = check_work_items(spconv::attention_backward_work_items(a));
+  if (st != SPCONV_OK) return st;
   if (a.total_q == 0 && a.total_k == 0) return SPCONV_OK;
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   return with_workspace(spconv::attention_backward_workspace_bytes(a), own, {&t.q, &t.k, &t.v, &t.out, &t.lse, &go, &gq, &gk, &gv}, stream,
@@ -1808,6 +1817,7 @@ spconv_status spconv_norm_rotary_forward(const spconv_norm_rotary* args, void* d
       a.t[i].y_head = out[i].head_stride;
     }
     st = check_apart(out[0], out[1]);
+    if (st == SPCONV_OK) st = check_work_items(spconv::norm_rotary_work_items(a));
     if (st != SPCONV_OK) return st;
     const hipError_t e = spconv::launch_norm_rotary(a, static_cast<hipStream_t>(hip_stream));
     return e == hipSuccess ? SPCONV_OK : hip_fail(e, "norm and rotation launch");
@@ -1848,6 +1858,8 @@ spconv_status spconv_rotary_table(float* d_table, int32_t extent, int32_t pairs,
   if (!(base > 0.0) || !std::isfinite(base) || !std::isfinite(position_scale)) {
     return fail(SPCONV_ERR_INVALID_ARG, "base = %g must be positive and finite, position_scale = %g finite", base, position_scale);
   }
+  const spconv_status st = check_work_items((static_cast<uint64_t>(extent) * pairs + 255) / 256 * 256);
+  if (st != SPCONV_OK) return st;
   const hipError_t e = spconv::launch_rotary_table(d_table, extent, pairs, base, position_scale, static_cast<hipStream_t>(hip_stream));
   return e == hipSuccess ? SPCONV_OK : hip_fail(e, "rotary table launch");
 }

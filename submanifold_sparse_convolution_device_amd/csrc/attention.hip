@@ -449,7 +449,21 @@ Plan make_forward_plan(const AttentionArgs& a) {
   return p;
 }
 
+// Workgroups of the attention kernel.
+int64_t forward_groups(const AttentionArgs& a, const Plan& p) {
+  const int64_t placed = p.chunks.slots > 0 ? p.chunks.slots + p.slots : placed_slots(p.slots, p.ordered ? 0 : slot_run(a, p.slots));
+  return placed * a.kv_heads * p.nsplit;
+}
+
 }  // namespace
+
+uint64_t attention_work_items(const AttentionArgs& a) {
+  const Plan p = make_forward_plan(a);
+  const uint64_t groups = static_cast<uint64_t>(forward_groups(a, p)) * 64 * p.waves;
+  const uint64_t rows = static_cast<uint64_t>(a.total_q) * a.heads;
+  const uint64_t join = p.chunks.slots > 0 ? (static_cast<uint64_t>(a.total_q) + a.batch + 2) * 256 : p.nsplit > 1 ? rows * (a.dim / 4) + 255 : 0;
+  return std::max(groups, join);
+}
 
 size_t attention_workspace_bytes(const AttentionArgs& a) {
   const Plan p = make_forward_plan(a);
@@ -471,8 +485,7 @@ hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t
     typedef decltype(t) T;
     constexpr int DP = decltype(dp)::value, DQ = decltype(dq)::value;
     const int run = p.ordered ? 0 : slot_run(a, p.slots), slots = static_cast<int>(p.slots);
-    const int64_t placed = p.chunks.slots > 0 ? p.chunks.slots + p.slots : placed_slots(p.slots, run);
-    const dim3 grid(static_cast<unsigned>(placed * a.kv_heads * p.nsplit));
+    const dim3 grid(static_cast<unsigned>(forward_groups(a, p)));
     if (p.waves == 1) k_attention<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, order, part_out, part_lse);
     else if (p.waves == 2) k_attention<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, order, part_out, part_lse);
     else k_attention<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, slots, run, p.nsplit, p.chunks, order, part_out, part_lse);

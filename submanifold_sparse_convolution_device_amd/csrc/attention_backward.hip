@@ -575,6 +575,10 @@ Plan make_backward_plan(const AttentionArgs& a) {
   return p;
 }
 
+// Workgroups of the query gradient and of the key and value gradients.
+int64_t q_groups(const AttentionArgs& a, const Plan& p) { return placed_slots(p.q_slots, p.ordered ? 0 : slot_run(a, p.q_slots)) * a.kv_heads * p.q_split; }
+int64_t k_groups(const AttentionArgs& a, const Plan& p) { return placed_slots(p.k_slots, p.ordered ? 0 : slot_run(a, p.k_slots)) * a.kv_heads * p.k_split; }
+
 struct Workspace {
   size_t stats, q, k, v, q_order, k_order, total;  // offsets in bytes
 };
@@ -594,6 +598,14 @@ Workspace layout(const AttentionArgs& a, const Plan& p) {
 }
 
 }  // namespace
+
+uint64_t attention_backward_work_items(const AttentionArgs& a) {
+  const Plan p = make_backward_plan(a);
+  uint64_t join = 0;
+  if (p.q_split > 1) join += static_cast<uint64_t>(a.total_q) * a.heads * (a.dim / 4) + 255;
+  if (p.k_split > 1) join += 2 * (static_cast<uint64_t>(a.total_k) * a.kv_heads * (a.dim / 4) + 255);
+  return std::max({join, static_cast<uint64_t>(q_groups(a, p)) * 64 * p.q_waves, static_cast<uint64_t>(k_groups(a, p)) * 64 * p.k_waves});
+}
 
 size_t attention_backward_workspace_bytes(const AttentionArgs& a) { return layout(a, make_backward_plan(a)).total; }
 
@@ -619,7 +631,7 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
     constexpr int DP = decltype(dp)::value, DQ = decltype(dq)::value;
     if (a.total_q > 0) {
       const int run = p.ordered ? 0 : slot_run(a, p.q_slots);
-      const dim3 grid(static_cast<unsigned>(placed_slots(p.q_slots, run) * a.kv_heads * p.q_split));
+      const dim3 grid(static_cast<unsigned>(q_groups(a, p)));
       if (p.q_waves == 1) k_attention_dq<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, stats, part_q);
       else if (p.q_waves == 2) k_attention_dq<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, stats, part_q);
       else k_attention_dq<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.q_slots), run, p.q_split, q_order, stats, part_q);
@@ -628,7 +640,7 @@ hipError_t launch_attention_backward(const AttentionArgs& a, void* workspace, hi
     }
     if (a.total_k > 0) {
       const int run = p.ordered ? 0 : slot_run(a, p.k_slots);
-      const dim3 grid(static_cast<unsigned>(placed_slots(p.k_slots, run) * a.kv_heads * p.k_split));
+      const dim3 grid(static_cast<unsigned>(k_groups(a, p)));
       if (p.k_waves == 1) k_attention_dkv<T, DP, DQ, 1><<<grid, 64, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, stats, part_k, part_v);
       else if (p.k_waves == 2) k_attention_dkv<T, DP, DQ, 2><<<grid, 128, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, stats, part_k, part_v);
       else k_attention_dkv<T, DP, DQ, 4><<<grid, 256, 0, stream>>>(a, static_cast<int>(p.k_slots), run, p.k_split, k_order, stats, part_k, part_v);

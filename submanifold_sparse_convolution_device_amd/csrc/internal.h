@@ -317,6 +317,11 @@ struct AttentionArgs {
   void* grad_v = nullptr;
   int64_t gq_row = 0, gq_head = 0, gk_row = 0, gk_head = 0, gv_row = 0, gv_head = 0;
 };
+// The most work items of a launch that the call makes; a dispatch holds
+// kMaxWorkItems.
+constexpr uint64_t kMaxWorkItems = (uint64_t(1) << 32) - 1;
+uint64_t attention_work_items(const AttentionArgs& a);
+uint64_t attention_backward_work_items(const AttentionArgs& a);
 size_t attention_workspace_bytes(const AttentionArgs& a);
 hipError_t launch_attention(const AttentionArgs& a, void* workspace, hipStream_t stream);
 size_t attention_backward_workspace_bytes(const AttentionArgs& a);
@@ -346,6 +351,7 @@ struct NormRotaryArgs {
   const int32_t* positions = nullptr;  // [rows][axes], row stride in elements
   int64_t pos_row = 0;
 };
+uint64_t norm_rotary_work_items(const NormRotaryArgs& a);
 hipError_t launch_norm_rotary(const NormRotaryArgs& a, hipStream_t stream);
 size_t norm_rotary_backward_workspace_bytes(const NormRotaryArgs& a);
 hipError_t launch_norm_rotary_backward(const NormRotaryArgs& a, void* workspace, hipStream_t stream);

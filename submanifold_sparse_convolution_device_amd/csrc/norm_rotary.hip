@@ -381,6 +381,11 @@ int64_t blocks_for(const NormRotaryArgs& a, const NormRotaryTensor& t, int64_t u
 
 }  // namespace
 
+uint64_t norm_rotary_work_items(const NormRotaryArgs& a) {
+  const int64_t upb = kWaves * 64 / lanes_per_unit(a) * kUnits;
+  return static_cast<uint64_t>(blocks_for(a, a.t[0], upb) + blocks_for(a, a.t[1], upb)) * (64 * kWaves);
+}
+
 hipError_t launch_norm_rotary(const NormRotaryArgs& a, hipStream_t stream) {
   if (a.rows == 0 || a.t[0].heads + a.t[1].heads == 0) return hipSuccess;
   return dispatch(a, [&](auto t, auto lanes, auto turn) -> hipError_t {
