@@ -65,7 +65,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   constexpr int KS = DQ / (2 * kPiece);      // pieces per half of a row
   constexpr int NL = (BN * PPR + NT - 1) / NT;  // pieces each thread copies per tile
   __shared__ uint4 ks[BUFS][kPlanes<T> * BN * PPR], vs[BUFS][kPlanes<T> * BN * PPR];
-  __shared__ int scrubbed[WAVES];  // whether the wave found infinities or NaN in values of edge tiles
+  __shared__ uint32_t scrubbed[WAVES];  // edge tiles in whose values the wave found infinities or NaN, by their number modulo 32
 
   // a tile's splits follow one another (nsplit is a power of two)
   const int split = static_cast<int>(blockIdx.x) & (nsplit - 1), id = static_cast<int>(blockIdx.x) >> __builtin_ctz(nsplit);
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       bool met = false;
 #pragma unroll
       for (int n = 0; n < NL; ++n) met |= scrub<T>(vr[n]);
-      if (__any(met)) scrubbed[wave] = 1;
+      if (__any(met)) scrubbed[wave] |= 1u << (jb & 31);
     }
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
@@ -267,23 +267,28 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   }
 
   if (jb0 < jb1) {
-    int met = 0;
+    uint32_t met = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) met |= scrubbed[w];  // (a barrier has passed since the last was set)
-    if (__builtin_amdgcn_readfirstlane(met)) {
+    met = __builtin_amdgcn_readfirstlane(static_cast<int>(met));
+    if (__builtin_expect(met != 0, 0)) {
       for (int jb = jb0; jb < jb1; ++jb) {
-        if (!is_edge(jb)) continue;
-        const int j1 = min(wg.lo + (jb + 1) * BN, lane_hi);
-        for (int j = max(wg.lo + jb * BN, lane_lo); has_row && j < j1; ++j) {
-          const T* src = vbase + j * a.v_row;
+        if ((met >> (jb & 31) & 1) == 0 || !is_edge(jb)) continue;
+#pragma unroll 1
+        for (int j0 = wg.lo + jb * BN; j0 < wg.lo + (jb + 1) * BN; j0 += 32) {
+          for (uint32_t bad = rows_not_finite(vbase, a.v_row, j0, sp.nk, a.dim, lane); bad != 0; bad &= bad - 1) {
+            const int j = j0 + __builtin_ctz(bad);
+            if (!has_row || j < lane_lo || j >= lane_hi) continue;
+            const T* src = vbase + j * a.v_row;
 #pragma unroll
-          for (int db = 0; db < DB; ++db)
+            for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int d = db * 32 + 4 * half + c_row(i);
-              const float x = d < a.dim ? to_f32(src[d]) : 0.f;
-              acc[db][i] += fabsf(x) < INFINITY ? 0.f : x;
-            }
+              for (int i = 0; i < 16; ++i) {
+                const int d = db * 32 + 4 * half + c_row(i);
+                const float x = d < a.dim ? to_f32(src[d]) : 0.f;
+                acc[db][i] += fabsf(x) < INFINITY ? 0.f : x;
+              }
+          }
         }
       }
     }

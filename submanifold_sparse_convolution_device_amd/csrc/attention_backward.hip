@@ -181,7 +181,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const int edge_hi = a.right >= 0 ? min(div_group(a, sp.r0) + shift + a.right + 1, edge_end) : edge_end;
   const int edge_lo = a.left >= 0 ? div_group(a, min(sp.r0 + BM, rows) - 1) + shift - a.left : 0;
   auto is_edge = [&](int jb) { return wg.lo + (jb + 1) * BN > edge_hi || wg.lo + jb * BN < edge_lo; };
-  uint64_t met_tiles = 0;  // edge tiles with such keys, by their number modulo 64
+  uint32_t met_tiles = 0;  // edge tiles with such keys, by their number modulo 32
   auto store = [&](int buf, int jb) {
     if (is_edge(jb)) {
       bool met = false;
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       for (int w = 0; w < WAVES; ++w) met |= scrubbed[buf][w];
       met = __builtin_amdgcn_readfirstlane(met);
       if (met) {
-        met_tiles |= uint64_t(1) << (jb & 63);
+        met_tiles |= 1u << (jb & 31);
         for (int b = 0; b < BN / 32; ++b)  // (every wave writes the same)
           bad_keys[buf][b] = rows_not_finite(kbase, a.k_row, wg.lo + jb * BN + 32 * b, sp.nk, a.dim, lane);
       }
@@ -260,22 +260,22 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   }
   if (met_tiles != 0) {
     for (int jb = jb0; jb < jb1; ++jb) {
-      if ((met_tiles >> (jb & 63) & 1) == 0 || !is_edge(jb)) continue;
-      const int j1 = min(wg.lo + (jb + 1) * BN, lane_hi);
-      for (int j = max(wg.lo + jb * BN, lane_lo); has_row && j < j1; ++j) {
-        const T* src = kbase + j * a.k_row;
-        bool bad = false;
-        for (int e = 0; e < a.dim; ++e) bad |= !(fabsf(to_f32(src[e])) < INFINITY);
-        if (!bad) continue;
+      if ((met_tiles >> (jb & 31) & 1) == 0 || !is_edge(jb)) continue;
+      for (int j0 = wg.lo + jb * BN; j0 < wg.lo + (jb + 1) * BN; j0 += 32) {
+        for (uint32_t bad = rows_not_finite(kbase, a.k_row, j0, sp.nk, a.dim, lane); bad != 0; bad &= bad - 1) {
+          const int j = j0 + __builtin_ctz(bad);
+          if (!has_row || j < lane_lo || j >= lane_hi) continue;
+          const T* src = kbase + j * a.k_row;
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
+          for (int db = 0; db < DB; ++db)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int d = db * 32 + 4 * half + c_row(i);
-            const float x = d < a.dim ? to_f32(src[d]) : 0.f;
-            // 0 times the value, or a NaN of the row's lse
-            acc[db][i] += 0.f * x + 0.f * lse2;
-          }
+            for (int i = 0; i < 16; ++i) {
+              const int d = db * 32 + 4 * half + c_row(i);
+              const float x = d < a.dim ? to_f32(src[d]) : 0.f;
+              // 0 times the value, or a NaN of the row's lse
+              acc[db][i] += 0.f * x + 0.f * lse2;
+            }
+        }
       }
     }
   }

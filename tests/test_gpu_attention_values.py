@@ -267,3 +267,31 @@ def test_fp32_scores_of_an_infinite_key_are_nan(sp, value, n):
     out, lse = sp.attention(q, k, v, cu, causal=True, return_lse=True)
     assert bool(torch.isnan(out[n // 2:]).all()) and bool(torch.isnan(lse[n // 2:]).all())
     assert bool(torch.isfinite(out[:n // 2]).all())
+
+
+# ------------------------------------------------------------------ time
+
+
+@pytest.mark.parametrize("dtype,causal", [("f32", False), ("f32", True), ("bf16", True)])
+def test_one_bad_value_costs_little(sp, dtype, causal):
+    """A value that is not finite is looked for in its own tile only: less than
+    three times a clean call, where going over every key again took 8 to 11
+    times one (4 in bf16)."""
+    n = 8000
+    q, k, v = _inputs(7, n, n, 2, 2, 64, dtype)[1]
+    cu = ref.offsets([n]).to(DEV)
+    bad = v.clone()
+    bad[n // 2, 0, 3] = math.nan
+
+    def fastest(x):
+        times = []
+        for _ in range(8):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            sp.attention(q, k, x, cu, causal=causal)
+            end.record()
+            end.synchronize()
+            times.append(start.elapsed_time(end))
+        return min(times)
+
+    assert fastest(bad) < 3 * fastest(v)
