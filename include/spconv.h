@@ -521,8 +521,11 @@ spconv_status spconv_select_dataflow(const void* d_feats, const void* d_weights,
  *
  * Infinities and NaN of a key or value row reach only the queries that see the
  * row, and those of a query or output gradient only the gradients of keys that
- * it sees.  An infinite value gives an infinite output (in F16, NaN where the
- * probability rounds to zero); F32 scores of an infinite query or key are NaN.
+ * it sees.  A score of -infinity is a probability of 0 (in F32 every score of
+ * an infinite query or key is NaN); a query that sees keys but has no other
+ * scores, or whose largest scaled score is not an fp32 number, gets NaN.  An
+ * infinite value gives an infinite output, or NaN where its probability
+ * rounds to 0 (2^-126 of the row's largest and below, in F16 2^-25).
  *
  * Scores, softmax statistics and all sums are fp32.  F16 and BF16 round the
  * probabilities (and the score gradients) to the dtype as operands of the

@@ -294,8 +294,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     }
   }
   const float sum = halves_sum(l);
-  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // a NaN stays one
-  const float lse = sum == 0.f ? -INFINITY : ln_scaled(m, sum);
+  // Without a term: 0 for a row that sees no key; NaN for one whose scores are
+  // all -inf, or whose largest is beyond fp32.  (A part of such scores counts
+  // as -inf when it is joined.)  A NaN stays one.
+  const bool none = max(lane_lo, WAVES == 1 ? chunk0 : 0) >= lane_hi;
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f && none ? 0.f : __builtin_nanf("");
+  const float lse = sum == 0.f ? (m == INFINITY ? __builtin_nanf("") : -INFINITY) : ln_scaled(m, sum);
   const int64_t row_out = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
   if (nsplit == 1 && (WAVES > 1 || part_row < 0)) {
     if (has_row && half == 0) a.lse[row_out] = lse;
@@ -315,10 +319,11 @@ template <class T>
 __device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* part_out, const float* part_lse, int64_t first,
                                            int64_t step, int parts, int64_t row_out) {
   __shared__ float4 acc_s[256];
-  __shared__ float top_s[256], sum_s[256];
+  __shared__ float top_s[256], sum_s[256], blank_s[256];
   const int quads = a.dim / 4, groups = 256 / quads, g = static_cast<int>(threadIdx.x) / quads, quad = static_cast<int>(threadIdx.x) - g * quads;
   float top = -INFINITY, sum = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float blank = 0.f;  // NaN if the row sees a key in a part without a term
   constexpr int kBatch = 4;  // parts whose loads are issued together
   for (int p0 = g; g < groups && p0 < parts; p0 += kBatch * groups) {
     float ls[kBatch];
@@ -331,7 +336,11 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* 
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (p0 + i * groups >= parts || ls[i] == -INFINITY) continue;
+      if (p0 + i * groups >= parts) continue;
+      if (ls[i] == -INFINITY) {
+        blank += o[i].x;
+        continue;
+      }
       const float now = fmaxf(top, ls[i]);
       const float keep = fast_exp2((top - now) * kLog2e), e = fast_exp2((ls[i] - now) * kLog2e);
       top = now;
@@ -345,13 +354,16 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* 
   acc_s[threadIdx.x] = x;
   top_s[threadIdx.x] = top;
   sum_s[threadIdx.x] = sum;
+  blank_s[threadIdx.x] = blank;
   __syncthreads();
   if (g != 0) return;
   float all = -INFINITY;
   for (int q = 0; q < groups; ++q) all = fmaxf(all, top_s[q * quads + quad]);
   sum = 0.f;
   x = make_float4(0.f, 0.f, 0.f, 0.f);
+  blank = 0.f;
   for (int q = 0; q < groups; ++q) {
+    blank += blank_s[q * quads + quad];
     // A group without parts has a sum of 0.  (Its maximum does not tell: parts
     // whose lse is NaN leave that at -inf as well, and must reach the row.)
     if (sum_s[q * quads + quad] == 0.f) continue;
@@ -363,7 +375,7 @@ __device__ __forceinline__ void join_parts(const AttentionArgs& a, const float* 
     x.z += e * o.z;
     x.w += e * o.w;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? blank : 1.f / sum;
   store4<T>(static_cast<T*>(a.out) + row_out * a.dim + 4 * quad, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
   if (quad == 0) a.lse[row_out] = sum == 0.f ? -INFINITY : all + ln_scaled(0.f, sum);
 }
@@ -381,19 +393,24 @@ __global__ __launch_bounds__(256) void k_attention_join(AttentionArgs a, int nsp
   const int quad = static_cast<int>(id - row * quads);
   float top = -INFINITY;
   for (int s = 0; s < nsplit; ++s) top = fmaxf(top, part_lse[s * rows + row]);
-  float sum = 0.f;
+  float sum = 0.f, blank = 0.f;  // blank: NaN if the row sees a key in a part without a term
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = 0; s < nsplit; ++s) {
     const float ls = part_lse[s * rows + row];
-    const float4 o = *reinterpret_cast<const float4*>(part_out + (s * rows + row) * a.dim + 4 * quad);
-    const float e = ls == -INFINITY ? 0.f : fast_exp2((ls - top) * kLog2e);
+    float4 o = *reinterpret_cast<const float4*>(part_out + (s * rows + row) * a.dim + 4 * quad);
+    float e = fast_exp2((ls - top) * kLog2e);
+    if (ls == -INFINITY) {
+      blank += o.x;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      e = 0.f;
+    }
     sum += e;
     x.x += e * o.x;
     x.y += e * o.y;
     x.z += e * o.z;
     x.w += e * o.w;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? blank : 1.f / sum;
   store4<T>(static_cast<T*>(a.out) + row * a.dim + 4 * quad, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
   if (quad == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + ln_scaled(0.f, sum);
 }

@@ -180,6 +180,41 @@ def test_one_infinite_component_of_a_key(sp, dtype, dim, n, at, how):
     _near("grad_v", gv[rest.to(DEV)], want["grad_v"][rest], want["grad_v_tol"][rest])
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("nq,nk,some", [(300, 300, 0), (1100, 1100, 0), (1, 3000, 0), (1, 3000, 1700), (1100, 1100, 900), (3, 400, 0)])
+def test_rows_whose_scores_are_all_minus_infinity(sp, dtype, nq, nk, some):
+    """Keys of which all (but one, `some`) score -inf with every query: no
+    probabilities, so NaN and lse -inf, or all weight on the one key.  Rows
+    that see no key stay 0.  In one pass, in splits and by parts."""
+    cu_q, cu_k = ref.offsets([nq, 2]), ref.offsets([nk, 0])
+    q, k, v = _inputs(nq + nk, nq + 2, nk, 2, 1, 32, dtype)[0]
+    q[:, :, 5] = -1.0
+    k[:, 0, 5] = math.inf
+    if some:
+        k[some, 0, 5] = 0.5
+    dev = tuple(t.to(DEV) for t in (q, k, v))
+    out, lse = sp.attention(*dev, cu_q.to(DEV), cu_k.to(DEV), return_lse=True)
+    assert bool((out[nq:] == 0).all()) and bool((lse[nq:] == -math.inf).all())
+    if some:
+        score = (q[:nq].double() * k[some, 0].double()).sum(-1) / 32 ** 0.5
+        assert torch.allclose(lse[:nq].double().cpu(), score, rtol=0, atol=80 * 2.0 ** -24 * 8)
+        assert bool(((out[:nq].double().cpu() - v[some].double()).abs() <= 2 * ref.U[DT[dtype]] * v[some].double().abs() + ref.tiny(DT[dtype])).all())
+        return
+    assert bool(torch.isnan(out[:nq]).all()) and bool((lse[:nq] == -math.inf).all())
+    grads = sp.attention_backward(torch.randn(q.shape).to(DT[dtype]).to(DEV), *dev, out, lse, cu_q.to(DEV), cu_k.to(DEV))
+    assert bool(torch.isnan(grads[0][:nq]).all()) and bool((grads[0][nq:] == 0).all())
+    assert bool(torch.isnan(grads[1]).all()) and bool(torch.isnan(grads[2]).all())
+
+
+@pytest.mark.parametrize("nq,nk", [(40, 40), (1, 3000)])
+def test_scores_beyond_fp32_are_not_zeros(sp, nq, nk):
+    """Finite operands whose scaled score is not an fp32 number: NaN, not the
+    result of a row without keys."""
+    q, k = torch.full((nq, 1, 16), 3e18, device=DEV), torch.full((nk, 1, 16), 3e18, device=DEV)
+    out, lse = sp.attention(q, k, k, ref.offsets([nq]).to(DEV), ref.offsets([nk]).to(DEV), scale=4.0, return_lse=True)
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
 # ------------------------------------------------------------------ lse
 
 
