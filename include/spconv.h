@@ -529,7 +529,8 @@ spconv_status spconv_select_dataflow(const void* d_feats, const void* d_weights,
  *
  * Scores, softmax statistics and all sums are fp32.  F16 and BF16 round the
  * probabilities (and the score gradients) to the dtype as operands of the
- * matrix instructions; F32 operands are used whole (split exactly into three
+ * matrix instructions, and take D from the rounded d_out for queries that see
+ * more than a few keys; F32 operands are used whole (split exactly into three
  * bf16 parts each, the products down to 2^-24 of each other summed in fp32).
  * Results are rounded once, to nearest even.  Every sum has a fixed order: the
  * same call gives the same bits.

@@ -62,6 +62,17 @@ __device__ __forceinline__ void rescale(float (&ds)[16], float& factor, floatx16
 }
 constexpr float kFirstFactor = 1.2676506002282294e30f;  // 2^100
 
+// D comes from the output as it was rounded, and where a row sees few keys
+// the dO v and D of its dS nearly cancel: the 16-bit gradients of q and k were
+// 2.1 times as far from 64 bits as results that are rounded once at 3 keys, 1.6
+// at 16 and 1.5 at 40 (all where values are nearly equal); from 100 on it is
+// the 1.45 that the rounded dS itself makes.  Waves whose rows see at most so
+// many keys together take D = sum_j P_ij dP_ij in a walk of their own before,
+// straight from memory.  It takes 260 instead of 231 us in 4000 windows of up
+// to 64 rows, 8 heads of 32, with the other two kernels; windows of up to 343
+// rows and long causal sequences show nothing of it.
+constexpr int kFewKeys = 64;
+
 // Rows per LDS tile of the side that a workgroup walks, and tiles of its two
 // tensors in LDS (two: one read, one filled; a lone wave stages through one).
 template <class T, int DP, int WAVES>
@@ -69,8 +80,10 @@ constexpr int kWalk = sizeof(T) == 4 ? 32 : DP == 32 ? (WAVES == 4 ? 128 : 64) :
 template <int WAVES>
 constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 
+// (A lone wave at heads of up to 128 needs 340 registers: 355 us for 2000
+// windows of up to 32 rows, 8 heads; held to 256 it spills and takes 385.)
 template <class T, int DP, int DQ, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int run, int nsplit, const int32_t* order,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && (DP < 128 || WAVES > 1) ? 2 : 1) void k_attention_dq(AttentionArgs a, int slots, int run, int nsplit, const int32_t* order,
                                                                                     float2* stats, float* part) {
   typedef Tile<T, DP> TL;
   constexpr int BN = kWalk<T, DP, WAVES>, BUFS = kBuffers<WAVES>, PPR = TL::PPR, DB = DP / 32, NT = 64 * WAVES;
@@ -98,7 +111,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
   const int head = kvh * a.group + (has_row ? r - tok * a.group : 0);
   const int64_t row_out = static_cast<int64_t>(sp.q0 + tok) * a.heads + head;
   Frag<T> qf[KS], gf[KS];
-  float dot = 0.f;
+  Raw<T> go[KS], ov[KS];
   {
     const T* src = static_cast<const T*>(a.q) + static_cast<int64_t>(sp.q0 + tok) * a.q_row + static_cast<int64_t>(head) * a.q_head;
     const T* gsrc = static_cast<const T*>(a.grad_out) + static_cast<int64_t>(sp.q0 + tok) * a.go_row + static_cast<int64_t>(head) * a.go_head;
@@ -107,28 +120,10 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     for (int t = 0; t < KS; ++t) {
       const int e = (2 * t + half) * kPiece;
       const bool ok = has_row && e < a.dim;
-      const Raw<T> g = load_piece(gsrc + e, ok), o = load_piece(osrc + e, ok);
+      go[t] = load_piece(gsrc + e, ok);
+      ov[t] = load_piece(osrc + e, ok);
       qf[t] = to_frag<T>(load_piece(src + e, ok));
-      gf[t] = to_frag<T>(g);
-      typedef T part_t __attribute__((ext_vector_type(16 / sizeof(T))));
-#pragma unroll
-      for (int w = 0; w < static_cast<int>(sizeof(T) / 2); ++w) {
-        const part_t ov = __builtin_bit_cast(part_t, o.v[w]), gv = __builtin_bit_cast(part_t, g.v[w]);
-#pragma unroll
-        for (int u = 0; u < static_cast<int>(16 / sizeof(T)); ++u) dot = __builtin_fmaf(to_f32(gv[u]), to_f32(ov[u]), dot);
-      }
     }
-  }
-  dot = halves_sum(dot);
-  // exp(s - lse) as exp2(s c - lse2); a row without keys, or past the end, has P = 0
-  float lse2 = INFINITY;
-  if (has_row) {
-    const float v = a.lse[row_out];
-    lse2 = v == -INFINITY ? INFINITY : log2_units(v) - kShift<T>;
-    // for the other kernel, in the order in which it walks the rows; a D that
-    // is not finite makes NaN of both
-    if (half == 0 && split == 0)
-      stats[static_cast<int64_t>(kvh) * a.total_q * a.group + static_cast<int64_t>(sp.q0) * a.group + r] = make_float2(__builtin_fmaf(0.f, dot, lse2), dot);
   }
   const int place = tok + shift;
   const int lane_lo = a.left >= 0 ? place - a.left : 0;
@@ -166,11 +161,72 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     }
   };
 
+  // The first tile's loads are on their way while D is made (heads of up to
+  // 64: the registers of larger ones do not hold both).
+  constexpr bool kEarly = DP <= 64 && sizeof(T) == 2;
+  if (kEarly && jb0 < jb1) load(jb0);
+
+  float dot = 0.f;
+#pragma unroll
+  for (int t = 0; t < KS; ++t) {
+    gf[t] = to_frag<T>(go[t]);
+    typedef T part_t __attribute__((ext_vector_type(16 / sizeof(T))));
+#pragma unroll
+    for (int w = 0; w < static_cast<int>(sizeof(T) / 2); ++w) {
+      const part_t o = __builtin_bit_cast(part_t, ov[t].v[w]), g = __builtin_bit_cast(part_t, go[t].v[w]);
+#pragma unroll
+      for (int u = 0; u < static_cast<int>(16 / sizeof(T)); ++u) dot = __builtin_fmaf(to_f32(g[u]), to_f32(o[u]), dot);
+    }
+  }
+  dot = halves_sum(dot);
+  // exp(s - lse) as exp2(s c - lse2); a row without keys, or past the end, has P = 0
+  float lse2 = INFINITY;
+  if (has_row) {
+    const float v = a.lse[row_out];
+    lse2 = v == -INFINITY ? INFINITY : log2_units(v) - kShift<T>;
+  }
+  const float c = a.scale * kLog2e;
+  if constexpr (sizeof(T) == 2) {
+    if (wave_on && wv.hi > wv.lo && wv.hi - wv.lo <= kFewKeys) {
+      float sum = 0.f;
+#pragma unroll 1
+      for (int j0 = wv.lo; j0 < wv.hi; j0 += 32) {
+        const auto kbuf = rows_buffer(kbase + j0 * a.k_row, sp.nk - j0, kb), vbuf = rows_buffer(vbase + j0 * a.v_row, sp.nk - j0, vb);
+        Raw<T> kp[KS], vp[KS];
+#pragma unroll
+        for (int t = 0; t < KS; ++t) {
+          const int piece = 2 * t + half;
+          const bool on = piece * kPiece < a.dim;
+          kp[t] = load_piece<T>(kbuf, on ? (lane & 31) * kb + piece * kPieceBytes<T> : kNowhere);
+          vp[t] = load_piece<T>(vbuf, on ? (lane & 31) * vb + piece * kPieceBytes<T> : kNowhere);
+        }
+        floatx16 s(0.f), dp(0.f);
+#pragma unroll
+        for (int t = 0; t < KS; ++t) {
+          s = mma_frag<T>(to_frag<T>(kp[t]), qf[t], s);
+          dp = mma_frag<T>(to_frag<T>(vp[t]), gf[t], dp);
+        }
+        settle();
+        const int first = lane_lo - j0 - 4 * half, end = lane_hi - j0 - 4 * half;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = fast_exp2(__builtin_fmaf(s[i], c, -lse2)) * dp[i];
+          sum += c_row(i) >= first && c_row(i) < end ? x : 0.f;
+        }
+      }
+      sum = halves_sum(sum) * (__is_same(T, _Float16) ? 6.103515625e-05f : 1.f);  // P's shift
+      dot = fabsf(dot) < INFINITY ? sum : dot;
+    }
+  }
+  // The statistics for the other kernel, in the order in which it walks the
+  // rows; a D that is not finite makes NaN of both.
+  if (has_row && half == 0 && split == 0)
+    stats[static_cast<int64_t>(kvh) * a.total_q * a.group + static_cast<int64_t>(sp.q0) * a.group + r] = make_float2(__builtin_fmaf(0.f, dot, lse2), dot);
+
   floatx16 acc[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) acc[db] = floatx16(0.f);
   float factor = kFirstFactor;
-  const float c = a.scale * kLog2e;
 
   // Edge tiles hold keys that some row of the workgroup does not see: these go
   // into LDS with their infinities and NaN as zeros.  A row that sees such a
@@ -199,7 +255,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
     }
   };
   if (jb0 < jb1) {
-    load(jb0);
+    if (!kEarly) load(jb0);
     if constexpr (BUFS == 2) store(0, jb0);
   }
   for (int jb = jb0; jb < jb1; ++jb) {
