@@ -47,6 +47,7 @@ constexpr int kBuffers = WAVES == 1 ? 1 : 2;
 struct Chunks {
   int slots = 0;  // 0: no chunks
   int shift = 0;
+  int rows = 0;  // flattened rows that a sequence of these has at most
 };
 __device__ __forceinline__ bool chunked(int rows, int nk) { return rows <= 32 && nk > 0; }
 
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 ? 2 : 1) void k_attentio
       chunk0 = sp.r0;
       chunk1 = sp.r0 + (1 << chunks.shift);
       sp.r0 = 0;
-      part_row = (static_cast<int64_t>(slot) * a.kv_heads + kvh) * 32;
+      part_row = (static_cast<int64_t>(slot) * a.kv_heads + kvh) * chunks.rows;
     } else {
       sp = find_span(a, false, a.group, tile_shift(WAVES), slot - chunks.slots, slots);
       if (!sp.any || chunked(sp.nq * a.group, sp.nk)) return;
@@ -425,8 +426,8 @@ __global__ __launch_bounds__(256) void k_attention_join_chunks(AttentionArgs a, 
   const int kvh = div_group(a, head), r = sp.r0 * a.group + head - kvh * a.group;
   const int slot0 = (sp.k0 >> chunks.shift) + sp.seq;
   const int parts = (sp.nk + (1 << chunks.shift) - 1) >> chunks.shift;
-  join_parts<T>(a, part_out, part_lse, (static_cast<int64_t>(slot0) * a.kv_heads + kvh) * 32 + r, static_cast<int64_t>(a.kv_heads) * 32,
-                parts, static_cast<int64_t>(sp.q0 + sp.r0) * a.heads + head);
+  join_parts<T>(a, part_out, part_lse, (static_cast<int64_t>(slot0) * a.kv_heads + kvh) * chunks.rows + r,
+                static_cast<int64_t>(a.kv_heads) * chunks.rows, parts, static_cast<int64_t>(sp.q0 + sp.r0) * a.heads + head);
 }
 
 __global__ __launch_bounds__(1024) void k_attention_order(AttentionArgs a, OrderJob job) { order_slots(a, job); }
@@ -461,7 +462,8 @@ Plan make_forward_plan(const AttentionArgs& a) {
     while (p.chunks.shift < 10 && (int64_t(1) << p.chunks.shift) < want) ++p.chunks.shift;
     p.chunks.slots = static_cast<int>(span_slots(a.total_k, a.batch, 1 << p.chunks.shift));
     p.slots = span_slots(rows, a.batch, 32);
-    p.parts = static_cast<int64_t>(p.chunks.slots) * a.kv_heads * 32;
+    p.chunks.rows = static_cast<int>(std::min<int64_t>(rows, 32));
+    p.parts = static_cast<int64_t>(p.chunks.slots) * a.kv_heads * p.chunks.rows;
     return p;
   }
   p.slots = span_slots(rows, a.batch, 32 * p.waves);

@@ -30,6 +30,13 @@ def test_sizes():
     assert sp.lib().spconv_attention_workspace(ctypes.byref(a), None, None) == 0
 
 
+def test_parts_are_sized_for_the_rows_there_are():
+    """One ungrouped query: a part is one row of each head, of chunks of at
+    least 64 keys."""
+    f, _ = sp.spconv_attention_workspace(_attention(total_q=1, total_k=64000, batch=1, heads=4, kv_heads=4))
+    assert 0 < f <= (1000 + 3) * 4 * (32 + 1) * 4
+
+
 def test_size_refusals():
     assert _status(sp.spconv_attention_workspace, _attention(heads=5)) == "SPCONV_ERR_INVALID_ARG"
     assert _status(sp.spconv_attention_workspace, _attention(head_dim=4)) == "SPCONV_ERR_UNSUPPORTED"
