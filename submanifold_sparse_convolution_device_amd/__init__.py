@@ -963,7 +963,8 @@ def attention(q, k, v, cu_q, cu_k=None, *, causal: bool = False, window=(-1, -1)
 
     Returns out [total_q, heads, head_dim], or (out, lse) with
     ``return_lse``: lse fp32 [total_q, heads], what
-    :func:`attention_backward` needs."""
+    :func:`attention_backward` needs.  Both calls may be captured in a graph
+    (their workspaces then come from torch's allocator, and stay the graph's)."""
     torch, L = _bind()
     a = _attention_args(q, k, v, cu_q, cu_k, causal, window, scale)
     if out is None:

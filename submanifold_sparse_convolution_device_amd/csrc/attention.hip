@@ -10,7 +10,7 @@
 // exponential takes two slots) beside DP / 4 matrix ones, so heads of 32 are
 // bound by the vector unit and heads of 128 by how the two units overlap.
 // Measured: 4 sequences of up to 8192 rows, 16 heads of 128 over 4 key heads,
-// causal bf16, 0.90 TFLOP of visible pairs: 1000 us, 900 TFLOP/s (matrix unit
+// causal bf16, 0.90 TFLOP of visible pairs: 1004 us, 897 TFLOP/s (matrix unit
 // 42% busy, vector unit 41%); 8 frames of up to 4000 rows, 8 heads of 32, f16:
 // 140 us, 522 TFLOP/s (vector unit 83% busy).
 //
@@ -443,7 +443,7 @@ struct Plan {
 
 // Sequences of few rows over long keys (32 flattened rows in the mean, keys
 // that fill a chunk) go by chunks: 24 single queries over up to 24000 keys,
-// 16 heads of 128 over 2, bf16, 311 MB: 80 us with the join (3.9 TB/s),
+// 16 heads of 128 over 2, bf16, 311 MB: 79 us with the join (4.0 TB/s),
 // against 130 us when every sequence's keys are cut into the same number of
 // parts.  Else the tiles of rows split the keys when they would leave SIMDs
 // idle.

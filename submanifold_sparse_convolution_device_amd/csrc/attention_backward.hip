@@ -12,11 +12,11 @@
 // on every run.
 //
 // Bound, as the forward, by the vector unit and its overlap with the matrix
-// unit for long sequences (causal f16, 14.6k rows, 8 heads of 64 over 2: 125
-// and 180 us for the 10 products' 0.12 TFLOP), and by the latency of each
+// unit for long sequences (causal f16, 14.6k rows, 8 heads of 64 over 2: 134
+// and 184 us for the 10 products' 0.12 TFLOP), and by the latency of each
 // workgroup's few dependent loads for short ones (1200 windows of up to 343
-// rows, 8 heads of 32, bf16: 222 and 300 us, of which 138 and 129 us remain
-// when no tile is walked; the bytes alone would take 125 and 124).
+// rows, 8 heads of 32, bf16: 227 and 305 us; the bytes alone would take 125 and
+// 124).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -14,7 +14,7 @@
 // is LPR lanes of one 16-byte piece each, and the units of a tensor run over
 // the lanes in memory order (heads within rows), so a wavefront's access is
 // one contiguous run as long as the heads are.  Measured: 800k rows of 16
-// heads of 32, bf16, three axes: 316 us, 5.2 TB/s, the rate of a large copy;
+// heads of 32, bf16, three axes: 313 us, 5.2 TB/s, the rate of a large copy;
 // one lane group per row that walks its heads, whose accesses are 64-byte
 // pieces, takes 486 us.  The gradient reads two tensors and writes one: 120k
 // rows of 20 heads of 128, bf16, 380 us (4.8 TB/s).
