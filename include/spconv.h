@@ -714,6 +714,162 @@ spconv_status spconv_norm_rotary_backward_noalloc(const spconv_norm_rotary* args
 spconv_status spconv_rotary_table(float* d_table, int32_t extent, int32_t pairs, double base, double position_scale,
                                   void* hip_stream);
 
+/* ---- Row norm with the residual's addition ----
+ *
+ * One pass over the rows of a block's residual stream:
+ *   h = x + residual,   y_j = h_j w_j / sqrt(mean_i(h_i^2) + eps).
+ * h is rounded to dtype as it is stored, and the norm is of the stored sum;
+ * without a residual (NULL) h is x and is not written.  channels is a multiple
+ * of 8, a row at most 2^15 bytes.  The arithmetic is fp32, each output rounded
+ * once.  Rows have strides in elements (multiples of 16 bytes, at least
+ * channels, at most 2^24 bytes) and start 16-byte aligned.
+ */
+typedef struct spconv_add_norm {
+  const void* x;        /* [rows][channels] */
+  const void* residual; /* [rows][channels], or NULL */
+  const void* weight;   /* [channels] in dtype, 16-byte aligned */
+  int64_t x_row_stride, residual_row_stride, rows;
+  int32_t channels;
+  float eps;
+  int32_t dtype; /* spconv_dtype */
+} spconv_add_norm;
+
+/* Writes d_h (NULL without a residual) and d_y.  Either may be x or the
+ * residual in its place (same pointer and stride); otherwise they share no
+ * byte with an input or each other.  Errors: INVALID_ARG, UNSUPPORTED (dtype,
+ * channels), DEVICE. */
+spconv_status spconv_add_norm_forward(const spconv_add_norm* args, void* d_h, int64_t h_row_stride, void* d_y,
+                                      int64_t y_row_stride, void* hip_stream);
+
+/*
+ * Gradients, from the stored sum (args->x holds the forward's h, args->residual
+ * is not read) and the gradients of y and of h (grad_h NULL: none):
+ *   grad_j = grad_h_j + r (g_j w_j - h_j r^2 mean_i(g_i w_i h_i)),  g = grad_y,
+ *   grad_weight_j = sum over rows of g_j h_j r  (fp32 [channels], NULL: not written);
+ * grad is the gradient of x and of the residual alike.  It may take the place
+ * of grad_y or grad_h.  Sums run in a fixed order.  Errors as for the forward,
+ * and OUT_OF_MEMORY (the partial sums live in the stream's workspace; the
+ * _noalloc variant takes the caller's, of spconv_add_norm_workspace bytes, and
+ * is the one that runs under graph capture).
+ */
+typedef struct spconv_add_norm_gradients {
+  const void* grad_h;
+  const void* grad_y;
+  void* grad;
+  float* grad_weight;
+  int64_t grad_h_row_stride, grad_y_row_stride, grad_row_stride;
+} spconv_add_norm_gradients;
+
+spconv_status spconv_add_norm_backward(const spconv_add_norm* args, const spconv_add_norm_gradients* grads,
+                                       void* hip_stream);
+spconv_status spconv_add_norm_workspace(int32_t channels, uint64_t* backward_bytes);
+spconv_status spconv_add_norm_backward_noalloc(const spconv_add_norm* args, const spconv_add_norm_gradients* grads,
+                                               void* d_workspace, uint64_t workspace_bytes, void* hip_stream);
+
+/* ---- Products of rows ----
+ *
+ * The matrix product of a block's projections and feed-forward, with its
+ * epilogue in the same pass:
+ *   pre = x W + b,   out = act(pre) + residual,
+ * x [rows][c_in], W [c_in][c_out] (the layout of a convolution's W[k]).
+ *
+ * With cu (device int32 [groups + 1], not decreasing) the rows are packed by
+ * group, group e holds the rows [cu[e], cu[e + 1]) and has its own
+ * W [groups][c_in][c_out] and b [groups][c_out]; groups may be empty.  Rows
+ * before cu[0] or after cu[groups] belong to none: their x and residual are
+ * not used, and their pre, out and gradients are zeros.  Nothing is read
+ * back to the host.  Offsets that break these rules give meaningless rows but
+ * no access outside the tensors.  cu NULL: one group of all rows.
+ *
+ * Any c_in and c_out in [1, 2^18]; rows have strides in elements, at least
+ * their length and at most 2^22 bytes.  x, W and grad_out start 16-byte
+ * aligned; where a row's length or stride is no multiple of 16 bytes the
+ * operand is first laid out in the workspace.  W and b are contiguous.
+ *
+ * Operands are multiplied in dtype and summed in fp32; F32 operands are used
+ * whole (split exactly into three bf16 parts each, as in attention above: an
+ * infinity among them gives NaN).  The epilogue is fp32 and each output is
+ * rounded once.  GELU is z times the normal distribution's integral (the
+ * error function's form), SILU is z / (1 + exp(-z)); RELU has slope 0 at 0.
+ * Every sum has a fixed order: the same call gives the same bits.
+ */
+typedef SPCONV_ENUM(spconv_activation) {
+  SPCONV_ACT_NONE = 0,
+  SPCONV_ACT_RELU = 1,
+  SPCONV_ACT_SILU = 2,
+  SPCONV_ACT_GELU = 3
+} spconv_activation;
+
+typedef struct spconv_linear {
+  const void* x;       /* [rows][c_in] */
+  const void* weight;  /* [groups][c_in][c_out] */
+  const int32_t* cu;   /* [groups + 1], or NULL (then groups = 1) */
+  int64_t x_row_stride, rows;
+  int32_t groups, c_in, c_out;
+  int32_t activation;  /* spconv_activation */
+  int32_t dtype;       /* spconv_dtype */
+} spconv_linear;
+
+typedef struct spconv_linear_epilogue {
+  const void* bias;      /* [groups][c_out] in dtype, or NULL */
+  const void* residual;  /* [rows][c_out], or NULL */
+  void* out;             /* [rows][c_out] */
+  void* pre;             /* [rows][c_out], or NULL: the product before the activation is not stored */
+  int64_t residual_row_stride, out_row_stride, pre_row_stride;
+} spconv_linear_epilogue;
+
+/* Writes every row of out (and pre).  out may be the residual in its place;
+ * otherwise the two share no byte with an input or each other.  Few rows
+ * split the contraction over workgroups and join the parts from the stream's
+ * workspace.  Asynchronous on hip_stream.  Errors: INVALID_ARG (also for a
+ * launch of 2^32 work items), UNSUPPORTED (dtype), OUT_OF_MEMORY, DEVICE. */
+spconv_status spconv_linear_forward(const spconv_linear* args, const spconv_linear_epilogue* epilogue, void* hip_stream);
+
+/*
+ * Gradients of pre = x W + b from grad_out, the gradient of pre
+ * ([rows][c_out]; after an activation, what spconv_activation_backward makes
+ * of out's; the residual's gradient is out's own):
+ *   grad_x = grad_out W^T,   grad_weight = x^T grad_out (fp32),
+ *   grad_bias = the column sums of grad_out (fp32).
+ * before not NULL: x is act(before), the activation of an earlier product
+ * stored as its pre, and grad_x is that product's: grad_out W^T act'(before),
+ * with act the args' activation (SPCONV_ACT_NONE is refused with before).
+ * grad_x or grad_weight may be NULL (not wanted), grad_bias too; grad_bias
+ * needs grad_weight.  The gradients share no byte with an input or each
+ * other.  A grad_out whose c_out is a multiple of 16 bytes needs such a row
+ * stride.  Errors as for the forward.
+ */
+typedef struct spconv_linear_gradients {
+  const void* grad_out; /* [rows][c_out] */
+  const void* before;   /* [rows][c_in], or NULL */
+  void* grad_x;         /* [rows][c_in] */
+  float* grad_weight;   /* [groups][c_in][c_out] */
+  float* grad_bias;     /* [groups][c_out] */
+  int64_t grad_out_row_stride, before_row_stride, grad_x_row_stride;
+} spconv_linear_gradients;
+
+spconv_status spconv_linear_backward(const spconv_linear* args, const spconv_linear_gradients* grads, void* hip_stream);
+
+/* The calls with a workspace of the caller's, as for attention:
+ * spconv_linear_workspace returns the bytes of both (from the sizes, strides
+ * and whether cu is NULL alone), and calls that need one run under graph
+ * capture as these variants. */
+spconv_status spconv_linear_workspace(const spconv_linear* args, uint64_t* forward_bytes, uint64_t* backward_bytes);
+spconv_status spconv_linear_forward_noalloc(const spconv_linear* args, const spconv_linear_epilogue* epilogue,
+                                            void* d_workspace, uint64_t workspace_bytes, void* hip_stream);
+spconv_status spconv_linear_backward_noalloc(const spconv_linear* args, const spconv_linear_gradients* grads,
+                                             void* d_workspace, uint64_t workspace_bytes, void* hip_stream);
+
+/*
+ * The gradient of an activation: d_grad_pre = d_grad_out x act'(d_pre) over
+ * [rows][channels], strides in elements, fp32 rounded once; d_grad_pre may be
+ * d_grad_out in its place.  Errors: INVALID_ARG, UNSUPPORTED (dtype), DEVICE.
+ */
+spconv_status spconv_activation_backward(const void* d_grad_out, int64_t grad_out_row_stride, const void* d_pre,
+                                         int64_t pre_row_stride, void* d_grad_pre, int64_t grad_pre_row_stride,
+                                         int64_t rows, int32_t channels, int32_t activation, spconv_dtype dtype,
+                                         void* hip_stream);
+
 /* Releases a map.  Its buffers go back, in the order of the build's stream,
  * to that stream's cache of map blocks (or to the pool); the caller must not
  * free a map while work on another stream still reads it.  NULL is ignored. */

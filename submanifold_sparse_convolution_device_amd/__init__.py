@@ -46,7 +46,11 @@ EXPORTED = (
     "spconv_attention_forward", "spconv_attention_backward", "spconv_norm_rotary_forward", "spconv_norm_rotary_backward",
     "spconv_rotary_table", "spconv_attention_workspace", "spconv_attention_forward_noalloc", "spconv_attention_backward_noalloc",
     "spconv_norm_rotary_workspace", "spconv_norm_rotary_backward_noalloc",
+    "spconv_add_norm_forward", "spconv_add_norm_backward", "spconv_add_norm_workspace", "spconv_add_norm_backward_noalloc",
+    "spconv_linear_forward", "spconv_linear_backward", "spconv_linear_workspace", "spconv_linear_forward_noalloc",
+    "spconv_linear_backward_noalloc", "spconv_activation_backward",
 )
+ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3}
 MAP_KINDS = {0: "submanifold", 1: "strided", 2: "transposed"}
 DATAFLOWS = {0: "fused", 1: "grouped"}
 
@@ -95,6 +99,38 @@ class spconv_norm_rotary_gradients(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("grad_q_row_stride", "grad_q_head_stride", "grad_k_row_stride",
                                                  "grad_k_head_stride")]
                 + [(n, ctypes.c_void_p) for n in ("grad_q_weight", "grad_k_weight")])
+
+
+class spconv_add_norm(ctypes.Structure):
+    """Mirror of the C struct spconv_add_norm."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "residual", "weight")]
+                + [(n, ctypes.c_int64) for n in ("x_row_stride", "residual_row_stride", "rows")]
+                + [("channels", ctypes.c_int32), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)])
+
+
+class spconv_add_norm_gradients(ctypes.Structure):
+    """Mirror of the C struct spconv_add_norm_gradients."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("grad_h", "grad_y", "grad", "grad_weight")]
+                + [(n, ctypes.c_int64) for n in ("grad_h_row_stride", "grad_y_row_stride", "grad_row_stride")])
+
+
+class spconv_linear(ctypes.Structure):
+    """Mirror of the C struct spconv_linear."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "weight", "cu")]
+                + [(n, ctypes.c_int64) for n in ("x_row_stride", "rows")]
+                + [(n, ctypes.c_int32) for n in ("groups", "c_in", "c_out", "activation", "dtype")])
+
+
+class spconv_linear_epilogue(ctypes.Structure):
+    """Mirror of the C struct spconv_linear_epilogue."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("bias", "residual", "out", "pre")]
+                + [(n, ctypes.c_int64) for n in ("residual_row_stride", "out_row_stride", "pre_row_stride")])
+
+
+class spconv_linear_gradients(ctypes.Structure):
+    """Mirror of the C struct spconv_linear_gradients."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("grad_out", "before", "grad_x", "grad_weight", "grad_bias")]
+                + [(n, ctypes.c_int64) for n in ("grad_out_row_stride", "before_row_stride", "grad_x_row_stride")])
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -190,6 +226,22 @@ def lib() -> ctypes.CDLL:
     L.spconv_norm_rotary_workspace.restype = ctypes.c_int
     L.spconv_norm_rotary_backward_noalloc.argtypes = [vp, vp, vp, ctypes.c_uint64, vp]
     L.spconv_norm_rotary_backward_noalloc.restype = ctypes.c_int
+    L.spconv_add_norm_forward.argtypes = [vp, vp, i64, vp, i64, vp]
+    L.spconv_add_norm_forward.restype = ctypes.c_int
+    L.spconv_add_norm_backward.argtypes = [vp, vp, vp]
+    L.spconv_add_norm_backward.restype = ctypes.c_int
+    L.spconv_add_norm_workspace.argtypes = [i32, vp]
+    L.spconv_add_norm_workspace.restype = ctypes.c_int
+    L.spconv_add_norm_backward_noalloc.argtypes = [vp, vp, vp, ctypes.c_uint64, vp]
+    L.spconv_add_norm_backward_noalloc.restype = ctypes.c_int
+    for name in ("spconv_linear_forward", "spconv_linear_backward"):
+        getattr(L, name).argtypes, getattr(L, name).restype = [vp, vp, vp], ctypes.c_int
+        f = getattr(L, name + "_noalloc")
+        f.argtypes, f.restype = [vp, vp, vp, ctypes.c_uint64, vp], ctypes.c_int
+    L.spconv_linear_workspace.argtypes = [vp, vp, vp]
+    L.spconv_linear_workspace.restype = ctypes.c_int
+    L.spconv_activation_backward.argtypes = [vp, i64, vp, i64, vp, i64, i64, i32, i32, ctypes.c_int, vp]
+    L.spconv_activation_backward.restype = ctypes.c_int
     L.spconv_rotary_table.argtypes = [vp, i32, i32, f64, f64, vp]
     L.spconv_rotary_table.restype = ctypes.c_int
     L.spconv_map_free.argtypes, L.spconv_map_free.restype = [vp], None
@@ -426,6 +478,63 @@ def spconv_rotary_table(d_table: int, extent: int, pairs: int, base: float, posi
     _check(lib().spconv_rotary_table(d_table, extent, pairs, float(base), float(position_scale), hip_stream))
 
 
+def spconv_add_norm_forward(args: spconv_add_norm, d_h: int, h_row_stride: int, d_y: int, y_row_stride: int,
+                            hip_stream: int) -> None:
+    _check(lib().spconv_add_norm_forward(ctypes.byref(args), d_h, h_row_stride, d_y, y_row_stride, hip_stream))
+
+
+def spconv_add_norm_backward(args: spconv_add_norm, grads: spconv_add_norm_gradients, hip_stream: int) -> None:
+    _check(lib().spconv_add_norm_backward(ctypes.byref(args), ctypes.byref(grads), hip_stream))
+
+
+def spconv_add_norm_workspace(channels: int) -> int:
+    """Bytes of workspace of the gradient."""
+    b = ctypes.c_uint64()
+    _check(lib().spconv_add_norm_workspace(channels, ctypes.byref(b)))
+    return b.value
+
+
+def spconv_add_norm_backward_noalloc(args: spconv_add_norm, grads: spconv_add_norm_gradients, d_workspace: int,
+                                     workspace_bytes: int, hip_stream: int) -> None:
+    _check(lib().spconv_add_norm_backward_noalloc(ctypes.byref(args), ctypes.byref(grads), d_workspace, workspace_bytes, hip_stream))
+
+
+def spconv_linear_forward(args: spconv_linear, epilogue: spconv_linear_epilogue, hip_stream: int) -> None:
+    _check(lib().spconv_linear_forward(ctypes.byref(args), ctypes.byref(epilogue), hip_stream))
+
+
+def spconv_linear_backward(args: spconv_linear, grads: spconv_linear_gradients, hip_stream: int) -> None:
+    _check(lib().spconv_linear_backward(ctypes.byref(args), ctypes.byref(grads), hip_stream))
+
+
+def spconv_linear_workspace(args: spconv_linear) -> Tuple[int, int]:
+    """Bytes of workspace of the forward and of the gradients."""
+    return _linear_workspace(ctypes.byref(args))
+
+
+def _linear_workspace(args) -> Tuple[int, int]:
+    f, b = ctypes.c_uint64(), ctypes.c_uint64()
+    _check(lib().spconv_linear_workspace(args, ctypes.byref(f), ctypes.byref(b)))
+    return f.value, b.value
+
+
+def spconv_linear_forward_noalloc(args: spconv_linear, epilogue: spconv_linear_epilogue, d_workspace: int, workspace_bytes: int,
+                                  hip_stream: int) -> None:
+    _check(lib().spconv_linear_forward_noalloc(ctypes.byref(args), ctypes.byref(epilogue), d_workspace, workspace_bytes, hip_stream))
+
+
+def spconv_linear_backward_noalloc(args: spconv_linear, grads: spconv_linear_gradients, d_workspace: int, workspace_bytes: int,
+                                   hip_stream: int) -> None:
+    _check(lib().spconv_linear_backward_noalloc(ctypes.byref(args), ctypes.byref(grads), d_workspace, workspace_bytes, hip_stream))
+
+
+def spconv_activation_backward(d_grad_out: int, grad_out_row_stride: int, d_pre: int, pre_row_stride: int, d_grad_pre: int,
+                               grad_pre_row_stride: int, rows: int, channels: int, activation: int, dtype: int,
+                               hip_stream: int) -> None:
+    _check(lib().spconv_activation_backward(d_grad_out, grad_out_row_stride, d_pre, pre_row_stride, d_grad_pre,
+                                            grad_pre_row_stride, rows, channels, activation, dtype, hip_stream))
+
+
 def spconv_map_free(handle: int) -> None:
     lib().spconv_map_free(handle)
 
@@ -477,6 +586,9 @@ _WORKSPACES = {
     "spconv_attention_forward": lambda a: _attention_workspace(a)[0],
     "spconv_attention_backward": lambda a: _attention_workspace(a)[1],
     "spconv_norm_rotary_backward": lambda a: spconv_norm_rotary_workspace(spconv_norm_rotary.from_buffer_copy(a).head_dim),
+    "spconv_add_norm_backward": lambda a: spconv_add_norm_workspace(spconv_add_norm.from_buffer_copy(a).channels),
+    "spconv_linear_forward": lambda a: _linear_workspace(a)[0],
+    "spconv_linear_backward": lambda a: _linear_workspace(a)[1],
 }
 
 
@@ -1113,3 +1225,198 @@ def norm_rotary_backward(grad_q_out, grad_k_out, q, k, q_weight=None, k_weight=N
                                          *(0 if w is None else w.data_ptr() for w in weights))
     _run(like.get_device(), L.spconv_norm_rotary_backward, a, g)
     return grads[0], grads[1], weights[0], weights[1]
+
+
+# ------------------------------------------------------------------ row norm and products
+
+_PACK_ADD_NORM = struct.Struct("@3P3qifi0q")
+_PACK_ADD_NORM_GRADIENTS = struct.Struct("@4P3q")
+_PACK_LINEAR = struct.Struct("@3P2q5i0q")
+_PACK_LINEAR_EPILOGUE = struct.Struct("@4P3q")
+_PACK_LINEAR_GRADIENTS = struct.Struct("@5P3q")
+_NO_ROWS = (0, 0)
+
+
+def _rows_tensor(name, t, like=None, shape=None):
+    """Checks a [rows, channels] tensor whose last dimension is contiguous;
+    returns (pointer, row stride)."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise SpconvError(1, f"{name} must be a [rows, channels] tensor on a HIP device")
+    rows, cols = t.shape
+    row, last = t.stride()
+    if last != 1 and cols > 1:
+        raise SpconvError(1, f"{name} must have a contiguous last dimension")
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
+        raise SpconvError(1, f"{name} must have the dtype and device of the other tensors")
+    if shape is not None and t.shape != shape:
+        raise SpconvError(1, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr(), (row if rows > 1 else cols)
+
+
+def _whole_tensor(name, t, shape, dtype, device: int):
+    if not (t.get_device() == device and t.dtype is dtype and t.is_contiguous() and t.shape == shape):
+        raise SpconvError(1, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the tensors' device")
+    return t.data_ptr()
+
+
+def _add_norm_args(x, residual, weight, eps):
+    """The packed spconv_add_norm of a call."""
+    xp, xr = _rows_tensor("x", x)
+    rp, rr = _NO_ROWS if residual is None else _rows_tensor("residual", residual, x, x.shape)
+    code = _dtype_code(x.dtype)
+    wp = _whole_tensor("weight", weight, x.shape[1:], x.dtype, x.get_device())
+    if not 0.0 <= eps < 3e38:
+        raise SpconvError(1, f"eps = {eps} must be finite and not negative")
+    return _PACK_ADD_NORM.pack(xp, rp, wp, xr, rr, x.shape[0], x.shape[1], eps, code)
+
+
+def add_norm(x, residual, weight, *, eps: float = 1e-6, out=None):
+    """The residual's addition and the RMS norm of whole rows in one pass:
+    h = x + residual and h * weight / sqrt(mean(h ** 2) + eps), for x and
+    residual [rows, channels] (f32, f16 or bf16; channels a multiple of 8, a
+    row at most 32 KB; row strides that are multiples of 16 bytes) and weight
+    [channels].
+
+    Returns (h, y): h is rounded to the dtype and the norm is of the rounded
+    sum.  ``residual`` None: no addition, h is x itself.  ``out``: two tensors
+    to write, which may be x and residual themselves (without a residual the
+    first is None)."""
+    torch, L = _bind()
+    a = _add_norm_args(x, residual, weight, eps)
+    if out is None:
+        out = (None if residual is None else torch.empty_like(x, memory_format=torch.contiguous_format),
+               torch.empty_like(x, memory_format=torch.contiguous_format))
+    h, y = out
+    if (h is None) != (residual is None):
+        raise SpconvError(1, "out must hold a tensor for the sum exactly when there is a residual")
+    hp = _NO_ROWS if h is None else _rows_tensor("out[0]", h, x, x.shape)
+    yp = _rows_tensor("out[1]", y, x, x.shape)
+    _run(x.get_device(), L.spconv_add_norm_forward, a, *hp, *yp)
+    return (x if h is None else h), y
+
+
+def add_norm_backward(grad_h, grad_y, h, weight, *, eps: float = 1e-6, grad=None):
+    """Gradients (grad, grad_weight) of :func:`add_norm` from the gradients of
+    its two results (grad_h None: nothing else read h), its h and its weight.
+    grad is the gradient of x and of the residual alike; grad_weight is fp32
+    [channels].  ``grad``: a tensor to write, which may be grad_h or grad_y
+    itself."""
+    torch, L = _bind()
+    a = _add_norm_args(h, None, weight, eps)
+    if grad is None:
+        grad = torch.empty_like(h, memory_format=torch.contiguous_format)
+    ghp, ghr = _NO_ROWS if grad_h is None else _rows_tensor("grad_h", grad_h, h, h.shape)
+    gyp, gyr = _rows_tensor("grad_y", grad_y, h, h.shape)
+    gp, gr = _rows_tensor("grad", grad, h, h.shape)
+    grad_weight = h.new_empty(h.shape[1], dtype=torch.float32)
+    g = _PACK_ADD_NORM_GRADIENTS.pack(ghp, gyp, gp, grad_weight.data_ptr(), ghr, gyr, gr)
+    _run(h.get_device(), L.spconv_add_norm_backward, a, g)
+    return grad, grad_weight
+
+
+def _activation_code(activation):
+    code = ACTIVATIONS.get(activation)
+    if code is None:
+        raise SpconvError(1, f"activation {activation!r} must be one of {', '.join(map(repr, ACTIVATIONS))}")
+    return code
+
+
+def _linear_args(x, weight, cu, activation):
+    """(packed spconv_linear, groups, c_out) of a call."""
+    xp, xr = _rows_tensor("x", x)
+    code = _dtype_code(x.dtype)
+    device = x.get_device()
+    rows, c_in = x.shape
+    if weight.dim() != (2 if cu is None else 3) or weight.shape[-2] != c_in:
+        raise SpconvError(1, f"weight must be [{'' if cu is None else 'groups, '}{c_in}, c_out], not {tuple(weight.shape)}")
+    wp = _whole_tensor("weight", weight, weight.shape, x.dtype, device)
+    groups, cp = 1, 0
+    if cu is not None:
+        groups = weight.shape[0]
+        cp = _offsets_tensor("cu", cu, device)
+        if cu.shape[0] != groups + 1:
+            raise SpconvError(1, f"cu must hold the {groups + 1} row offsets of {groups} groups, not {cu.shape[0]}")
+    c_out = weight.shape[-1]
+    return _PACK_LINEAR.pack(xp, wp, cp, xr, rows, groups, c_in, c_out, _activation_code(activation), code), groups, c_out
+
+
+def linear(x, weight, bias=None, *, activation: Optional[str] = None, residual=None, cu=None, out=None, return_pre: bool = False):
+    """The matrix product of rows with its epilogue in the same pass:
+    activation(x @ weight + bias) + residual, for x [rows, c_in] and weight
+    [c_in, c_out] (f32, f16 or bf16, sums in fp32; any sizes).  ``activation``
+    is None, "relu", "silu" or "gelu" (the error function's).
+
+    ``cu``: int32 [groups + 1] row offsets on the device; the rows
+    cu[e] .. cu[e + 1] take weight[e] and bias[e] of weight
+    [groups, c_in, c_out] and bias [groups, c_out].  Groups may be empty; rows
+    of none (before cu[0], after cu[-1]) give zeros.
+
+    Returns out [rows, c_out] (``out``: a tensor to write, which may be the
+    residual), or (out, pre) with ``return_pre``: pre = x @ weight + bias, what
+    :func:`activation_backward` and the ``pre`` of :func:`linear_backward`
+    need.  The calls may be captured in a graph."""
+    torch, L = _bind()
+    a, groups, c_out = _linear_args(x, weight, cu, activation)
+    shape = torch.Size((x.shape[0], c_out))
+    device = x.get_device()
+    bp = 0 if bias is None else _whole_tensor("bias", bias, torch.Size((c_out,) if cu is None else (groups, c_out)), x.dtype, device)
+    rp, rr = _NO_ROWS if residual is None else _rows_tensor("residual", residual, x, shape)
+    if out is None:
+        out = x.new_empty(shape)
+    op, orow = _rows_tensor("out", out, x, shape)
+    pre, pp, pr = None, 0, 0
+    if return_pre:
+        pre = x.new_empty(shape)
+        pp, pr = pre.data_ptr(), c_out
+    _run(device, L.spconv_linear_forward, a, _PACK_LINEAR_EPILOGUE.pack(bp, rp, op, pp, rr, orow, pr))
+    return (out, pre) if return_pre else out
+
+
+def linear_backward(grad_out, x, weight, *, pre=None, activation: Optional[str] = None, cu=None, grad_x=None,
+                    inputs: bool = True, weights: bool = True):
+    """Gradients (grad_x, grad_weight, grad_bias) of x @ weight + bias from the
+    gradient of that product [rows, c_out] (after an activation: what
+    :func:`activation_backward` returns; the residual's gradient is the
+    output's own).  The weight's and the bias's are fp32, in their shapes.
+
+    ``pre`` and ``activation``: x is the activation of an earlier product that
+    was stored as pre [rows, c_in], and grad_x is then the gradient of pre.
+    ``cu`` as in :func:`linear`.  ``grad_x``: a tensor to write.  ``inputs`` or
+    ``weights`` False leaves those gradients out (None)."""
+    torch, L = _bind()
+    if (pre is None) != (activation is None):
+        raise SpconvError(1, "pre and its activation go together")
+    a, groups, c_out = _linear_args(x, weight, cu, activation)
+    gp, gr = _rows_tensor("grad_out", grad_out, x, torch.Size((x.shape[0], c_out)))
+    pp, pr = _NO_ROWS if pre is None else _rows_tensor("pre", pre, x, x.shape)
+    xp, xr = _NO_ROWS
+    if inputs:
+        if grad_x is None:
+            grad_x = torch.empty_like(x, memory_format=torch.contiguous_format)
+        xp, xr = _rows_tensor("grad_x", grad_x, x, x.shape)
+    else:
+        grad_x = None
+    grad_weight = grad_bias = None
+    wp = bp = 0
+    if weights:
+        grad_weight = x.new_empty(weight.shape, dtype=torch.float32)
+        grad_bias = x.new_empty((c_out,) if cu is None else (groups, c_out), dtype=torch.float32)
+        wp, bp = grad_weight.data_ptr(), grad_bias.data_ptr()
+    _run(x.get_device(), L.spconv_linear_backward, a, _PACK_LINEAR_GRADIENTS.pack(gp, pp, xp, wp, bp, gr, pr, xr))
+    return grad_x, grad_weight, grad_bias
+
+
+def activation_backward(grad_out, pre, activation: Optional[str], *, out=None):
+    """The gradient of an activation's argument: grad_out times the
+    activation's derivative at pre, both [rows, channels] of one dtype, rounded
+    once.  ``out``: a tensor to write, which may be grad_out."""
+    torch, L = _bind()
+    gp, gr = _rows_tensor("grad_out", grad_out)
+    pp, pr = _rows_tensor("pre", pre, grad_out, grad_out.shape)
+    if out is None:
+        out = torch.empty_like(grad_out, memory_format=torch.contiguous_format)
+    op, orow = _rows_tensor("out", out, grad_out, grad_out.shape)
+    rows, channels = grad_out.shape
+    _run(grad_out.get_device(), L.spconv_activation_backward, gp, gr, pp, pr, op, orow, rows, channels,
+         _activation_code(activation), _dtype_code(grad_out.dtype))
+    return out

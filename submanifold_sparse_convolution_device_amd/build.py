@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspconv.so")
 SOURCES = ["api.hip", "map_build.hip", "map_strided.hip", "forward.hip", "forward_tiled.hip", "forward_wide.hip",
-           "backward.hip", "grouped.hip", "attention.hip", "attention_backward.hip", "norm_rotary.hip"]
+           "backward.hip", "grouped.hip", "attention.hip", "attention_backward.hip", "norm_rotary.hip",
+           "add_norm.hip", "linear.hip", "linear_f32.hip", "linear_f16.hip", "linear_bf16.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",

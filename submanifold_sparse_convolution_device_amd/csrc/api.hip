@@ -911,6 +911,301 @@ spconv_status norm_rotary_backward(const spconv_norm_rotary* args, const spconv_
                         [&](void* ws) { return spconv::launch_norm_rotary_backward(a, ws, stream); });
 }
 
+// ---- Row norm with the residual's addition, products of rows ----
+
+spconv_status check_dtype(int32_t dtype) {
+  if (dtype == SPCONV_F32 || dtype == SPCONV_F16 || dtype == SPCONV_BF16) return SPCONV_OK;
+  return fail(SPCONV_ERR_UNSUPPORTED, "dtype %d not supported", dtype);
+}
+
+// A tensor [rows][dim] with a row stride of at least dim.  `piece`: addresses
+// and strides are multiples of that many bytes.
+Strided row_tensor(const char* name, const void* p, int64_t rows, int64_t row_stride, int64_t dim, uint64_t es) {
+  return {name, p, rows, row_stride, 1, 0, dim, es};
+}
+spconv_status check_rows(const Strided& t, uint64_t base_piece, uint64_t stride_piece, int64_t most_bytes) {
+  if (t.rows == 0) return SPCONV_OK;
+  if (t.p == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "%s is NULL", t.name);
+  if (reinterpret_cast<uintptr_t>(t.p) % base_piece != 0) return fail(SPCONV_ERR_INVALID_ARG, "%s is not %llu-byte aligned", t.name, (unsigned long long)base_piece);
+  if (t.row_stride < t.dim || t.row_stride > most_bytes / static_cast<int64_t>(t.es) || static_cast<uint64_t>(t.row_stride) * t.es % stride_piece != 0) {
+    return fail(SPCONV_ERR_INVALID_ARG, "%s: row stride %lld must be at least %lld, at most %lld bytes and a multiple of %llu bytes", t.name,
+                (long long)t.row_stride, (long long)t.dim, (long long)most_bytes, (unsigned long long)stride_piece);
+  }
+  return SPCONV_OK;
+}
+// `out` keeps apart from `in`, or (in_place) is it.
+spconv_status check_apart_or_same(const Strided& out, const Strided& in, bool in_place) {
+  if (in_place && out.p == in.p && out.row_stride == in.row_stride) return SPCONV_OK;
+  return check_apart(out, in);
+}
+
+spconv_status add_norm_args(const spconv_add_norm* x, spconv::AddNormArgs* a) {
+  if (x == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "args is NULL");
+  const spconv_status st = check_dtype(x->dtype);
+  if (st != SPCONV_OK) return st;
+  const int64_t es = x->dtype == SPCONV_F32 ? 4 : 2;
+  if (x->channels < 8 || x->channels % 8 != 0 || x->channels > 32768 / es) {
+    return fail(SPCONV_ERR_UNSUPPORTED, "channels = %d must be a multiple of 8 in [8, %lld]", x->channels, (long long)(32768 / es));
+  }
+  if (x->rows < 0 || x->rows > (int64_t(1) << 30)) return fail(SPCONV_ERR_INVALID_ARG, "rows = %lld must lie in [0, 2^30]", (long long)x->rows);
+  if (!(x->eps >= 0.f) || !std::isfinite(x->eps)) return fail(SPCONV_ERR_INVALID_ARG, "eps = %g must be finite and not negative", x->eps);
+  if (x->weight == nullptr || !aligned16(x->weight)) return fail(SPCONV_ERR_INVALID_ARG, "weight is NULL or not 16-byte aligned");
+  a->weight = x->weight;
+  a->rows = static_cast<int32_t>(x->rows);
+  a->channels = x->channels;
+  a->dtype = x->dtype;
+  a->eps = x->eps;
+  return check_work_items(spconv::add_norm_work_items(*a));
+}
+
+spconv_status add_norm_forward(const spconv_add_norm* args, void* d_h, int64_t h_row_stride, void* d_y, int64_t y_row_stride, void* hip_stream) {
+  g_last_error.clear();
+  spconv::AddNormArgs a;
+  spconv_status st = add_norm_args(args, &a);
+  if (st != SPCONV_OK) return st;
+  const uint64_t es = a.dtype == SPCONV_F32 ? 4u : 2u;
+  const bool add = args->residual != nullptr;
+  const int64_t sum_rows = add ? a.rows : 0;  // (tensors of no rows are not looked at)
+  const Strided x = row_tensor("x", args->x, a.rows, args->x_row_stride, a.channels, es);
+  const Strided residual = row_tensor("residual", args->residual, sum_rows, args->residual_row_stride, a.channels, es);
+  const Strided h = row_tensor("h", d_h, sum_rows, h_row_stride, a.channels, es);
+  const Strided y = row_tensor("y", d_y, a.rows, y_row_stride, a.channels, es);
+  const Strided weight = row_tensor("weight", a.weight, 1, a.channels, a.channels, es);
+  if (!add && a.rows > 0 && d_h != nullptr) return fail(SPCONV_ERR_INVALID_ARG, "h is given without a residual");
+  for (const Strided* t : {&x, &residual, &h, &y}) {
+    st = check_rows(*t, 16, 16, kMaxRowBytes);
+    if (st != SPCONV_OK) return st;
+  }
+  for (const Strided* out : {&h, &y}) {
+    for (const Strided* in : {&x, &residual}) {
+      st = check_apart_or_same(*out, *in, true);
+      if (st != SPCONV_OK) return st;
+    }
+    st = check_apart(*out, weight);
+    if (st != SPCONV_OK) return st;
+  }
+  st = check_apart(h, y);
+  if (st != SPCONV_OK) return st;
+  a.x = x.p;
+  a.x_row = x.row_stride;
+  a.residual = residual.p;
+  a.residual_row = residual.row_stride;
+  a.h = d_h;
+  a.h_row = h_row_stride;
+  a.y = d_y;
+  a.y_row = y_row_stride;
+  const hipError_t e = spconv::launch_add_norm(a, static_cast<hipStream_t>(hip_stream));
+  return e == hipSuccess ? SPCONV_OK : hip_fail(e, "add and norm launch");
+}
+
+spconv_status add_norm_backward(const spconv_add_norm* args, const spconv_add_norm_gradients* grads, const CallerWorkspace* own, void* hip_stream) {
+  g_last_error.clear();
+  spconv::AddNormArgs a;
+  spconv_status st = add_norm_args(args, &a);
+  if (st != SPCONV_OK) return st;
+  if (grads == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grads is NULL");
+  if (reinterpret_cast<uintptr_t>(grads->grad_weight) & 3u) return fail(SPCONV_ERR_INVALID_ARG, "grad_weight must be 4-byte aligned");
+  const uint64_t es = a.dtype == SPCONV_F32 ? 4u : 2u;
+  const Strided h = row_tensor("x (the sum h)", args->x, a.rows, args->x_row_stride, a.channels, es);
+  const Strided gh = row_tensor("grad_h", grads->grad_h, grads->grad_h == nullptr ? 0 : a.rows, grads->grad_h_row_stride, a.channels, es);
+  const Strided gy = row_tensor("grad_y", grads->grad_y, a.rows, grads->grad_y_row_stride, a.channels, es);
+  const Strided grad = row_tensor("grad", grads->grad, a.rows, grads->grad_row_stride, a.channels, es);
+  const Strided weight = row_tensor("weight", a.weight, 1, a.channels, a.channels, es);
+  const Strided gw = row_tensor("grad_weight", grads->grad_weight, grads->grad_weight == nullptr ? 0 : 1, a.channels, a.channels, 4);
+  for (const Strided* t : {&h, &gh, &gy, &grad}) {
+    st = check_rows(*t, 16, 16, kMaxRowBytes);
+    if (st != SPCONV_OK) return st;
+  }
+  st = check_apart(grad, h);
+  if (st == SPCONV_OK) st = check_apart_or_same(grad, gh, true);
+  if (st == SPCONV_OK) st = check_apart_or_same(grad, gy, true);
+  if (st == SPCONV_OK) st = check_apart(grad, weight);
+  for (const Strided* t : {&h, &gh, &gy, &grad, &weight})
+    if (st == SPCONV_OK) st = check_apart(gw, *t);
+  if (st != SPCONV_OK) return st;
+  a.h = const_cast<void*>(h.p);
+  a.h_row = h.row_stride;
+  a.grad_h = gh.p;
+  a.grad_h_row = gh.row_stride;
+  a.grad_y = gy.p;
+  a.grad_y_row = gy.row_stride;
+  a.grad = grads->grad;
+  a.grad_row = grad.row_stride;
+  a.grad_weight = grads->grad_weight;
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  return with_workspace(spconv::add_norm_backward_workspace_bytes(a), own, {&h, &gh, &gy, &grad, &weight, &gw}, stream, "add and norm backward launch",
+                        [&](void* ws) { return spconv::launch_add_norm_backward(a, ws, stream); });
+}
+
+constexpr int64_t kMaxLinearRowBytes = int64_t(1) << 22;
+
+// The sizes of a product, all that its workspace depends on.
+spconv_status linear_sizes(const spconv_linear* x, spconv::LinearArgs* a) {
+  if (x == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "args is NULL");
+  const spconv_status st = check_dtype(x->dtype);
+  if (st != SPCONV_OK) return st;
+  if (x->c_in < 1 || x->c_out < 1 || x->c_in > (1 << 18) || x->c_out > (1 << 18)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "c_in = %d and c_out = %d must lie in [1, 2^18]", x->c_in, x->c_out);
+  }
+  if (x->rows < 0 || x->rows > (int64_t(1) << 30)) return fail(SPCONV_ERR_INVALID_ARG, "rows = %lld must lie in [0, 2^30]", (long long)x->rows);
+  if (x->groups < 1 || x->groups > 65535) return fail(SPCONV_ERR_INVALID_ARG, "groups = %d must lie in [1, 65535]", x->groups);
+  if (x->cu == nullptr && x->groups != 1) return fail(SPCONV_ERR_INVALID_ARG, "groups = %d need their row offsets", x->groups);
+  if (x->activation < SPCONV_ACT_NONE || x->activation > SPCONV_ACT_GELU) return fail(SPCONV_ERR_INVALID_ARG, "activation = %d is none", x->activation);
+  const int64_t es = x->dtype == SPCONV_F32 ? 4 : 2;
+  if (x->rows > 0 && (x->x_row_stride < x->c_in || x->x_row_stride > kMaxLinearRowBytes / es)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "x: row stride %lld must be at least %d and at most 2^22 bytes", (long long)x->x_row_stride, x->c_in);
+  }
+  a->x_row = x->x_row_stride;
+  a->cu = x->cu;
+  a->rows = static_cast<int32_t>(x->rows);
+  a->groups = x->groups;
+  a->c_in = x->c_in;
+  a->c_out = x->c_out;
+  a->act = x->activation;
+  a->dtype = x->dtype;
+  a->grad_out_row = x->c_out;  // (or any whole number of pieces, which needs no more workspace)
+  return SPCONV_OK;
+}
+
+struct LinearTensors {
+  Strided x, weight, cu;
+};
+spconv_status linear_args(const spconv_linear* x, spconv::LinearArgs* a, LinearTensors* t) {
+  const spconv_status st = linear_sizes(x, a);
+  if (st != SPCONV_OK) return st;
+  const uint64_t es = a->dtype == SPCONV_F32 ? 4u : 2u;
+  t->x = row_tensor("x", x->x, a->rows, x->x_row_stride, a->c_in, es);
+  t->weight = row_tensor("weight", x->weight, static_cast<int64_t>(a->groups) * a->c_in, a->c_out, a->c_out, es);
+  t->cu = row_tensor("cu", x->cu, x->cu == nullptr ? 0 : 1, a->groups + 1, a->groups + 1, 4);
+  spconv_status e = check_rows(t->x, 16, es, kMaxLinearRowBytes);
+  if (e == SPCONV_OK) e = check_rows(t->weight, 16, es, kMaxLinearRowBytes);
+  if (e == SPCONV_OK) e = check_rows(t->cu, 4, 4, int64_t(1) << 40);
+  a->x = x->x;
+  a->weight = x->weight;
+  return e;
+}
+
+spconv_status linear_forward(const spconv_linear* args, const spconv_linear_epilogue* epilogue, const CallerWorkspace* own, void* hip_stream) {
+  g_last_error.clear();
+  spconv::LinearArgs a;
+  LinearTensors t;
+  spconv_status st = linear_args(args, &a, &t);
+  if (st != SPCONV_OK) return st;
+  if (epilogue == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "epilogue is NULL");
+  const uint64_t es = t.x.es;
+  const spconv_linear_epilogue& p = *epilogue;
+  const Strided bias = row_tensor("bias", p.bias, p.bias == nullptr ? 0 : a.groups, a.c_out, a.c_out, es);
+  const Strided residual = row_tensor("residual", p.residual, p.residual == nullptr ? 0 : a.rows, p.residual_row_stride, a.c_out, es);
+  const Strided pre = row_tensor("pre", p.pre, p.pre == nullptr ? 0 : a.rows, p.pre_row_stride, a.c_out, es);
+  const Strided out = row_tensor("out", p.out, a.rows, p.out_row_stride, a.c_out, es);
+  for (const Strided* s : {&bias, &residual, &pre, &out}) {
+    st = check_rows(*s, es, es, kMaxLinearRowBytes);
+    if (st != SPCONV_OK) return st;
+  }
+  for (const Strided* o : {&out, &pre}) {
+    for (const Strided& in : {t.x, t.weight, t.cu, bias}) {
+      st = check_apart(*o, in);
+      if (st != SPCONV_OK) return st;
+    }
+    st = check_apart_or_same(*o, residual, o == &out);
+    if (st != SPCONV_OK) return st;
+  }
+  st = check_apart(out, pre);
+  if (st == SPCONV_OK) st = check_work_items(spconv::linear_work_items(a, false));
+  if (st != SPCONV_OK) return st;
+  if (a.rows == 0) return SPCONV_OK;
+  a.bias = p.bias;
+  a.residual = p.residual;
+  a.residual_row = p.residual_row_stride;
+  a.pre = p.pre;
+  a.pre_row = p.pre_row_stride;
+  a.out = p.out;
+  a.out_row = p.out_row_stride;
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  return with_workspace(spconv::linear_workspace_bytes(a), own, {&t.x, &t.weight, &t.cu, &bias, &residual, &pre, &out}, stream, "linear launch",
+                        [&](void* ws) { return spconv::launch_linear(a, ws, stream); });
+}
+
+spconv_status linear_backward(const spconv_linear* args, const spconv_linear_gradients* grads, const CallerWorkspace* own, void* hip_stream) {
+  g_last_error.clear();
+  spconv::LinearArgs a;
+  LinearTensors t;
+  spconv_status st = linear_args(args, &a, &t);
+  if (st != SPCONV_OK) return st;
+  if (grads == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grads is NULL");
+  const uint64_t es = t.x.es;
+  const spconv_linear_gradients& g = *grads;
+  if (g.before != nullptr && a.act == SPCONV_ACT_NONE) return fail(SPCONV_ERR_INVALID_ARG, "before needs its activation");
+  if (g.grad_bias != nullptr && g.grad_weight == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "grad_bias needs grad_weight");
+  const Strided go = row_tensor("grad_out", g.grad_out, a.rows, g.grad_out_row_stride, a.c_out, es);
+  const Strided before = row_tensor("before", g.before, g.before == nullptr ? 0 : a.rows, g.before_row_stride, a.c_in, es);
+  const Strided gx = row_tensor("grad_x", g.grad_x, g.grad_x == nullptr ? 0 : a.rows, g.grad_x_row_stride, a.c_in, es);
+  const Strided gw = row_tensor("grad_weight", g.grad_weight, g.grad_weight == nullptr ? 0 : static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.c_out, 4);
+  const Strided gb = row_tensor("grad_bias", g.grad_bias, g.grad_bias == nullptr ? 0 : a.groups, a.c_out, a.c_out, 4);
+  st = check_rows(go, 16, a.c_out * es % 16 == 0 ? 16 : es, kMaxLinearRowBytes);
+  for (const Strided* s : {&before, &gx})
+    if (st == SPCONV_OK) st = check_rows(*s, es, es, kMaxLinearRowBytes);
+  for (const Strided* s : {&gw, &gb})
+    if (st == SPCONV_OK) st = check_rows(*s, 4, 4, kMaxLinearRowBytes);
+  for (const Strided* o : {&gx, &gw, &gb})
+    for (const Strided& in : {t.x, t.weight, t.cu, go, before})
+      if (st == SPCONV_OK) st = check_apart(*o, in);
+  if (st == SPCONV_OK) st = check_apart(gx, gw);
+  if (st == SPCONV_OK) st = check_apart(gx, gb);
+  if (st == SPCONV_OK) st = check_apart(gw, gb);
+  if (st != SPCONV_OK) return st;
+  a.grad_out = g.grad_out;
+  if (a.rows > 0) a.grad_out_row = g.grad_out_row_stride;
+  a.before = g.before;
+  a.before_row = g.before_row_stride;
+  a.grad_x = g.grad_x;
+  a.grad_x_row = g.grad_x_row_stride;
+  a.grad_weight = g.grad_weight;
+  a.grad_bias = g.grad_bias;
+  st = check_work_items(spconv::linear_work_items(a, true));
+  if (st != SPCONV_OK) return st;
+  if (a.grad_weight == nullptr && (a.rows == 0 || a.grad_x == nullptr)) return SPCONV_OK;
+  hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  return with_workspace(spconv::linear_backward_workspace_bytes(a), own, {&t.x, &t.weight, &t.cu, &go, &before, &gx, &gw, &gb}, stream,
+                        "linear backward launch", [&](void* ws) { return spconv::launch_linear_backward(a, ws, stream); });
+}
+
+spconv_status activation_backward(const void* d_grad_out, int64_t grad_out_row_stride, const void* d_pre, int64_t pre_row_stride, void* d_grad_pre,
+                                  int64_t grad_pre_row_stride, int64_t rows, int32_t channels, int32_t activation, int32_t dtype, void* hip_stream) {
+  g_last_error.clear();
+  spconv_status st = check_dtype(dtype);
+  if (st != SPCONV_OK) return st;
+  if (rows < 0 || rows > (int64_t(1) << 30) || channels < 1 || channels > (1 << 18)) {
+    return fail(SPCONV_ERR_INVALID_ARG, "rows = %lld must lie in [0, 2^30] and channels = %d in [1, 2^18]", (long long)rows, channels);
+  }
+  if (activation < SPCONV_ACT_NONE || activation > SPCONV_ACT_GELU) return fail(SPCONV_ERR_INVALID_ARG, "activation = %d is none", activation);
+  const uint64_t es = dtype == SPCONV_F32 ? 4u : 2u;
+  const Strided g = row_tensor("grad_out", d_grad_out, rows, grad_out_row_stride, channels, es);
+  const Strided pre = row_tensor("pre", d_pre, rows, pre_row_stride, channels, es);
+  const Strided out = row_tensor("grad_pre", d_grad_pre, rows, grad_pre_row_stride, channels, es);
+  for (const Strided* t : {&g, &pre, &out}) {
+    st = check_rows(*t, es, es, kMaxLinearRowBytes);
+    if (st != SPCONV_OK) return st;
+  }
+  st = check_apart_or_same(out, g, true);
+  if (st == SPCONV_OK) st = check_apart(out, pre);
+  if (st == SPCONV_OK) st = check_work_items(static_cast<uint64_t>(rows) * ((channels + 7) / 8) + 256);
+  if (st != SPCONV_OK) return st;
+  spconv::ActivationArgs a;
+  a.grad = d_grad_out;
+  a.pre = d_pre;
+  a.out = d_grad_pre;
+  a.grad_row = grad_out_row_stride;
+  a.pre_row = pre_row_stride;
+  a.out_row = grad_pre_row_stride;
+  a.rows = static_cast<int32_t>(rows);
+  a.cols = channels;
+  a.act = activation;
+  a.dtype = dtype;
+  const hipError_t e = spconv::launch_activation_backward(a, static_cast<hipStream_t>(hip_stream));
+  return e == hipSuccess ? SPCONV_OK : hip_fail(e, "activation backward launch");
+}
+
 // Nothing throws across the ABI: a host allocation that fails becomes a status.
 template <class F>
 spconv_status guarded(F&& f) {
@@ -1869,6 +2164,76 @@ void spconv_map_free(spconv_map* map) {
   if (map->block != nullptr) release_block(map->device, map->stream, map->block, map->block_bytes);
   if (map->slot != nullptr) release_slot(map->device, map->slot);
   delete map;
+}
+
+spconv_status spconv_add_norm_forward(const spconv_add_norm* args, void* d_h, int64_t h_row_stride, void* d_y, int64_t y_row_stride,
+                                      void* hip_stream) {
+  return guarded([&] { return add_norm_forward(args, d_h, h_row_stride, d_y, y_row_stride, hip_stream); });
+}
+
+spconv_status spconv_add_norm_backward(const spconv_add_norm* args, const spconv_add_norm_gradients* grads, void* hip_stream) {
+  return guarded([&] { return add_norm_backward(args, grads, nullptr, hip_stream); });
+}
+
+spconv_status spconv_add_norm_backward_noalloc(const spconv_add_norm* args, const spconv_add_norm_gradients* grads, void* d_workspace,
+                                               uint64_t workspace_bytes, void* hip_stream) {
+  const CallerWorkspace own = {d_workspace, workspace_bytes};
+  return guarded([&] { return add_norm_backward(args, grads, &own, hip_stream); });
+}
+
+spconv_status spconv_add_norm_workspace(int32_t channels, uint64_t* backward_bytes) {
+  return guarded([&]() -> spconv_status {
+    g_last_error.clear();
+    if (backward_bytes == nullptr) return fail(SPCONV_ERR_INVALID_ARG, "backward_bytes is NULL");
+    if (channels < 8 || channels % 8 != 0 || channels > 16384) {
+      return fail(SPCONV_ERR_UNSUPPORTED, "channels = %d must be a multiple of 8 in [8, 16384]", channels);
+    }
+    spconv::AddNormArgs a;
+    a.channels = channels;
+    *backward_bytes = spconv::add_norm_backward_workspace_bytes(a);
+    return SPCONV_OK;
+  });
+}
+
+spconv_status spconv_linear_forward(const spconv_linear* args, const spconv_linear_epilogue* epilogue, void* hip_stream) {
+  return guarded([&] { return linear_forward(args, epilogue, nullptr, hip_stream); });
+}
+
+spconv_status spconv_linear_forward_noalloc(const spconv_linear* args, const spconv_linear_epilogue* epilogue, void* d_workspace,
+                                            uint64_t workspace_bytes, void* hip_stream) {
+  const CallerWorkspace own = {d_workspace, workspace_bytes};
+  return guarded([&] { return linear_forward(args, epilogue, &own, hip_stream); });
+}
+
+spconv_status spconv_linear_backward(const spconv_linear* args, const spconv_linear_gradients* grads, void* hip_stream) {
+  return guarded([&] { return linear_backward(args, grads, nullptr, hip_stream); });
+}
+
+spconv_status spconv_linear_backward_noalloc(const spconv_linear* args, const spconv_linear_gradients* grads, void* d_workspace,
+                                             uint64_t workspace_bytes, void* hip_stream) {
+  const CallerWorkspace own = {d_workspace, workspace_bytes};
+  return guarded([&] { return linear_backward(args, grads, &own, hip_stream); });
+}
+
+spconv_status spconv_linear_workspace(const spconv_linear* args, uint64_t* forward_bytes, uint64_t* backward_bytes) {
+  return guarded([&]() -> spconv_status {
+    g_last_error.clear();
+    spconv::LinearArgs a;
+    const spconv_status st = linear_sizes(args, &a);
+    if (st != SPCONV_OK) return st;
+    if (forward_bytes != nullptr) *forward_bytes = a.rows == 0 ? 0 : spconv::linear_workspace_bytes(a);
+    if (backward_bytes != nullptr) *backward_bytes = spconv::linear_backward_workspace_bytes(a);
+    return SPCONV_OK;
+  });
+}
+
+spconv_status spconv_activation_backward(const void* d_grad_out, int64_t grad_out_row_stride, const void* d_pre, int64_t pre_row_stride,
+                                         void* d_grad_pre, int64_t grad_pre_row_stride, int64_t rows, int32_t channels, int32_t activation,
+                                         spconv_dtype dtype, void* hip_stream) {
+  return guarded([&] {
+    return activation_backward(d_grad_out, grad_out_row_stride, d_pre, pre_row_stride, d_grad_pre, grad_pre_row_stride, rows, channels,
+                               activation, static_cast<int32_t>(dtype), hip_stream);
+  });
 }
 
 }  // extern "C"

@@ -358,4 +358,103 @@ hipError_t launch_norm_rotary_backward(const NormRotaryArgs& a, void* workspace,
 hipError_t launch_rotary_table(float* table, int32_t extent, int32_t pairs, double base, double scale,
                                hipStream_t stream);
 
+// ---- Products of packed rows (linear.hip, linear_kernels.h) ----
+// One matrix product over rows or over groups of rows.
+//   kByRows:      out[m][:] = a[m][:] b            (b [k][n]: a row's product)
+//   kByRowsT:     out[m][:] = a[m][:] b^T          (b [n][k]: its gradient)
+//   kOverRows:    out = sum over rows of a[row][:]^T b[row][:]  (the weights')
+enum ProductForm { kByRows = 0, kByRowsT = 1, kOverRows = 2 };
+// Bits of `wide`: 16-byte accesses fit the tensor.
+enum : uint32_t { kWideOut = 1, kWidePre = 2, kWideBefore = 4, kWideResidual = 8 };
+struct ProductArgs {
+  const void* a = nullptr;
+  const void* b = nullptr;
+  int64_t a_row = 0, b_row = 0;  // row strides in elements
+  int64_t b_group = 0;           // elements between two groups' b (by rows)
+  int32_t a_cols = 0, b_cols = 0;  // readable elements of a row: whole 16-byte pieces, zeros past the ones there are
+  const int32_t* cu = nullptr;   // groups + 1 row offsets, NULL: all rows are group 0
+  int32_t groups = 1;
+  int32_t rows = 0;
+  int32_t m = 0, n = 0, k = 0;  // by rows: n columns, k contracted; over rows: [m][n] sums
+  FastDiv by_unit;               // rows of a slot: a tile's, or those of one part of a group
+  int32_t slots = 0, tiles = 0, tiles_n = 0;  // tiles of the columns (by rows) or of the sums (over rows)
+  int32_t splits = 1, k_split = 0;            // parts of k (by rows) and k of each, a multiple of the step
+  // parts: fp32 sums [split][rows][n_part] or [slot][m][n_part]; NULL: out is written
+  float* part = nullptr;
+  int32_t n_part = 0;
+  // by rows
+  const void* bias = nullptr;      // [groups][n]
+  const void* residual = nullptr;  // [rows][n]
+  const void* before = nullptr;    // [rows][n]: out is multiplied by the slope of act there
+  void* pre = nullptr;             // [rows][n]: the product before act
+  void* out = nullptr;             // [rows][n]; over rows: fp32 [groups][m][n]
+  int64_t residual_row = 0, before_row = 0, pre_row = 0, out_row = 0;
+  int32_t act = 0;
+  uint32_t wide = 0;
+  // over rows: the column sums of b, fp32 [groups][n], or their parts [slot][n_part]
+  float* sums = nullptr;
+  float* sums_part = nullptr;
+};
+
+// Workgroup shapes: rows x columns of a tile (linear_kernels.h).
+enum ProductShape { kTinyShape, kNarrowShape, kMediumShape, kLargeShape };
+hipError_t launch_product_f32(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
+hipError_t launch_product_f16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
+hipError_t launch_product_bf16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
+
+struct LinearArgs {
+  const void* x = nullptr;
+  const void* weight = nullptr;  // [groups][c_in][c_out]
+  int64_t x_row = 0;
+  const int32_t* cu = nullptr;
+  int32_t rows = 0, groups = 1, c_in = 0, c_out = 0, act = 0, dtype = 0;
+  // forward
+  const void* bias = nullptr;
+  const void* residual = nullptr;
+  void* out = nullptr;
+  void* pre = nullptr;
+  int64_t residual_row = 0, out_row = 0, pre_row = 0;
+  // backward
+  const void* grad_out = nullptr;
+  const void* before = nullptr;
+  void* grad_x = nullptr;
+  float* grad_weight = nullptr;
+  float* grad_bias = nullptr;
+  int64_t grad_out_row = 0, before_row = 0, grad_x_row = 0;
+};
+uint64_t linear_work_items(const LinearArgs& a, bool backward);
+size_t linear_workspace_bytes(const LinearArgs& a);
+size_t linear_backward_workspace_bytes(const LinearArgs& a);
+hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t stream);
+hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, hipStream_t stream);
+// grad_pre = grad x act'(pre) over [rows][cols], strides in elements.
+struct ActivationArgs {
+  const void* grad = nullptr;
+  const void* pre = nullptr;
+  void* out = nullptr;
+  int64_t grad_row = 0, pre_row = 0, out_row = 0;
+  int32_t rows = 0, cols = 0, act = 0, dtype = 0;
+};
+hipError_t launch_activation_backward(const ActivationArgs& a, hipStream_t stream);
+
+// ---- Row norm with the residual's addition (add_norm.hip) ----
+struct AddNormArgs {
+  const void* x = nullptr;         // [rows][channels], strides in elements
+  const void* residual = nullptr;  // NULL: none
+  const void* weight = nullptr;    // [channels]
+  void* h = nullptr;               // x + residual (NULL without a residual: h is x)
+  void* y = nullptr;
+  const void* grad_h = nullptr;  // NULL: none
+  const void* grad_y = nullptr;
+  void* grad = nullptr;
+  float* grad_weight = nullptr;
+  int64_t x_row = 0, residual_row = 0, h_row = 0, y_row = 0, grad_h_row = 0, grad_y_row = 0, grad_row = 0;
+  int32_t rows = 0, channels = 0, dtype = 0;
+  float eps = 0.f;
+};
+uint64_t add_norm_work_items(const AddNormArgs& a);
+hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t stream);
+size_t add_norm_backward_workspace_bytes(const AddNormArgs& a);
+hipError_t launch_add_norm_backward(const AddNormArgs& a, void* workspace, hipStream_t stream);
+
 }  // namespace spconv

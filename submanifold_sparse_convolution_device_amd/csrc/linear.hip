@@ -1,0 +1,405 @@
+// Products of packed rows with their epilogue, and their gradients: the plan
+// of each call (tile shape, parts of the contraction, operands that have to be
+// laid out first), the joins of the parts, and the activation's gradient.
+//
+//   forward:   out = act(x W + b) + residual            one product by rows
+//   backward:  grad_x = grad W^T (x act'(before))       by rows, W transposed
+//              grad_W = x^T grad, grad_b = sum of grad  over rows, one pass
+//
+// The products themselves are in linear_kernels.h.
+#include <algorithm>
+
+#include "linear_common.h"
+
+namespace spconv {
+namespace {
+
+using lin::Segment;
+
+// ---- Laying out ----
+// Rows of whole 16-byte pieces are read as they lie; other row lengths (or
+// strides) are copied first, to rows padded with zeros.
+template <class E>
+__global__ __launch_bounds__(256) void k_lay_out(const E* src, int64_t src_row, int64_t rows, int cols, E* dst, int dst_cols) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E));
+  typedef E vec __attribute__((ext_vector_type(N)));
+  const int pieces = dst_cols / N;
+  const int64_t total = rows * pieces;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = i / pieces;
+    const int col = static_cast<int>(i - row * pieces) * N;
+    vec v;
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = col + j < cols ? src[row * src_row + col + j] : static_cast<E>(0);
+    *reinterpret_cast<vec*>(dst + row * dst_cols + col) = v;
+  }
+}
+
+// ---- Joining ----
+// By rows: the parts of k summed in their order, then the epilogue; 8 columns
+// a thread.
+template <class T>
+__global__ __launch_bounds__(256) void k_join_rows(ProductArgs a) {
+  const int pieces = a.n_part / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= static_cast<int64_t>(a.rows) * pieces) return;
+  const int64_t row = i / pieces;
+  const int col = static_cast<int>(i - row * pieces) * 8, there = min(a.n - col, 8);
+  int group = 0;
+  if (a.cu != nullptr) {  // the segment: the last bound at or before the row
+    int lo = 0, hi = a.groups + 2;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (attn::bound(a.cu, a.groups, a.rows, mid) <= row) lo = mid;
+      else hi = mid;
+    }
+    group = lo == 0 || lo == a.groups + 1 ? -1 : lo - 1;
+  }
+  float v[8] = {}, bias[8] = {};
+  if (group >= 0) {
+    const float* p = a.part + row * a.n_part + col;
+    const int64_t step = static_cast<int64_t>(a.rows) * a.n_part;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+      const float4 x = *reinterpret_cast<const float4*>(p + s * step), y = *reinterpret_cast<const float4*>(p + s * step + 4);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+    }
+    if (a.bias != nullptr) lin::load8<T>(static_cast<const T*>(a.bias) + static_cast<int64_t>(group) * a.n + col, there, false, bias);
+  }
+  lin::finish8<T>(a, row, col, there, group >= 0, bias, v);
+}
+
+// Over rows: the parts of each group summed in their order; a group without
+// rows gives zeros.  Row m of the sums is the column sums of b.
+__global__ __launch_bounds__(256) void k_join_groups(ProductArgs a) {
+  const int group = blockIdx.y;
+  const int pieces = a.n_part / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= static_cast<int64_t>(a.m + (a.sums != nullptr)) * pieces) return;
+  const int m = static_cast<int>(i / pieces), col = static_cast<int>(i - static_cast<int64_t>(m) * pieces) * 4;
+  int first = 0, rows = a.rows;
+  if (a.cu != nullptr) {
+    const int r0 = attn::bound(a.cu, a.groups, a.rows, group + 1), r1 = attn::bound(a.cu, a.groups, a.rows, group + 2);
+    rows = max(r1 - r0, 0);
+    first = lin::segment_start(a, group + 1);
+  }
+  const int unit = a.by_unit.d, parts = rows == 0 ? 0 : fast_div(rows - 1, a.by_unit) + 1;
+  (void)unit;
+  const bool sums = m == a.m;
+  const float* p = sums ? a.sums_part + static_cast<int64_t>(first) * a.n_part + col
+                        : a.part + (static_cast<int64_t>(first) * a.m + m) * a.n_part + col;
+  const int64_t step = sums ? a.n_part : static_cast<int64_t>(a.m) * a.n_part;
+  float v[4] = {};
+#pragma unroll 8
+  for (int s = 0; s < parts; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(p + s * step);
+    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+  }
+  float* dst = sums ? a.sums + static_cast<int64_t>(group) * a.n + col : static_cast<float*>(a.out) + (static_cast<int64_t>(group) * a.m + m) * a.n + col;
+  if ((a.wide & kWideOut) && !sums && col + 4 <= a.n) {
+    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < a.n) dst[j] = v[j];
+  }
+}
+
+// ---- The activation's gradient ----
+template <class T>
+__global__ __launch_bounds__(256) void k_activation_backward(ActivationArgs a, int pieces, FastDiv by_pieces, bool wide) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= static_cast<int64_t>(a.rows) * pieces) return;
+  const int64_t row = i < (int64_t(1) << 31) ? fast_div(static_cast<int>(i), by_pieces) : i / pieces;
+  const int col = static_cast<int>(i - row * pieces) * 8, there = min(a.cols - col, 8);
+  float g[8], z[8];
+  lin::load8<T>(static_cast<const T*>(a.grad) + row * a.grad_row + col, there, wide, g);
+  lin::load8<T>(static_cast<const T*>(a.pre) + row * a.pre_row + col, there, wide, z);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] *= lin::slope<T>(a.act, z[j]);
+  lin::store8<T>(static_cast<T*>(a.out) + row * a.out_row + col, there, wide, g);
+}
+
+// ---- The plan ----
+int64_t size_of(int dtype) { return dtype == 0 ? 4 : 2; }
+bool whole_pieces(int64_t elements, int dtype) { return elements * size_of(dtype) % 16 == 0; }
+int32_t padded(int32_t cols) { return (cols + 7) / 8 * 8; }
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Takes pieces of a workspace one after another; without one it counts.
+struct Carver {
+  char* base;
+  size_t at = 0;
+  void* take(size_t bytes) {
+    void* p = base == nullptr ? nullptr : base + at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  }
+};
+
+// An operand and, where it has to be laid out first, its copy.
+struct Operand {
+  const void* p;
+  int64_t row;
+  int32_t cols;
+  void* copy;
+};
+Operand operand(const void* p, int64_t row_stride, int64_t rows, int32_t cols, int dtype, Carver* w) {
+  if (whole_pieces(cols, dtype) && whole_pieces(row_stride, dtype)) return {p, row_stride, cols, nullptr};
+  const int32_t c = padded(cols);
+  void* copy = w->take(static_cast<size_t>(rows) * c * size_of(dtype));
+  return {copy, c, c, copy};
+}
+hipError_t lay_out(const Operand& o, const void* src, int64_t row_stride, int64_t rows, int32_t cols, int dtype, hipStream_t stream) {
+  if (o.cols == cols && whole_pieces(row_stride, dtype)) return hipSuccess;
+  const int64_t pieces = rows * (o.cols * size_of(dtype) / 16);
+  if (pieces == 0) return hipSuccess;
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((pieces + 255) / 256, 8192));
+  if (dtype == 0) {
+    k_lay_out<uint32_t><<<blocks, 256, 0, stream>>>(static_cast<const uint32_t*>(src), row_stride, rows, cols, static_cast<uint32_t*>(o.copy), o.cols);
+  } else {
+    k_lay_out<uint16_t><<<blocks, 256, 0, stream>>>(static_cast<const uint16_t*>(src), row_stride, rows, cols, static_cast<uint16_t*>(o.copy), o.cols);
+  }
+  return hipGetLastError();
+}
+
+struct ShapeSize {
+  int bm, bn, bk, threads;
+};
+ShapeSize shape_size(int dtype, ProductShape s) {
+  if (dtype == 0) {
+    if (s == kTinyShape) return {32, 128, 32, 256};
+    if (s == kNarrowShape) return {128, 32, 32, 256};
+    return {128, 128, 32, 256};
+  }
+  if (s == kTinyShape) return {32, 128, 64, 256};
+  if (s == kNarrowShape) return {128, 64, 64, 256};
+  if (s == kMediumShape) return {128, 128, 64, 256};
+  return {256, 256, 64, 512};
+}
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Workgroups that fill the chip: two on each of 256 CUs.
+constexpr int64_t kFill = 512;
+
+struct Product {
+  ProductArgs a;
+  ProductForm form;
+  ProductShape shape;
+  int dtype;
+  uint64_t items() const {
+    const uint64_t blocks = static_cast<uint64_t>(a.slots) * static_cast<uint64_t>(a.tiles) * (form == kOverRows ? 1 : a.splits);
+    return blocks * shape_size(dtype, shape).threads;
+  }
+};
+
+// Sizes of a product by rows: rows x k times k x n of each group.
+Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t rows, int32_t groups, int32_t k, int32_t n, Carver* w) {
+  Product p;
+  p.form = form;
+  p.dtype = dtype;
+  const int64_t each = rows / groups;
+  p.shape = each <= 32 ? kTinyShape : n <= (dtype == 0 ? 32 : 64) ? kNarrowShape : kMediumShape;
+  if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 256 && div_up(rows, 256) * div_up(n, 256) >= 200) p.shape = kLargeShape;
+  const ShapeSize s = shape_size(dtype, p.shape);
+  ProductArgs& a = p.a;
+  a.cu = cu;
+  a.groups = groups;
+  a.rows = rows;
+  a.n = n;
+  a.k = k;
+  a.by_unit = make_fast_div(s.bm);
+  a.slots = static_cast<int32_t>(cu == nullptr ? div_up(rows, s.bm) : rows / s.bm + groups + 2);
+  a.tiles = a.tiles_n = static_cast<int32_t>(div_up(n, s.bn));
+  const int64_t steps = div_up(k, s.bk), blocks = std::max<int64_t>(1, static_cast<int64_t>(a.slots) * a.tiles);
+  int64_t splits = 1;
+  if (blocks * 2 <= kFill && steps >= 8) splits = std::min(kFill / blocks, steps / 4);
+  a.k_split = static_cast<int32_t>(div_up(steps, splits) * s.bk);
+  a.splits = static_cast<int32_t>(div_up(k, a.k_split));
+  a.n_part = padded(n);
+  if (a.splits > 1) a.part = static_cast<float*>(w->take(static_cast<size_t>(a.splits) * rows * a.n_part * sizeof(float)));
+  return p;
+}
+
+// Sizes of a product over the rows of each group: m x n sums.
+Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t groups, int32_t m, int32_t n, Carver* w) {
+  Product p;
+  p.form = kOverRows;
+  p.dtype = dtype;
+  p.shape = n <= (dtype == 0 ? 32 : 64) ? kNarrowShape : kMediumShape;
+  if (dtype != 0 && p.shape == kMediumShape && div_up(m, 256) * div_up(n, 256) >= 200) p.shape = kLargeShape;
+  const ShapeSize s = shape_size(dtype, p.shape);
+  ProductArgs& a = p.a;
+  a.cu = cu;
+  a.groups = groups;
+  a.rows = rows;
+  a.m = m;
+  a.n = n;
+  a.tiles_n = static_cast<int32_t>(div_up(n, s.bn));
+  a.tiles = static_cast<int32_t>(div_up(m, s.bm) * a.tiles_n);
+  a.n_part = padded(n);
+  const int64_t parts = std::min<int64_t>(kFill / a.tiles, rows / 256);
+  if (parts <= 1 || parts <= groups) {  // every group is one part
+    a.by_unit = make_fast_div(1 << 30);
+    a.slots = cu == nullptr ? 1 : groups + 2;
+  } else {
+    const int64_t unit = div_up(div_up(rows, parts), s.bk) * s.bk;
+    a.by_unit = make_fast_div(static_cast<int32_t>(unit));
+    a.slots = static_cast<int32_t>(cu == nullptr ? div_up(rows, unit) : rows / unit + groups + 2);
+    a.part = static_cast<float*>(w->take(static_cast<size_t>(a.slots) * m * a.n_part * sizeof(float)));
+    a.sums_part = static_cast<float*>(w->take(static_cast<size_t>(a.slots) * a.n_part * sizeof(float)));
+  }
+  return p;
+}
+
+hipError_t run_product(const Product& p, hipStream_t stream) {
+  if (p.dtype == 0) return launch_product_f32(p.a, p.form, p.shape, stream);
+  if (p.dtype == 1) return launch_product_f16(p.a, p.form, p.shape, stream);
+  return launch_product_bf16(p.a, p.form, p.shape, stream);
+}
+
+hipError_t run_by_rows(const Product& p, hipStream_t stream) {
+  if (p.a.rows == 0) return hipSuccess;
+  const hipError_t e = run_product(p, stream);
+  if (e != hipSuccess || p.a.splits == 1) return e;
+  const unsigned blocks = static_cast<unsigned>(div_up(static_cast<int64_t>(p.a.rows) * (p.a.n_part / 8), 256));
+  if (p.dtype == 0) k_join_rows<float><<<blocks, 256, 0, stream>>>(p.a);
+  else if (p.dtype == 1) k_join_rows<_Float16><<<blocks, 256, 0, stream>>>(p.a);
+  else k_join_rows<__bf16><<<blocks, 256, 0, stream>>>(p.a);
+  return hipGetLastError();
+}
+
+uint32_t wide(const void* p, int64_t row_stride, int dtype, uint32_t bit) { return aligned(p) && whole_pieces(row_stride, dtype) ? bit : 0; }
+
+struct Forward {
+  Operand x, w;
+  Product p;
+  size_t bytes;
+};
+Forward plan_forward(const LinearArgs& a, void* workspace) {
+  Forward f;
+  Carver c{static_cast<char*>(workspace)};
+  f.x = operand(a.x, a.x_row, a.rows, a.c_in, a.dtype, &c);
+  f.w = operand(a.weight, a.c_out, static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.dtype, &c);
+  f.p = plan_by_rows(kByRows, a.dtype, a.cu, a.rows, a.groups, a.c_in, a.c_out, &c);
+  f.bytes = c.at;
+  return f;
+}
+
+struct Backward {
+  Operand x, w, g;
+  Product gx, gw;
+  size_t bytes;
+};
+Backward plan_backward(const LinearArgs& a, void* workspace) {
+  Backward b;
+  Carver c{static_cast<char*>(workspace)};
+  b.x = operand(a.x, a.x_row, a.rows, a.c_in, a.dtype, &c);
+  b.g = operand(a.grad_out, a.grad_out_row, a.rows, a.c_out, a.dtype, &c);
+  b.w = operand(a.weight, a.c_out, static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.dtype, &c);
+  // (the two products run one after the other: their parts may share a place)
+  Carver c1 = c, c2 = c;
+  b.gx = plan_by_rows(kByRowsT, a.dtype, a.cu, a.rows, a.groups, a.c_out, a.c_in, &c1);
+  b.gw = plan_over_rows(a.dtype, a.cu, a.rows, a.groups, a.c_in, a.c_out, &c2);
+  b.bytes = std::max(c1.at, c2.at);
+  return b;
+}
+
+}  // namespace
+
+uint64_t linear_work_items(const LinearArgs& a, bool backward) {
+  if (!backward) return plan_forward(a, nullptr).p.items();
+  const Backward b = plan_backward(a, nullptr);
+  const uint64_t join = static_cast<uint64_t>(div_up(static_cast<int64_t>(a.c_in + 1) * (b.gw.a.n_part / 4), 256)) * 256 * a.groups;
+  return std::max({b.gx.items(), b.gw.items(), b.gw.a.part == nullptr && b.gw.a.slots <= a.groups + 2 ? uint64_t(0) : join});
+}
+
+size_t linear_workspace_bytes(const LinearArgs& a) { return plan_forward(a, nullptr).bytes; }
+size_t linear_backward_workspace_bytes(const LinearArgs& a) { return plan_backward(a, nullptr).bytes; }
+
+hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  Forward f = plan_forward(a, workspace);
+  hipError_t e = lay_out(f.x, a.x, a.x_row, a.rows, a.c_in, a.dtype, stream);
+  if (e == hipSuccess) e = lay_out(f.w, a.weight, a.c_out, static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.dtype, stream);
+  if (e != hipSuccess) return e;
+  ProductArgs& p = f.p.a;
+  p.a = f.x.p;
+  p.a_row = f.x.row;
+  p.a_cols = f.x.cols;
+  p.b = f.w.p;
+  p.b_row = f.w.row;
+  p.b_cols = f.w.cols;
+  p.b_group = static_cast<int64_t>(a.c_in) * f.w.row;
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.residual_row = a.residual_row;
+  p.pre = a.pre;
+  p.pre_row = a.pre_row;
+  p.out = a.out;
+  p.out_row = a.out_row;
+  p.act = a.act;
+  p.wide = wide(a.out, a.out_row, a.dtype, kWideOut) | wide(a.pre, a.pre_row, a.dtype, kWidePre) | wide(a.residual, a.residual_row, a.dtype, kWideResidual);
+  return run_by_rows(f.p, stream);
+}
+
+hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, hipStream_t stream) {
+  Backward b = plan_backward(a, workspace);
+  hipError_t e = lay_out(b.g, a.grad_out, a.grad_out_row, a.rows, a.c_out, a.dtype, stream);
+  if (e == hipSuccess && a.grad_weight != nullptr) e = lay_out(b.x, a.x, a.x_row, a.rows, a.c_in, a.dtype, stream);
+  if (e == hipSuccess && a.grad_x != nullptr) e = lay_out(b.w, a.weight, a.c_out, static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.dtype, stream);
+  if (e != hipSuccess) return e;
+  if (a.grad_x != nullptr) {
+    ProductArgs& p = b.gx.a;
+    p.a = b.g.p;
+    p.a_row = b.g.row;
+    p.a_cols = b.g.cols;
+    p.b = b.w.p;
+    p.b_row = b.w.row;
+    p.b_cols = b.w.cols;
+    p.b_group = static_cast<int64_t>(a.c_in) * b.w.row;
+    p.before = a.before;
+    p.before_row = a.before_row;
+    p.act = a.act;
+    p.out = a.grad_x;
+    p.out_row = a.grad_x_row;
+    p.wide = wide(a.grad_x, a.grad_x_row, a.dtype, kWideOut) | wide(a.before, a.before_row, a.dtype, kWideBefore);
+    e = run_by_rows(b.gx, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (a.grad_weight != nullptr) {
+    ProductArgs& p = b.gw.a;
+    p.a = b.x.p;
+    p.a_row = b.x.row;
+    p.a_cols = b.x.cols;
+    p.b = b.g.p;
+    p.b_row = b.g.row;
+    p.b_cols = b.g.cols;
+    p.out = a.grad_weight;
+    p.sums = a.grad_bias;
+    if (a.grad_bias == nullptr) p.sums_part = nullptr;
+    p.wide = wide(a.grad_weight, a.c_out, 0, kWideOut);
+    e = run_product(b.gw, stream);
+    if (e != hipSuccess || p.part == nullptr) return e;
+    const int64_t threads = static_cast<int64_t>(p.m + 1) * (p.n_part / 4);
+    k_join_groups<<<dim3(static_cast<unsigned>(div_up(threads, 256)), static_cast<unsigned>(p.groups)), 256, 0, stream>>>(p);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_activation_backward(const ActivationArgs& a, hipStream_t stream) {
+  const int pieces = (a.cols + 7) / 8;
+  const int64_t total = static_cast<int64_t>(a.rows) * pieces;
+  if (total == 0) return hipSuccess;
+  const bool w = wide(a.grad, a.grad_row, a.dtype, 1) && wide(a.pre, a.pre_row, a.dtype, 1) && wide(a.out, a.out_row, a.dtype, 1);
+  const unsigned blocks = static_cast<unsigned>(div_up(total, 256));
+  const FastDiv by = make_fast_div(pieces);
+  if (a.dtype == 0) k_activation_backward<float><<<blocks, 256, 0, stream>>>(a, pieces, by, w);
+  else if (a.dtype == 1) k_activation_backward<_Float16><<<blocks, 256, 0, stream>>>(a, pieces, by, w);
+  else k_activation_backward<__bf16><<<blocks, 256, 0, stream>>>(a, pieces, by, w);
+  return hipGetLastError();
+}
+
+}  // namespace spconv

@@ -1,0 +1,8 @@
+// The matrix products of packed rows in bf16.
+#include "linear_kernels.h"
+
+namespace spconv {
+hipError_t launch_product_bf16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream) {
+  return lin::launch_typed<__bf16>(a, form, shape, stream);
+}
+}  // namespace spconv

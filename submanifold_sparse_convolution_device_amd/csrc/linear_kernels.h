@@ -1,0 +1,378 @@
+// The matrix products of packed rows, for one type (linear_f32.hip,
+// linear_f16.hip and linear_bf16.hip hold an instance each).
+//
+//   by rows:    out[m][n] = sum_k a[m][k] b[k][n]      b rows along k (the weights as they lie)
+//   by rows T:  out[m][n] = sum_k a[m][k] b[n][k]      b rows along n (the same weights, transposed)
+//   over rows:  out[m][n] = sum_r a[r][m] b[r][n]      both rows along the contraction
+//
+// A workgroup computes a BM x BN tile of one group of rows, or of one part of
+// its contraction; its wavefronts WR x WC share it in tiles of 32 x 32
+// products.  Per step of BK contracted values it loads its part of both
+// operands in 16-byte pieces (rows, columns and contracted values that do not
+// exist come back as zeros from the buffer's bounds check), and puts them into
+// LDS as they lie in memory: an operand whose rows run along the contraction
+// is read with the transposing LDS read, the other one piece by piece.  The
+// next step's loads are in flight during this step's products.  fp32 operands
+// go into LDS as three bf16 planes (attention_common.h).
+//
+// The products run as C^T = B^T A^T, so a lane holds 4 neighbouring columns of
+// one row; the sums pass through the wavefront's own LDS into whole rows, 8
+// columns a lane, for the epilogue (finish8) and 16-byte accesses.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "linear_common.h"
+
+namespace spconv {
+namespace lin {
+
+using attn::Frag;
+using attn::Raw;
+using attn::floatx16;
+using attn::kPlanes;
+
+// Orders a wavefront's own LDS accesses.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// One operand's part of a step: ROWS rows of PPR pieces, by NT threads.
+template <class T, int ROWS, int PPR, int NT>
+struct Stage {
+  static constexpr int kCount = (ROWS * PPR + NT - 1) / NT;
+  static constexpr bool kWhole = ROWS * PPR % NT == 0;
+  static_assert(NT % PPR == 0 && ((PPR & (PPR - 1)) == 0) && PPR >= 4, "a thread's pieces share a column");
+  Raw<T> r[kCount];
+
+  // base: the first piece; rows_left rows and cols_left columns (whole
+  // 16-byte pieces) exist from there.
+  __device__ __forceinline__ void load(const T* base, int64_t stride, int rows_left, int cols_left, int tid) {
+    const uint32_t row_bytes = static_cast<uint32_t>(stride) * sizeof(T);  // (at most 2^22: 2^30 for a tile)
+    const int rows = min(max(rows_left, 0), ROWS);
+    const int bytes = rows > 0 && cols_left > 0 ? (rows - 1) * static_cast<int>(row_bytes) + min(cols_left, PPR * 8) * static_cast<int>(sizeof(T)) : 0;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, attn::kBufferWord3);
+    const int piece = tid % PPR, row = tid / PPR;
+#pragma unroll
+    for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) {
+      const bool on = piece * 8 + h * 4 < cols_left;
+      const uint32_t v0 = on ? row * row_bytes + (piece * 8 * sizeof(T) + 16 * h) : attn::kNowhere;
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) {
+        const uint32_t v = v0 + static_cast<uint32_t>(i * (NT / PPR)) * row_bytes;
+        r[i].v[h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, static_cast<int>(kWhole || row + i * (NT / PPR) < ROWS ? v : attn::kNowhere), 0, 0));
+      }
+    }
+  }
+
+  // The place of a piece: its index XOR-ed with a function of the row.
+  // ALONG: the contraction runs along a row, and 16 lanes read one piece of 16
+  // rows; else 16 lanes read 4 rows x 32 bytes (transposed).
+  template <bool ALONG>
+  __device__ static __forceinline__ int at(int row, int piece) {
+    if constexpr (ALONG) {
+      return row * PPR + (piece ^ (PPR == 8 ? row & 7 : row >> 1 & 3));
+    } else if constexpr (PPR >= 16) {
+      return row * PPR + (piece ^ ((row & 3) << 2 ^ (row & 2)));
+    } else if constexpr (PPR == 8) {
+      return row * PPR + (piece ^ (row & 3) << 1);
+    } else {
+      return row * PPR + (piece ^ (row & 2));
+    }
+  }
+
+  template <bool ALONG>
+  __device__ __forceinline__ void store(uint4* lds, int tid) const {
+    const int piece = tid % PPR, row = tid / PPR;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const Frag<T> f = attn::to_frag<T>(r[i]);
+      const int w = row + i * (NT / PPR);
+      if (kWhole || w < ROWS) {
+#pragma unroll
+        for (int p = 0; p < kPlanes<T>; ++p) lds[p * ROWS * PPR + at<ALONG>(w, piece)] = f.v[p];
+      }
+    }
+  }
+
+  // The operand of 32 rows (columns, where the contraction runs along the
+  // tile's rows) from x0 and 16 contracted values from 16 t.
+  template <bool ALONG>
+  __device__ static __forceinline__ Frag<T> frag(const uint4* lds, int x0, int t, int lane) {
+    Frag<T> f;
+    if constexpr (ALONG) {
+      const int place = at<true>(x0 + (lane & 31), 2 * t + (lane >> 5));
+#pragma unroll
+      for (int p = 0; p < kPlanes<T>; ++p) f.v[p] = lds[p * ROWS * PPR + place];
+    } else {
+      // lane g of 16 addresses 4 columns of row g / 4, and receives column g of the four rows
+      const int g = lane & 15, row = 16 * t + 8 * (lane >> 5) + (g >> 2), col = x0 + 16 * (lane >> 4 & 1) + 4 * (g & 3);
+#pragma unroll
+      for (int p = 0; p < kPlanes<T>; ++p) {
+        uint2 half[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const char* src = reinterpret_cast<const char*>(lds + p * ROWS * PPR + at<false>(row + 4 * u, col / 8)) + (col & 4) * 2;
+          half[u] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn::lds_s16x4*)src));
+        }
+        f.v[p] = make_uint4(half[0].x, half[0].y, half[1].x, half[1].y);
+      }
+    }
+    return f;
+  }
+};
+
+// A workgroup's shape.
+template <int BM_, int BN_, int WR_, int WC_, int BK_, int STAGES_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, BK = BK_, STAGES = STAGES_;
+  static constexpr int NT = 64 * WR * WC, TM = BM / WR, TN = BN / WC;
+};
+
+template <class T, class S, int FORM>
+struct Kernel {
+  static constexpr bool kAlongA = FORM != kOverRows, kAlongB = FORM == kByRowsT;
+  static constexpr int kRowsA = kAlongA ? S::BM : S::BK, kPprA = (kAlongA ? S::BK : S::BM) / 8;
+  static constexpr int kRowsB = kAlongB ? S::BN : S::BK, kPprB = (kAlongB ? S::BK : S::BN) / 8;
+  typedef Stage<T, kRowsA, kPprA, S::NT> A;
+  typedef Stage<T, kRowsB, kPprB, S::NT> B;
+  static constexpr int kPiecesA = kRowsA * kPprA * kPlanes<T>, kPieces = kPiecesA + kRowsB * kPprB * kPlanes<T>;
+  static constexpr int kOutStride = S::TN + 4;  // floats of a staged row of sums
+  static constexpr int kOutPieces = S::WR * S::WC * 32 * kOutStride / 4;
+  static constexpr int kLds = std::max(kPieces * S::STAGES, std::max(kOutPieces, S::NT * 2));
+};
+
+template <class T, class S, int FORM>
+__global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
+  typedef Kernel<T, S, FORM> K;
+  __shared__ uint4 lds[K::kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / S::WC, wc = wave % S::WC;
+
+  // Consecutive workgroups go to the 8 XCDs in turn; each XCD takes a
+  // consecutive eighth of the tiles, so that tiles that share rows or weights
+  // share its L2.
+  const int total = gridDim.x, eighth = total / 8, over = total % 8;
+  const int xcd = blockIdx.x % 8;
+  int at = blockIdx.x / 8 + xcd * eighth + min(xcd, over);
+  int slot, m0, n0, k0 = 0, k1, split = 0;
+  if constexpr (FORM == kOverRows) {
+    slot = at / a.tiles;
+    const int tile = at - slot * a.tiles;
+    m0 = tile / a.tiles_n * S::BM;
+    n0 = tile % a.tiles_n * S::BN;
+  } else {
+    // 4 slots by all columns at a time: what runs together shares both sides
+    const int per = a.slots * a.tiles;
+    split = at / per;
+    at -= split * per;
+    const int band = at / (4 * a.tiles), high = min(4, a.slots - 4 * band);
+    at -= band * 4 * a.tiles;
+    slot = 4 * band + at % high;
+    n0 = at / high * S::BN;
+    m0 = 0;
+    k0 = split * a.k_split;
+  }
+  const Segment seg = find_segment(a, slot);
+  const int rows = seg.hi - seg.lo;
+  if constexpr (FORM == kOverRows) {
+    // (a part without rows is written only where it is the whole sum)
+    if (seg.group < 0 || (rows <= 0 && (a.part != nullptr || !seg.first))) return;
+    k1 = max(rows, 0);
+  } else {
+    if (rows <= 0 || (seg.group < 0 && a.part != nullptr)) return;
+    k1 = seg.group < 0 ? 0 : min(a.k, k0 + a.k_split);
+  }
+
+  const T* A0 = static_cast<const T*>(a.a) + static_cast<int64_t>(seg.lo) * a.a_row;
+  const T* B0 = static_cast<const T*>(a.b) + (FORM == kOverRows ? static_cast<int64_t>(seg.lo) * a.b_row : static_cast<int64_t>(max(seg.group, 0)) * a.b_group);
+  typename K::A sa;
+  typename K::B sb;
+  auto fetch = [&](int k) {
+    if constexpr (FORM == kOverRows) {
+      sa.load(A0 + static_cast<int64_t>(k) * a.a_row + m0, a.a_row, k1 - k, a.a_cols - m0, tid);
+      sb.load(B0 + static_cast<int64_t>(k) * a.b_row + n0, a.b_row, k1 - k, a.b_cols - n0, tid);
+    } else {
+      sa.load(A0 + k, a.a_row, rows, a.a_cols - k, tid);
+      if constexpr (FORM == kByRows) {
+        sb.load(B0 + static_cast<int64_t>(k) * a.b_row + n0, a.b_row, a.k - k, a.b_cols - n0, tid);
+      } else {
+        sb.load(B0 + static_cast<int64_t>(n0) * a.b_row + k, a.b_row, a.n - n0, a.b_cols - k, tid);
+      }
+    }
+  };
+  float column[8] = {};  // over rows: this thread's share of the sums of 8 columns of b
+  const bool sums = FORM == kOverRows && m0 == 0 && (a.sums != nullptr || a.sums_part != nullptr);
+  auto put = [&](uint4* to) {
+    if constexpr (FORM == kOverRows) {
+      if (sums) {
+#pragma unroll
+        for (int i = 0; i < K::B::kCount; ++i) {
+          float v[8];
+          unpack8<T>(sb.r[i], v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) column[j] += v[j];
+        }
+      }
+    }
+    sa.template store<K::kAlongA>(to, tid);
+    sb.template store<K::kAlongB>(to + K::kPiecesA, tid);
+  };
+
+  constexpr int RB = S::TM / 32, CB = S::TN / 32;
+  floatx16 acc[RB][CB] = {};
+  auto multiply = [&](const uint4* from) {
+#pragma unroll
+    for (int t = 0; t < S::BK / 16; ++t) {
+      Frag<T> fa[RB], fb[CB];
+#pragma unroll
+      for (int i = 0; i < RB; ++i) fa[i] = K::A::template frag<K::kAlongA>(from, wr * S::TM + 32 * i, t, lane);
+#pragma unroll
+      for (int j = 0; j < CB; ++j) fb[j] = K::B::template frag<K::kAlongB>(from + K::kPiecesA, wc * S::TN + 32 * j, t, lane);
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < CB; ++j) acc[i][j] = attn::mma_frag<T>(fb[j], fa[i], acc[i][j]);
+    }
+    attn::settle();
+  };
+
+  if (k0 < k1) {
+    fetch(k0);
+    if constexpr (S::STAGES == 2) {
+      // One barrier a step: it ends the writes of this step's buffer and the
+      // reads of the other one, which the step's end fills.
+      put(lds);
+      int buf = 0;
+      for (int k = k0; k < k1; k += S::BK) {
+        __syncthreads();
+        const bool more = k + S::BK < k1;
+        if (more) fetch(k + S::BK);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(lds + buf * K::kPieces);
+        if (more) put(lds + (buf ^ 1) * K::kPieces);
+        buf ^= 1;
+      }
+    } else {
+      for (int k = k0; k < k1; k += S::BK) {
+        __syncthreads();
+        put(lds);
+        __syncthreads();
+        if (k + S::BK < k1) fetch(k + S::BK);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(lds);
+      }
+    }
+  }
+
+  if constexpr (FORM == kOverRows) {
+    if (sums) {
+      // the threads of one column piece, in the order of their rows
+      constexpr int PPR = K::kPprB, GROUPS = S::NT / PPR;
+      float* stage = reinterpret_cast<float*>(lds);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) stage[(tid / PPR) * (PPR * 8) + tid % PPR * 8 + j] = column[j];
+      __syncthreads();
+      for (int c = tid; c < S::BN; c += S::NT) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int q = 0; q < GROUPS; ++q) v += stage[q * (PPR * 8) + c];
+        if (n0 + c < a.n) {
+          if (a.part != nullptr) a.sums_part[static_cast<int64_t>(slot) * a.n_part + n0 + c] = v;
+          else a.sums[static_cast<int64_t>(seg.group) * a.n + n0 + c] = v;
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  // The sums, 32 rows at a time.
+  float* stage = reinterpret_cast<float*>(lds) + wave * 32 * K::kOutStride;
+  constexpr int LPR = S::TN / 8, RPP = 64 / LPR;  // lanes of a row, rows of a pass
+  const int col = n0 + wc * S::TN + lane % LPR * 8;
+  const int there = min(max(a.n - col, 0), 8);
+  float bias[8] = {};
+  if (FORM == kByRows && a.part == nullptr && a.bias != nullptr && there > 0 && seg.group >= 0)
+    load8<T>(static_cast<const T*>(a.bias) + static_cast<int64_t>(seg.group) * a.n + col, there, false, bias);
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    wave_order();
+#pragma unroll
+    for (int j = 0; j < CB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(stage + (lane & 31) * K::kOutStride + 32 * j + 8 * q + 4 * (lane >> 5)) =
+            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+    wave_order();
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += RPP) {
+      const int r = r0 + lane / LPR, m = wr * S::TM + 32 * i + r;
+      float v[8];
+      const float4 lo = *reinterpret_cast<const float4*>(stage + r * K::kOutStride + lane % LPR * 8);
+      const float4 hi = *reinterpret_cast<const float4*>(stage + r * K::kOutStride + lane % LPR * 8 + 4);
+      v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+      if constexpr (FORM == kOverRows) {
+        if (m0 + m < a.m && there > 0) {
+          if (a.part != nullptr) store8<float>(a.part + (static_cast<int64_t>(slot) * a.m + m0 + m) * a.n_part + col, 8, true, v);
+          else store8<float>(static_cast<float*>(a.out) + (static_cast<int64_t>(seg.group) * a.m + m0 + m) * a.n + col, there, a.wide & kWideOut, v);
+        }
+      } else if (m < rows && there > 0) {
+        const int64_t row = static_cast<int64_t>(seg.lo) + m;
+        if (a.part != nullptr) store8<float>(a.part + (static_cast<int64_t>(split) * a.rows + row) * a.n_part + col, 8, true, v);
+        else finish8<T>(a, row, col, there, seg.group >= 0, bias, v);
+      }
+    }
+  }
+}
+
+// ---- The shapes ----
+// kTiny: few rows of each group, more columns; kNarrow: few columns; kMedium;
+// kLarge: whole large products.
+template <class T>
+struct Shapes;
+template <class T>
+struct Shapes16 {
+  typedef Shape<32, 128, 1, 4, 64, 2> Tiny;
+  typedef Shape<128, 64, 4, 1, 64, 2> Narrow;
+  typedef Shape<128, 128, 2, 2, 64, 2> Medium;
+  typedef Shape<256, 256, 2, 4, 64, 2> Large;
+};
+template <>
+struct Shapes<float> {
+  typedef Shape<32, 128, 1, 4, 32, 1> Tiny;
+  typedef Shape<128, 32, 4, 1, 32, 1> Narrow;
+  typedef Shape<128, 128, 2, 2, 32, 1> Medium;
+  typedef Medium Large;
+};
+template <>
+struct Shapes<_Float16> : Shapes16<_Float16> {};
+template <>
+struct Shapes<__bf16> : Shapes16<__bf16> {};
+
+template <class T, class S, int FORM>
+hipError_t launch_shape(const ProductArgs& a, hipStream_t stream) {
+  const int64_t blocks = static_cast<int64_t>(a.slots) * a.tiles * (FORM == kOverRows ? 1 : a.splits);
+  if (blocks == 0) return hipSuccess;
+  k_product<T, S, FORM><<<static_cast<unsigned>(blocks), S::NT, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_typed(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream) {
+  auto by_form = [&](auto s) -> hipError_t {
+    typedef decltype(s) S;
+    if (form == kByRows) return launch_shape<T, S, kByRows>(a, stream);
+    if (form == kByRowsT) return launch_shape<T, S, kByRowsT>(a, stream);
+    return launch_shape<T, S, kOverRows>(a, stream);
+  };
+  if (shape == kTinyShape) return by_form(typename Shapes<T>::Tiny{});
+  if (shape == kNarrowShape) return by_form(typename Shapes<T>::Narrow{});
+  if (shape == kMediumShape) return by_form(typename Shapes<T>::Medium{});
+  return by_form(typename Shapes<T>::Large{});
+}
+
+}  // namespace lin
+}  // namespace spconv
