@@ -246,7 +246,7 @@ constexpr int64_t kBackwardBlocks = 1024;
 
 uint64_t add_norm_work_items(const AddNormArgs& a) {
   uint64_t items = 0;
-  dispatch(a, [&](auto, auto lanes, auto) -> hipError_t {
+  (void)dispatch(a, [&](auto, auto lanes, auto) -> hipError_t {
     constexpr int rpb = kThreads / decltype(lanes)::value;
     items = (static_cast<uint64_t>(a.rows) + rpb - 1) / rpb * kThreads;
     return hipSuccess;

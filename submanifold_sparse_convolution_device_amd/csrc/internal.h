@@ -364,8 +364,6 @@ hipError_t launch_rotary_table(float* table, int32_t extent, int32_t pairs, doub
 //   kByRowsT:     out[m][:] = a[m][:] b^T          (b [n][k]: its gradient)
 //   kOverRows:    out = sum over rows of a[row][:]^T b[row][:]  (the weights')
 enum ProductForm { kByRows = 0, kByRowsT = 1, kOverRows = 2 };
-// Bits of `wide`: 16-byte accesses fit the tensor.
-enum : uint32_t { kWideOut = 1, kWidePre = 2, kWideBefore = 4, kWideResidual = 8 };
 struct ProductArgs {
   const void* a = nullptr;
   const void* b = nullptr;
@@ -384,20 +382,19 @@ struct ProductArgs {
   int32_t n_part = 0;
   // by rows
   const void* bias = nullptr;      // [groups][n]
-  const void* residual = nullptr;  // [rows][n]
-  const void* before = nullptr;    // [rows][n]: out is multiplied by the slope of act there
+  const void* side = nullptr;      // [rows][n], kByRows: the residual; kByRowsT: where the slope of act multiplies out
   void* pre = nullptr;             // [rows][n]: the product before act
   void* out = nullptr;             // [rows][n]; over rows: fp32 [groups][m][n]
-  int64_t residual_row = 0, before_row = 0, pre_row = 0, out_row = 0;
+  int64_t side_row = 0, pre_row = 0, out_row = 0;
   int32_t act = 0;
-  uint32_t wide = 0;
+  bool whole = false;  // n is a multiple of 8 and the tensors from bias to out take 16-byte accesses
   // over rows: the column sums of b, fp32 [groups][n], or their parts [slot][n_part]
   float* sums = nullptr;
   float* sums_part = nullptr;
 };
 
 // Workgroup shapes: rows x columns of a tile (linear_kernels.h).
-enum ProductShape { kTinyShape, kNarrowShape, kMediumShape, kLargeShape };
+enum ProductShape { kTinyShape, kNarrowShape, kMediumShape, kLargeShape, kStreamShape };
 hipError_t launch_product_f32(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
 hipError_t launch_product_f16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
 hipError_t launch_product_bf16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);

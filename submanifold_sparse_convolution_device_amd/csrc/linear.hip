@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256) void k_lay_out(const E* src, int64_t src_row, 
 // ---- Joining ----
 // By rows: the parts of k summed in their order, then the epilogue; 8 columns
 // a thread.
-template <class T>
+template <class T, int FORM>
 __global__ __launch_bounds__(256) void k_join_rows(ProductArgs a) {
   const int pieces = a.n_part / 8;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -55,8 +55,10 @@ __global__ __launch_bounds__(256) void k_join_rows(ProductArgs a) {
     }
     group = lo == 0 || lo == a.groups + 1 ? -1 : lo - 1;
   }
-  float v[8] = {}, bias[8] = {};
+  float v[8] = {}, bias[8] = {}, side[8] = {};
   if (group >= 0) {
+    if (a.bias != nullptr) lin::load_some8<T>(static_cast<const T*>(a.bias) + static_cast<int64_t>(group) * a.n + col, there, a.whole, bias);
+    if (a.side != nullptr) lin::load_some8<T>(lin::side_row<T>(a, row) + col, there, a.whole, side);
     const float* p = a.part + row * a.n_part + col;
     const int64_t step = static_cast<int64_t>(a.rows) * a.n_part;
 #pragma unroll 4
@@ -64,9 +66,11 @@ __global__ __launch_bounds__(256) void k_join_rows(ProductArgs a) {
       const float4 x = *reinterpret_cast<const float4*>(p + s * step), y = *reinterpret_cast<const float4*>(p + s * step + 4);
       v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
     }
-    if (a.bias != nullptr) lin::load8<T>(static_cast<const T*>(a.bias) + static_cast<int64_t>(group) * a.n + col, there, false, bias);
   }
-  lin::finish8<T>(a, row, col, there, group >= 0, bias, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] += bias[j];
+  lin::finish<T, FORM, 8>(a, group >= 0, a.side != nullptr && group >= 0, [&](int j) { return side[j]; }, v,
+                          [&](T* to, int64_t stride, const float (&x)[8]) { lin::store_some8<T>(to + row * stride + col, there, a.whole, x); });
 }
 
 // Over rows: the parts of each group summed in their order; a group without
@@ -83,8 +87,7 @@ __global__ __launch_bounds__(256) void k_join_groups(ProductArgs a) {
     rows = max(r1 - r0, 0);
     first = lin::segment_start(a, group + 1);
   }
-  const int unit = a.by_unit.d, parts = rows == 0 ? 0 : fast_div(rows - 1, a.by_unit) + 1;
-  (void)unit;
+  const int parts = rows == 0 ? 0 : fast_div(rows - 1, a.by_unit) + 1;
   const bool sums = m == a.m;
   const float* p = sums ? a.sums_part + static_cast<int64_t>(first) * a.n_part + col
                         : a.part + (static_cast<int64_t>(first) * a.m + m) * a.n_part + col;
@@ -96,7 +99,7 @@ __global__ __launch_bounds__(256) void k_join_groups(ProductArgs a) {
     v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
   }
   float* dst = sums ? a.sums + static_cast<int64_t>(group) * a.n + col : static_cast<float*>(a.out) + (static_cast<int64_t>(group) * a.m + m) * a.n + col;
-  if ((a.wide & kWideOut) && !sums && col + 4 <= a.n) {
+  if (a.whole && !sums) {
     *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
 #pragma unroll
@@ -107,17 +110,16 @@ __global__ __launch_bounds__(256) void k_join_groups(ProductArgs a) {
 
 // ---- The activation's gradient ----
 template <class T>
-__global__ __launch_bounds__(256) void k_activation_backward(ActivationArgs a, int pieces, FastDiv by_pieces, bool wide) {
+__global__ __launch_bounds__(256) void k_activation_backward(ActivationArgs a, int pieces, FastDiv by_pieces, bool whole) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(a.rows) * pieces) return;
   const int64_t row = i < (int64_t(1) << 31) ? fast_div(static_cast<int>(i), by_pieces) : i / pieces;
   const int col = static_cast<int>(i - row * pieces) * 8, there = min(a.cols - col, 8);
   float g[8], z[8];
-  lin::load8<T>(static_cast<const T*>(a.grad) + row * a.grad_row + col, there, wide, g);
-  lin::load8<T>(static_cast<const T*>(a.pre) + row * a.pre_row + col, there, wide, z);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) g[j] *= lin::slope<T>(a.act, z[j]);
-  lin::store8<T>(static_cast<T*>(a.out) + row * a.out_row + col, there, wide, g);
+  lin::load_some8<T>(static_cast<const T*>(a.grad) + row * a.grad_row + col, there, whole, g);
+  lin::load_some8<T>(static_cast<const T*>(a.pre) + row * a.pre_row + col, there, whole, z);
+  lin::times_slope<T, 8>(a.act, [&](int j) { return z[j]; }, g);
+  lin::store_some8<T>(static_cast<T*>(a.out) + row * a.out_row + col, there, whole, g);
 }
 
 // ---- The plan ----
@@ -228,7 +230,7 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   p.form = kOverRows;
   p.dtype = dtype;
   p.shape = n <= (dtype == 0 ? 32 : 64) ? kNarrowShape : kMediumShape;
-  if (dtype != 0 && p.shape == kMediumShape && div_up(m, 256) * div_up(n, 256) >= 200) p.shape = kLargeShape;
+  if (dtype != 0 && p.shape == kMediumShape && m > 128 && n > 128) p.shape = kLargeShape;
   const ShapeSize s = shape_size(dtype, p.shape);
   ProductArgs& a = p.a;
   a.cu = cu;
@@ -239,7 +241,7 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   a.tiles_n = static_cast<int32_t>(div_up(n, s.bn));
   a.tiles = static_cast<int32_t>(div_up(m, s.bm) * a.tiles_n);
   a.n_part = padded(n);
-  const int64_t parts = std::min<int64_t>(kFill / a.tiles, rows / 256);
+  const int64_t parts = std::min<int64_t>((p.shape == kLargeShape ? 256 : kFill) / a.tiles, rows / 256);
   if (parts <= 1 || parts <= groups) {  // every group is one part
     a.by_unit = make_fast_div(1 << 30);
     a.slots = cu == nullptr ? 1 : groups + 2;
@@ -259,18 +261,34 @@ hipError_t run_product(const Product& p, hipStream_t stream) {
   return launch_product_bf16(p.a, p.form, p.shape, stream);
 }
 
-hipError_t run_by_rows(const Product& p, hipStream_t stream) {
+// Whether a product keeps its weights in registers.
+bool streams(const Product& p) {
+  const ProductArgs& a = p.a;
+  if (!a.whole || a.splits > 1 || p.shape == kTinyShape) return false;
+  return p.dtype == 0 ? a.k <= 128 && a.n > 64 : a.k <= 256 && a.n >= 64;
+}
+
+hipError_t run_by_rows(Product& p, hipStream_t stream) {
   if (p.a.rows == 0) return hipSuccess;
+  if (streams(p)) p.shape = kStreamShape;
   const hipError_t e = run_product(p, stream);
   if (e != hipSuccess || p.a.splits == 1) return e;
   const unsigned blocks = static_cast<unsigned>(div_up(static_cast<int64_t>(p.a.rows) * (p.a.n_part / 8), 256));
-  if (p.dtype == 0) k_join_rows<float><<<blocks, 256, 0, stream>>>(p.a);
-  else if (p.dtype == 1) k_join_rows<_Float16><<<blocks, 256, 0, stream>>>(p.a);
-  else k_join_rows<__bf16><<<blocks, 256, 0, stream>>>(p.a);
+  auto join = [&](auto t) {
+    typedef decltype(t) T;
+    if (p.form == kByRows) k_join_rows<T, kByRows><<<blocks, 256, 0, stream>>>(p.a);
+    else k_join_rows<T, kByRowsT><<<blocks, 256, 0, stream>>>(p.a);
+  };
+  if (p.dtype == 0) join(0.f);
+  else if (p.dtype == 1) join(static_cast<_Float16>(0));
+  else join(static_cast<__bf16>(0.f));
   return hipGetLastError();
 }
 
-uint32_t wide(const void* p, int64_t row_stride, int dtype, uint32_t bit) { return aligned(p) && whole_pieces(row_stride, dtype) ? bit : 0; }
+// Whether rows of `cols` values take 16-byte accesses, 8 values at a time (NULL: nothing is accessed).
+bool whole_rows(const void* p, int64_t row_stride, int64_t cols, int dtype) {
+  return p == nullptr || (aligned(p) && whole_pieces(row_stride, dtype) && cols % 8 == 0);
+}
 
 struct Forward {
   Operand x, w;
@@ -333,14 +351,15 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t strea
   p.b_cols = f.w.cols;
   p.b_group = static_cast<int64_t>(a.c_in) * f.w.row;
   p.bias = a.bias;
-  p.residual = a.residual;
-  p.residual_row = a.residual_row;
+  p.side = a.residual;
+  p.side_row = a.residual_row;
   p.pre = a.pre;
   p.pre_row = a.pre_row;
   p.out = a.out;
   p.out_row = a.out_row;
   p.act = a.act;
-  p.wide = wide(a.out, a.out_row, a.dtype, kWideOut) | wide(a.pre, a.pre_row, a.dtype, kWidePre) | wide(a.residual, a.residual_row, a.dtype, kWideResidual);
+  p.whole = whole_rows(a.out, a.out_row, a.c_out, a.dtype) && whole_rows(a.pre, a.pre_row, a.c_out, a.dtype) &&
+            whole_rows(a.residual, a.residual_row, a.c_out, a.dtype) && whole_rows(a.bias, a.c_out, a.c_out, a.dtype);
   return run_by_rows(f.p, stream);
 }
 
@@ -359,12 +378,12 @@ hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, hipStrea
     p.b_row = b.w.row;
     p.b_cols = b.w.cols;
     p.b_group = static_cast<int64_t>(a.c_in) * b.w.row;
-    p.before = a.before;
-    p.before_row = a.before_row;
+    p.side = a.before;
+    p.side_row = a.before_row;
     p.act = a.act;
     p.out = a.grad_x;
     p.out_row = a.grad_x_row;
-    p.wide = wide(a.grad_x, a.grad_x_row, a.dtype, kWideOut) | wide(a.before, a.before_row, a.dtype, kWideBefore);
+    p.whole = whole_rows(a.grad_x, a.grad_x_row, a.c_in, a.dtype) && whole_rows(a.before, a.before_row, a.c_in, a.dtype);
     e = run_by_rows(b.gx, stream);
     if (e != hipSuccess) return e;
   }
@@ -379,7 +398,7 @@ hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, hipStrea
     p.out = a.grad_weight;
     p.sums = a.grad_bias;
     if (a.grad_bias == nullptr) p.sums_part = nullptr;
-    p.wide = wide(a.grad_weight, a.c_out, 0, kWideOut);
+    p.whole = whole_rows(a.grad_weight, a.c_out, a.c_out, 0);
     e = run_product(b.gw, stream);
     if (e != hipSuccess || p.part == nullptr) return e;
     const int64_t threads = static_cast<int64_t>(p.m + 1) * (p.n_part / 4);
@@ -393,7 +412,8 @@ hipError_t launch_activation_backward(const ActivationArgs& a, hipStream_t strea
   const int pieces = (a.cols + 7) / 8;
   const int64_t total = static_cast<int64_t>(a.rows) * pieces;
   if (total == 0) return hipSuccess;
-  const bool w = wide(a.grad, a.grad_row, a.dtype, 1) && wide(a.pre, a.pre_row, a.dtype, 1) && wide(a.out, a.out_row, a.dtype, 1);
+  const bool w = whole_rows(a.grad, a.grad_row, a.cols, a.dtype) && whole_rows(a.pre, a.pre_row, a.cols, a.dtype) &&
+                 whole_rows(a.out, a.out_row, a.cols, a.dtype);
   const unsigned blocks = static_cast<unsigned>(div_up(total, 256));
   const FastDiv by = make_fast_div(pieces);
   if (a.dtype == 0) k_activation_backward<float><<<blocks, 256, 0, stream>>>(a, pieces, by, w);

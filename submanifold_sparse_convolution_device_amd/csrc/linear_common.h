@@ -24,6 +24,7 @@ __device__ __forceinline__ int segment_start(const ProductArgs& a, int s) {
 }
 
 struct Segment {
+  int seg;
   int group;   // -1: rows of no group
   int lo, hi;  // this slot's rows
   bool first;  // the segment's first slot
@@ -35,7 +36,7 @@ __device__ __forceinline__ Segment find_segment(const ProductArgs& a, int slot) 
   Segment g;
   const int unit = a.by_unit.d;
   if (a.cu == nullptr) {
-    g.group = 0;
+    g.seg = g.group = 0;
     g.lo = slot * unit;
     g.hi = min(a.rows, g.lo + min(unit, a.rows));
     g.first = slot == 0;
@@ -53,8 +54,9 @@ __device__ __forceinline__ Segment find_segment(const ProductArgs& a, int slot) 
   }
   const int s = __builtin_amdgcn_readfirstlane(lo);
   const int r0 = attn::bound(a.cu, a.groups, a.rows, s), r1 = attn::bound(a.cu, a.groups, a.rows, s + 1);
-  const int64_t nth = slot - (fast_div(r0, a.by_unit) + s);
+  const int64_t nth = max(slot - (fast_div(r0, a.by_unit) + s), 0);  // (below 0 with decreasing offsets alone)
   const int64_t from = r0 + nth * unit;
+  g.seg = s;
   g.group = s == 0 || s == a.groups + 1 ? -1 : s - 1;
   g.lo = static_cast<int>(min(from, static_cast<int64_t>(max(r1, r0))));
   g.hi = static_cast<int>(min(from + unit, static_cast<int64_t>(max(r1, r0))));
@@ -70,76 +72,84 @@ __device__ __forceinline__ float sigmoid(float z) {
 }
 
 // The normal distribution's lower tail at -a, a >= 0, as t (c1 + c2 t + ...
-// + c6 t^5) e with t = 1 / (1 + 0.3 a) and e = exp(-a^2 / 2).  The
-// coefficients are a fit to erfcx of the smallest relative error, 7.6e-6 for
-// a up to 13.5: a 64th of fp16's rounding, a 500th of bf16's.
+// + c6 t^5) e with t = 1 / (1 + 0.31 a) and e = exp(-a^2 / 2).  The
+// coefficients are a fit to erfcx of the smallest relative error, 4.7e-6 for
+// a up to 13.5: a hundredth of fp16's rounding, a 400th of bf16's.  (One
+// coefficient fewer leaves 2.9e-5.)
 __device__ __forceinline__ float tail(float a, float e) {
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, a, 1.f));
-  float p = -0.07751068f;
-  p = __builtin_fmaf(p, t, 0.21727989f);
-  p = __builtin_fmaf(p, t, -0.01836866f);
-  p = __builtin_fmaf(p, t, 0.14496221f);
-  p = __builtin_fmaf(p, t, 0.1135486f);
-  p = __builtin_fmaf(p, t, 0.12009241f);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31f, a, 1.f));
+  float p = -0.073935856f;
+  p = __builtin_fmaf(p, t, 0.180469782f);
+  p = __builtin_fmaf(p, t, 0.0157236098f);
+  p = __builtin_fmaf(p, t, 0.133440446f);
+  p = __builtin_fmaf(p, t, 0.120438788f);
+  p = __builtin_fmaf(p, t, 0.123860916f);
   return p * t * e;
 }
 
-// act(z) and its derivative.  fp32 takes the library's functions, whose errors
-// are of fp32's size; 16-bit types the unit's exponential and reciprocal.
+// act(z) and its derivative, of N values with one branch.  fp32 takes the
+// library's functions, whose errors are of fp32's size; 16-bit types the
+// unit's exponential and reciprocal.
 template <class T>
-__device__ __forceinline__ float activate(int act, float z) {
-  if (act == kRelu) return z <= 0.f ? 0.f : z;  // (a NaN stays)
-  if (act == kSilu) {
-    if constexpr (sizeof(T) == 4) return z / (1.f + expf(-z));
-    return z * sigmoid(z);
-  }
-  if (act == kGelu) {
-    if constexpr (sizeof(T) == 4) return 0.5f * z * (1.f + erff(z * 0.70710678f));
-    const float t = tail(fabsf(z), attn::fast_exp2(z * z * (-0.5f * attn::kLog2e)));
-    return z * (z < 0.f ? t : 1.f - t);
-  }
-  return z;
+__device__ __forceinline__ float relu(float z) {
+  return z <= 0.f ? 0.f : z;  // (a NaN stays)
 }
 template <class T>
-__device__ __forceinline__ float slope(int act, float z) {
-  if (act == kRelu) return z > 0.f ? 1.f : 0.f;
-  if (act == kSilu) {
-    float s;
-    if constexpr (sizeof(T) == 4) {
-      s = 1.f / (1.f + expf(-z));
-    } else {
-      s = sigmoid(z);
-    }
-    return s * (1.f + z * (1.f - s));
+__device__ __forceinline__ float silu(float z) {
+  if constexpr (sizeof(T) == 4) return z / (1.f + expf(-z));
+  return z * sigmoid(z);
+}
+template <class T>
+__device__ __forceinline__ float gelu(float z) {
+  if constexpr (sizeof(T) == 4) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+  // z - z t above 0, z t below
+  return relu<T>(z) - fabsf(z) * tail(fabsf(z), attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e))));
+}
+template <class T>
+__device__ __forceinline__ float silu_slope(float z) {
+  const float s = sizeof(T) == 4 ? 1.f / (1.f + expf(-z)) : sigmoid(z);
+  return s * (1.f + z * (1.f - s));
+}
+template <class T>
+__device__ __forceinline__ float gelu_slope(float z) {
+  constexpr float inv_root = 0.3989422804014327f;  // 1 / sqrt(2 pi)
+  if constexpr (sizeof(T) == 4) return 0.5f * (1.f + erff(z * 0.70710678f)) + z * inv_root * expf(-0.5f * z * z);
+  const float e = attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e)));
+  const float t = tail(fabsf(z), e);
+  return (z < 0.f ? t : 1.f - t) + z * inv_root * e;
+}
+// f(i) for i < N, 4 at a time: the registers of all N together do not fit.
+template <int N, class F>
+__device__ __forceinline__ void by_fours(F&& f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    f(i);
+    if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
   }
-  if (act == kGelu) {
-    constexpr float inv_root = 0.3989422804014327f;  // 1 / sqrt(2 pi)
-    if constexpr (sizeof(T) == 4) return 0.5f * (1.f + erff(z * 0.70710678f)) + z * inv_root * expf(-0.5f * z * z);
-    const float e = attn::fast_exp2(z * z * (-0.5f * attn::kLog2e));
-    const float t = tail(fabsf(z), e);
-    return (z < 0.f ? t : 1.f - t) + z * inv_root * e;
+}
+template <class T, int N>
+__device__ __forceinline__ void activate(int act, float (&v)[N]) {
+  if (act == kRelu) {
+    by_fours<N>([&](int i) { v[i] = relu<T>(v[i]); });
+  } else if (act == kSilu) {
+    by_fours<N>([&](int i) { v[i] = silu<T>(v[i]); });
+  } else if (act == kGelu) {
+    by_fours<N>([&](int i) { v[i] = gelu<T>(v[i]); });
   }
-  return 1.f;
+}
+// v times the slope at z(i).
+template <class T, int N, class Z>
+__device__ __forceinline__ void times_slope(int act, Z&& z, float (&v)[N]) {
+  if (act == kRelu) {
+    by_fours<N>([&](int i) { v[i] *= z(i) > 0.f ? 1.f : 0.f; });
+  } else if (act == kSilu) {
+    by_fours<N>([&](int i) { v[i] *= silu_slope<T>(z(i)); });
+  } else if (act == kGelu) {
+    by_fours<N>([&](int i) { v[i] *= gelu_slope<T>(z(i)); });
+  }
 }
 
 // ---- 8 columns of a row ----
-// `there` of them exist; wide: all do and the address is 16-byte aligned.
-template <class T>
-__device__ __forceinline__ void load8(const T* p, int there, bool wide, float (&v)[8]) {
-  if (wide && there == 8) {
-    constexpr int E = 16 / static_cast<int>(sizeof(T));
-    typedef T vec __attribute__((ext_vector_type(E)));
-#pragma unroll
-    for (int i = 0; i < 8; i += E) {
-      const vec x = __builtin_bit_cast(vec, *reinterpret_cast<const uint4*>(p + i));
-#pragma unroll
-      for (int j = 0; j < E; ++j) v[i + j] = static_cast<float>(x[j]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < there ? static_cast<float>(p[i]) : 0.f;
-  }
-}
 template <class T>
 __device__ __forceinline__ void unpack8(const attn::Raw<T>& r, float (&v)[8]) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
@@ -148,17 +158,52 @@ __device__ __forceinline__ void unpack8(const attn::Raw<T>& r, float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(__builtin_bit_cast(vec, r.v[i / E])[i % E]);
 }
 template <class T>
-__device__ __forceinline__ void store8(T* p, int there, bool wide, const float (&v)[8]) {
-  if (wide && there == 8) {
-    constexpr int E = 16 / static_cast<int>(sizeof(T));
-    typedef T vec __attribute__((ext_vector_type(E)));
+__device__ __forceinline__ float element(const attn::Raw<T>& r, int i) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  typedef T vec __attribute__((ext_vector_type(E)));
+  return static_cast<float>(__builtin_bit_cast(vec, r.v[i / E])[i % E]);
+}
+// 16-byte accesses (p is aligned).
+template <class T>
+__device__ __forceinline__ attn::Raw<T> load_raw8(const T* p) {
+  return attn::load_piece<T>(p, true);
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  typedef T vec __attribute__((ext_vector_type(E)));
 #pragma unroll
-    for (int i = 0; i < 8; i += E) {
-      vec x;
+  for (int i = 0; i < 8; i += E) {
+    vec x;
 #pragma unroll
-      for (int j = 0; j < E; ++j) x[j] = static_cast<T>(v[i + j]);
-      *reinterpret_cast<uint4*>(p + i) = __builtin_bit_cast(uint4, x);
-    }
+    for (int j = 0; j < E; ++j) x[j] = static_cast<T>(v[i + j]);
+    *reinterpret_cast<uint4*>(p + i) = __builtin_bit_cast(uint4, x);
+  }
+}
+// A piece whose first `cols` values exist (whole 16 bytes of them), zeros for
+// the others and for a row that does not (on).
+template <class T>
+__device__ __forceinline__ attn::Raw<T> load_piece_of(const T* p, bool on, int cols) {
+  attn::Raw<T> r;
+#pragma unroll
+  for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h)
+    r.v[h] = on && 4 * h < cols ? reinterpret_cast<const uint4*>(p)[h] : make_uint4(0, 0, 0, 0);
+  return r;
+}
+// The first `there` of 8, one by one unless all are there and aligned.
+template <class T>
+__device__ __forceinline__ void load_some8(const T* p, int there, bool whole, float (&v)[8]) {
+  if (whole) {
+    unpack8<T>(load_raw8<T>(p), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < there ? static_cast<float>(p[i]) : 0.f;
+  }
+}
+template <class T>
+__device__ __forceinline__ void store_some8(T* p, int there, bool whole, const float (&v)[8]) {
+  if (whole) {
+    store8<T>(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -166,37 +211,32 @@ __device__ __forceinline__ void store8(T* p, int there, bool wide, const float (
   }
 }
 
-// The sums of 8 columns to the output: bias, the stored product (pre),
-// activation or the slope of the activation before, residual; fp32 until here,
-// each output rounded once.
+// The sums (with the bias) of N values of a row or of several to the output,
+// in fp32 until each output is rounded once.  By rows: the stored product
+// (pre), activation, residual; by rows T: times the slope of the activation
+// before.  side(i) is the residual's or before's value.  Rows of no group come
+// with sums of zero.
+template <class T, int FORM, int N, class Side, class Store>
+__device__ __forceinline__ void finish(const ProductArgs& a, bool in_group, bool sides, Side&& side, float (&v)[N], Store&& store) {
+  if constexpr (FORM == kByRows) {
+    if (a.pre != nullptr) store(static_cast<T*>(a.pre), a.pre_row, v);
+    if (in_group) {
+      activate<T, N>(a.act, v);
+      if (sides) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += side(i);
+      }
+    }
+  } else {
+    if (sides) times_slope<T, N>(a.act, side, v);
+  }
+  store(static_cast<T*>(a.out), a.out_row, v);
+}
+
+// Where a row's part of `side` begins.
 template <class T>
-__device__ __forceinline__ void finish8(const ProductArgs& a, int64_t row, int col, int there, bool in_group, const float (&bias)[8], float (&v)[8]) {
-  if (!in_group) {  // rows of no group
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (a.pre != nullptr) store8<T>(static_cast<T*>(a.pre) + row * a.pre_row + col, there, a.wide & kWidePre, v);
-    store8<T>(static_cast<T*>(a.out) + row * a.out_row + col, there, a.wide & kWideOut, v);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] += bias[i];
-  if (a.pre != nullptr) store8<T>(static_cast<T*>(a.pre) + row * a.pre_row + col, there, a.wide & kWidePre, v);
-  if (a.before != nullptr) {
-    float z[8];
-    load8<T>(static_cast<const T*>(a.before) + row * a.before_row + col, there, a.wide & kWideBefore, z);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= slope<T>(a.act, z[i]);
-  } else if (a.act != kIdentity) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate<T>(a.act, v[i]);
-  }
-  if (a.residual != nullptr) {
-    float r[8];
-    load8<T>(static_cast<const T*>(a.residual) + row * a.residual_row + col, there, a.wide & kWideResidual, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
-  }
-  store8<T>(static_cast<T*>(a.out) + row * a.out_row + col, there, a.wide & kWideOut, v);
+__device__ __forceinline__ const T* side_row(const ProductArgs& a, int64_t row) {
+  return static_cast<const T*>(a.side) + row * a.side_row;
 }
 
 }  // namespace lin

@@ -19,6 +19,9 @@
 // one row; the sums pass through the wavefront's own LDS into whole rows, 8
 // columns a lane, for the epilogue (finish8) and 16-byte accesses.
 #pragma once
+#ifndef AH2
+#define AH2 2
+#endif
 
 #include <algorithm>
 #include <type_traits>
@@ -73,7 +76,7 @@ struct Stage {
   template <bool ALONG>
   __device__ static __forceinline__ int at(int row, int piece) {
     if constexpr (ALONG) {
-      return row * PPR + (piece ^ (PPR == 8 ? row & 7 : row >> 1 & 3));
+      return row * PPR + (piece ^ (PPR >= 16 ? row & 15 : PPR == 8 ? row >> 1 & 7 : row >> 2 & 3));
     } else if constexpr (PPR >= 16) {
       return row * PPR + (piece ^ ((row & 3) << 2 ^ (row & 2)));
     } else if constexpr (PPR == 8) {
@@ -145,7 +148,10 @@ struct Kernel {
 };
 
 template <class T, class S, int FORM>
-__global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
+#ifndef MOCC
+#define MOCC 1
+#endif
+__global__ __launch_bounds__(S::NT, (S::NT == 256 && S::BN == 128 && S::BM == 128) ? MOCC : 1) void k_product(ProductArgs a) {
   typedef Kernel<T, S, FORM> K;
   __shared__ uint4 lds[K::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -185,6 +191,13 @@ __global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
     if (rows <= 0 || (seg.group < 0 && a.part != nullptr)) return;
     k1 = seg.group < 0 ? 0 : min(a.k, k0 + a.k_split);
   }
+
+  // The bias of this lane's columns, on its way during the products.
+  constexpr int LPR = S::TN / 8, RPP = 64 / LPR;  // lanes of a row, rows of a pass of the epilogue
+  const int col = n0 + wc * S::TN + lane % LPR * 8;
+  float bias[8] = {};
+  if (FORM == kByRows && a.whole && a.part == nullptr && a.bias != nullptr && seg.group >= 0 && col < a.n)
+    unpack8<T>(load_raw8<T>(static_cast<const T*>(a.bias) + static_cast<int64_t>(seg.group) * a.n + col), bias);
 
   const T* A0 = static_cast<const T*>(a.a) + static_cast<int64_t>(seg.lo) * a.a_row;
   const T* B0 = static_cast<const T*>(a.b) + (FORM == kOverRows ? static_cast<int64_t>(seg.lo) * a.b_row : static_cast<int64_t>(max(seg.group, 0)) * a.b_group);
@@ -291,14 +304,21 @@ __global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
 
   // The sums, 32 rows at a time.
   float* stage = reinterpret_cast<float*>(lds) + wave * 32 * K::kOutStride;
-  constexpr int LPR = S::TN / 8, RPP = 64 / LPR;  // lanes of a row, rows of a pass
-  const int col = n0 + wc * S::TN + lane % LPR * 8;
-  const int there = min(max(a.n - col, 0), 8);
-  float bias[8] = {};
-  if (FORM == kByRows && a.part == nullptr && a.bias != nullptr && there > 0 && seg.group >= 0)
-    load8<T>(static_cast<const T*>(a.bias) + static_cast<int64_t>(seg.group) * a.n + col, there, false, bias);
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
+    constexpr int PASSES = 32 / RPP;
+    const int mi = wr * S::TM + 32 * i;  // first row in the tile
+    const int64_t first = FORM == kOverRows ? static_cast<int64_t>(seg.group) * a.m + m0 + mi : static_cast<int64_t>(seg.lo) + mi;  // of out
+    const int limit = (FORM == kOverRows ? a.m - m0 : rows) - mi;  // rows there are
+    Raw<T> side[PASSES];
+    const bool sides = FORM != kOverRows && a.whole && a.part == nullptr && a.side != nullptr && seg.group >= 0;
+    if (sides) {
+#pragma unroll
+      for (int q = 0; q < PASSES; ++q) {
+        const int r = q * RPP + lane / LPR;
+        side[q] = attn::load_piece<T>(side_row<T>(a, first + r) + col, r < limit && col < a.n);
+      }
+    }
     wave_order();
 #pragma unroll
     for (int j = 0; j < CB; ++j)
@@ -307,24 +327,263 @@ __global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
         *reinterpret_cast<float4*>(stage + (lane & 31) * K::kOutStride + 32 * j + 8 * q + 4 * (lane >> 5)) =
             make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
     wave_order();
+    if (a.part != nullptr || a.whole) {
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += RPP) {
-      const int r = r0 + lane / LPR, m = wr * S::TM + 32 * i + r;
-      float v[8];
-      const float4 lo = *reinterpret_cast<const float4*>(stage + r * K::kOutStride + lane % LPR * 8);
-      const float4 hi = *reinterpret_cast<const float4*>(stage + r * K::kOutStride + lane % LPR * 8 + 4);
-      v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-      if constexpr (FORM == kOverRows) {
-        if (m0 + m < a.m && there > 0) {
-          if (a.part != nullptr) store8<float>(a.part + (static_cast<int64_t>(slot) * a.m + m0 + m) * a.n_part + col, 8, true, v);
-          else store8<float>(static_cast<float*>(a.out) + (static_cast<int64_t>(seg.group) * a.m + m0 + m) * a.n + col, there, a.wide & kWideOut, v);
+      for (int q = 0; q < PASSES; ++q) {
+        const int r = q * RPP + lane / LPR;
+        float v[8];
+        const float4 lo = *reinterpret_cast<const float4*>(stage + r * K::kOutStride + lane % LPR * 8);
+        const float4 hi = *reinterpret_cast<const float4*>(stage + r * K::kOutStride + lane % LPR * 8 + 4);
+        v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+        if (r >= limit || col >= a.n) continue;
+        if (a.part != nullptr) {
+          const int64_t row = FORM == kOverRows ? static_cast<int64_t>(slot) * a.m + m0 + mi + r : static_cast<int64_t>(split) * a.rows + first + r;
+          store8<float>(a.part + row * a.n_part + col, v);
+        } else if constexpr (FORM == kOverRows) {
+          store8<float>(static_cast<float*>(a.out) + (first + r) * a.n + col, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += bias[j];
+          finish<T, FORM, 8>(a, seg.group >= 0, sides, [&](int j) { return element<T>(side[q], j); }, v, [&](T* to, int64_t stride, const float (&x)[8]) { store8<T>(to + (first + r) * stride + col, x); });
         }
-      } else if (m < rows && there > 0) {
-        const int64_t row = static_cast<int64_t>(seg.lo) + m;
-        if (a.part != nullptr) store8<float>(a.part + (static_cast<int64_t>(split) * a.rows + row) * a.n_part + col, 8, true, v);
-        else finish8<T>(a, row, col, there, seg.group >= 0, bias, v);
+      }
+    } else {
+      // Rows without 16-byte places: a lane a column, so that stores follow
+      // one another.
+      constexpr int LANES = S::TN < 64 ? S::TN : 64, ROWS = 64 / LANES;
+#pragma unroll 1
+      for (int c0 = 0; c0 < S::TN; c0 += LANES) {
+        const int c = c0 + lane % LANES, at = n0 + wc * S::TN + c;
+        if (at >= a.n) continue;
+        float b = 0.f;
+        if (FORM == kByRows && a.bias != nullptr && seg.group >= 0) b = static_cast<float>(static_cast<const T*>(a.bias)[static_cast<int64_t>(seg.group) * a.n + at]);
+#pragma unroll 4
+        for (int r = lane / LANES; r < min(32, limit); r += ROWS) {
+          float v[1] = {stage[r * K::kOutStride + c] + b};
+          if constexpr (FORM == kOverRows) {
+            static_cast<float*>(a.out)[(first + r) * a.n + at] = v[0];
+          } else {
+            const bool beside = a.side != nullptr && seg.group >= 0;
+            const float z = beside ? static_cast<float>(side_row<T>(a, first + r)[at]) : 0.f;
+            finish<T, FORM, 1>(a, seg.group >= 0, beside, [&](int) { return z; }, v, [&](T* to, int64_t stride, const float (&x)[1]) { to[(first + r) * stride + at] = static_cast<T>(x[0]); });
+          }
+        }
       }
     }
+  }
+}
+
+// ---- Weights in registers ----
+// By rows with a short contraction (16 KS values at most): a workgroup of
+// WR x WC wavefronts keeps its columns of the weights in registers, CW blocks
+// of 32 a wavefront, and walks a run of slots of BM rows.  A tile's rows are
+// loaded one tile ahead and pass through LDS, where the WC wavefronts of the
+// same rows read them; the weights are read once, and a tile ends in one
+// barrier.  The sums go to memory straight from the registers: an exchange
+// between the halves of a wavefront gives each lane 8 neighbouring columns of
+// a row.  OCC: wavefronts on a SIMD.
+template <int KS_, int WR_, int WC_, int RW_, int OCC_>
+struct StreamShape {
+  static constexpr int KS = KS_, WR = WR_, WC = WC_, RW = RW_, OCC = OCC_;
+  static constexpr int NT = 64 * WR * WC, BM = 32 * WR * RW, BN = 32 * WC;
+  static constexpr int PER_CU = OCC * 4 / (WR * WC);
+};
+
+template <class T, class S, int FORM>
+__global__ __launch_bounds__(S::NT, S::OCC) void k_stream(ProductArgs a, int chunks, int per) {
+  constexpr int KS = S::KS, WC = S::WC, RW = S::RW;
+  typedef Stage<T, S::BM, 2 * KS, S::NT> A;
+  typedef Stage<T, 16, 4, 64> W;  // 16 contracted values by 32 columns, a wavefront's own
+  constexpr int PIECES = S::BM * 2 * KS * kPlanes<T>;
+  __shared__ uint4 lds[2 * PIECES];
+  __shared__ uint4 weights_lds[FORM == kByRows ? S::NT * kPlanes<T> : 1];  // a wavefront's own
+  __shared__ float4 bias_lds[S::BN / 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / WC, wc = wave % WC, half = lane >> 5;
+  // The workgroups of one run of slots, one for each tile of columns, follow
+  // one another on one XCD, whose L2 then serves all but the first.
+  const int xcd = blockIdx.x % 8, j = blockIdx.x / 8;
+  const int chunk = j / a.tiles * 8 + xcd, n0 = j % a.tiles * S::BN;
+  if (chunk >= chunks) return;
+  const int n_wave = n0 + wc * 32;
+
+  // The walk over the slots: segment, its bounds and first slot, the next one's.
+  struct Walk {
+    int slot, seg, r0, r1, first, next;
+  };
+  const int end = min((chunk + 1) * per, a.slots);
+  auto group_of = [&](const Walk& w) { return a.cu == nullptr ? 0 : w.seg == 0 || w.seg == a.groups + 1 ? -1 : w.seg - 1; };
+  auto rows_of = [&](const Walk& w) { return w.slot < end ? min(w.r1 - w.r0 - (w.slot - w.first) * S::BM, S::BM) : 0; };
+  auto settle_walk = [&](Walk& w) {  // on to a slot with rows, or the end
+    if (a.cu == nullptr) return;
+    while (w.slot < end) {
+      while (w.slot >= w.next) {
+        ++w.seg;
+        w.r0 = w.r1;
+        w.first = w.next;
+        w.r1 = max(__builtin_amdgcn_readfirstlane(attn::bound(a.cu, a.groups, a.rows, w.seg + 1)), w.r0);
+        w.next = w.seg > a.groups ? end : fast_div(w.r1, a.by_unit) + w.seg + 1;
+      }
+      if (rows_of(w) > 0) return;
+      ++w.slot;
+    }
+  };
+  Walk cur;
+  cur.slot = chunk * per;
+  if (a.cu == nullptr) {
+    cur.seg = 0, cur.r0 = 0, cur.r1 = a.rows, cur.first = 0, cur.next = a.slots;
+  } else {
+    const Segment g = find_segment(a, min(cur.slot, a.slots - 1));
+    cur.seg = g.seg;
+    cur.r0 = __builtin_amdgcn_readfirstlane(attn::bound(a.cu, a.groups, a.rows, g.seg));
+    cur.r1 = max(__builtin_amdgcn_readfirstlane(attn::bound(a.cu, a.groups, a.rows, g.seg + 1)), cur.r0);
+    cur.first = min(fast_div(cur.r0, a.by_unit) + g.seg, cur.slot);
+    cur.next = g.seg > a.groups ? end : fast_div(cur.r1, a.by_unit) + g.seg + 1;
+  }
+  settle_walk(cur);
+  if (cur.slot >= end) return;
+
+  A sa;
+  auto fetch = [&](const Walk& w) {
+    const int rows = group_of(w) < 0 ? 0 : rows_of(w);
+    const int64_t lo = w.r0 + static_cast<int64_t>(w.slot - w.first) * S::BM;
+    sa.load(static_cast<const T*>(a.a) + lo * a.a_row, a.a_row, rows, a.a_cols, tid);
+  };
+  fetch(cur);
+  int group = -2, buf = 0;
+  Frag<T> fb[KS];
+  auto load_weights = [&](int g) {
+    const T* B = static_cast<const T*>(a.b) + static_cast<int64_t>(g) * a.b_group;
+    if constexpr (FORM == kByRows) {
+      uint4* mine = weights_lds + wave * 64 * kPlanes<T>;
+      constexpr int STEP = sizeof(T) == 4 ? 4 : 8;  // loads in flight
+#pragma unroll
+      for (int t0 = 0; t0 < KS; t0 += STEP) {
+        W w[STEP];
+#pragma unroll
+        for (int t = 0; t < STEP && t0 + t < KS; ++t)
+          w[t].load(B + static_cast<int64_t>(16 * (t0 + t)) * a.b_row + n_wave, a.b_row, a.k - 16 * (t0 + t), a.b_cols - n_wave, lane);
+#pragma unroll
+        for (int t = 0; t < STEP && t0 + t < KS; ++t) {
+          wave_order();
+          w[t].template store<false>(mine, lane);
+          wave_order();
+          fb[t0 + t] = W::template frag<false>(mine, 0, 0, lane);
+        }
+      }
+      __syncthreads();  // (the last tile's products have read the last group's bias)
+      for (int c = tid; c < S::BN; c += S::NT)
+        reinterpret_cast<float*>(bias_lds)[c] =
+            a.bias != nullptr && n0 + c < a.n ? static_cast<float>(static_cast<const T*>(a.bias)[static_cast<int64_t>(g) * a.n + n0 + c]) : 0.f;
+    } else {
+      const int n = n_wave + (lane & 31);
+#pragma unroll
+      for (int t = 0; t < KS; ++t)
+        fb[t] = attn::to_frag<T>(load_piece_of<T>(B + static_cast<int64_t>(n) * a.b_row + 16 * t + 8 * half, n < a.n, a.b_cols - 16 * t - 8 * half));
+    }
+  };
+  // A wavefront's tile: its sums, and where they go.
+  floatx16 acc[RW] = {};
+  Raw<T> side[RW][2];
+  int64_t row = 0;  // of this lane's first block
+  int left = 0;     // rows from there on
+  bool in_group = false, sides = false;
+  auto multiply = [&](const Walk& w, int g) {
+    row = w.r0 + static_cast<int64_t>(w.slot - w.first) * S::BM + wr * (32 * RW) + (lane & 31);
+    left = rows_of(w) - wr * (32 * RW) - (lane & 31);
+    in_group = g >= 0;
+    sides = a.side != nullptr && in_group;
+    if (sides) {
+#pragma unroll
+      for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int col = n_wave + 16 * p + 8 * half;
+          side[i][p] = attn::load_piece<T>(side_row<T>(a, row + 32 * i) + col, 32 * i < left && col < a.n);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (FORM == kByRows && a.bias != nullptr && in_group) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 b = bias_lds[wc * 8 + 2 * q + half];
+#pragma unroll
+        for (int i = 0; i < RW; ++i) acc[i][4 * q] = b.x, acc[i][4 * q + 1] = b.y, acc[i][4 * q + 2] = b.z, acc[i][4 * q + 3] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
+    }
+    if (in_group) {
+            constexpr int AHEAD = RW == 2 ? 2 : 3;  // operands on their way from LDS
+      Frag<T> fa[KS][RW];
+      auto read = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < RW; ++i) fa[t][i] = A::template frag<true>(lds + buf * PIECES, (wr * RW + i) * 32, t, lane);
+      };
+#pragma unroll
+      for (int t = 0; t < AHEAD; ++t) read(t);
+#pragma unroll
+      for (int t = 0; t < KS; ++t) {
+        if (t + AHEAD < KS) read(t + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) acc[i] = attn::mma_frag<T>(fb[t], fa[t][i], acc[i]);
+      }
+    }
+    attn::settle();
+  };
+  auto emit = [&]() {
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      float v[16];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = acc[i][8 * p + e], y = acc[i][8 * p + 4 + e];  // scalars first: a bit cast of a vector's element reads element 0
+          const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y), false, false);
+          const uint32_t r0 = r[0], r1 = r[1];
+          v[8 * p + e] = __builtin_bit_cast(float, r0);
+          v[8 * p + 4 + e] = __builtin_bit_cast(float, r1);
+        }
+      finish<T, FORM, 16>(a, in_group, sides, [&](int e) { return element<T>(side[i][e / 8], e % 8); }, v, [&](T* to, int64_t stride, const float (&x)[16]) {
+        T* dst = to + (row + 32 * i) * stride + n_wave + 8 * half;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float u[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = x[8 * b + e];
+          if (32 * i < left && n_wave + 16 * b + 8 * half < a.n) store8<T>(dst + 16 * b, u);
+        }
+      });
+    }
+  };
+  sa.template store<true>(lds, tid);
+  while (true) {
+    const int g = group_of(cur);
+    if (g != group) {
+      group = g;
+      if (g >= 0) load_weights(g);
+    }
+    Walk nxt = cur;
+    ++nxt.slot;
+    settle_walk(nxt);
+    __syncthreads();
+    const bool more = nxt.slot < end;
+    if (more) fetch(nxt);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(cur, g);
+    // The next tile goes into LDS before this one's values leave: the wait for
+    // its loads is then none for the stores.
+    if (more) sa.template store<true>(lds + (buf ^ 1) * PIECES, tid);
+    __builtin_amdgcn_sched_barrier(0);
+    emit();
+    if (!more) return;
+    cur = nxt;
+    buf ^= 1;
   }
 }
 
@@ -337,7 +596,13 @@ template <class T>
 struct Shapes16 {
   typedef Shape<32, 128, 1, 4, 64, 2> Tiny;
   typedef Shape<128, 64, 4, 1, 64, 2> Narrow;
-  typedef Shape<128, 128, 2, 2, 64, 2> Medium;
+#ifndef MED
+#define MED 128, 128, 2, 2, 64, 2
+#endif
+#ifndef MOCC
+#define MOCC 1
+#endif
+  typedef Shape<MED> Medium;
   typedef Shape<256, 256, 2, 4, 64, 2> Large;
 };
 template <>
@@ -360,6 +625,41 @@ hipError_t launch_shape(const ProductArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Runs of slots: as many workgroups as run at once, a whole number of runs for
+// each XCD.
+template <class T, class S, int FORM>
+hipError_t launch_stream(ProductArgs a, hipStream_t stream) {
+  a.by_unit = make_fast_div(S::BM);
+  a.slots = a.cu == nullptr ? (a.rows + S::BM - 1) / S::BM : a.rows / S::BM + a.groups + 2;
+  a.tiles = a.tiles_n = (a.n + S::BN - 1) / S::BN;
+  int chunks = std::max(8, 256 * S::PER_CU / a.tiles / 8 * 8);
+  chunks = std::min(chunks, a.slots);
+  const int per = (a.slots + chunks - 1) / chunks;
+  chunks = (a.slots + per - 1) / per;
+  const int64_t blocks = static_cast<int64_t>((chunks + 7) / 8 * 8) * a.tiles;
+  k_stream<T, S, FORM><<<static_cast<unsigned>(blocks), S::NT, 0, stream>>>(a, chunks, per);
+  return hipGetLastError();
+}
+template <class T, int FORM>
+hipError_t launch_stream_sized(const ProductArgs& a, hipStream_t stream) {
+  if constexpr (sizeof(T) == 4) {
+    if (a.k <= 64) return launch_stream<T, StreamShape<4, 1, 4, 1, 3>, FORM>(a, stream);
+    return launch_stream<T, StreamShape<8, 1, 4, 1, 2>, FORM>(a, stream);
+  } else {
+    auto by_columns = [&](auto ks) -> hipError_t {
+      constexpr int KS = decltype(ks)::value;
+      if (a.n <= 64) return launch_stream<T, StreamShape<KS, 4, 2, 1, 4>, FORM>(a, stream);
+      if (a.n <= 128) return launch_stream<T, StreamShape<KS, 2, 4, 1, 4>, FORM>(a, stream);
+      return launch_stream<T, StreamShape<KS, 1, 8, 1, 4>, FORM>(a, stream);
+    };
+    if (a.k <= 64) return by_columns(std::integral_constant<int, 4>{});
+    if (a.k <= 128) return by_columns(std::integral_constant<int, 8>{});
+    if (a.n <= 64) return launch_stream<T, StreamShape<16, 4, 2, 1, 2>, FORM>(a, stream);
+    if (a.n <= 128) return launch_stream<T, StreamShape<16, 2, 4, 1, 2>, FORM>(a, stream);
+    return launch_stream<T, StreamShape<16, 1, 8, 2, 2>, FORM>(a, stream);
+  }
+}
+
 template <class T>
 hipError_t launch_typed(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream) {
   auto by_form = [&](auto s) -> hipError_t {
@@ -368,6 +668,7 @@ hipError_t launch_typed(const ProductArgs& a, ProductForm form, ProductShape sha
     if (form == kByRowsT) return launch_shape<T, S, kByRowsT>(a, stream);
     return launch_shape<T, S, kOverRows>(a, stream);
   };
+  if (shape == kStreamShape) return form == kByRows ? launch_stream_sized<T, kByRows>(a, stream) : launch_stream_sized<T, kByRowsT>(a, stream);
   if (shape == kTinyShape) return by_form(typename Shapes<T>::Tiny{});
   if (shape == kNarrowShape) return by_form(typename Shapes<T>::Narrow{});
   if (shape == kMediumShape) return by_form(typename Shapes<T>::Medium{});

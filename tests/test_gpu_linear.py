@@ -12,8 +12,12 @@ pytestmark = pytest.mark.gpu
 # rows, c_in, c_out: one row, tiles' edges, lengths that are no whole pieces,
 # few and many columns, few rows by a long contraction, single values
 SIZES = [(1, 8, 8), (1, 2048, 264), (5, 20, 19), (33, 64, 64), (64, 96, 20), (127, 40, 136), (300, 257, 131), (1000, 1, 1),
-         (257, 512, 384), (2000, 72, 300), (513, 640, 264), (31, 1000, 33), (4097, 33, 7)]
-GROUPS = [[0, 5, 0, 1, 64, 130, 0], [3] * 70, [1], [0, 0, 0], [700, 1, 129, 0, 40], [0] * 130 + [9, 200] + [0] * 5]
+         (257, 512, 384), (2000, 72, 300), (513, 640, 264), (31, 1000, 33), (4097, 33, 7),
+         # contractions short enough for weights in registers, one tile and many of each workgroup
+         (40, 16, 64), (300, 256, 136), (1000, 200, 64), (700, 136, 128), (30001, 256, 1024), (333, 128, 72), (40000, 128, 264),
+         (20000, 64, 96), (20000, 248, 88)]
+GROUPS = [[0, 5, 0, 1, 64, 130, 0], [3] * 70, [1], [0, 0, 0], [700, 1, 129, 0, 40], [0] * 130 + [9, 200] + [0] * 5,
+          [3000, 0, 1, 5000, 33, 0, 7000], [150, 0, 0, 31, 400]]
 
 
 def _draw(dtype, *shape, seed, scale=1.0):
@@ -91,7 +95,7 @@ def test_forward_groups(dtype, at):
     lengths, dt = GROUPS[at], DTYPES[dtype]
     before, after = (0, 0) if at % 2 else (3, 37)
     rows = before + sum(lengths) + after
-    c_in, c_out = [(64, 96), (24, 130), (31, 5), (128, 64), (96, 272), (520, 136)][at]
+    c_in, c_out = [(64, 96), (24, 130), (31, 5), (128, 64), (96, 272), (520, 136), (256, 320), (200, 104)][at]
     if rows == 0:
         rows = 4
     x, w, b = _case(dt, rows, c_in, c_out, 100 + at, len(lengths))
@@ -157,7 +161,7 @@ def test_backward_groups(dtype, at):
     lengths, dt = GROUPS[at], DTYPES[dtype]
     before, after = (3, 37) if at % 2 else (0, 0)
     rows = max(before + sum(lengths) + after, 2)
-    c_in, c_out = [(64, 96), (24, 130), (31, 5), (128, 64), (96, 272), (136, 72)][at]
+    c_in, c_out = [(64, 96), (24, 130), (31, 5), (128, 64), (96, 272), (136, 72), (320, 256), (64, 128)][at]
     x, w, _ = _case(dt, rows, c_in, c_out, 500 + at, len(lengths))
     grad = _draw(dt, rows, c_out, seed=600 + at)
     pre = _draw(dt, rows, c_in, seed=700 + at) if at % 3 == 1 else None
