@@ -394,7 +394,7 @@ struct ProductArgs {
 };
 
 // Workgroup shapes: rows x columns of a tile (linear_kernels.h).
-enum ProductShape { kTinyShape, kNarrowShape, kMediumShape, kLargeShape, kStreamShape };
+enum ProductShape { kFewShape, kFewWideShape, kFewShortShape, kNarrowShape, kMediumShape, kLargeShape, kStreamShape };
 hipError_t launch_product_f32(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
 hipError_t launch_product_f16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
 hipError_t launch_product_bf16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);

@@ -8,6 +8,7 @@
 //
 // The products themselves are in linear_kernels.h.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear_common.h"
 
@@ -73,38 +74,57 @@ __global__ __launch_bounds__(256) void k_join_rows(ProductArgs a) {
                           [&](T* to, int64_t stride, const float (&x)[8]) { lin::store_some8<T>(to + row * stride + col, there, a.whole, x); });
 }
 
-// Over rows: the parts of each group summed in their order; a group without
-// rows gives zeros.  Row m of the sums is the column sums of b.
+// Over rows: the parts of each group summed in a fixed order; a group without
+// rows gives zeros.  Row m of the sums is the column sums of b.  4 columns a
+// thread, LANES threads for them that take the parts in turn and join in LDS:
+// hundreds of parts of small sums would be a long chain of loads for one
+// (512 parts of 64 x 64: 22 us, with 16 lanes JOINUS).
+template <int LANES>
 __global__ __launch_bounds__(256) void k_join_groups(ProductArgs a) {
+  constexpr int QUADS = 256 / LANES;
+  __shared__ float4 stage[LANES > 1 ? 256 : 1];
   const int group = blockIdx.y;
   const int pieces = a.n_part / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.m + (a.sums != nullptr)) * pieces) return;
-  const int m = static_cast<int>(i / pieces), col = static_cast<int>(i - static_cast<int64_t>(m) * pieces) * 4;
+  const int lane = threadIdx.x / QUADS;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * QUADS + threadIdx.x % QUADS;
+  const bool there = i < static_cast<int64_t>(a.m + (a.sums != nullptr)) * pieces;
+  const int m = there ? static_cast<int>(i / pieces) : 0, col = there ? static_cast<int>(i - static_cast<int64_t>(m) * pieces) * 4 : 0;
   int first = 0, rows = a.rows;
   if (a.cu != nullptr) {
     const int r0 = attn::bound(a.cu, a.groups, a.rows, group + 1), r1 = attn::bound(a.cu, a.groups, a.rows, group + 2);
     rows = max(r1 - r0, 0);
     first = lin::segment_start(a, group + 1);
   }
-  const int parts = rows == 0 ? 0 : fast_div(rows - 1, a.by_unit) + 1;
+  const int parts = rows == 0 || !there ? 0 : fast_div(rows - 1, a.by_unit) + 1;
   const bool sums = m == a.m;
   const float* p = sums ? a.sums_part + static_cast<int64_t>(first) * a.n_part + col
                         : a.part + (static_cast<int64_t>(first) * a.m + m) * a.n_part + col;
   const int64_t step = sums ? a.n_part : static_cast<int64_t>(a.m) * a.n_part;
-  float v[4] = {};
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int s = 0; s < parts; ++s) {
+  for (int s = lane; s < parts; s += LANES) {
     const float4 x = *reinterpret_cast<const float4*>(p + s * step);
-    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
   }
+  if constexpr (LANES > 1) {
+    stage[threadIdx.x] = v;
+    __syncthreads();
+    if (lane > 0) return;
+#pragma unroll
+    for (int q = 1; q < LANES; ++q) {
+      const float4 x = stage[q * QUADS + threadIdx.x];
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+  }
+  if (!there) return;
   float* dst = sums ? a.sums + static_cast<int64_t>(group) * a.n + col : static_cast<float*>(a.out) + (static_cast<int64_t>(group) * a.m + m) * a.n + col;
   if (a.whole && !sums) {
-    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(dst) = v;
   } else {
+    const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (col + j < a.n) dst[j] = v[j];
+      if (col + j < a.n) dst[j] = x[j];
   }
 }
 
@@ -168,13 +188,15 @@ hipError_t lay_out(const Operand& o, const void* src, int64_t row_stride, int64_
 struct ShapeSize {
   int bm, bn, bk, threads;
 };
-ShapeSize shape_size(int dtype, ProductShape s) {
+ShapeSize shape_size(int dtype, ProductForm form, ProductShape s) {
+  const int few = dtype == 0 ? 32 : 64;  // contracted values of a wavefront's chunk
+  if (s == kFewShape) return {32, 32, few * 8, 512};
+  if (s == kFewWideShape) return {32, 64, few * 8, 512};
+  if (s == kFewShortShape) return {32, form == kByRows ? 64 : 32, few * 4, 256};
   if (dtype == 0) {
-    if (s == kTinyShape) return {32, 128, 32, 256};
     if (s == kNarrowShape) return {128, 32, 32, 256};
     return {128, 128, 32, 256};
   }
-  if (s == kTinyShape) return {32, 128, 64, 256};
   if (s == kNarrowShape) return {128, 64, 64, 256};
   if (s == kMediumShape) return {128, 128, 64, 256};
   return {256, 256, 64, 512};
@@ -192,7 +214,7 @@ struct Product {
   int dtype;
   uint64_t items() const {
     const uint64_t blocks = static_cast<uint64_t>(a.slots) * static_cast<uint64_t>(a.tiles) * (form == kOverRows ? 1 : a.splits);
-    return blocks * shape_size(dtype, shape).threads;
+    return blocks * shape_size(dtype, form, shape).threads;
   }
 };
 
@@ -202,9 +224,14 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
   p.form = form;
   p.dtype = dtype;
   const int64_t each = rows / groups;
-  p.shape = each <= 32 ? kTinyShape : n <= (dtype == 0 ? 32 : 64) ? kNarrowShape : kMediumShape;
+  if (each <= 128) {
+    const int64_t wide = (rows / 32 + groups) * div_up(n, 64);  // workgroups of 64 columns
+    p.shape = wide < 256 ? kFewShape : k <= 1024 ? kFewShortShape : kFewWideShape;
+  } else {
+    p.shape = n <= (dtype == 0 ? 32 : 64) ? kNarrowShape : kMediumShape;
+  }
   if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 256 && div_up(rows, 256) * div_up(n, 256) >= 200) p.shape = kLargeShape;
-  const ShapeSize s = shape_size(dtype, p.shape);
+  const ShapeSize s = shape_size(dtype, p.form, p.shape);
   ProductArgs& a = p.a;
   a.cu = cu;
   a.groups = groups;
@@ -216,7 +243,11 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
   a.tiles = a.tiles_n = static_cast<int32_t>(div_up(n, s.bn));
   const int64_t steps = div_up(k, s.bk), blocks = std::max<int64_t>(1, static_cast<int64_t>(a.slots) * a.tiles);
   int64_t splits = 1;
-  if (blocks * 2 <= kFill && steps >= 8) splits = std::min(kFill / blocks, steps / 4);
+  if (each <= 128) {
+    if (blocks * 2 <= 256) splits = std::max<int64_t>(1, std::min(256 / blocks, steps));
+  } else if (blocks * 2 <= kFill && steps >= 8) {
+    splits = std::min(kFill / blocks, steps / 4);
+  }
   a.k_split = static_cast<int32_t>(div_up(steps, splits) * s.bk);
   a.splits = static_cast<int32_t>(div_up(k, a.k_split));
   a.n_part = padded(n);
@@ -230,8 +261,8 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   p.form = kOverRows;
   p.dtype = dtype;
   p.shape = n <= (dtype == 0 ? 32 : 64) ? kNarrowShape : kMediumShape;
-  if (dtype != 0 && p.shape == kMediumShape && m > 128 && n > 128) p.shape = kLargeShape;
-  const ShapeSize s = shape_size(dtype, p.shape);
+  if (dtype != 0 && p.shape == kMediumShape && m > 128 && n > 128 && div_up(m, 256) * div_up(n, 256) * (rows / 64) >= 32 * 256) p.shape = kLargeShape;
+  const ShapeSize s = shape_size(dtype, p.form, p.shape);
   ProductArgs& a = p.a;
   a.cu = cu;
   a.groups = groups;
@@ -241,7 +272,7 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   a.tiles_n = static_cast<int32_t>(div_up(n, s.bn));
   a.tiles = static_cast<int32_t>(div_up(m, s.bm) * a.tiles_n);
   a.n_part = padded(n);
-  const int64_t parts = std::min<int64_t>((p.shape == kLargeShape ? 256 : kFill) / a.tiles, rows / 256);
+  const int64_t parts = std::min<int64_t>((p.shape == kLargeShape ? 256 : kFill) / a.tiles, rows / 128);
   if (parts <= 1 || parts <= groups) {  // every group is one part
     a.by_unit = make_fast_div(1 << 30);
     a.slots = cu == nullptr ? 1 : groups + 2;
@@ -255,6 +286,14 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   return p;
 }
 
+// The join over rows: 4 columns a thread, and the lanes that share the parts
+// of one group (their number on average).
+int64_t join_pieces(const ProductArgs& a) { return static_cast<int64_t>(a.m + 1) * (a.n_part / 4); }
+int join_lanes(const ProductArgs& a) {
+  const int parts = a.slots / a.groups;
+  return parts >= 32 ? 16 : parts >= 8 ? 4 : 1;
+}
+
 hipError_t run_product(const Product& p, hipStream_t stream) {
   if (p.dtype == 0) return launch_product_f32(p.a, p.form, p.shape, stream);
   if (p.dtype == 1) return launch_product_f16(p.a, p.form, p.shape, stream);
@@ -264,7 +303,7 @@ hipError_t run_product(const Product& p, hipStream_t stream) {
 // Whether a product keeps its weights in registers.
 bool streams(const Product& p) {
   const ProductArgs& a = p.a;
-  if (!a.whole || a.splits > 1 || p.shape == kTinyShape) return false;
+  if (!a.whole || a.splits > 1 || p.shape == kFewShape || p.shape == kFewWideShape || p.shape == kFewShortShape) return false;
   return p.dtype == 0 ? a.k <= 128 && a.n > 64 : a.k <= 256 && a.n >= 64;
 }
 
@@ -329,8 +368,10 @@ Backward plan_backward(const LinearArgs& a, void* workspace) {
 uint64_t linear_work_items(const LinearArgs& a, bool backward) {
   if (!backward) return plan_forward(a, nullptr).p.items();
   const Backward b = plan_backward(a, nullptr);
-  const uint64_t join = static_cast<uint64_t>(div_up(static_cast<int64_t>(a.c_in + 1) * (b.gw.a.n_part / 4), 256)) * 256 * a.groups;
-  return std::max({b.gx.items(), b.gw.items(), b.gw.a.part == nullptr && b.gw.a.slots <= a.groups + 2 ? uint64_t(0) : join});
+  const ProductArgs& p = b.gw.a;
+  const bool joined = p.by_unit.d != (1 << 30);
+  const uint64_t join = joined ? static_cast<uint64_t>(div_up(join_pieces(p), 256 / join_lanes(p))) * 256 * a.groups : 0;
+  return std::max({b.gx.items(), b.gw.items(), join});
 }
 
 size_t linear_workspace_bytes(const LinearArgs& a) { return plan_forward(a, nullptr).bytes; }
@@ -401,8 +442,15 @@ hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, hipStrea
     p.whole = whole_rows(a.grad_weight, a.c_out, a.c_out, 0);
     e = run_product(b.gw, stream);
     if (e != hipSuccess || p.part == nullptr) return e;
-    const int64_t threads = static_cast<int64_t>(p.m + 1) * (p.n_part / 4);
-    k_join_groups<<<dim3(static_cast<unsigned>(div_up(threads, 256)), static_cast<unsigned>(p.groups)), 256, 0, stream>>>(p);
+    auto join = [&](auto lanes) {
+      constexpr int LANES = decltype(lanes)::value;
+      k_join_groups<LANES><<<dim3(static_cast<unsigned>(div_up(join_pieces(p), 256 / LANES)), static_cast<unsigned>(p.groups)), 256, 0, stream>>>(p);
+    };
+    switch (join_lanes(p)) {
+      case 1: join(std::integral_constant<int, 1>{}); break;
+      case 4: join(std::integral_constant<int, 4>{}); break;
+      default: join(std::integral_constant<int, 16>{}); break;
+    }
     return hipGetLastError();
   }
   return hipSuccess;

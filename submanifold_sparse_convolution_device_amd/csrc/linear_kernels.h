@@ -19,9 +19,6 @@
 // one row; the sums pass through the wavefront's own LDS into whole rows, 8
 // columns a lane, for the epilogue (finish8) and 16-byte accesses.
 #pragma once
-#ifndef AH2
-#define AH2 2
-#endif
 
 #include <algorithm>
 #include <type_traits>
@@ -128,6 +125,7 @@ struct Stage {
 };
 
 // A workgroup's shape.
+// STAGES: LDS buffers.
 template <int BM_, int BN_, int WR_, int WC_, int BK_, int STAGES_>
 struct Shape {
   static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, BK = BK_, STAGES = STAGES_;
@@ -148,10 +146,7 @@ struct Kernel {
 };
 
 template <class T, class S, int FORM>
-#ifndef MOCC
-#define MOCC 1
-#endif
-__global__ __launch_bounds__(S::NT, (S::NT == 256 && S::BN == 128 && S::BM == 128) ? MOCC : 1) void k_product(ProductArgs a) {
+__global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
   typedef Kernel<T, S, FORM> K;
   __shared__ uint4 lds[K::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -218,7 +213,8 @@ __global__ __launch_bounds__(S::NT, (S::NT == 256 && S::BN == 128 && S::BM == 12
   };
   float column[8] = {};  // over rows: this thread's share of the sums of 8 columns of b
   const bool sums = FORM == kOverRows && m0 == 0 && (a.sums != nullptr || a.sums_part != nullptr);
-  auto put = [&](uint4* to) {
+  auto put_a = [&](uint4* to) { sa.template store<K::kAlongA>(to, tid); };
+  auto put_b = [&](uint4* to) {
     if constexpr (FORM == kOverRows) {
       if (sums) {
 #pragma unroll
@@ -230,24 +226,34 @@ __global__ __launch_bounds__(S::NT, (S::NT == 256 && S::BN == 128 && S::BM == 12
         }
       }
     }
-    sa.template store<K::kAlongA>(to, tid);
     sb.template store<K::kAlongB>(to + K::kPiecesA, tid);
   };
 
-  constexpr int RB = S::TM / 32, CB = S::TN / 32;
+  constexpr int RB = S::TM / 32, CB = S::TN / 32, STEPS = S::BK / 16;
   floatx16 acc[RB][CB] = {};
-  auto multiply = [&](const uint4* from) {
+  // The products of a step; between(t) runs before those of 16 values t.
+  auto multiply = [&](const uint4* from, auto&& between) {
+    Frag<T> fa[STEPS][RB], fb[STEPS][CB];
+    auto read = [&](int t) {
 #pragma unroll
-    for (int t = 0; t < S::BK / 16; ++t) {
-      Frag<T> fa[RB], fb[CB];
+      for (int i = 0; i < RB; ++i) fa[t][i] = K::A::template frag<K::kAlongA>(from, wr * S::TM + 32 * i, t, lane);
 #pragma unroll
-      for (int i = 0; i < RB; ++i) fa[i] = K::A::template frag<K::kAlongA>(from, wr * S::TM + 32 * i, t, lane);
+      for (int j = 0; j < CB; ++j) fb[t][j] = K::B::template frag<K::kAlongB>(from + K::kPiecesA, wc * S::TN + 32 * j, t, lane);
+    };
+    // (over rows, with the column sums, two sets of operands do not fit beside large tiles)
+    constexpr bool TWO = FORM != kOverRows || RB * CB <= 4;
+    if (TWO) read(0);
 #pragma unroll
-      for (int j = 0; j < CB; ++j) fb[j] = K::B::template frag<K::kAlongB>(from + K::kPiecesA, wc * S::TN + 32 * j, t, lane);
+    for (int t = 0; t < STEPS; ++t) {
+      if (!TWO) read(t);
+      else if (t + 1 < STEPS) read(t + 1);
+      between(t);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < CB; ++j) acc[i][j] = attn::mma_frag<T>(fb[j], fa[i], acc[i][j]);
+        for (int j = 0; j < CB; ++j) acc[i][j] = attn::mma_frag<T>(fb[t][j], fa[t][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
     attn::settle();
   };
@@ -256,26 +262,31 @@ __global__ __launch_bounds__(S::NT, (S::NT == 256 && S::BN == 128 && S::BM == 12
     fetch(k0);
     if constexpr (S::STAGES == 2) {
       // One barrier a step: it ends the writes of this step's buffer and the
-      // reads of the other one, which the step's end fills.
-      put(lds);
+      // reads of the other one, which is filled between this step's products.
+      put_a(lds);
+      put_b(lds);
       int buf = 0;
       for (int k = k0; k < k1; k += S::BK) {
         __syncthreads();
         const bool more = k + S::BK < k1;
         if (more) fetch(k + S::BK);
         __builtin_amdgcn_sched_barrier(0);
-        multiply(lds + buf * K::kPieces);
-        if (more) put(lds + (buf ^ 1) * K::kPieces);
+        uint4* other = lds + (buf ^ 1) * K::kPieces;
+        multiply(lds + buf * K::kPieces, [&](int t) {
+          if (t == STEPS - 2 && more) put_a(other);
+          if (t == STEPS - 1 && more) put_b(other);
+        });
         buf ^= 1;
       }
     } else {
       for (int k = k0; k < k1; k += S::BK) {
         __syncthreads();
-        put(lds);
+        put_a(lds);
+        put_b(lds);
         __syncthreads();
         if (k + S::BK < k1) fetch(k + S::BK);
         __builtin_amdgcn_sched_barrier(0);
-        multiply(lds);
+        multiply(lds, [](int) {});
       }
     }
   }
@@ -587,27 +598,138 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_stream(ProductArgs a, int chu
   }
 }
 
+// ---- Few rows ----
+// By rows with up to 32 rows of a group: a workgroup computes 32 rows by 32 CB
+// columns, and its 8 wavefronts take chunks of KC contracted values in turn,
+// each by itself: the rows' operands come straight from memory, the weights'
+// through the wavefront's own LDS (transposed) or straight, the next chunk's
+// loads in flight during a chunk.  No wavefront waits for another before the
+// sums of all 8 are joined in LDS.
+template <class T, int CB, int WAVES_, int FORM>
+struct Few {
+  static constexpr int KC = sizeof(T) == 4 ? 32 : 64, WAVES = WAVES_;
+  typedef Stage<T, KC, 4 * CB, 64> W;
+  static constexpr int kMine = FORM == kByRows ? KC * 4 * CB * kPlanes<T> : 0;  // a wavefront's weights
+  static constexpr int kStride = 32 * CB + 4;                                   // floats of a row of sums
+  static constexpr int kLds = std::max(WAVES * kMine, WAVES * 32 * kStride / 4);
+};
+
+template <class T, int CB, int WAVES, int FORM>
+__global__ __launch_bounds__(64 * WAVES) void k_few(ProductArgs a) {
+  typedef Few<T, CB, WAVES, FORM> F;
+  constexpr int KC = F::KC, STEPS = KC / 16;
+  __shared__ uint4 lds[F::kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+  // a consecutive eighth of the tiles for each XCD (as in k_product): neighbouring columns share lines
+  const int eighth = gridDim.x / 8, over = gridDim.x % 8, xcd = blockIdx.x % 8;
+  int at = blockIdx.x / 8 + xcd * eighth + min(xcd, over);
+  const int per = a.slots * a.tiles, split = at / per;
+  at -= split * per;
+  const int slot = at / a.tiles, n0 = (at - slot * a.tiles) * (32 * CB);
+  const Segment seg = find_segment(a, slot);
+  const int rows = seg.hi - seg.lo;
+  if (rows <= 0 || (seg.group < 0 && a.part != nullptr)) return;
+  const int k0 = split * a.k_split, k1 = seg.group < 0 ? k0 : min(a.k, k0 + a.k_split);
+  const int a_end = k1 == a.k ? a.a_cols : k1, b_end = k1 == a.k ? a.b_cols : k1;  // (whole pieces)
+
+  const T* A0 = static_cast<const T*>(a.a) + (seg.lo + static_cast<int64_t>(lane & 31)) * a.a_row;
+  const T* B0 = static_cast<const T*>(a.b) + static_cast<int64_t>(max(seg.group, 0)) * a.b_group;
+  const bool row_there = (lane & 31) < rows;
+  Raw<T> ra[STEPS], rb[FORM == kByRows ? 1 : STEPS][CB];
+  typename F::W w;
+  auto fetch = [&](int k) {
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) ra[t] = load_piece_of<T>(A0 + k + 16 * t + 8 * half, row_there, a_end - (k + 16 * t + 8 * half));
+    if constexpr (FORM == kByRows) {
+      w.load(B0 + static_cast<int64_t>(k) * a.b_row + n0, a.b_row, k1 - k, a.b_cols - n0, lane);
+    } else {
+#pragma unroll
+      for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          const int n = n0 + 32 * c + (lane & 31);
+          rb[t][c] = load_piece_of<T>(B0 + static_cast<int64_t>(n) * a.b_row + k + 16 * t + 8 * half, n < a.n, b_end - (k + 16 * t + 8 * half));
+        }
+    }
+  };
+  floatx16 acc[CB] = {};
+  uint4* mine = lds + wave * F::kMine;
+  int k = k0 + wave * KC;
+  if (k < k1) fetch(k);
+  while (k < k1) {
+    Frag<T> fa[STEPS], fb[STEPS][CB];
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) fa[t] = attn::to_frag<T>(ra[t]);
+    if constexpr (FORM == kByRows) {
+      wave_order();
+      w.template store<false>(mine, lane);
+      wave_order();
+#pragma unroll
+      for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) fb[t][c] = F::W::template frag<false>(mine, 32 * c, t, lane);
+    } else {
+#pragma unroll
+      for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) fb[t][c] = attn::to_frag<T>(rb[t][c]);
+    }
+    k += KC * F::WAVES;
+    if (k < k1) fetch(k);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+      for (int c = 0; c < CB; ++c) acc[c] = attn::mma_frag<T>(fb[t][c], fa[t], acc[c]);
+    attn::settle();
+  }
+  attn::settle();
+  __syncthreads();
+  float* stage = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(stage + (wave * 32 + (lane & 31)) * F::kStride + 32 * c + 8 * q + 4 * half) =
+          make_float4(acc[c][4 * q], acc[c][4 * q + 1], acc[c][4 * q + 2], acc[c][4 * q + 3]);
+  __syncthreads();
+  // 8 columns of a row a thread, the wavefronts' sums in their order
+  static_assert(64 * WAVES >= 128 * CB, "a thread a piece");
+  if (tid >= 128 * CB) return;
+  const int r = tid / (4 * CB), c = tid % (4 * CB) * 8, col = n0 + c, there = min(a.n - col, 8);
+  if (r >= rows || there <= 0) return;
+  const int64_t row = static_cast<int64_t>(seg.lo) + r;
+  const bool in_group = seg.group >= 0, sides = a.part == nullptr && a.side != nullptr && in_group;
+  float v[8] = {}, z[8] = {}, bias[8] = {};
+  if (FORM == kByRows && a.part == nullptr && a.bias != nullptr && in_group)
+    load_some8<T>(static_cast<const T*>(a.bias) + static_cast<int64_t>(seg.group) * a.n + col, there, a.whole, bias);
+  if (sides) load_some8<T>(side_row<T>(a, row) + col, there, a.whole, z);
+#pragma unroll
+  for (int q = 0; q < F::WAVES; ++q) {
+    const float4 lo = *reinterpret_cast<const float4*>(stage + (q * 32 + r) * F::kStride + c), hi = *reinterpret_cast<const float4*>(stage + (q * 32 + r) * F::kStride + c + 4);
+    v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w, v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+  }
+  if (a.part != nullptr) {
+    store8<float>(a.part + (static_cast<int64_t>(split) * a.rows + row) * a.n_part + col, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += bias[i];
+  finish<T, FORM, 8>(a, in_group, sides, [&](int i) { return z[i]; }, v, [&](T* to, int64_t stride, const float (&x)[8]) { store_some8<T>(to + row * stride + col, there, a.whole, x); });
+}
+
 // ---- The shapes ----
-// kTiny: few rows of each group, more columns; kNarrow: few columns; kMedium;
-// kLarge: whole large products.
+// kNarrow: few columns; kMedium; kLarge: whole large products.
 template <class T>
 struct Shapes;
 template <class T>
 struct Shapes16 {
-  typedef Shape<32, 128, 1, 4, 64, 2> Tiny;
   typedef Shape<128, 64, 4, 1, 64, 2> Narrow;
-#ifndef MED
-#define MED 128, 128, 2, 2, 64, 2
-#endif
-#ifndef MOCC
-#define MOCC 1
-#endif
-  typedef Shape<MED> Medium;
+  typedef Shape<128, 128, 2, 2, 64, 2> Medium;
   typedef Shape<256, 256, 2, 4, 64, 2> Large;
 };
 template <>
 struct Shapes<float> {
-  typedef Shape<32, 128, 1, 4, 32, 1> Tiny;
   typedef Shape<128, 32, 4, 1, 32, 1> Narrow;
   typedef Shape<128, 128, 2, 2, 32, 1> Medium;
   typedef Medium Large;
@@ -669,7 +791,20 @@ hipError_t launch_typed(const ProductArgs& a, ProductForm form, ProductShape sha
     return launch_shape<T, S, kOverRows>(a, stream);
   };
   if (shape == kStreamShape) return form == kByRows ? launch_stream_sized<T, kByRows>(a, stream) : launch_stream_sized<T, kByRowsT>(a, stream);
-  if (shape == kTinyShape) return by_form(typename Shapes<T>::Tiny{});
+  if (shape == kFewShape || shape == kFewWideShape || shape == kFewShortShape) {
+    auto few = [&](auto cb, auto waves) -> hipError_t {
+      constexpr int CB = decltype(cb)::value, WAVES = decltype(waves)::value;
+      const int64_t blocks = static_cast<int64_t>(a.slots) * a.tiles * a.splits;
+      if (form == kByRows) k_few<T, CB, WAVES, kByRows><<<static_cast<unsigned>(blocks), 64 * WAVES, 0, stream>>>(a);
+      else k_few<T, CB, WAVES, kByRowsT><<<static_cast<unsigned>(blocks), 64 * WAVES, 0, stream>>>(a);
+      return hipGetLastError();
+    };
+    typedef std::integral_constant<int, 1> One;
+    typedef std::integral_constant<int, 2> Two;
+    if (shape == kFewShortShape) return form == kByRows ? few(Two{}, std::integral_constant<int, 4>{}) : few(One{}, std::integral_constant<int, 4>{});
+    if (shape == kFewShape) return few(One{}, std::integral_constant<int, 8>{});
+    return few(Two{}, std::integral_constant<int, 8>{});
+  }
   if (shape == kNarrowShape) return by_form(typename Shapes<T>::Narrow{});
   if (shape == kMediumShape) return by_form(typename Shapes<T>::Medium{});
   return by_form(typename Shapes<T>::Large{});
