@@ -193,13 +193,12 @@ ShapeSize shape_size(int dtype, ProductForm form, ProductShape s) {
   if (s == kFewShape) return {32, 32, few * 8, 512};
   if (s == kFewWideShape) return {32, 64, few * 8, 512};
   if (s == kFewShortShape) return {32, form == kByRows ? 64 : 32, few * 4, 256};
-  if (dtype == 0) {
-    if (s == kNarrowShape) return {128, 32, 32, 256};
-    return {128, 128, 32, 256};
-  }
-  if (s == kNarrowShape) return {128, 64, 64, 256};
-  if (s == kMediumShape) return {128, 128, 64, 256};
-  return {256, 256, 64, 512};
+  auto of = [](auto x) { return ShapeSize{decltype(x)::BM, decltype(x)::BN, decltype(x)::BK, decltype(x)::NT}; };
+  auto by_shape = [&](auto shapes) {
+    typedef decltype(shapes) S;
+    return s == kNarrowShape ? of(typename S::Narrow{}) : s == kMediumShape ? of(typename S::Medium{}) : of(typename S::Large{});
+  };
+  return dtype == 0 ? by_shape(lin::Shapes<float>{}) : by_shape(lin::Shapes<_Float16>{});
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -228,7 +227,8 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
     const int64_t wide = (rows / 32 + groups) * div_up(n, 64);  // workgroups of 64 columns
     p.shape = wide < 256 ? kFewShape : k <= 1024 ? kFewShortShape : kFewWideShape;
   } else {
-    p.shape = n <= (dtype == 0 ? 32 : 64) ? kNarrowShape : kMediumShape;
+    const int64_t medium = (rows / 128 + (cu == nullptr ? 1 : groups)) * div_up(n, 128);
+    p.shape = n <= (dtype == 0 ? 32 : 64) || medium < 256 ? kNarrowShape : kMediumShape;
   }
   if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 256 && div_up(rows, 256) * div_up(n, 256) >= 200) p.shape = kLargeShape;
   const ShapeSize s = shape_size(dtype, p.form, p.shape);

@@ -64,6 +64,35 @@ __device__ __forceinline__ Segment find_segment(const ProductArgs& a, int slot) 
   return g;
 }
 
+// ---- Workgroup shapes of the tiled products ----
+// BM x BN tiles by WR x WC wavefronts, BK contracted values a step.
+// STAGES: LDS buffers.
+template <int BM_, int BN_, int WR_, int WC_, int BK_, int STAGES_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, BK = BK_, STAGES = STAGES_;
+  static constexpr int NT = 64 * WR * WC, TM = BM / WR, TN = BN / WC;
+};
+// Narrow: few columns, or too few tiles to fill the chip; Medium; Large: whole
+// large products.
+template <class T>
+struct Shapes;
+template <class T>
+struct Shapes16 {
+  typedef Shape<128, 64, 4, 1, 64, 2> Narrow;
+  typedef Shape<128, 128, 2, 2, 64, 2> Medium;
+  typedef Shape<256, 256, 2, 4, 64, 2> Large;
+};
+template <>
+struct Shapes<float> {
+  typedef Shape<128, 32, 4, 1, 32, 1> Narrow;
+  typedef Shape<128, 128, 2, 2, 32, 1> Medium;
+  typedef Medium Large;
+};
+template <>
+struct Shapes<_Float16> : Shapes16<_Float16> {};
+template <>
+struct Shapes<__bf16> : Shapes16<__bf16> {};
+
 // ---- Activations ----
 enum Act { kIdentity = 0, kRelu = 1, kSilu = 2, kGelu = 3 };
 

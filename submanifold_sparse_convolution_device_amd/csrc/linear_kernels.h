@@ -124,14 +124,6 @@ struct Stage {
   }
 };
 
-// A workgroup's shape.
-// STAGES: LDS buffers.
-template <int BM_, int BN_, int WR_, int WC_, int BK_, int STAGES_>
-struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, BK = BK_, STAGES = STAGES_;
-  static constexpr int NT = 64 * WR * WC, TM = BM / WR, TN = BN / WC;
-};
-
 template <class T, class S, int FORM>
 struct Kernel {
   static constexpr bool kAlongA = FORM != kOverRows, kAlongB = FORM == kByRowsT;
@@ -718,27 +710,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_few(ProductArgs a) {
   finish<T, FORM, 8>(a, in_group, sides, [&](int i) { return z[i]; }, v, [&](T* to, int64_t stride, const float (&x)[8]) { store_some8<T>(to + row * stride + col, there, a.whole, x); });
 }
 
-// ---- The shapes ----
-// kNarrow: few columns; kMedium; kLarge: whole large products.
-template <class T>
-struct Shapes;
-template <class T>
-struct Shapes16 {
-  typedef Shape<128, 64, 4, 1, 64, 2> Narrow;
-  typedef Shape<128, 128, 2, 2, 64, 2> Medium;
-  typedef Shape<256, 256, 2, 4, 64, 2> Large;
-};
-template <>
-struct Shapes<float> {
-  typedef Shape<128, 32, 4, 1, 32, 1> Narrow;
-  typedef Shape<128, 128, 2, 2, 32, 1> Medium;
-  typedef Medium Large;
-};
-template <>
-struct Shapes<_Float16> : Shapes16<_Float16> {};
-template <>
-struct Shapes<__bf16> : Shapes16<__bf16> {};
-
+// ---- Launches ----
 template <class T, class S, int FORM>
 hipError_t launch_shape(const ProductArgs& a, hipStream_t stream) {
   const int64_t blocks = static_cast<int64_t>(a.slots) * a.tiles * (FORM == kOverRows ? 1 : a.splits);
