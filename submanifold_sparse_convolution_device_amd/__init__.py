@@ -1237,19 +1237,24 @@ _PACK_LINEAR_GRADIENTS = struct.Struct("@5P3q")
 _NO_ROWS = (0, 0)
 
 
-def _rows_tensor(name, t, like=None, shape=None):
+def _rows_tensor(name, t):
     """Checks a [rows, channels] tensor whose last dimension is contiguous;
     returns (pointer, row stride)."""
     if t.dim() != 2 or not t.is_cuda:
         raise SpconvError(1, f"{name} must be a [rows, channels] tensor on a HIP device")
-    rows, cols = t.shape
+    return _like_rows(name, t, t.shape, t.dtype, t.get_device())
+
+
+def _like_rows(name, t, shape, dtype, device: int):
+    """The same of a tensor that must have this shape, dtype and device."""
+    if t.shape != shape:
+        raise SpconvError(1, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != device:
+        raise SpconvError(1, f"{name} must have the dtype and device of the other tensors")
     row, last = t.stride()
+    rows, cols = shape
     if last != 1 and cols > 1:
         raise SpconvError(1, f"{name} must have a contiguous last dimension")
-    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
-        raise SpconvError(1, f"{name} must have the dtype and device of the other tensors")
-    if shape is not None and t.shape != shape:
-        raise SpconvError(1, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
     return t.data_ptr(), (row if rows > 1 else cols)
 
 
@@ -1260,14 +1265,15 @@ def _whole_tensor(name, t, shape, dtype, device: int):
 
 
 def _add_norm_args(x, residual, weight, eps):
-    """The packed spconv_add_norm of a call."""
+    """(packed spconv_add_norm, shape, dtype, device) of a call."""
     xp, xr = _rows_tensor("x", x)
-    rp, rr = _NO_ROWS if residual is None else _rows_tensor("residual", residual, x, x.shape)
-    code = _dtype_code(x.dtype)
-    wp = _whole_tensor("weight", weight, x.shape[1:], x.dtype, x.get_device())
+    shape, dtype, device = x.shape, x.dtype, x.get_device()
+    rp, rr = _NO_ROWS if residual is None else _like_rows("residual", residual, shape, dtype, device)
+    code = _dtype_code(dtype)
+    wp = _whole_tensor("weight", weight, shape[1:], dtype, device)
     if not 0.0 <= eps < 3e38:
         raise SpconvError(1, f"eps = {eps} must be finite and not negative")
-    return _PACK_ADD_NORM.pack(xp, rp, wp, xr, rr, x.shape[0], x.shape[1], eps, code)
+    return _PACK_ADD_NORM.pack(xp, rp, wp, xr, rr, shape[0], shape[1], eps, code), shape, dtype, device
 
 
 def add_norm(x, residual, weight, *, eps: float = 1e-6, out=None):
@@ -1282,16 +1288,23 @@ def add_norm(x, residual, weight, *, eps: float = 1e-6, out=None):
     to write, which may be x and residual themselves (without a residual the
     first is None)."""
     torch, L = _bind()
-    a = _add_norm_args(x, residual, weight, eps)
+    a, shape, dtype, device = _add_norm_args(x, residual, weight, eps)
+    hp, hr = _NO_ROWS
     if out is None:
-        out = (None if residual is None else torch.empty_like(x, memory_format=torch.contiguous_format),
-               torch.empty_like(x, memory_format=torch.contiguous_format))
-    h, y = out
-    if (h is None) != (residual is None):
-        raise SpconvError(1, "out must hold a tensor for the sum exactly when there is a residual")
-    hp = _NO_ROWS if h is None else _rows_tensor("out[0]", h, x, x.shape)
-    yp = _rows_tensor("out[1]", y, x, x.shape)
-    _run(x.get_device(), L.spconv_add_norm_forward, a, *hp, *yp)
+        whole = torch.contiguous_format
+        h = None if residual is None else torch.empty_like(x, memory_format=whole)
+        y = torch.empty_like(x, memory_format=whole)
+        if h is not None:
+            hp, hr = h.data_ptr(), shape[1]
+        yp, yr = y.data_ptr(), shape[1]
+    else:
+        h, y = out
+        if (h is None) != (residual is None):
+            raise SpconvError(1, "out must hold a tensor for the sum exactly when there is a residual")
+        if h is not None:
+            hp, hr = _like_rows("out[0]", h, shape, dtype, device)
+        yp, yr = _like_rows("out[1]", y, shape, dtype, device)
+    _run(device, L.spconv_add_norm_forward, a, hp, hr, yp, yr)
     return (x if h is None else h), y
 
 
@@ -1302,15 +1315,15 @@ def add_norm_backward(grad_h, grad_y, h, weight, *, eps: float = 1e-6, grad=None
     [channels].  ``grad``: a tensor to write, which may be grad_h or grad_y
     itself."""
     torch, L = _bind()
-    a = _add_norm_args(h, None, weight, eps)
+    a, shape, dtype, device = _add_norm_args(h, None, weight, eps)
     if grad is None:
         grad = torch.empty_like(h, memory_format=torch.contiguous_format)
-    ghp, ghr = _NO_ROWS if grad_h is None else _rows_tensor("grad_h", grad_h, h, h.shape)
-    gyp, gyr = _rows_tensor("grad_y", grad_y, h, h.shape)
-    gp, gr = _rows_tensor("grad", grad, h, h.shape)
-    grad_weight = h.new_empty(h.shape[1], dtype=torch.float32)
+    ghp, ghr = _NO_ROWS if grad_h is None else _like_rows("grad_h", grad_h, shape, dtype, device)
+    gyp, gyr = _like_rows("grad_y", grad_y, shape, dtype, device)
+    gp, gr = _like_rows("grad", grad, shape, dtype, device)
+    grad_weight = h.new_empty(shape[1], dtype=torch.float32)
     g = _PACK_ADD_NORM_GRADIENTS.pack(ghp, gyp, gp, grad_weight.data_ptr(), ghr, gyr, gr)
-    _run(h.get_device(), L.spconv_add_norm_backward, a, g)
+    _run(device, L.spconv_add_norm_backward, a, g)
     return grad, grad_weight
 
 
@@ -1322,22 +1335,24 @@ def _activation_code(activation):
 
 
 def _linear_args(x, weight, cu, activation):
-    """(packed spconv_linear, groups, c_out) of a call."""
+    """(packed spconv_linear, shape of x, c_out, shape of a bias, dtype,
+    device) of a call."""
     xp, xr = _rows_tensor("x", x)
-    code = _dtype_code(x.dtype)
-    device = x.get_device()
-    rows, c_in = x.shape
-    if weight.dim() != (2 if cu is None else 3) or weight.shape[-2] != c_in:
-        raise SpconvError(1, f"weight must be [{'' if cu is None else 'groups, '}{c_in}, c_out], not {tuple(weight.shape)}")
-    wp = _whole_tensor("weight", weight, weight.shape, x.dtype, device)
-    groups, cp = 1, 0
+    shape, dtype, device = x.shape, x.dtype, x.get_device()
+    code = _dtype_code(dtype)
+    of = weight.shape
+    if len(of) != (2 if cu is None else 3) or of[-2] != shape[1]:
+        raise SpconvError(1, f"weight must be [{'' if cu is None else 'groups, '}{shape[1]}, c_out], not {tuple(of)}")
+    wp = _whole_tensor("weight", weight, of, dtype, device)
+    c_out = of[-1]
+    groups, cp, bias_shape = 1, 0, of[1:]
     if cu is not None:
-        groups = weight.shape[0]
+        groups, bias_shape = of[0], _TORCH.Size((of[0], c_out))
         cp = _offsets_tensor("cu", cu, device)
         if cu.shape[0] != groups + 1:
             raise SpconvError(1, f"cu must hold the {groups + 1} row offsets of {groups} groups, not {cu.shape[0]}")
-    c_out = weight.shape[-1]
-    return _PACK_LINEAR.pack(xp, wp, cp, xr, rows, groups, c_in, c_out, _activation_code(activation), code), groups, c_out
+    a = _PACK_LINEAR.pack(xp, wp, cp, xr, shape[0], groups, shape[1], c_out, _activation_code(activation), code)
+    return a, shape, c_out, bias_shape, dtype, device
 
 
 def linear(x, weight, bias=None, *, activation: Optional[str] = None, residual=None, cu=None, out=None, return_pre: bool = False):
@@ -1356,14 +1371,15 @@ def linear(x, weight, bias=None, *, activation: Optional[str] = None, residual=N
     :func:`activation_backward` and the ``pre`` of :func:`linear_backward`
     need.  The calls may be captured in a graph."""
     torch, L = _bind()
-    a, groups, c_out = _linear_args(x, weight, cu, activation)
-    shape = torch.Size((x.shape[0], c_out))
-    device = x.get_device()
-    bp = 0 if bias is None else _whole_tensor("bias", bias, torch.Size((c_out,) if cu is None else (groups, c_out)), x.dtype, device)
-    rp, rr = _NO_ROWS if residual is None else _rows_tensor("residual", residual, x, shape)
+    a, (rows, _), c_out, bias_shape, dtype, device = _linear_args(x, weight, cu, activation)
+    shape = torch.Size((rows, c_out))
+    bp = 0 if bias is None else _whole_tensor("bias", bias, bias_shape, dtype, device)
+    rp, rr = _NO_ROWS if residual is None else _like_rows("residual", residual, shape, dtype, device)
     if out is None:
         out = x.new_empty(shape)
-    op, orow = _rows_tensor("out", out, x, shape)
+        op, orow = out.data_ptr(), c_out
+    else:
+        op, orow = _like_rows("out", out, shape, dtype, device)
     pre, pp, pr = None, 0, 0
     if return_pre:
         pre = x.new_empty(shape)
@@ -1386,23 +1402,23 @@ def linear_backward(grad_out, x, weight, *, pre=None, activation: Optional[str] 
     torch, L = _bind()
     if (pre is None) != (activation is None):
         raise SpconvError(1, "pre and its activation go together")
-    a, groups, c_out = _linear_args(x, weight, cu, activation)
-    gp, gr = _rows_tensor("grad_out", grad_out, x, torch.Size((x.shape[0], c_out)))
-    pp, pr = _NO_ROWS if pre is None else _rows_tensor("pre", pre, x, x.shape)
+    a, shape, c_out, bias_shape, dtype, device = _linear_args(x, weight, cu, activation)
+    gp, gr = _like_rows("grad_out", grad_out, torch.Size((shape[0], c_out)), dtype, device)
+    pp, pr = _NO_ROWS if pre is None else _like_rows("pre", pre, shape, dtype, device)
     xp, xr = _NO_ROWS
     if inputs:
         if grad_x is None:
             grad_x = torch.empty_like(x, memory_format=torch.contiguous_format)
-        xp, xr = _rows_tensor("grad_x", grad_x, x, x.shape)
+        xp, xr = _like_rows("grad_x", grad_x, shape, dtype, device)
     else:
         grad_x = None
     grad_weight = grad_bias = None
     wp = bp = 0
     if weights:
         grad_weight = x.new_empty(weight.shape, dtype=torch.float32)
-        grad_bias = x.new_empty((c_out,) if cu is None else (groups, c_out), dtype=torch.float32)
+        grad_bias = x.new_empty(bias_shape, dtype=torch.float32)
         wp, bp = grad_weight.data_ptr(), grad_bias.data_ptr()
-    _run(x.get_device(), L.spconv_linear_backward, a, _PACK_LINEAR_GRADIENTS.pack(gp, pp, xp, wp, bp, gr, pr, xr))
+    _run(device, L.spconv_linear_backward, a, _PACK_LINEAR_GRADIENTS.pack(gp, pp, xp, wp, bp, gr, pr, xr))
     return grad_x, grad_weight, grad_bias
 
 
@@ -1412,11 +1428,11 @@ def activation_backward(grad_out, pre, activation: Optional[str], *, out=None):
     once.  ``out``: a tensor to write, which may be grad_out."""
     torch, L = _bind()
     gp, gr = _rows_tensor("grad_out", grad_out)
-    pp, pr = _rows_tensor("pre", pre, grad_out, grad_out.shape)
+    shape, dtype, device = grad_out.shape, grad_out.dtype, grad_out.get_device()
+    pp, pr = _like_rows("pre", pre, shape, dtype, device)
     if out is None:
         out = torch.empty_like(grad_out, memory_format=torch.contiguous_format)
-    op, orow = _rows_tensor("out", out, grad_out, grad_out.shape)
-    rows, channels = grad_out.shape
-    _run(grad_out.get_device(), L.spconv_activation_backward, gp, gr, pp, pr, op, orow, rows, channels,
-         _activation_code(activation), _dtype_code(grad_out.dtype))
+    op, orow = _like_rows("out", out, shape, dtype, device)
+    _run(device, L.spconv_activation_backward, gp, gr, pp, pr, op, orow, shape[0], shape[1], _activation_code(activation),
+         _dtype_code(dtype))
     return out
