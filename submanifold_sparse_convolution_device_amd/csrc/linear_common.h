@@ -118,34 +118,39 @@ __device__ __forceinline__ float tail(float a, float e) {
 
 // act(z) and its derivative, of N values with one branch.  fp32 takes the
 // library's functions, whose errors are of fp32's size; 16-bit types the
-// unit's exponential and reciprocal.
+// unit's exponential and reciprocal.  An infinite z gives the limit, as a
+// stored product past fp16's range needs it: a factor z beside one that is 0
+// there is held finite, and a NaN stays one through the other.
+__device__ __forceinline__ float held(float z) { return __builtin_amdgcn_fmed3f(z, -1e30f, 1e30f); }
+
 template <class T>
 __device__ __forceinline__ float relu(float z) {
   return z <= 0.f ? 0.f : z;  // (a NaN stays)
 }
 template <class T>
 __device__ __forceinline__ float silu(float z) {
-  if constexpr (sizeof(T) == 4) return z / (1.f + expf(-z));
-  return z * sigmoid(z);
+  // (to -inf the value is -0; held on that side alone)
+  if constexpr (sizeof(T) == 4) return fmaxf(z, -1e30f) / (1.f + expf(-z));
+  return fmaxf(z, -1e30f) * sigmoid(z);
 }
 template <class T>
 __device__ __forceinline__ float gelu(float z) {
-  if constexpr (sizeof(T) == 4) return 0.5f * z * (1.f + erff(z * 0.70710678f));
-  // z - z t above 0, z t below
-  return relu<T>(z) - fabsf(z) * tail(fabsf(z), attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e))));
+  if constexpr (sizeof(T) == 4) return 0.5f * fmaxf(z, -1e30f) * (1.f + erff(z * 0.70710678f));
+  // z - z t above 0, z t below (a NaN comes from the second part)
+  return __builtin_amdgcn_fmed3f(z, 0.f, __builtin_inff()) - __builtin_amdgcn_fmed3f(fabsf(z), 0.f, 1e30f) * tail(fabsf(z), attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e))));
 }
 template <class T>
 __device__ __forceinline__ float silu_slope(float z) {
   const float s = sizeof(T) == 4 ? 1.f / (1.f + expf(-z)) : sigmoid(z);
-  return s * (1.f + z * (1.f - s));
+  return s * (1.f + held(z) * (1.f - s));
 }
 template <class T>
 __device__ __forceinline__ float gelu_slope(float z) {
   constexpr float inv_root = 0.3989422804014327f;  // 1 / sqrt(2 pi)
-  if constexpr (sizeof(T) == 4) return 0.5f * (1.f + erff(z * 0.70710678f)) + z * inv_root * expf(-0.5f * z * z);
+  if constexpr (sizeof(T) == 4) return 0.5f * (1.f + erff(z * 0.70710678f)) + held(z) * inv_root * expf(-0.5f * z * z);
   const float e = attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e)));
   const float t = tail(fabsf(z), e);
-  return (z < 0.f ? t : 1.f - t) + z * inv_root * e;
+  return (z < 0.f ? t : 1.f - t) + held(z) * inv_root * e;
 }
 // f(i) for i < N, 4 at a time: the registers of all N together do not fit.
 template <int N, class F>

@@ -1,5 +1,7 @@
 """Products of rows with their epilogue, over one batch and over groups, and
 their gradients, against the formulas in 64 bits."""
+import math
+
 import pytest
 import torch
 
@@ -300,6 +302,28 @@ def test_activation_backward(dtype, activation, rows, cols):
     assert bool(((s - diff).abs() < 1e-8)[away].all())
     same = grad.clone()
     assert sp.activation_backward(same, pre, activation, out=same) is same and torch.equal(same, got)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("activation,ends,slopes", [
+    ("relu", (0.0, math.inf), (0.0, 1.0)), ("silu", (0.0, math.inf), (0.0, 1.0)), ("gelu", (0.0, math.inf), (0.0, 1.0))])
+def test_activations_at_the_ends(dtype, activation, ends, slopes):
+    """Infinite and largest values take the activation's limits: a stored
+    product past fp16's range is infinite, its gradient is not NaN."""
+    dt = DTYPES[dtype]
+    far = torch.finfo(dt).max
+    pre = torch.tensor([-math.inf, -far, -1000.0, 1000.0, far, math.inf, math.nan], dtype=dt).cuda()
+    got = sp.activation_backward(torch.ones_like(pre)[None], pre[None], activation)[0].tolist()
+    assert got[:6] == [slopes[0]] * 3 + [slopes[1]] * 3
+    if activation != "relu":
+        assert math.isnan(got[6])
+    # an infinite sum in bf16 (the planes of fp32 hold no infinity, and fp16 products cannot reach one)
+    top = far if dt == torch.bfloat16 else 2.0 ** 15
+    x = torch.tensor([-top, -1000.0, 1000.0, top], dtype=dt).cuda()[:, None]
+    w = torch.tensor([[1.0, top if dt == torch.bfloat16 else 1.0]], dtype=dt).cuda()
+    out = sp.linear(x, w, activation=activation)
+    assert out[:2].abs().max().item() == ends[0]
+    assert out[2:, 0].tolist() == x[2:, 0].tolist() and out[3, 1].item() == (ends[1] if dt == torch.bfloat16 else top)
 
 
 def test_gradient_against_differences():
