@@ -228,7 +228,7 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
     p.shape = wide < 256 ? kFewShape : k <= 1024 ? kFewShortShape : kFewWideShape;
   } else {
     const int64_t medium = (rows / 128 + (cu == nullptr ? 1 : groups)) * div_up(n, 128);
-    p.shape = n <= (dtype == 0 ? 32 : 64) || medium < 256 ? kNarrowShape : kMediumShape;
+    p.shape = n <= 64 || medium < 256 ? kNarrowShape : kMediumShape;
   }
   if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 256 && div_up(rows, 256) * div_up(n, 256) >= 200) p.shape = kLargeShape;
   const ShapeSize s = shape_size(dtype, p.form, p.shape);
@@ -260,7 +260,8 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   Product p;
   p.form = kOverRows;
   p.dtype = dtype;
-  p.shape = n <= (dtype == 0 ? 32 : 64) ? kNarrowShape : kMediumShape;
+  const int64_t medium = div_up(m, 128) * div_up(n, 128);
+  p.shape = n <= 64 || medium * rows < (dtype == 0 ? 1 << 16 : 1 << 19) ? kNarrowShape : kMediumShape;
   if (dtype != 0 && p.shape == kMediumShape && m > 128 && n > 128 && div_up(m, 256) * div_up(n, 256) * (rows / 64) >= 32 * 256) p.shape = kLargeShape;
   const ShapeSize s = shape_size(dtype, p.form, p.shape);
   ProductArgs& a = p.a;

@@ -182,6 +182,17 @@ def test_parts_of_groups(dtype):
     _check_backward(x, w, _draw(dt, sum(lengths) + 77, 48, seed=12), cu=_offsets(lengths))
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,c_in,c_out", [(140011, 256, 200), (90011, 520, 500)])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_tiles_of_large_sums(dtype, rows, c_in, c_out, grouped):
+    """Weight gradients whose sums go by the larger tiles."""
+    dt = DTYPES[dtype]
+    lengths = [rows - 40010, 0, 9, 40000]
+    x, w, _ = _case(dt, rows, c_in, c_out, 13, len(lengths) if grouped else None)
+    _check_backward(x, w, _draw(dt, rows, c_out, seed=14), cu=_offsets(lengths) if grouped else None)
+
+
 def test_fp32_is_whole():
     """The rms error of fp32 products: additions leave about sqrt(k) / 2^25 of
     the result's rms, 2^-20 at k = 1024, and twice that is allowed; operands
