@@ -230,7 +230,8 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
     const int64_t medium = (rows / 128 + (cu == nullptr ? 1 : groups)) * div_up(n, 128);
     p.shape = n <= 64 || medium < 256 ? kNarrowShape : kMediumShape;
   }
-  if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 256 && div_up(rows, 256) * div_up(n, 256) >= 200) p.shape = kLargeShape;
+  const int64_t large = div_up(rows, 256) * div_up(n, 256);
+  if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 256 && 4 * large >= 3 * 256 * div_up(large, 256)) p.shape = kLargeShape;
   const ShapeSize s = shape_size(dtype, p.form, p.shape);
   ProductArgs& a = p.a;
   a.cu = cu;
@@ -245,7 +246,7 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
   int64_t splits = 1;
   if (each <= 128) {
     if (blocks * 2 <= 256) splits = std::max<int64_t>(1, std::min(256 / blocks, steps));
-  } else if (blocks * 2 <= kFill && steps >= 8) {
+  } else if (p.shape != kLargeShape && blocks * 2 <= kFill && steps >= 8) {
     splits = std::min(kFill / blocks, steps / 4);
   }
   a.k_split = static_cast<int32_t>(div_up(steps, splits) * s.bk);
@@ -253,6 +254,29 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
   a.n_part = padded(n);
   if (a.splits > 1) a.part = static_cast<float*>(w->take(static_cast<size_t>(a.splits) * rows * a.n_part * sizeof(float)));
   return p;
+}
+
+// Rows at the start of a dense product that go by whole rounds of the largest
+// tiles, where all of them together would leave most of the last round's CUs
+// without one (0: the product is one launch).
+int32_t whole_rounds(int dtype, const int32_t* cu, int32_t rows, int32_t k, int32_t n) {
+  const int64_t columns = div_up(n, 256), large = div_up(rows, 256) * columns;
+  if (dtype == 0 || cu != nullptr || k < 512 || n < 256 || large <= 256 || 4 * large >= 3 * 256 * div_up(large, 256)) return 0;
+  return static_cast<int32_t>(large / 256 * 256 / columns * 256);
+}
+
+// A product by rows: one launch, or the whole rounds and the rows after them.
+struct ByRows {
+  Product p, rest;
+  int32_t head;
+  uint64_t items() const { return head == 0 ? p.items() : std::max(p.items(), rest.items()); }
+};
+ByRows plan_all_rows(ProductForm form, int dtype, const int32_t* cu, int32_t rows, int32_t groups, int32_t k, int32_t n, Carver* w) {
+  ByRows b;
+  b.head = whole_rounds(dtype, cu, rows, k, n);
+  b.p = plan_by_rows(form, dtype, cu, b.head == 0 ? rows : b.head, groups, k, n, w);
+  if (b.head != 0) b.rest = plan_by_rows(form, dtype, cu, rows - b.head, groups, k, n, w);
+  return b;
 }
 
 // Sizes of a product over the rows of each group: m x n sums.
@@ -330,9 +354,37 @@ bool whole_rows(const void* p, int64_t row_stride, int64_t cols, int dtype) {
   return p == nullptr || (aligned(p) && whole_pieces(row_stride, dtype) && cols % 8 == 0);
 }
 
+// (b.p.a holds the operands and the epilogue of all rows)
+hipError_t run_all_rows(ByRows& b, hipStream_t stream) {
+  const hipError_t e = run_by_rows(b.p, stream);
+  if (e != hipSuccess || b.head == 0) return e;
+  const ProductArgs& all = b.p.a;
+  ProductArgs& a = b.rest.a;
+  const int64_t size = size_of(b.p.dtype);
+  auto after = [&](const void* p, int64_t row) { return p == nullptr ? nullptr : static_cast<const char*>(p) + b.head * row * size; };
+  auto out_after = [&](void* p, int64_t row) { return p == nullptr ? nullptr : static_cast<char*>(p) + b.head * row * size; };
+  a.a = after(all.a, all.a_row);
+  a.a_row = all.a_row;
+  a.a_cols = all.a_cols;
+  a.b = all.b;
+  a.b_row = all.b_row;
+  a.b_cols = all.b_cols;
+  a.b_group = all.b_group;
+  a.bias = all.bias;
+  a.side = after(all.side, all.side_row);
+  a.side_row = all.side_row;
+  a.pre = out_after(all.pre, all.pre_row);
+  a.pre_row = all.pre_row;
+  a.out = out_after(all.out, all.out_row);
+  a.out_row = all.out_row;
+  a.act = all.act;
+  a.whole = all.whole;
+  return run_by_rows(b.rest, stream);
+}
+
 struct Forward {
   Operand x, w;
-  Product p;
+  ByRows p;
   size_t bytes;
 };
 Forward plan_forward(const LinearArgs& a, void* workspace) {
@@ -340,14 +392,15 @@ Forward plan_forward(const LinearArgs& a, void* workspace) {
   Carver c{static_cast<char*>(workspace)};
   f.x = operand(a.x, a.x_row, a.rows, a.c_in, a.dtype, &c);
   f.w = operand(a.weight, a.c_out, static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.dtype, &c);
-  f.p = plan_by_rows(kByRows, a.dtype, a.cu, a.rows, a.groups, a.c_in, a.c_out, &c);
+  f.p = plan_all_rows(kByRows, a.dtype, a.cu, a.rows, a.groups, a.c_in, a.c_out, &c);
   f.bytes = c.at;
   return f;
 }
 
 struct Backward {
   Operand x, w, g;
-  Product gx, gw;
+  ByRows gx;
+  Product gw;
   size_t bytes;
 };
 Backward plan_backward(const LinearArgs& a, void* workspace) {
@@ -358,7 +411,7 @@ Backward plan_backward(const LinearArgs& a, void* workspace) {
   b.w = operand(a.weight, a.c_out, static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.dtype, &c);
   // (the two products run one after the other: their parts may share a place)
   Carver c1 = c, c2 = c;
-  b.gx = plan_by_rows(kByRowsT, a.dtype, a.cu, a.rows, a.groups, a.c_out, a.c_in, &c1);
+  b.gx = plan_all_rows(kByRowsT, a.dtype, a.cu, a.rows, a.groups, a.c_out, a.c_in, &c1);
   b.gw = plan_over_rows(a.dtype, a.cu, a.rows, a.groups, a.c_in, a.c_out, &c2);
   b.bytes = std::max(c1.at, c2.at);
   return b;
@@ -384,7 +437,7 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t strea
   hipError_t e = lay_out(f.x, a.x, a.x_row, a.rows, a.c_in, a.dtype, stream);
   if (e == hipSuccess) e = lay_out(f.w, a.weight, a.c_out, static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.dtype, stream);
   if (e != hipSuccess) return e;
-  ProductArgs& p = f.p.a;
+  ProductArgs& p = f.p.p.a;
   p.a = f.x.p;
   p.a_row = f.x.row;
   p.a_cols = f.x.cols;
@@ -402,7 +455,7 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t strea
   p.act = a.act;
   p.whole = whole_rows(a.out, a.out_row, a.c_out, a.dtype) && whole_rows(a.pre, a.pre_row, a.c_out, a.dtype) &&
             whole_rows(a.residual, a.residual_row, a.c_out, a.dtype) && whole_rows(a.bias, a.c_out, a.c_out, a.dtype);
-  return run_by_rows(f.p, stream);
+  return run_all_rows(f.p, stream);
 }
 
 hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, hipStream_t stream) {
@@ -412,7 +465,7 @@ hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, hipStrea
   if (e == hipSuccess && a.grad_x != nullptr) e = lay_out(b.w, a.weight, a.c_out, static_cast<int64_t>(a.groups) * a.c_in, a.c_out, a.dtype, stream);
   if (e != hipSuccess) return e;
   if (a.grad_x != nullptr) {
-    ProductArgs& p = b.gx.a;
+    ProductArgs& p = b.gx.p.a;
     p.a = b.g.p;
     p.a_row = b.g.row;
     p.a_cols = b.g.cols;
@@ -426,7 +479,7 @@ hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, hipStrea
     p.out = a.grad_x;
     p.out_row = a.grad_x_row;
     p.whole = whole_rows(a.grad_x, a.grad_x_row, a.c_in, a.dtype) && whole_rows(a.before, a.before_row, a.c_in, a.dtype);
-    e = run_by_rows(b.gx, stream);
+    e = run_all_rows(b.gx, stream);
     if (e != hipSuccess) return e;
   }
   if (a.grad_weight != nullptr) {

@@ -116,6 +116,19 @@ def test_large_tiles(dtype):
     _check_backward(x, w, _draw(dt, 12900, 1032, seed=2))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,c_out", [(13057, 1032), (13057, 1031), (13500, 1032)])
+def test_rows_after_whole_rounds(dtype, rows, c_out):
+    """One tile's rows more than the largest tiles take in one round."""
+    dt = DTYPES[dtype]
+    x, w, b = _case(dt, rows, 584, c_out, 8)
+    _check_forward(x, w, b, "gelu", _draw(dt, rows, c_out, seed=1))
+    x, w, _ = _case(dt, rows, c_out, 584, 8)
+    pre = x.clone()
+    _check_backward(x[:, :32].contiguous(), w[:32], _draw(dt, rows, 584, seed=2))
+    _check_backward(_draw(dt, rows, c_out, seed=3), w, _draw(dt, rows, 584, seed=4), pre=pre, activation="gelu")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_large_sums(dtype):
     """The weight gradient's largest tiles, and weights larger than a tile row."""
