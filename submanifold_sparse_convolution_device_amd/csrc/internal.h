@@ -376,6 +376,7 @@ struct ProductArgs {
   int32_t m = 0, n = 0, k = 0;  // by rows: n columns, k contracted; over rows: [m][n] sums
   FastDiv by_unit;               // rows of a slot: a tile's, or those of one part of a group
   int32_t slots = 0, tiles = 0, tiles_n = 0;  // tiles of the columns (by rows) or of the sums (over rows)
+  bool by_tiles = false;                      // over the rows of groups: a slot's tiles are spread over the XCDs, else the slots
   int32_t splits = 1, k_split = 0;            // parts of k (by rows) and k of each, a multiple of the step
   // parts: fp32 sums [split][rows][n_part] or [slot][m][n_part]; NULL: out is written
   float* part = nullptr;
@@ -392,6 +393,14 @@ struct ProductArgs {
   float* sums = nullptr;
   float* sums_part = nullptr;
 };
+
+// Workgroups of a product (but one with its weights in registers).
+inline int64_t product_blocks(const ProductArgs& a, ProductForm form) {
+  const int64_t slots = a.slots, tiles = a.tiles;
+  if (form != kOverRows) return slots * tiles * a.splits;
+  if (a.cu == nullptr) return slots * tiles;
+  return a.by_tiles ? slots * ((tiles + 7) / 8 * 8) : (slots + 7) / 8 * 8 * tiles;
+}
 
 // Workgroup shapes: rows x columns of a tile (linear_kernels.h).
 enum ProductShape { kFewShape, kFewWideShape, kFewShortShape, kNarrowShape, kMediumShape, kLargeShape, kStreamShape };

@@ -212,8 +212,7 @@ struct Product {
   ProductShape shape;
   int dtype;
   uint64_t items() const {
-    const uint64_t blocks = static_cast<uint64_t>(a.slots) * static_cast<uint64_t>(a.tiles) * (form == kOverRows ? 1 : a.splits);
-    return blocks * shape_size(dtype, form, shape).threads;
+    return static_cast<uint64_t>(product_blocks(a, form)) * shape_size(dtype, form, shape).threads;
   }
 };
 
@@ -297,14 +296,17 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   a.tiles_n = static_cast<int32_t>(div_up(n, s.bn));
   a.tiles = static_cast<int32_t>(div_up(m, s.bm) * a.tiles_n);
   a.n_part = padded(n);
-  const int64_t parts = std::min<int64_t>((p.shape == kLargeShape ? 256 : kFill) / a.tiles, rows / 128);
+  const int64_t fill = (p.shape == kLargeShape ? 256 : kFill) / a.tiles;
+  const int64_t parts = std::min<int64_t>(cu != nullptr && 4 * groups <= fill ? fill - groups : fill, rows / 128);
   if (parts <= 1 || parts <= groups) {  // every group is one part
     a.by_unit = make_fast_div(1 << 30);
     a.slots = cu == nullptr ? 1 : groups + 2;
+    a.by_tiles = a.tiles >= 8;
   } else {
     const int64_t unit = div_up(div_up(rows, parts), s.bk) * s.bk;
     a.by_unit = make_fast_div(static_cast<int32_t>(unit));
     a.slots = static_cast<int32_t>(cu == nullptr ? div_up(rows, unit) : rows / unit + groups + 2);
+    a.by_tiles = a.tiles >= 32;
     a.part = static_cast<float*>(w->take(static_cast<size_t>(a.slots) * m * a.n_part * sizeof(float)));
     a.sums_part = static_cast<float*>(w->take(static_cast<size_t>(a.slots) * a.n_part * sizeof(float)));
   }

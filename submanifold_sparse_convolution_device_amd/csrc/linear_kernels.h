@@ -146,14 +146,24 @@ __global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
 
   // Consecutive workgroups go to the 8 XCDs in turn; each XCD takes a
   // consecutive eighth of the tiles, so that tiles that share rows or weights
-  // share its L2.
+  // share its L2.  Over groups, whose lengths may differ by any factor, an
+  // eighth of them could be nearly all of the work: there every group's sums
+  // are spread over the XCDs, by their tiles or by the group's parts.
   const int total = gridDim.x, eighth = total / 8, over = total % 8;
   const int xcd = blockIdx.x % 8;
   int at = blockIdx.x / 8 + xcd * eighth + min(xcd, over);
   int slot, m0, n0, k0 = 0, k1, split = 0;
   if constexpr (FORM == kOverRows) {
-    slot = at / a.tiles;
-    const int tile = at - slot * a.tiles;
+    int tile;
+    if (a.cu == nullptr) {
+      slot = at / a.tiles;
+      tile = at - slot * a.tiles;
+    } else {
+      const int j = blockIdx.x / 8, run = a.by_tiles ? (a.tiles + 7) / 8 : a.tiles, nth = j / run;
+      slot = a.by_tiles ? nth : 8 * nth + xcd;
+      tile = j - nth * run + (a.by_tiles ? xcd * run : 0);
+      if (slot >= a.slots || tile >= a.tiles) return;
+    }
     m0 = tile / a.tiles_n * S::BM;
     n0 = tile % a.tiles_n * S::BN;
   } else {
@@ -713,7 +723,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_few(ProductArgs a) {
 // ---- Launches ----
 template <class T, class S, int FORM>
 hipError_t launch_shape(const ProductArgs& a, hipStream_t stream) {
-  const int64_t blocks = static_cast<int64_t>(a.slots) * a.tiles * (FORM == kOverRows ? 1 : a.splits);
+  const int64_t blocks = product_blocks(a, static_cast<ProductForm>(FORM));
   if (blocks == 0) return hipSuccess;
   k_product<T, S, FORM><<<static_cast<unsigned>(blocks), S::NT, 0, stream>>>(a);
   return hipGetLastError();
@@ -766,7 +776,7 @@ hipError_t launch_typed(const ProductArgs& a, ProductForm form, ProductShape sha
   if (shape == kFewShape || shape == kFewWideShape || shape == kFewShortShape) {
     auto few = [&](auto cb, auto waves) -> hipError_t {
       constexpr int CB = decltype(cb)::value, WAVES = decltype(waves)::value;
-      const int64_t blocks = static_cast<int64_t>(a.slots) * a.tiles * a.splits;
+      const int64_t blocks = product_blocks(a, form);
       if (form == kByRows) k_few<T, CB, WAVES, kByRows><<<static_cast<unsigned>(blocks), 64 * WAVES, 0, stream>>>(a);
       else k_few<T, CB, WAVES, kByRowsT><<<static_cast<unsigned>(blocks), 64 * WAVES, 0, stream>>>(a);
       return hipGetLastError();

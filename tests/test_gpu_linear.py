@@ -206,6 +206,17 @@ def test_tiles_of_large_sums(dtype, rows, c_in, c_out, grouped):
     _check_backward(x, w, _draw(dt, rows, c_out, seed=14), cu=_offsets(lengths) if grouped else None)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("lengths", [[1, 0, 700, 3, 90, 0, 0, 2, 400], [0, 1, 5800, 199], [5000, 0, 1000]])
+def test_many_tiles_of_groups(dtype, lengths):
+    """Weight gradients of many tiles a group, lengths far apart: one part a
+    group, and several."""
+    dt = DTYPES[dtype]
+    rows = sum(lengths) + 21
+    x, w, _ = _case(dt, rows, 1000, 328, 15, len(lengths))
+    _check_backward(x, w, _draw(dt, rows, 328, seed=16), cu=_offsets(lengths, 17))
+
+
 def test_fp32_is_whole():
     """The rms error of fp32 products: additions leave about sqrt(k) / 2^25 of
     the result's rms, 2^-20 at k = 1024, and twice that is allowed; operands
