@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256) void k_join_rows(ProductArgs a) {
 // rows gives zeros.  Row m of the sums is the column sums of b.  4 columns a
 // thread, LANES threads for them that take the parts in turn and join in LDS:
 // hundreds of parts of small sums would be a long chain of loads for one
-// (512 parts of 64 x 64: 22 us, with 16 lanes JOINUS).
+// (512 parts of 64 x 64 in bf16: 22 us, with 16 lanes 5.7).
 template <int LANES>
 __global__ __launch_bounds__(256) void k_join_groups(ProductArgs a) {
   constexpr int QUADS = 256 / LANES;
@@ -217,6 +217,22 @@ struct Product {
 };
 
 // Sizes of a product by rows: rows x k times k x n of each group.
+//
+// Groups of 128 rows at most on average go by independent wavefronts (k_few):
+// their time is that of the weights' way from memory, and tiles of 128 rows
+// would have few workgroups and a barrier a step (bf16: 5 rows 2048 -> 8192
+// 13.3 us by tiles, 10.2; 100 rows 256 -> 4096 9.3 and 5.8; 64 rows 1024 ->
+// 1024 10.6 and 8.5).  32 columns a workgroup while 64 would leave CUs
+// without one; 4 wavefronts where the contraction gives 8 of them two chunks
+// or fewer (32 groups of 64 rows 512 -> 1024: 10.4 us, with 8 13.6), 8 for
+// the others (16 rows 512 -> 2048: 4.2, with 4 6.4).
+//
+// More rows go by tiles.  Narrow ones for up to 64 columns (f32, 80,000 rows
+// 256 -> 64: 42 us by 128 columns, 31) and while tiles of 128 columns are
+// fewer than CUs (bf16: 3,000 rows 1024 -> 1024 29.5 and 20.7).  The largest
+// where they fill three quarters of their rounds of one workgroup a CU
+// (8192 x 4096 x 4096: 250 us, by 128 x 128 322; 9,000 rows, half of the last
+// round: 342 and 352; 6,000 rows: 224 and 236; 5,000 rows: 223 and 205).
 Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t rows, int32_t groups, int32_t k, int32_t n, Carver* w) {
   Product p;
   p.form = form;
@@ -242,6 +258,12 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
   a.slots = static_cast<int32_t>(cu == nullptr ? div_up(rows, s.bm) : rows / s.bm + groups + 2);
   a.tiles = a.tiles_n = static_cast<int32_t>(div_up(n, s.bn));
   const int64_t steps = div_up(k, s.bk), blocks = std::max<int64_t>(1, static_cast<int64_t>(a.slots) * a.tiles);
+  // Parts of the contraction, where the tiles alone leave CUs without work:
+  // up to 256 workgroups of few rows (1 row in f32, 2048 -> 264: 9.4 us with
+  // half as many, 8.7; grad_x of 5 rows 2048 -> 8192 16.9 and 13.6); up to two
+  // on a CU of tiles, parts of four steps at least.  Never of the largest
+  // tiles, of which one fills a CU (65,536 rows 1024 -> 256 in two parts 90
+  // us, whole 44).
   int64_t splits = 1;
   if (each <= 128) {
     if (blocks * 2 <= 256) splits = std::max<int64_t>(1, std::min(256 / blocks, steps));
@@ -257,7 +279,8 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
 
 // Rows at the start of a dense product that go by whole rounds of the largest
 // tiles, where all of them together would leave most of the last round's CUs
-// without one (0: the product is one launch).
+// without one (0: the product is one launch).  (bf16: 65,537 rows 1024 -> 256
+// 60 us by smaller tiles, 55 in two launches; 4097 x 4096 x 4096 194 and 140.)
 int32_t whole_rounds(int dtype, const int32_t* cu, int32_t rows, int32_t k, int32_t n) {
   const int64_t columns = div_up(n, 256), large = div_up(rows, 256) * columns;
   if (dtype == 0 || cu != nullptr || k < 512 || n < 256 || large <= 256 || 4 * large >= 3 * 256 * div_up(large, 256)) return 0;
@@ -279,6 +302,13 @@ ByRows plan_all_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
 }
 
 // Sizes of a product over the rows of each group: m x n sums.
+//
+// Narrow tiles for up to 64 columns, and while the sum is short: more tiles
+// make for fewer parts to join (bf16, 256 x 256 sums: 100,000 rows 39 us by
+// 128 columns, 33; 1024 x 1024: 2,500 rows 28.9 and 24.2, 20,000 rows 64 and
+// 70; f32, 256 x 256: 2,500 rows 19.0 and 14.9, 20,000 rows 33 and 33, 80,000
+// rows 73 and 109).  The largest for long sums (400,000 rows of 256 x 1024:
+// 310 us by 128 x 128, 266; but 65,537 rows of 1024 x 256 60 and 66).
 Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t groups, int32_t m, int32_t n, Carver* w) {
   Product p;
   p.form = kOverRows;
@@ -296,16 +326,23 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   a.tiles_n = static_cast<int32_t>(div_up(n, s.bn));
   a.tiles = static_cast<int32_t>(div_up(m, s.bm) * a.tiles_n);
   a.n_part = padded(n);
+  // Parts of 128 rows at least (f32, 20,011 rows of 128 x 192: 28.2 us, with
+  // 256 31.4).  A group may end in a part of few rows: room for one each, that
+  // all parts run in one round (16 groups of 12,500 rows of 512 x 512: 162 us,
+  // without it 223).
   const int64_t fill = (p.shape == kLargeShape ? 256 : kFill) / a.tiles;
   const int64_t parts = std::min<int64_t>(cu != nullptr && 4 * groups <= fill ? fill - groups : fill, rows / 128);
   if (parts <= 1 || parts <= groups) {  // every group is one part
     a.by_unit = make_fast_div(1 << 30);
     a.slots = cu == nullptr ? 1 : groups + 2;
-    a.by_tiles = a.tiles >= 8;
+    a.by_tiles = a.tiles >= 8;  // (16 groups of 3600 x 1304, the last with a fifth of 18,540 rows: 630 us in eighths, 327)
   } else {
     const int64_t unit = div_up(div_up(rows, parts), s.bk) * s.bk;
     a.by_unit = make_fast_div(static_cast<int32_t>(unit));
     a.slots = static_cast<int32_t>(cu == nullptr ? div_up(rows, unit) : rows / unit + groups + 2);
+    // (a part's tiles share rows: spread only where many do.  8 groups of 2,500
+    // rows of 512 x 1024: 61 us by parts, 49 by tiles; 4 groups of 25,000 rows
+    // of 512 x 512: 79 and 106)
     a.by_tiles = a.tiles >= 32;
     a.part = static_cast<float*>(w->take(static_cast<size_t>(a.slots) * m * a.n_part * sizeof(float)));
     a.sums_part = static_cast<float*>(w->take(static_cast<size_t>(a.slots) * a.n_part * sizeof(float)));
@@ -327,7 +364,10 @@ hipError_t run_product(const Product& p, hipStream_t stream) {
   return launch_product_bf16(p.a, p.form, p.shape, stream);
 }
 
-// Whether a product keeps its weights in registers.
+// Whether a product keeps its weights in registers: the contraction fits them,
+// and the columns fill a workgroup's (bf16, against tiles: 400,000 rows 256 ->
+// 1024 293 us and 562, 128 -> 128 36 and 52, 64 -> 64 21 and 28; f32, 100,000
+// rows 128 -> 256 46 and 68).
 bool streams(const Product& p) {
   const ProductArgs& a = p.a;
   if (!a.whole || a.splits > 1 || p.shape == kFewShape || p.shape == kFewWideShape || p.shape == kFewShortShape) return false;

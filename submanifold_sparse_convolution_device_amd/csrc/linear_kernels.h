@@ -15,6 +15,14 @@
 // next step's loads are in flight during this step's products.  fp32 operands
 // go into LDS as three bf16 planes (attention_common.h).
 //
+// Bound by the matrix cores where sums are long: 8192 x 4096 x 4096 at 1.0 to
+// 1.1 PFLOP/s (f16: 275 us by rows, 262 transposed, 264 over rows), as the
+// chip's power holds its clock (about 2 GHz) under such products: they are
+// issued in 48% of the cycles, LDS is busy in 33%.  Writing the next step's
+// tiles between the products rather than after them took 291 us to 275 there;
+// two steps of loads in flight, halves of a workgroup in opposite phases and
+// the epilogue between the next tile's products were no faster or slower.
+//
 // The products run as C^T = B^T A^T, so a lane holds 4 neighbouring columns of
 // one row; the sums pass through the wavefront's own LDS into whole rows, 8
 // columns a lane, for the epilogue (finish8) and 16-byte accesses.
@@ -395,6 +403,10 @@ __global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
 // barrier.  The sums go to memory straight from the registers: an exchange
 // between the halves of a wavefront gives each lane 8 neighbouring columns of
 // a row.  OCC: wavefronts on a SIMD.
+//
+// Bound by memory and, with an activation, by the vector units: 400,000 rows
+// 256 -> 1024 in bf16 are 1.02 GB, 293 to 327 us (3.1 to 3.5 TB/s); gelu's 20 or so vector
+// cycles an element beside the products make it 435 us.
 template <int KS_, int WR_, int WC_, int RW_, int OCC_>
 struct StreamShape {
   static constexpr int KS = KS_, WR = WR_, WC = WC_, RW = RW_, OCC = OCC_;
@@ -530,7 +542,7 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_stream(ProductArgs a, int chu
         for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
     }
     if (in_group) {
-            constexpr int AHEAD = RW == 2 ? 2 : 3;  // operands on their way from LDS
+      constexpr int AHEAD = RW == 2 ? 2 : 3;  // operands on their way from LDS
       Frag<T> fa[KS][RW];
       auto read = [&](int t) {
 #pragma unroll
@@ -601,12 +613,14 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_stream(ProductArgs a, int chu
 }
 
 // ---- Few rows ----
-// By rows with up to 32 rows of a group: a workgroup computes 32 rows by 32 CB
+// By rows with up to 128 rows of a group: a workgroup computes 32 rows by 32 CB
 // columns, and its 8 wavefronts take chunks of KC contracted values in turn,
 // each by itself: the rows' operands come straight from memory, the weights'
 // through the wavefront's own LDS (transposed) or straight, the next chunk's
 // loads in flight during a chunk.  No wavefront waits for another before the
-// sums of all 8 are joined in LDS.
+// sums of all 8 are joined in LDS.  Bound by the weights' way from memory:
+// 5 rows 2048 -> 8192 in bf16 are 34 MB, 9.4 us (3.6 TB/s, a launch and the
+// join within it).
 template <class T, int CB, int WAVES_, int FORM>
 struct Few {
   static constexpr int KC = sizeof(T) == 4 ? 32 : 64, WAVES = WAVES_;
@@ -744,6 +758,12 @@ hipError_t launch_stream(ProductArgs a, hipStream_t stream) {
   k_stream<T, S, FORM><<<static_cast<unsigned>(blocks), S::NT, 0, stream>>>(a, chunks, per);
   return hipGetLastError();
 }
+// The shape by the columns there are, so that few are computed in vain
+// (400,000 rows in bf16, 256 -> 64: 44 us by 64 columns, 52 by 128; 256 ->
+// 128: 61 by 128, 80 by 256), then by the registers that the weights leave:
+// two row blocks a wavefront for the longest contraction, with two wavefronts
+// on a SIMD (256 -> 1024: 327 us, by one block 365).  f32, as three planes,
+// has registers for 128 columns (200,000 rows 128 -> 256: 94 us, by 64 125).
 template <class T, int FORM>
 hipError_t launch_stream_sized(const ProductArgs& a, hipStream_t stream) {
   if constexpr (sizeof(T) == 4) {
