@@ -217,6 +217,19 @@ def test_many_tiles_of_groups(dtype, lengths):
     _check_backward(x, w, _draw(dt, rows, 328, seed=16), cu=_offsets(lengths, 17))
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,c_in,c_out,lengths", [
+    (37, 4104, 4096, None), (128, 2048, 2056, None), (128, 3000, 2056, None), (40, 4096, 264, [3, 0, 37]),
+    (5120, 1032, 512, [40] * 128), (2000, 512, 1032, [0, 900, 1, 1000, 0, 0] + [3] * 33), (700, 2048, 512, [20] * 35)])
+def test_rows_by_wavefronts_or_tiles(dtype, rows, c_in, c_out, lengths):
+    """Both sides of the choice for few rows of a group."""
+    dt = DTYPES[dtype]
+    cu = None if lengths is None else _offsets(lengths)
+    x, w, b = _case(dt, rows, c_in, c_out, 17, None if lengths is None else len(lengths))
+    _check_forward(x, w, b, "silu", _draw(dt, rows, c_out, seed=1), cu)
+    _check_backward(x, w, _draw(dt, rows, c_out, seed=2), _draw(dt, rows, c_in, seed=3), "relu", cu)
+
+
 def test_fp32_is_whole():
     """The rms error of fp32 products: additions leave about sqrt(k) / 2^25 of
     the result's rms, 2^-20 at k = 1024, and twice that is allowed; operands
