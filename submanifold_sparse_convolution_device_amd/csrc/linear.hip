@@ -244,10 +244,11 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
   Product p;
   p.form = form;
   p.dtype = dtype;
-  const int64_t each = rows / groups, products = static_cast<int64_t>(rows) * k * n;
+  const int64_t each = rows / groups;
+  const double products = static_cast<double>(rows) * k * n;
   const bool transposed16 = dtype != 0 && form == kByRowsT;
   const int most = transposed16 || (dtype != 0 && cu == nullptr && k > 1024) ? (cu == nullptr ? 29 : 28) : 30;
-  const bool few = each <= (transposed16 ? 16 : 32) || (each <= 128 && products <= int64_t(1) << most);
+  const bool few = each <= (transposed16 ? 16 : 32) || (each <= 128 && products <= static_cast<double>(1 << most));
   if (few) {
     const int64_t wide = (rows / 32 + groups) * div_up(n, 64);  // workgroups of 64 columns
     p.shape = wide < 256 ? kFewShape : k <= 1024 ? kFewShortShape : kFewWideShape;

@@ -129,6 +129,28 @@ def test_rows_after_whole_rounds(dtype, rows, c_out):
     _check_backward(_draw(dt, rows, c_out, seed=3), w, _draw(dt, rows, 584, seed=4), pre=pre, activation="gelu")
 
 
+def test_rows_after_whole_rounds_in_place():
+    """The same with strided rows, the residual in its place, and captured."""
+    dt, rows, c_in, c_out = torch.bfloat16, 13061, 1536, 1032
+    x = _draw(dt, rows, c_in + 24, seed=1)[:, 16:16 + c_in]
+    _, w, b = _case(dt, 8, c_in, c_out, 18)
+    wide = _draw(dt, rows, c_out + 40, seed=2)
+    kept = wide.clone()
+    residual = wide[:, 32:32 + c_out]
+    first = _check_forward(x, w, b, "gelu", residual, out=residual).clone()
+    assert torch.equal(wide[:, :32], kept[:, :32]) and torch.equal(wide[:, 32 + c_out:], kept[:, 32 + c_out:])
+    before = kept[:, 32:32 + c_out].contiguous()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        made = sp.linear(x, w, b, activation="gelu", residual=before)
+    for turn in range(3):
+        made.zero_()
+        sp.linear(_draw(dt, 40, 8192, seed=turn), _draw(dt, 8192, 264, seed=9))  # (the stream's workspace in other hands)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(made, first)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_large_sums(dtype):
     """The weight gradient's largest tiles, and weights larger than a tile row."""
