@@ -791,6 +791,7 @@ spconv_status spconv_add_norm_backward_noalloc(const spconv_add_norm* args, cons
  * infinity among them gives NaN).  The epilogue is fp32 and each output is
  * rounded once.  GELU is z times the normal distribution's integral (the
  * error function's form), SILU is z / (1 + exp(-z)); RELU has slope 0 at 0.
+ * At infinite z an activation and its slope take their limits.
  * Every sum has a fixed order: the same call gives the same bits.
  */
 typedef SPCONV_ENUM(spconv_activation) {

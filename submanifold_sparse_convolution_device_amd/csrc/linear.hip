@@ -222,15 +222,13 @@ struct Product {
 // rows would have few workgroups and a barrier a step (bf16: 5 rows 2048 ->
 // 8192 13.3 us by tiles, 10.2; 100 rows 256 -> 4096 9.3 and 5.8; 64 rows 1024
 // -> 1024 10.6 and 8.5).  Every 32 rows read the weights anew, from L2, so up
-// to 32 rows of a group on average (16 for 16-bit rows by transposed weights,
-// read piece by piece), or up to 128 in products small enough that the
-// barriers cost more (bf16, groups of 1024 -> 1024: 8 of 80 rows 12.8 us by
-// wavefronts, 17.5 by tiles; 32 of 80 rows 28.8 and 24.7, 128 of 120 135 and
-// 107; transposed, 8 of 40 rows 15.9 and 16.2, 8 of 80 19.2 and 16.7, 128 of
-// 120 265 and 101; one group: 120 rows 2048 -> 2048 11.9 and 15.3, 40 rows
-// 4096 -> 4096 19.4 and 17.6; f32, 256 -> 512: 32 groups of 80 rows 17.4 and
-// 21.2, 128 groups 49 and 45).  32 columns a workgroup while 64 would leave CUs
-// without one; 4 wavefronts where the contraction gives 8 of them two chunks
+// to 32 rows of a group on average, or up to 128 in products small enough that
+// the barriers cost more (bf16, groups of 1024 -> 1024: 8 of 80 rows 11.4 us
+// by wavefronts, 17.5 by tiles; 32 of 40 rows 22.2 and 23.8, 32 of 120 29.9
+// and 25.4, 128 of 120 114 and 108, transposed 133 and 101; one group: 120
+// rows 2048 -> 2048 10.5 and 15.3, 40 rows 4096 -> 4096 19.4 and 17.6; f32,
+// 256 -> 512: 32 groups of 80 rows 17.4 and 21.2, 128 groups 49 and 45).  32
+// columns a workgroup while 64 would leave CUs without one; 4 wavefronts where the contraction gives 8 of them two chunks
 // or fewer (32 groups of 64 rows 512 -> 1024: 10.4 us, with 8 13.6), 8 for
 // the others (16 rows 512 -> 2048: 4.2, with 4 6.4).
 //
@@ -246,9 +244,8 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
   p.dtype = dtype;
   const int64_t each = rows / groups;
   const double products = static_cast<double>(rows) * k * n;
-  const bool transposed16 = dtype != 0 && form == kByRowsT;
-  const int most = transposed16 || (dtype != 0 && cu == nullptr && k > 1024) ? (cu == nullptr ? 29 : 28) : 30;
-  const bool few = each <= (transposed16 ? 16 : 32) || (each <= 128 && products <= static_cast<double>(1 << most));
+  const double most = dtype != 0 && cu == nullptr && k > 1024 ? 1 << 29 : 1 << 30;
+  const bool few = each <= 32 || (each <= 128 && products <= most);
   if (few) {
     const int64_t wide = (rows / 32 + groups) * div_up(n, 64);  // workgroups of 64 columns
     p.shape = wide < 256 ? kFewShape : k <= 1024 ? kFewShortShape : kFewWideShape;

@@ -615,17 +615,24 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_stream(ProductArgs a, int chu
 // ---- Few rows ----
 // By rows with up to 128 rows of a group: a workgroup computes 32 rows by 32 CB
 // columns, and its 8 wavefronts take chunks of KC contracted values in turn,
-// each by itself: the rows' operands come straight from memory, the weights'
-// through the wavefront's own LDS (transposed) or straight, the next chunk's
-// loads in flight during a chunk.  No wavefront waits for another before the
+// each by itself: both operands pass through the wavefront's own LDS, so that
+// its loads are of whole lines, with the next chunk's in flight during a
+// chunk (bf16, transposed: 128 groups of 20 rows 1024 -> 1024 46 us, 70 with
+// operands straight from memory, a line's quarter a lane; 8 groups of 80 rows
+// 11.7 and 18.9).  fp32 rows come straight, as their planes would take more of
+// LDS than the loads gain (32 groups of 20 rows 512 -> 256 13.4 us by LDS,
+// 11.3).  No wavefront waits for another before the
 // sums of all 8 are joined in LDS.  Bound by the weights' way from memory:
 // 5 rows 2048 -> 8192 in bf16 are 34 MB, 9.4 us (3.6 TB/s, a launch and the
 // join within it).
 template <class T, int CB, int WAVES_, int FORM>
 struct Few {
   static constexpr int KC = sizeof(T) == 4 ? 32 : 64, WAVES = WAVES_;
-  typedef Stage<T, KC, 4 * CB, 64> W;
-  static constexpr int kMine = FORM == kByRows ? KC * 4 * CB * kPlanes<T> : 0;  // a wavefront's weights
+  typedef std::conditional_t<FORM == kByRows, Stage<T, KC, 4 * CB, 64>, Stage<T, 32 * CB, KC / 8, 64>> W;
+  typedef Stage<T, 32, KC / 8, 64> A;
+  static constexpr bool kStageRows = sizeof(T) == 2;
+  static constexpr int kMineW = KC * 4 * CB * kPlanes<T>;                    // a wavefront's weights
+  static constexpr int kMine = kMineW + (kStageRows ? 32 * KC / 8 : 0);  // and its rows
   static constexpr int kStride = 32 * CB + 4;                                   // floats of a row of sums
   static constexpr int kLds = std::max(WAVES * kMine, WAVES * 32 * kStride / 4);
 };
@@ -648,24 +655,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_few(ProductArgs a) {
   const int k0 = split * a.k_split, k1 = seg.group < 0 ? k0 : min(a.k, k0 + a.k_split);
   const int a_end = k1 == a.k ? a.a_cols : k1, b_end = k1 == a.k ? a.b_cols : k1;  // (whole pieces)
 
-  const T* A0 = static_cast<const T*>(a.a) + (seg.lo + static_cast<int64_t>(lane & 31)) * a.a_row;
+  const T* A0 = static_cast<const T*>(a.a) + static_cast<int64_t>(seg.lo) * a.a_row;
   const T* B0 = static_cast<const T*>(a.b) + static_cast<int64_t>(max(seg.group, 0)) * a.b_group;
   const bool row_there = (lane & 31) < rows;
-  Raw<T> ra[STEPS], rb[FORM == kByRows ? 1 : STEPS][CB];
+  Raw<T> ra[F::kStageRows ? 1 : STEPS];
+  typename F::A rows_stage;
   typename F::W w;
   auto fetch = [&](int k) {
-#pragma unroll
-    for (int t = 0; t < STEPS; ++t) ra[t] = load_piece_of<T>(A0 + k + 16 * t + 8 * half, row_there, a_end - (k + 16 * t + 8 * half));
-    if constexpr (FORM == kByRows) {
-      w.load(B0 + static_cast<int64_t>(k) * a.b_row + n0, a.b_row, k1 - k, a.b_cols - n0, lane);
+    if constexpr (F::kStageRows) {
+      rows_stage.load(A0 + k, a.a_row, rows, a_end - k, lane);
     } else {
 #pragma unroll
       for (int t = 0; t < STEPS; ++t)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          const int n = n0 + 32 * c + (lane & 31);
-          rb[t][c] = load_piece_of<T>(B0 + static_cast<int64_t>(n) * a.b_row + k + 16 * t + 8 * half, n < a.n, b_end - (k + 16 * t + 8 * half));
-        }
+        ra[t] = load_piece_of<T>(A0 + (lane & 31) * a.a_row + k + 16 * t + 8 * half, row_there, a_end - (k + 16 * t + 8 * half));
+    }
+    if constexpr (FORM == kByRows) {
+      w.load(B0 + static_cast<int64_t>(k) * a.b_row + n0, a.b_row, k1 - k, a.b_cols - n0, lane);
+    } else {
+      w.load(B0 + static_cast<int64_t>(n0) * a.b_row + k, a.b_row, a.n - n0, b_end - k, lane);
     }
   };
   floatx16 acc[CB] = {};
@@ -674,22 +681,19 @@ __global__ __launch_bounds__(64 * WAVES) void k_few(ProductArgs a) {
   if (k < k1) fetch(k);
   while (k < k1) {
     Frag<T> fa[STEPS], fb[STEPS][CB];
+    wave_order();
+    w.template store<FORM != kByRows>(mine, lane);
+    if constexpr (F::kStageRows) rows_stage.template store<true>(mine + F::kMineW, lane);
+    wave_order();
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t) fa[t] = attn::to_frag<T>(ra[t]);
-    if constexpr (FORM == kByRows) {
-      wave_order();
-      w.template store<false>(mine, lane);
-      wave_order();
-#pragma unroll
-      for (int t = 0; t < STEPS; ++t)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) fb[t][c] = F::W::template frag<false>(mine, 32 * c, t, lane);
-    } else {
-#pragma unroll
-      for (int t = 0; t < STEPS; ++t)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) fb[t][c] = attn::to_frag<T>(rb[t][c]);
+    for (int t = 0; t < STEPS; ++t) {
+      if constexpr (F::kStageRows) fa[t] = F::A::template frag<true>(mine + F::kMineW, 0, t, lane);
+      else fa[t] = attn::to_frag<T>(ra[t]);
     }
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+      for (int c = 0; c < CB; ++c) fb[t][c] = F::W::template frag<FORM != kByRows>(mine, 32 * c, t, lane);
     k += KC * F::WAVES;
     if (k < k1) fetch(k);
     __builtin_amdgcn_sched_barrier(0);
