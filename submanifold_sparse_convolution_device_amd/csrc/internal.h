@@ -403,7 +403,7 @@ inline int64_t product_blocks(const ProductArgs& a, ProductForm form) {
 }
 
 // Workgroup shapes: rows x columns of a tile (linear_kernels.h).
-enum ProductShape { kFewShape, kFewWideShape, kFewShortShape, kNarrowShape, kMediumShape, kLargeShape, kStreamShape };
+enum ProductShape { kFewShape, kFewWideShape, kFewShortShape, kNarrowShape, kHalfShape, kMediumShape, kLargeShape, kStreamShape };
 hipError_t launch_product_f32(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
 hipError_t launch_product_f16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);
 hipError_t launch_product_bf16(const ProductArgs& a, ProductForm form, ProductShape shape, hipStream_t stream);

@@ -196,7 +196,7 @@ ShapeSize shape_size(int dtype, ProductForm form, ProductShape s) {
   auto of = [](auto x) { return ShapeSize{decltype(x)::BM, decltype(x)::BN, decltype(x)::BK, decltype(x)::NT}; };
   auto by_shape = [&](auto shapes) {
     typedef decltype(shapes) S;
-    return s == kNarrowShape ? of(typename S::Narrow{}) : s == kMediumShape ? of(typename S::Medium{}) : of(typename S::Large{});
+    return s == kNarrowShape ? of(typename S::Narrow{}) : s == kHalfShape ? of(typename S::Half{}) : s == kMediumShape ? of(typename S::Medium{}) : of(typename S::Large{});
   };
   return dtype == 0 ? by_shape(lin::Shapes<float>{}) : by_shape(lin::Shapes<_Float16>{});
 }
@@ -234,7 +234,11 @@ struct Product {
 //
 // More rows go by tiles.  Narrow ones for up to 64 columns (f32, 80,000 rows
 // 256 -> 64: 42 us by 128 columns, 31) and while tiles of 128 columns are
-// fewer than CUs (bf16: 3,000 rows 1024 -> 1024 29.5 and 20.7).  The largest
+// fewer than CUs (bf16: 3,000 rows 1024 -> 1024 29.5 and 20.7).  In f32 those
+// have 32 columns, or 64, whose rows are split into planes half as often,
+// where these fill the CUs or the contraction is long enough for parts of it
+// (69,924 rows 2448 -> 64 290 and 229 us, 2,500 rows 1024 -> 512 41 and 32;
+// but 20,000 rows 256 -> 64 14.6 and 20.3).  The largest
 // where they fill three quarters of their rounds of one workgroup a CU
 // (8192 x 4096 x 4096: 250 us, by 128 x 128 322; 9,000 rows, half of the last
 // round: 342 and 352; 6,000 rows: 224 and 236; 5,000 rows: 223 and 205).
@@ -252,6 +256,8 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
   } else {
     const int64_t medium = (rows / 128 + (cu == nullptr ? 1 : groups)) * div_up(n, 128);
     p.shape = n <= 64 || medium < 256 ? kNarrowShape : kMediumShape;
+    const int64_t half = (rows / 128 + (cu == nullptr ? 1 : groups)) * div_up(n, 64);
+    if (dtype == 0 && p.shape == kNarrowShape && n > 32 && (half >= 256 || k >= 1024)) p.shape = kHalfShape;
   }
   const int64_t large = div_up(rows, 256) * div_up(n, 256);
   if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 256 && 4 * large >= 3 * 256 * div_up(large, 256)) p.shape = kLargeShape;
@@ -315,7 +321,9 @@ ByRows plan_all_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
 // make for fewer parts to join (bf16, 256 x 256 sums: 100,000 rows 39 us by
 // 128 columns, 33; 1024 x 1024: 2,500 rows 28.9 and 24.2, 20,000 rows 64 and
 // 70; f32, 256 x 256: 2,500 rows 19.0 and 14.9, 20,000 rows 33 and 33, 80,000
-// rows 73 and 109).  The largest for long sums (400,000 rows of 256 x 1024:
+// rows 73 and 109); 64 columns in f32 by tiles of as many for longer ones, as
+// above (78,075 rows of 3176 x 40 335 and 251 us, 20,000 rows of 256 x 64 19.8
+// and 20.6).  The largest for long sums (400,000 rows of 256 x 1024:
 // 310 us by 128 x 128, 266; but 65,537 rows of 1024 x 256 60 and 66).
 Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t groups, int32_t m, int32_t n, Carver* w) {
   Product p;
@@ -323,6 +331,7 @@ Product plan_over_rows(int dtype, const int32_t* cu, int32_t rows, int32_t group
   p.dtype = dtype;
   const int64_t medium = div_up(m, 128) * div_up(n, 128);
   p.shape = n <= 64 || medium * rows < (dtype == 0 ? 1 << 16 : 1 << 19) ? kNarrowShape : kMediumShape;
+  if (dtype == 0 && n > 32 && n <= 64 && medium * rows >= 1 << 17) p.shape = kHalfShape;
   if (dtype != 0 && p.shape == kMediumShape && m > 128 && n > 128 && div_up(m, 256) * div_up(n, 256) * (rows / 64) >= 32 * 256) p.shape = kLargeShape;
   const ShapeSize s = shape_size(dtype, p.form, p.shape);
   ProductArgs& a = p.a;

@@ -72,19 +72,21 @@ struct Shape {
   static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, BK = BK_, STAGES = STAGES_;
   static constexpr int NT = 64 * WR * WC, TM = BM / WR, TN = BN / WC;
 };
-// Narrow: few columns, or too few tiles to fill the chip; Medium; Large: whole
-// large products.
+// Narrow: few columns, or too few tiles to fill the chip; Half (f32): up to 64
+// columns; Medium; Large: whole large products.
 template <class T>
 struct Shapes;
 template <class T>
 struct Shapes16 {
   typedef Shape<128, 64, 4, 1, 64, 2> Narrow;
+  typedef Narrow Half;
   typedef Shape<128, 128, 2, 2, 64, 2> Medium;
   typedef Shape<256, 256, 2, 4, 64, 2> Large;
 };
 template <>
 struct Shapes<float> {
   typedef Shape<128, 32, 4, 1, 32, 1> Narrow;
+  typedef Shape<128, 64, 4, 1, 32, 1> Half;
   typedef Shape<128, 128, 2, 2, 32, 1> Medium;
   typedef Medium Large;
 };

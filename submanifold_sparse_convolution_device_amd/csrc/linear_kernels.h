@@ -812,6 +812,7 @@ hipError_t launch_typed(const ProductArgs& a, ProductForm form, ProductShape sha
     return few(Two{}, std::integral_constant<int, 8>{});
   }
   if (shape == kNarrowShape) return by_form(typename Shapes<T>::Narrow{});
+  if (shape == kHalfShape) return by_form(typename Shapes<T>::Half{});
   if (shape == kMediumShape) return by_form(typename Shapes<T>::Medium{});
   return by_form(typename Shapes<T>::Large{});
 }

@@ -252,6 +252,16 @@ def test_rows_by_wavefronts_or_tiles(dtype, rows, c_in, c_out, lengths):
     _check_backward(x, w, _draw(dt, rows, c_out, seed=2), _draw(dt, rows, c_in, seed=3), "relu", cu)
 
 
+@pytest.mark.parametrize("rows,c_in,c_out,lengths", [
+    (2500, 1032, 500, None), (40011, 40, 264, None), (70001, 264, 57, None), (35000, 300, 64, [0, 20000, 33, 14900])])
+def test_fp32_by_64_columns(rows, c_in, c_out, lengths):
+    """Tiles of 64 columns, of the product and of both gradients."""
+    cu = None if lengths is None else _offsets(lengths)
+    x, w, b = _case(torch.float32, rows, c_in, c_out, 19, None if lengths is None else len(lengths))
+    _check_forward(x, w, b, "silu", None, cu)
+    _check_backward(x, w, _draw(torch.float32, rows, c_out, seed=2), cu=cu)
+
+
 def test_fp32_is_whole():
     """The rms error of fp32 products: additions leave about sqrt(k) / 2^25 of
     the result's rms, 2^-20 at k = 1024, and twice that is allowed; operands
