@@ -241,7 +241,10 @@ struct Product {
 // but 20,000 rows 256 -> 64 14.6 and 20.3).  The largest
 // where they fill three quarters of their rounds of one workgroup a CU
 // (8192 x 4096 x 4096: 250 us, by 128 x 128 322; 9,000 rows, half of the last
-// round: 342 and 352; 6,000 rows: 224 and 236; 5,000 rows: 223 and 205).
+// round: 342 and 352; 6,000 rows: 224 and 236; 5,000 rows: 223 and 205), or
+// five eighths of one where the contraction is long (5,700 rows 4096 -> 2048:
+// 122 us by 128 x 128, 110; 10,000 rows 2048 -> 1024 65 and 62; 21,000 rows 768
+// -> 512 31 and 32).
 Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t rows, int32_t groups, int32_t k, int32_t n, Carver* w) {
   Product p;
   p.form = form;
@@ -260,7 +263,8 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
     if (dtype == 0 && p.shape == kNarrowShape && n > 32 && (half >= 256 || k >= 1024)) p.shape = kHalfShape;
   }
   const int64_t large = div_up(rows, 256) * div_up(n, 256);
-  if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 256 && 4 * large >= 3 * 256 * div_up(large, 256)) p.shape = kLargeShape;
+  const bool filled = 4 * large >= 3 * 256 * div_up(large, 256) || (large >= 160 && large <= 256 && k >= 2048);
+  if (dtype != 0 && p.shape == kMediumShape && k >= 512 && n >= 192 && filled) p.shape = kLargeShape;
   const ShapeSize s = shape_size(dtype, p.form, p.shape);
   ProductArgs& a = p.a;
   a.cu = cu;
@@ -297,7 +301,7 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
 // 60 us by smaller tiles, 55 in two launches; 4097 x 4096 x 4096 194 and 140.)
 int32_t whole_rounds(int dtype, const int32_t* cu, int32_t rows, int32_t k, int32_t n) {
   const int64_t columns = div_up(n, 256), large = div_up(rows, 256) * columns;
-  if (dtype == 0 || cu != nullptr || k < 512 || n < 256 || large <= 256 || 4 * large >= 3 * 256 * div_up(large, 256)) return 0;
+  if (dtype == 0 || cu != nullptr || k < 512 || n < 192 || large <= 256 || 4 * large >= 3 * 256 * div_up(large, 256)) return 0;
   return static_cast<int32_t>(large / 256 * 256 / columns * 256);
 }
 
