@@ -236,7 +236,7 @@ struct Product {
 // 256 -> 64: 42 us by 128 columns, 31) and while tiles of 128 columns are
 // fewer than CUs (bf16: 3,000 rows 1024 -> 1024 29.5 and 20.7).  In f32 those
 // have 32 columns, or 64, whose rows are split into planes half as often,
-// where these fill the CUs or the contraction is long enough for parts of it
+// where these fill the CUs twice or the contraction is long enough for parts
 // (69,924 rows 2448 -> 64 290 and 229 us, 2,500 rows 1024 -> 512 41 and 32;
 // but 20,000 rows 256 -> 64 14.6 and 20.3).  The largest
 // where they fill three quarters of their rounds of one workgroup a CU
@@ -260,7 +260,7 @@ Product plan_by_rows(ProductForm form, int dtype, const int32_t* cu, int32_t row
     const int64_t medium = (rows / 128 + (cu == nullptr ? 1 : groups)) * div_up(n, 128);
     p.shape = n <= 64 || medium < 256 ? kNarrowShape : kMediumShape;
     const int64_t half = (rows / 128 + (cu == nullptr ? 1 : groups)) * div_up(n, 64);
-    if (dtype == 0 && p.shape == kNarrowShape && n > 32 && (half >= 256 || k >= 1024)) p.shape = kHalfShape;
+    if (dtype == 0 && p.shape == kNarrowShape && n > 32 && (half >= 512 || k >= 1024)) p.shape = kHalfShape;
   }
   const int64_t large = div_up(rows, 256) * div_up(n, 256);
   const bool filled = 4 * large >= 3 * 256 * div_up(large, 256) || (large >= 160 && large <= 256 && k >= 2048);
