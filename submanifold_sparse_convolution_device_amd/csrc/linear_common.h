@@ -124,6 +124,9 @@ __device__ __forceinline__ float tail(float a, float e) {
 // stored product past fp16's range needs it: a factor z beside one that is 0
 // there is held finite, and a NaN stays one through the other.
 __device__ __forceinline__ float held(float z) { return __builtin_amdgcn_fmed3f(z, -1e30f, 1e30f); }
+// z from `low` up, in one instruction (a maximum takes two, the first for NaN):
+// the largest fp32 value stands for infinity, which it rounds to in 16 bits.
+__device__ __forceinline__ float from(float low, float z) { return __builtin_amdgcn_fmed3f(z, low, 3.402823466e38f); }
 
 template <class T>
 __device__ __forceinline__ float relu(float z) {
@@ -133,13 +136,13 @@ template <class T>
 __device__ __forceinline__ float silu(float z) {
   // (to -inf the value is -0; held on that side alone)
   if constexpr (sizeof(T) == 4) return fmaxf(z, -1e30f) / (1.f + expf(-z));
-  return fmaxf(z, -1e30f) * sigmoid(z);
+  return from(-1e30f, z) * sigmoid(z);
 }
 template <class T>
 __device__ __forceinline__ float gelu(float z) {
   if constexpr (sizeof(T) == 4) return 0.5f * fmaxf(z, -1e30f) * (1.f + erff(z * 0.70710678f));
   // z - z t above 0, z t below (a NaN comes from the second part)
-  return __builtin_amdgcn_fmed3f(z, 0.f, __builtin_inff()) - __builtin_amdgcn_fmed3f(fabsf(z), 0.f, 1e30f) * tail(fabsf(z), attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e))));
+  return from(0.f, z) - __builtin_amdgcn_fmed3f(fabsf(z), 0.f, 1e30f) * tail(fabsf(z), attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e))));
 }
 template <class T>
 __device__ __forceinline__ float silu_slope(float z) {
