@@ -396,9 +396,9 @@ __global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
 
 // ---- Weights in registers ----
 // By rows with a short contraction (16 KS values at most): a workgroup of
-// WR x WC wavefronts keeps its columns of the weights in registers, CW blocks
-// of 32 a wavefront, and walks a run of slots of BM rows.  A tile's rows are
-// loaded one tile ahead and pass through LDS, where the WC wavefronts of the
+// WR x WC wavefronts keeps its columns of the weights in registers, 32 a
+// wavefront, and walks a run of slots of BM rows, RW blocks of 32 a wavefront.
+// A tile's rows are loaded one tile ahead and pass through LDS, where the WC wavefronts of the
 // same rows read them; the weights are read once, and a tile ends in one
 // barrier.  The sums go to memory straight from the registers: an exchange
 // between the halves of a wavefront gives each lane 8 neighbouring columns of
@@ -614,17 +614,16 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_stream(ProductArgs a, int chu
 
 // ---- Few rows ----
 // By rows with up to 128 rows of a group: a workgroup computes 32 rows by 32 CB
-// columns, and its 8 wavefronts take chunks of KC contracted values in turn,
+// columns, and its 4 or 8 wavefronts take chunks of KC contracted values in turn,
 // each by itself: both operands pass through the wavefront's own LDS, so that
 // its loads are of whole lines, with the next chunk's in flight during a
 // chunk (bf16, transposed: 128 groups of 20 rows 1024 -> 1024 46 us, 70 with
 // operands straight from memory, a line's quarter a lane; 8 groups of 80 rows
 // 11.7 and 18.9).  fp32 rows come straight, as their planes would take more of
 // LDS than the loads gain (32 groups of 20 rows 512 -> 256 13.4 us by LDS,
-// 11.3).  No wavefront waits for another before the
-// sums of all 8 are joined in LDS.  Bound by the weights' way from memory:
-// 5 rows 2048 -> 8192 in bf16 are 34 MB, 9.4 us (3.6 TB/s, a launch and the
-// join within it).
+// 11.3).  No wavefront waits for another before the sums of all of them are
+// joined in LDS.  Bound by the weights' way from memory: 5 rows 2048 -> 8192
+// in bf16 are 34 MB, 7.5 us (4.5 TB/s).
 template <class T, int CB, int WAVES_, int FORM>
 struct Few {
   static constexpr int KC = sizeof(T) == 4 ? 32 : 64, WAVES = WAVES_;
