@@ -15,7 +15,7 @@ UNIT = 2.0 ** -24
 DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 # the largest slope of gelu (1.1290) and silu (1.0999)
 STEEPEST = 1.13
-# an activation in 16-bit types: the tail's fit (7.6e-6) and a few units of the
+# an activation in 16-bit types: the tail's fit (1.2e-5 of at most 1/2) and a few units of the
 # exponential and reciprocal; in fp32 a few units of the library's functions
 ACT_ERROR = {torch.float32: 8 * UNIT, torch.float16: 1e-5, torch.bfloat16: 1e-5}
 
