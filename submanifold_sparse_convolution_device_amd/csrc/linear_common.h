@@ -102,23 +102,21 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + attn::fast_exp2(z * -attn::kLog2e));
 }
 
-// The normal distribution's lower tail at -a, a >= 0, is tail(a) exp(-a^2 / 2)
-// with tail(a) = c0 + c1 t + ... + c5 t^5, t = 1 / (1 + 0.36 a).  The
-// coefficients are a fit to erfcx of the smallest relative error, 1.2e-5 for a
-// up to 13.5, where the exponential ends: a fortieth of fp16's rounding, a
-// 160th of bf16's.  (c1 t + ... + c6 t^6 leaves 4.7e-6 for one instruction
-// more an element, a fifteenth of gelu.)
-__device__ __forceinline__ float tail(float a) {
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.36f, a, 1.f));
-  float p = -0.0988995433f;
-  p = __builtin_fmaf(p, t, 0.255400628f);
-  p = __builtin_fmaf(p, t, 0.034114074f);
-  p = __builtin_fmaf(p, t, 0.169156834f);
-  p = __builtin_fmaf(p, t, 0.140026048f);
-  return __builtin_fmaf(p, t, 0.000198978378f);
+// The normal distribution's lower tail at -a, a >= 0, as t (c1 + c2 t + ...
+// + c6 t^5) e with t = 1 / (1 + 0.31 a) and e = exp(-a^2 / 2).  The
+// coefficients are a fit to erfcx of the smallest relative error, 4.7e-6 for
+// a up to 13.5: a hundredth of fp16's rounding, a 400th of bf16's.  (One
+// coefficient fewer leaves 2.9e-5.)
+__device__ __forceinline__ float tail(float a, float e) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31f, a, 1.f));
+  float p = -0.073935856f;
+  p = __builtin_fmaf(p, t, 0.180469782f);
+  p = __builtin_fmaf(p, t, 0.0157236098f);
+  p = __builtin_fmaf(p, t, 0.133440446f);
+  p = __builtin_fmaf(p, t, 0.120438788f);
+  p = __builtin_fmaf(p, t, 0.123860916f);
+  return p * t * e;
 }
-// exp(-z^2 / 2)
-__device__ __forceinline__ float bell(float z) { return attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e))); }
 
 // act(z) and its derivative, of N values with one branch.  fp32 takes the
 // library's functions, whose errors are of fp32's size; 16-bit types the
@@ -144,7 +142,7 @@ template <class T>
 __device__ __forceinline__ float gelu(float z) {
   if constexpr (sizeof(T) == 4) return 0.5f * fmaxf(z, -1e30f) * (1.f + erff(z * 0.70710678f));
   // z - z t above 0, z t below (a NaN comes from the second part)
-  return from(0.f, z) - __builtin_amdgcn_fmed3f(fabsf(z), 0.f, 1e30f) * (tail(fabsf(z)) * bell(z));
+  return from(0.f, z) - __builtin_amdgcn_fmed3f(fabsf(z), 0.f, 1e30f) * tail(fabsf(z), attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e))));
 }
 template <class T>
 __device__ __forceinline__ float silu_slope(float z) {
@@ -155,7 +153,8 @@ template <class T>
 __device__ __forceinline__ float gelu_slope(float z) {
   constexpr float inv_root = 0.3989422804014327f;  // 1 / sqrt(2 pi)
   if constexpr (sizeof(T) == 4) return 0.5f * (1.f + erff(z * 0.70710678f)) + held(z) * inv_root * expf(-0.5f * z * z);
-  const float e = bell(z), t = tail(fabsf(z)) * e;
+  const float e = attn::fast_exp2(z * (z * (-0.5f * attn::kLog2e)));
+  const float t = tail(fabsf(z), e);
   return (z < 0.f ? t : 1.f - t) + held(z) * inv_root * e;
 }
 // f(i) for i < N, 4 at a time: the registers of all N together do not fit.

@@ -405,8 +405,8 @@ __global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
 // a row.  OCC: wavefronts on a SIMD.
 //
 // Bound by memory and, with an activation, by the vector units: 400,000 rows
-// 256 -> 1024 in bf16 are 1.02 GB, 293 to 327 us (3.1 to 3.5 TB/s); gelu's 14
-// vector instructions an element beside the products make it 416 us.
+// 256 -> 1024 in bf16 are 1.02 GB, 293 to 327 us (3.1 to 3.5 TB/s); gelu's 15
+// vector instructions an element beside the products make it 418 us.
 template <int KS_, int WR_, int WC_, int RW_, int OCC_>
 struct StreamShape {
   static constexpr int KS = KS_, WR = WR_, WC = WC_, RW = RW_, OCC = OCC_;

@@ -1,0 +1,40 @@
+"""Values of the activations inside the products of rows, seen past the rounding
+of the output: a residual that cancels the activation leaves its error."""
+import math
+
+import pytest
+import torch
+
+import submanifold_sparse_convolution_device_amd as sp
+from linear_reference import DTYPES, UNIT, act, rounding, smallest
+
+pytestmark = pytest.mark.gpu
+
+
+def _one(dtype, z, activation, residual=None):
+    """activation(z) + residual of single values, through products by 1."""
+    eye = torch.ones(1, 1, dtype=dtype, device="cuda")
+    return sp.linear(z[:, None].contiguous(), eye, activation=activation, residual=None if residual is None else residual[:, None].contiguous())[:, 0]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_gelu_below_its_rounding(dtype):
+    """gelu is z less |z| times the normal distribution's lower tail at -|z|,
+    or that product alone.  The tail's fit is off by 4.7e-6 of it.  Up to
+    |z| = 4 the exponential's argument is at most 11.6 (in powers of two) and
+    rounded twice and by its constant, 2.5 x 2^-24 of it: 1.2e-6 of the
+    result; the exponential, the reciprocal, the polynomial and the products
+    are off by a unit of 2^-23 each at most, ten of them 1.2e-6: 7.1e-6 of the
+    tail's product in all.  The difference and the addition of the residual
+    round by 2^-24 of z and of the residual, the output once."""
+    dt = DTYPES[dtype]
+    z = torch.cat([torch.linspace(-4, 4, 20001), torch.logspace(-3, 0, 2000), -torch.logspace(-3, 0, 2000)]).to(dt).cuda()
+    ref = act("gelu", z.double())
+    residual = (-ref).to(dt)
+    got = _one(dt, z, "gelu", residual).double()
+    want = ref + residual.double()
+    below = z.double().abs() * 0.5 * torch.erfc(z.double().abs() / math.sqrt(2))
+    bound = 7.1e-6 * below + UNIT * (z.double().abs() + residual.double().abs())
+    bound = bound + rounding(dt) * (want.abs() + bound) + smallest(dt)
+    over = (got - want).abs() / bound
+    assert float(over.max()) <= 1, f"{float(over.max())} of the bound at z = {float(z[over.argmax()])}"
