@@ -38,3 +38,30 @@ def test_gelu_below_its_rounding(dtype):
     bound = bound + rounding(dt) * (want.abs() + bound) + smallest(dt)
     over = (got - want).abs() / bound
     assert float(over.max()) <= 1, f"{float(over.max())} of the bound at z = {float(z[over.argmax()])}"
+
+
+@pytest.mark.parametrize("rows", [6, 300])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("activation", ["relu", "silu", "gelu"])
+def test_infinite_sums_with_a_residual(dtype, activation, rows):
+    """The activation of an infinite sum is infinite (or 0) when the residual
+    is added, whatever its size, in each of the products: few rows (6 and, by
+    parts of a long contraction, 1), tiles, and weights in registers."""
+    dt = DTYPES[dtype]
+    big = torch.finfo(dt).max
+    inf = math.inf
+    for c_in, c_out in ((8, 64), (8, 7), (2048, 64), (600, 64)):
+        x = torch.zeros(rows, c_in, dtype=dt, device="cuda")
+        x[:, 0] = torch.tensor([inf, inf, inf, -inf, inf, 1.0], dtype=dt).cuda().repeat(rows // 6)
+        w = torch.zeros(c_in, c_out, dtype=dt, device="cuda")
+        w[0] = 1
+        residual = torch.tensor([-big, -inf, inf, 5.0, 0.0, -big], dtype=dt).cuda().repeat(rows // 6)[:, None].expand(rows, c_out).contiguous()
+        for place in (None, residual.clone()):
+            res = residual if place is None else place
+            got, pre = sp.linear(x, w, activation=activation, residual=res, out=place, return_pre=True)
+            assert bool((pre[0::6] == inf).all()) and bool((pre[3::6] == -inf).all())
+            for at, want in ((0, inf), (2, inf), (3, 5.0), (4, inf), (5, -big)):
+                assert bool((got[at::6] == want).all()), (c_in, c_out, at, got[at, 0].item())
+            assert bool(got[1::6].isnan().all()), (c_in, c_out, got[1, 0].item())
+        one = sp.linear(x[:1], w, activation=activation, residual=residual[:1])
+        assert bool((one == inf).all())
