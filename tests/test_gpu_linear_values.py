@@ -65,3 +65,24 @@ def test_infinite_sums_with_a_residual(dtype, activation, rows):
             assert bool(got[1::6].isnan().all()), (c_in, c_out, got[1, 0].item())
         one = sp.linear(x[:1], w, activation=activation, residual=residual[:1])
         assert bool((one == inf).all())
+
+
+def test_fp32_gelu_keeps_its_lower_tail():
+    """Relative bounds down to z = -12, where gelu is -2e-32.  The error
+    function's argument z / sqrt 2 is off by 1.3 x 2^-24 of it (the constant's
+    rounding and the product's), which changes a tail exp(-z^2 / 2) / |z| by
+    1.3 (z^2 + 1) / 2^24 of it; the exponential's argument by 2 roundings, z^2
+    / 2^24.  The library's functions may be off by 16 units of 2^-23 (erfc)
+    and 3 (exp), a product or sum by a rounding."""
+    z = torch.cat([torch.linspace(-12, 12, 40001), -torch.logspace(-4, 0, 1000)]).float().cuda()
+    zd = z.double()
+    phi = 0.5 * torch.erfc(-zd / math.sqrt(2))
+    ref = zd * phi
+    share = (1.3 * (zd * zd + 1) * (zd < 0) + 1.3 * (zd >= 0) + 36) * UNIT
+    got = _one(torch.float32, z, "gelu").double()
+    over = (got - ref).abs() / (share * ref.abs() + 1e-300)
+    assert float(over.max()) <= 1, f"value: {float(over.max())} of the bound at z = {float(z[over.argmax()])}"
+    bell = zd * torch.exp(-0.5 * zd * zd) / math.sqrt(2 * math.pi)
+    got = sp.activation_backward(torch.ones_like(z)[None], z[None], "gelu")[0].double()
+    over = (got - (phi + bell)).abs() / (share * phi + (zd * zd + 12) * UNIT * bell.abs() + UNIT * (phi + bell).abs())
+    assert float(over.max()) <= 1, f"slope: {float(over.max())} of the bound at z = {float(z[over.argmax()])}"
