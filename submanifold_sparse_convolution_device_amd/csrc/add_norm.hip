@@ -58,6 +58,21 @@ __device__ __forceinline__ float row_sum(float v, float (&lds)[2][4], int turn) 
   return v;
 }
 
+// 1 / sqrt(mean + eps) of a row's sum of squares.  The unit's reciprocal root
+// is off by up to a unit of 2^-23, a root and a division by two roundings; the
+// step of Newton's method with its remainder in twice the precision leaves
+// one.  (r is a factor of a whole row: its error does not average out in what
+// sums over the row.)  Zeros, infinities and values below the normal range
+// have no remainder to work with.
+__device__ __forceinline__ float row_scale(float sq, const AddNormArgs& a) {
+  const float x = sq / static_cast<float>(a.channels) + a.eps;
+  if (!(x >= 1e-37f && x < 1e37f)) return 1.f / sqrtf(x);
+  const float r = __builtin_amdgcn_rsqf(x);
+  const float p = x * r, rest = __builtin_fmaf(x, r, -p);  // x r = p + rest
+  const float e = __builtin_fmaf(-p, r, 1.f) - rest * r;   // 1 - x r^2
+  return __builtin_fmaf(0.5f * r, e, r);
+}
+
 template <class T, int LANES, int P>
 __global__ __launch_bounds__(kThreads) void k_add_norm(AddNormArgs a) {
   constexpr int E = kE<T>, RPB = kThreads / LANES;
@@ -92,7 +107,7 @@ __global__ __launch_bounds__(kThreads) void k_add_norm(AddNormArgs a) {
 #pragma unroll
     for (int u = 0; u < E; ++u) sq = __builtin_fmaf(h[i][u], h[i][u], sq);
   }
-  const float r = 1.f / sqrtf(row_sum<LANES>(sq, sums, 0) / static_cast<float>(a.channels) + a.eps);
+  const float r = row_scale(row_sum<LANES>(sq, sums, 0), a);
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int e = (i * LANES + lane) * E;
@@ -147,13 +162,12 @@ __global__ __launch_bounds__(kThreads) void k_add_norm_backward(AddNormArgs a, f
         th = __builtin_fmaf(g[u] * w[i][u], h[u], th);
       }
     }
-    const float inv = 1.f / static_cast<float>(a.channels);
     sq = row_sum<LANES>(sq, sums, turn);
     if constexpr (LANES > 64) turn ^= 1;
     th = row_sum<LANES>(th, sums, turn);
     if constexpr (LANES > 64) turn ^= 1;
-    const float r = 1.f / sqrtf(sq * inv + a.eps);
-    const float m = th * inv * r * r;
+    const float r = row_scale(sq, a);
+    const float m = th / static_cast<float>(a.channels) * r * r;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int e = (i * LANES + lane) * E;
