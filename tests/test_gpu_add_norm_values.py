@@ -40,3 +40,25 @@ def test_factor_at_the_ends():
         else:
             # (squares below the normal range keep few bits: 2^-140 has 9)
             assert bool(((y - want).abs() <= (2.0 ** -8 if value == 2.0 ** -70 else 2.0 ** -22)).all()), (value, y[0, 0].item())
+
+
+@pytest.mark.parametrize("rows,channels", [(100003, 96), (24001, 1024), (400000, 32)])
+def test_weight_gradient_sums(rows, channels):
+    """The rms error of the weight gradient, in roundings: one leaves 0.425 x
+    2^-24 of a value in the mean (uniform in a step, over the steps' places
+    between two powers of two).  Terms of either sign add up to the root of
+    the sum of their squares, which measures the error: a chain of m additions
+    leaves the mean error of (m + 1) / 2 roundings of its sum.  The rows of one
+    lane are a chain of at most 13 (100003 rows by 512 workgroups of 16, 24001
+    by 512 of 4, 400000 by 1024 of 32), 7 roundings; a term's product and its
+    row's factor 2.5; a workgroup's sum and the last one, each rounded from 64
+    bits, 2: 11.5.  22 allowed, as the error of 32 columns is 11.5 +- 2.9."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    h, gy = (torch.randn(rows, channels, generator=g, device="cuda") for _ in range(2))
+    w = torch.ones(channels, device="cuda")
+    _, gw = sp.add_norm_backward(None, gy, h, w)
+    x = h.double()
+    terms = gy.double() * x / torch.sqrt(x.square().mean(-1, keepdim=True) + 1e-6)
+    far = (gw.double() - terms.sum(0)).square().mean().sqrt() / terms.square().sum(0).mean().sqrt()
+    roundings = (float(far) / (0.425 * UNIT)) ** 2
+    assert roundings <= 22, roundings
