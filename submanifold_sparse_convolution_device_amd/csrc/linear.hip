@@ -314,7 +314,16 @@ struct ByRows {
 ByRows plan_all_rows(ProductForm form, int dtype, const int32_t* cu, int32_t rows, int32_t groups, int32_t k, int32_t n, Carver* w) {
   ByRows b;
   b.head = whole_rounds(dtype, cu, rows, k, n);
+  const Carver before = *w;
   b.p = plan_by_rows(form, dtype, cu, b.head == 0 ? rows : b.head, groups, k, n, w);
+  if (b.head != 0 && b.p.shape != kLargeShape) {
+    // (many columns: whole rows of tiles are too little of a round for the
+    // largest ones, and two launches would read all weights twice for nothing:
+    // bf16, 300 rows 1024 -> 33,000 63 us, in one 49)
+    b.head = 0;
+    *w = before;
+    b.p = plan_by_rows(form, dtype, cu, rows, groups, k, n, w);
+  }
   if (b.head != 0) b.rest = plan_by_rows(form, dtype, cu, rows - b.head, groups, k, n, w);
   return b;
 }
