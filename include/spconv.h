@@ -736,8 +736,8 @@ typedef struct spconv_add_norm {
 
 /* Writes d_h (NULL without a residual) and d_y.  Either may be x or the
  * residual in its place (same pointer and stride); otherwise they share no
- * byte with an input or each other.  Errors: INVALID_ARG, UNSUPPORTED (dtype,
- * channels), DEVICE. */
+ * byte with an input or each other.  Errors: INVALID_ARG (also for a launch of
+ * 2^32 work items), UNSUPPORTED (dtype, channels), DEVICE. */
 spconv_status spconv_add_norm_forward(const spconv_add_norm* args, void* d_h, int64_t h_row_stride, void* d_y,
                                       int64_t y_row_stride, void* hip_stream);
 
@@ -788,7 +788,8 @@ spconv_status spconv_add_norm_backward_noalloc(const spconv_add_norm* args, cons
  *
  * Operands are multiplied in dtype and summed in fp32; F32 operands are used
  * whole (split exactly into three bf16 parts each, as in attention above: an
- * infinity among them gives NaN).  The epilogue is fp32 and each output is
+ * infinity among them gives NaN, and an operand below 2^-109 in size loses what
+ * lies below 2^-133 of it).  The epilogue is fp32 and each output is
  * rounded once.  GELU is z times the normal distribution's integral (the
  * error function's form), SILU is z / (1 + exp(-z)); RELU has slope 0 at 0.
  * At infinite z an activation and its slope take their limits.

@@ -211,8 +211,8 @@ __global__ __launch_bounds__(kThreads) void k_add_norm_backward(AddNormArgs a, f
 
 // dw[c] = sum over the blocks' partial sums, in a fixed order: 32 columns by
 // 32 shares of the blocks a workgroup.  In 64 bits, as the sums of a block's
-// rows above: in fp32 these chains, whose sums are the largest, left as much
-// as all additions before (100,003 rows of 96 in f32: 1.7e-7 of the gradient's
+// rows above: in fp32 these chains, whose sums are the largest, left more than
+// all additions before (100,003 rows of 96 in f32: 1.7e-7 of the gradient's
 // norm, 0.8e-7 so).
 __global__ __launch_bounds__(1024) void k_add_norm_weight_sum(const float* part, int blocks, int channels, float* dw) {
   __shared__ double stage[32][33];

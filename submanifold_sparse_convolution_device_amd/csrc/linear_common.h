@@ -72,8 +72,10 @@ struct Shape {
   static constexpr int BM = BM_, BN = BN_, WR = WR_, WC = WC_, BK = BK_, STAGES = STAGES_;
   static constexpr int NT = 64 * WR * WC, TM = BM / WR, TN = BN / WC;
 };
-// Narrow: few columns, or too few tiles to fill the chip; Half (f32): up to 64
-// columns; Medium; Large: whole large products.
+// Narrow: few columns, or too few tiles to fill the chip; Half (f32): 64
+// columns a tile for up to as many, and by rows also in Narrow's place where
+// its tiles fill the CUs twice or the contraction is long; Medium; Large:
+// whole large products.
 template <class T>
 struct Shapes;
 template <class T>

@@ -15,17 +15,19 @@
 // next step's loads are in flight during this step's products.  fp32 operands
 // go into LDS as three bf16 planes (attention_common.h).
 //
-// Bound by the matrix cores where sums are long: 8192 x 4096 x 4096 at 1.0 to
-// 1.1 PFLOP/s (f16: 275 us by rows, 262 transposed, 264 over rows), as the
-// chip's power holds its clock (about 2 GHz) under such products: they are
-// issued in 48% of the cycles, LDS is busy in 33%.  Writing the next step's
-// tiles between the products rather than after them took 291 us to 275 there;
-// two steps of loads in flight, halves of a workgroup in opposite phases and
-// the epilogue between the next tile's products were no faster or slower.
+// Where sums are long the matrix cores are busy in 53% of the cycles, LDS in
+// 33%, at a clock of about 2 GHz: 8192 x 4096 x 4096 at 1.0 to 1.1 PFLOP/s (f16:
+// 273 us by rows, 268 transposed, 279 over rows).  The library's products there
+// take 0.72 to 0.89 of the time by rows and transposed and 0.91 to 1.04 over
+// rows, so the clock alone is not what bounds these; the operands' way through
+// registers into LDS between the products may be.  Writing the next step's
+// tiles between the products rather than after them took 291 us to 275 by rows;
+// two steps of loads in flight, halves of a workgroup in opposite phases and the
+// epilogue between the next tile's products were no faster or slower.
 //
 // The products run as C^T = B^T A^T, so a lane holds 4 neighbouring columns of
 // one row; the sums pass through the wavefront's own LDS into whole rows, 8
-// columns a lane, for the epilogue (finish8) and 16-byte accesses.
+// columns a lane, for the epilogue (finish) and 16-byte accesses.
 #pragma once
 
 #include <algorithm>
@@ -406,7 +408,7 @@ __global__ __launch_bounds__(S::NT) void k_product(ProductArgs a) {
 //
 // Bound by memory and, with an activation, by the vector units: 400,000 rows
 // 256 -> 1024 in bf16 are 1.02 GB, 293 to 327 us (3.1 to 3.5 TB/s); gelu's 15
-// vector instructions an element beside the products make it 418 us.
+// vector instructions an element beside the products make it 416 us.
 template <int KS_, int WR_, int WC_, int RW_, int OCC_>
 struct StreamShape {
   static constexpr int KS = KS_, WR = WR_, WC = WC_, RW = RW_, OCC = OCC_;
@@ -613,8 +615,9 @@ __global__ __launch_bounds__(S::NT, S::OCC) void k_stream(ProductArgs a, int chu
 }
 
 // ---- Few rows ----
-// By rows with up to 128 rows of a group: a workgroup computes 32 rows by 32 CB
-// columns, and its 4 or 8 wavefronts take chunks of KC contracted values in turn,
+// By rows with up to 128 rows of a group on average (a group may have any
+// number): a workgroup computes 32 rows by 32 CB columns, and its 4 or 8
+// wavefronts take chunks of KC contracted values in turn,
 // each by itself: both operands pass through the wavefront's own LDS, so that
 // its loads are of whole lines, with the next chunk's in flight during a
 // chunk (bf16, transposed: 128 groups of 20 rows 1024 -> 1024 46 us, 70 with
